@@ -29,7 +29,11 @@ EXPORTS = ("fp8sg_status_string", "fp8sg_version", "amp_norm_workspace_len", "fp
            "fp8_scaled_linear_bwd_rowwise", "fp8_scaled_linear_bwd_unscale", "fp8_gemm_unscale",
            "fp8_scaled_linear_bwd_delayed_unscale", "fp8_scaled_linear_bwd_rowwise_unscale",
            "fp8_quantize_from_amax", "amp_unscale_check_norm_noalloc", "fp8_amax_f16",
-           "fp8_quantize_f16", "fp8_gemm_kmajor", "fp8_gemm_kmajor_unscale", "fp8_linear_copies")
+           "fp8_quantize_f16", "fp8_gemm_kmajor", "fp8_gemm_kmajor_unscale", "fp8_linear_copies",
+           "mxfp4_code_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize",
+           "mxfp4_gemm", "mxfp4_linear_fwd", "mxfp4_linear_bwd", "mxfp4_linear_apply",
+           "act8_quantize", "act8_dequantize", "swiglu_fwd", "swiglu_bwd", "layer_norm_fwd",
+           "layer_norm_workspace_len", "layer_norm_bwd")
 MAX_HISTORY = 1024
 MAX_DIM = 1 << 29     # largest matrix dimension an entry point takes
 MAX_ELEMS = 1 << 35   # largest tensor, in elements
@@ -117,6 +121,7 @@ def lib():
                                                         ctypes.POINTER(_BwdWsRW), P, P, P, P, P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = i
+    _bind_mx(L)
     _lib = L
     return L
 
@@ -789,3 +794,12 @@ def amp_update_scale(scale: torch.Tensor, growth_tracker: torch.Tensor, found_in
     _check(lib().amp_update_scale(_ptr(scale), _ptr(growth_tracker), _ptr(found_inf),
                                   growth_factor, backoff_factor, growth_interval, _stream(stream)),
            "amp_update_scale")
+
+
+# The microscaled formats, the gated activation and the layer norm (the
+# module uses the checks above, so it is imported last).
+from .mx import (MX_FIT, MX_FLOOR, Act8, Mxfp4, Mxfp4LinearSaved, Mxfp4LinearWs,  # noqa: E402, F401
+                 act8_dequantize, act8_quantize, layer_norm_bwd, layer_norm_fwd,
+                 layer_norm_workspace_len, mxfp4_dequantize, mxfp4_gemm, mxfp4_linear_apply,
+                 mxfp4_linear_bwd, mxfp4_linear_fwd, mxfp4_quantize, swiglu_bwd, swiglu_fwd)
+from .mx import bind as _bind_mx  # noqa: E402

@@ -1,0 +1,157 @@
+// Device helpers of the microscaled formats: MXFP4 matrices (mxfp4_operand in
+// the C ABI) and 8-bit activation checkpoints (fp8sg_act8).
+//
+// A block of 32 values shares one power of two 2^(s - 127).  Its exponent comes
+// from the bits of the block's largest magnitude, and dividing by a power of
+// two is exact, so quantising needs no rounding but the element's own: the
+// gfx950 converts take the scale as an operand, divide by it and round to
+// nearest even with saturation (checked over every bf16 and fp16 value and
+// scales from 2^-127 to 2^125 against the definition).
+#pragma once
+
+#include "common.hpp"
+#include "launch_mx.hpp"
+
+namespace fp8sg {
+
+// ---- element types (fp8sg_out values): one element as fp32, exactly
+template <int T>
+struct ElemOf { typedef uint16_t type; };
+template <>
+struct ElemOf<FP8SG_OUT_F32> { typedef float type; };
+template <int T>
+using Elem = typename ElemOf<T>::type;
+
+template <int T>
+__device__ __forceinline__ float to_f32(Elem<T> v) {
+  if constexpr (T == FP8SG_OUT_BF16) return __uint_as_float((uint32_t)v << 16);
+  else if constexpr (T == FP8SG_OUT_F16) return (float)__builtin_bit_cast(_Float16, v);
+  else return v;
+}
+// fp32 -> element, rounded once to nearest even
+template <int T>
+__device__ __forceinline__ Elem<T> from_f32(float v) {
+  if constexpr (T == FP8SG_OUT_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else if constexpr (T == FP8SG_OUT_F16) return __builtin_bit_cast(uint16_t, (_Float16)fp32_value(v));
+  else return v;
+}
+
+// ---- block scales
+// Scale byte of a block whose largest magnitude has the fp32 bits `amax` (sign
+// cleared): floor(log2 amax) is the exponent field, so floor(log2 amax) - emax
+// + 127 = field - emax.  `fit` raises it by one where the mantissa exceeds the
+// largest element's (kMant: 1.5 for e2m1's 6, 1.75 for e4m3's 448), up to
+// 254 - emax - 2, where the largest element times the scale is still finite
+// (floor never exceeds that).  Subnormal magnitudes count as field 0: they
+// lie below 2^-126, far under the smallest scale's range.
+template <int EMAX, uint32_t kMant>
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax, bool fit) {
+  if (amax >= 0x7F800000u) return 255u;
+  int e = (int)(amax >> 23) - EMAX;
+  if (fit && (amax & 0x7FFFFFu) > kMant) e = e + 1 < 254 - EMAX ? e + 1 : 254 - EMAX;
+  return (uint32_t)(e > 0 ? e : 0);
+}
+__device__ __forceinline__ uint32_t fp4_scale(uint32_t amax, bool fit) {
+  return block_scale<2, 0x400000u>(amax, fit);
+}
+__device__ __forceinline__ uint32_t act8_scale(uint32_t amax) {
+  return block_scale<8, 0x600000u>(amax, true);
+}
+// 2^(s - 127) as fp32 (s = 0: the subnormal 2^-127); s = 255: NaN
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  if (s == 255u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(s ? s << 23 : 0x00400000u);
+}
+
+// Two fp32 values to one byte of e2m1 codes (first value in the low half).
+__device__ __forceinline__ uint32_t fp4_pair(float a, float b, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a, b, scale, 0) & 0xFFu;
+}
+
+// e4m3 codes of values in a block with scale byte s: v * 2^(127 - s) is exact
+// (or far below half the smallest code), and a magnitude past 448, possible
+// only where the scale is at its upper end, is clamped.
+__device__ __forceinline__ float act8_inv(uint32_t s) {
+  // 2^(127 - s), s in [0, 246]: exponent field 254 - s >= 8
+  return __uint_as_float((254u - s) << 23);
+}
+__device__ __forceinline__ float act8_clamp(float v) { return fminf(fmaxf(v, -kE4M3Max), kE4M3Max); }
+// Eight values of a block with scale byte s to eight codes (s = 255: zeros).
+__device__ __forceinline__ uint2 act8_codes(const float (&v)[8], uint32_t s) {
+  if (s == 255u) return make_uint2(0, 0);
+  const float inv = act8_inv(s);
+  return make_uint2(cvt4<FP8SG_E4M3FN>(act8_clamp(v[0] * inv), act8_clamp(v[1] * inv), act8_clamp(v[2] * inv),
+                                       act8_clamp(v[3] * inv)),
+                    cvt4<FP8SG_E4M3FN>(act8_clamp(v[4] * inv), act8_clamp(v[5] * inv), act8_clamp(v[6] * inv),
+                                       act8_clamp(v[7] * inv)));
+}
+// Eight codes back to values.
+__device__ __forceinline__ void act8_values(uint2 q, uint32_t s, float (&v)[8]) {
+  const float sc = scale_value(s);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = (int)(h ? q.y : q.x);
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    v[4 * h] = lo[0] * sc;
+    v[4 * h + 1] = lo[1] * sc;
+    v[4 * h + 2] = hi[0] * sc;
+    v[4 * h + 3] = hi[1] * sc;
+  }
+}
+// Largest magnitude (fp32 bits) of the 32 values that four neighbouring lanes
+// hold eight each of; every lane of the four gets it.  All lanes active.
+__device__ __forceinline__ uint32_t quad_amax(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t a = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+    m = a > m ? a : m;
+  }
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false);
+  m = o > m ? o : m;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false);
+  return o > m ? o : m;
+}
+
+// ---- eight consecutive elements of a row.  VEC: the address is 16-byte
+// aligned and all eight are in range; otherwise element by element, those at
+// or past `n` reading 0 and not written.  S: non-temporal.
+template <int T, bool VEC, bool S>
+__device__ __forceinline__ void load8(const Elem<T>* p, int n, float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (T == FP8SG_OUT_F32) {
+      const uint4 a = ld16<S>(p), b = ld16<S>(p + 4);
+      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+      constexpr bool H = T == FP8SG_OUT_F16;
+      const uint4 a = ld16<S>(p);
+      v[0] = in_lo<H>(a.x); v[1] = in_hi<H>(a.x); v[2] = in_lo<H>(a.y); v[3] = in_hi<H>(a.y);
+      v[4] = in_lo<H>(a.z); v[5] = in_hi<H>(a.z); v[6] = in_lo<H>(a.w); v[7] = in_hi<H>(a.w);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? to_f32<T>(p[e]) : 0.f;
+  }
+}
+template <int T, bool VEC, bool S>
+__device__ __forceinline__ void store8(Elem<T>* p, int n, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (T == FP8SG_OUT_F32) {
+      st16<S>(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+      st16<S>(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (uint32_t)from_f32<T>(v[2 * e]) | ((uint32_t)from_f32<T>(v[2 * e + 1]) << 16);
+      st16<S>(p, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = from_f32<T>(v[e]);
+  }
+}
+
+}  // namespace fp8sg

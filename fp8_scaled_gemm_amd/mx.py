@@ -1,0 +1,445 @@
+"""Binding of the microscaled formats (MXFP4 matrices, 8-bit activation
+checkpoints), the gated activation and the layer norm: include/fp8sg.h's entry
+points of the same names, on the current torch stream.  Its names are those of
+the package (`import fp8_scaled_gemm_amd as F; F.mxfp4_gemm(...)`).
+
+Argument marshalling only, as in the package itself: every buffer's dtype,
+shape, strides and device are checked here, before the library is called.
+"""
+import ctypes
+
+import torch
+
+from . import _check, _need, _ptr, _stream, lib
+
+MX_FLOOR, MX_FIT = 0, 1
+
+_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _Pair(ctypes.Structure):  # mxfp4_operand and fp8sg_act8
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+
+
+class _LinSaved(ctypes.Structure):
+    _fields_ = [("x_qT", _Pair), ("w_qT", _Pair)]
+
+
+class _LinWs(ctypes.Structure):
+    _fields_ = [("x_q", _Pair), ("w_q", _Pair), ("gy_q", _Pair), ("gy_qT", _Pair)]
+
+
+def bind(L):
+    """Argument types of this module's entry points."""
+    P, i64, i, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    L.mxfp4_code_bytes.argtypes = L.mxfp4_scale_bytes.argtypes = [i64, i64]
+    L.mxfp4_quantize.argtypes = [P, i, i64, i64, i, P, P, P]
+    L.mxfp4_dequantize.argtypes = [P, i64, i64, P, i, P]
+    L.mxfp4_gemm.argtypes = [P, P, P, i, i64, i64, i64, P]
+    L.mxfp4_linear_fwd.argtypes = [P, P, i, i64, i64, i64, i, P, P, P, i, P]
+    L.mxfp4_linear_bwd.argtypes = [P, i, i64, i64, i64, i, P, P, P, P, i, P]
+    L.mxfp4_linear_apply.argtypes = [P, i, P, i64, i64, i64, i, P, P, i, P]
+    L.act8_quantize.argtypes = [P, i, i64, i64, P, P]
+    L.act8_dequantize.argtypes = [P, i64, i64, P, i, P]
+    L.swiglu_fwd.argtypes = [P, i64, P, i64, i, i64, i64, P, P, P, P]
+    L.swiglu_bwd.argtypes = [P, P, i64, P, i64, P, P, i, i64, i64, P, i64, P, i64, P]
+    L.layer_norm_fwd.argtypes = [P, i, P, P, i, i64, i64, f32, P, P, P, P, P]
+    L.layer_norm_workspace_len.argtypes = [i64, i64]
+    L.layer_norm_bwd.argtypes = [P, P, P, i, P, i, P, P, i64, i64, P, P, P, P, i64, P]
+    for name in ("mxfp4_code_bytes", "mxfp4_scale_bytes", "layer_norm_workspace_len"):
+        getattr(L, name).restype = i64
+
+
+def _here(*tensors):
+    """Every tensor is on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("tensor arguments must be device tensors")
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}: "
+                             "call under torch.cuda.device(...)")
+
+
+def _type(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    ty = _TYPE.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16, float16 or float32")
+    return ty
+
+
+def _rule(rule):
+    if rule not in (MX_FLOOR, MX_FIT):
+        raise ValueError(f"rule must be MX_FLOOR or MX_FIT, not {rule!r}")
+    return rule
+
+
+def _matrix(t, name):
+    """(rows, cols) of a contiguous matrix; leading dimensions count as rows."""
+    _type(t, name)
+    if t.dim() < 1:
+        raise ValueError(f"{name}: expected at least one dimension")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    cols = t.shape[-1]
+    return (t.numel() // cols if cols else _rows(t)), cols
+
+
+def _rows(t):
+    n = 1
+    for d in t.shape[:-1]:
+        n *= d
+    return n
+
+
+def _bytes(rows, k, what, fn):
+    n = fn(rows, k)
+    if n < 0:
+        raise ValueError(f"{what}: {rows} x {k} is outside the size limits")
+    return n
+
+
+class Mxfp4:
+    """An MXFP4 matrix, rows x k (mxfp4_operand): codes q and scales s, two
+    uint8 device tensors, uninitialised until a call writes them."""
+
+    def __init__(self, rows: int, k: int, device="cuda", tensors=None):
+        self.rows, self.k = rows, k
+        L = lib()
+        nq = _bytes(rows, k, "Mxfp4", L.mxfp4_code_bytes)
+        ns = _bytes(rows, k, "Mxfp4", L.mxfp4_scale_bytes)
+        if tensors is None:
+            self.q = torch.empty(nq, dtype=torch.uint8, device=device)
+            self.s = torch.empty(ns, dtype=torch.uint8, device=device)
+        else:  # the two buffers of another Mxfp4 of the same size
+            self.q, self.s = tensors
+            _need(self.q, "q", torch.uint8, numel=nq)
+            _need(self.s, "s", torch.uint8, numel=ns)
+
+    def tensors(self):
+        return self.q, self.s
+
+    def c(self):
+        return _Pair(self.q.data_ptr(), self.s.data_ptr())
+
+
+class Act8:
+    """An 8-bit checkpoint of a rows x cols activation (fp8sg_act8)."""
+
+    def __init__(self, rows: int, cols: int, device="cuda", tensors=None):
+        if rows < 0 or cols < 0:
+            raise ValueError(f"Act8: {rows} x {cols}")
+        self.rows, self.cols = rows, cols
+        blocks = -(-cols // 32)
+        if tensors is None:
+            self.q = torch.empty((rows, 32 * blocks), dtype=torch.uint8, device=device)
+            self.s = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+        else:
+            self.q, self.s = tensors
+            _need(self.q, "q", torch.uint8, shape=(rows, 32 * blocks))
+            _need(self.s, "s", torch.uint8, shape=(rows, blocks))
+
+    def tensors(self):
+        return self.q, self.s
+
+    def c(self):
+        return _Pair(self.q.data_ptr(), self.s.data_ptr())
+
+
+def _need_codes(m, name, kind, rows, cols):
+    if not isinstance(m, kind):
+        raise TypeError(f"{name}: expected {kind.__name__}, got {type(m).__name__}")
+    got = (m.rows, m.k) if kind is Mxfp4 else (m.rows, m.cols)
+    if got != (rows, cols):
+        raise ValueError(f"{name}: {got[0]} x {got[1]}, expected {rows} x {cols}")
+
+
+def _ref(pair):
+    return ctypes.addressof(pair) if pair is not None else None
+
+
+# ------------------------------------------------------------------- MXFP4
+
+def mxfp4_quantize(x: torch.Tensor, q: Mxfp4 = None, qT: Mxfp4 = None, rule: int = MX_FLOOR, stream=None):
+    """Codes of x (rows x cols) along its rows into q (rows x cols) and / or along
+    its columns into qT (cols x rows)."""
+    rows, cols = _matrix(x, "x")
+    if q is None and qT is None:
+        raise ValueError("mxfp4_quantize: q or qT is needed")
+    args = []
+    for m, name, shape in ((q, "q", (rows, cols)), (qT, "qT", (cols, rows))):
+        if m is not None:
+            _need_codes(m, name, Mxfp4, *shape)
+            _here(m.q, m.s)
+        args.append(m.c() if m is not None else None)
+    _here(x)
+    _check(lib().mxfp4_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _rule(rule), _ref(args[0]), _ref(args[1]),
+                                _stream(stream)), "mxfp4_quantize")
+
+
+def mxfp4_dequantize(m: Mxfp4, y: torch.Tensor, stream=None):
+    """The values of m's codes into y (rows x k)."""
+    rows, k = _matrix(y, "y")
+    _need_codes(m, "m", Mxfp4, rows, k)
+    _here(y, m.q, m.s)
+    c = m.c()
+    _check(lib().mxfp4_dequantize(_ref(c), rows, k, _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_dequantize")
+
+
+def mxfp4_gemm(A: Mxfp4, B: Mxfp4, C: torch.Tensor, stream=None):
+    """C[M,N] = A[M,K] B[N,K]^T in C's dtype."""
+    M, N = _matrix(C, "C")
+    for m, name in ((A, "A"), (B, "B")):
+        if not isinstance(m, Mxfp4):
+            raise TypeError(f"{name}: expected Mxfp4, got {type(m).__name__}")
+    _need_codes(A, "A", Mxfp4, M, A.k)
+    _need_codes(B, "B", Mxfp4, N, A.k)
+    _here(C, A.q, A.s, B.q, B.s)
+    a, b = A.c(), B.c()
+    _check(lib().mxfp4_gemm(_ref(a), _ref(b), _ptr(C), _TYPE[C.dtype], M, N, A.k, _stream(stream)), "mxfp4_gemm")
+
+
+class Mxfp4LinearSaved:
+    """What the forward of an M x N x K MXFP4 linear leaves for its backward."""
+
+    def __init__(self, M, N, K, device="cuda", tensors=None):
+        self.dims = (M, N, K)
+        t = tensors or (None, None, None, None)
+        self.x_qT = Mxfp4(K, M, device, t[0:2] if tensors else None)
+        self.w_qT = Mxfp4(K, N, device, t[2:4] if tensors else None)
+
+    def tensors(self):
+        return self.x_qT.tensors() + self.w_qT.tensors()
+
+    def c(self):
+        return _LinSaved(self.x_qT.c(), self.w_qT.c())
+
+
+class Mxfp4LinearWs:
+    """Operands that live within one forward or backward call.  The two calls
+    use different ones; calls that may overlap in time need a workspace each."""
+
+    def __init__(self, M, N, K, device="cuda", forward=True, backward=True):
+        self.dims = (M, N, K)
+        self.x_q = Mxfp4(M, K, device) if forward else None
+        self.w_q = Mxfp4(N, K, device) if forward else None
+        self.gy_q = Mxfp4(M, N, device) if backward else None
+        self.gy_qT = Mxfp4(N, M, device) if backward else None
+
+    def c(self):
+        return _LinWs(*[m.c() if m is not None else _Pair() for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT)])
+
+
+def _linear(obj, kind, name, dims, fields):
+    if not isinstance(obj, kind):
+        raise TypeError(f"{name}: expected {kind.__name__}, got {type(obj).__name__}")
+    if obj.dims != dims:
+        raise ValueError(f"{name}: made for a layer of {obj.dims}, not {dims}")
+    for f in fields:
+        m = getattr(obj, f)
+        if m is None:
+            raise ValueError(f"{name}: made without {f}")
+        _here(m.q, m.s)
+
+
+def mxfp4_linear_fwd(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSaved, y: torch.Tensor,
+                     rule: int = MX_FLOOR, stream=None):
+    """y[M,N] = x[M,K] w[N,K]^T with both operands quantised to MXFP4; saved (or
+    None) receives what the backward needs."""
+    M, K = _matrix(x, "x")
+    N, K2 = _matrix(w, "w")
+    if w.dtype != x.dtype:
+        raise TypeError(f"w: dtype {w.dtype}, expected x's {x.dtype}")
+    if K2 != K:
+        raise ValueError(f"w: {K2} columns, expected {K}")
+    _type(y, "y")
+    _need(y, "y", y.dtype, shape=x.shape[:-1] + (N,))
+    _here(x, w, y)
+    _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("x_q", "w_q"))
+    sv = None
+    if saved is not None:
+        _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
+        sv = saved.c()
+    wc = ws.c()
+    _check(lib().mxfp4_linear_fwd(_ptr(x), _ptr(w), _TYPE[x.dtype], M, N, K, _rule(rule), _ref(wc), _ref(sv),
+                                  _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_linear_fwd")
+
+
+def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSaved, gx: torch.Tensor,
+                     gw: torch.Tensor, rule: int = MX_FLOOR, stream=None):
+    """gx[M,K] = gy[M,N] W and gw[N,K] = gy^T x from what the forward saved."""
+    M, N = _matrix(gy, "gy")
+    M2, K = _matrix(gx, "gx")
+    if M2 != M:
+        raise ValueError(f"gx: {M2} rows, expected {M}")
+    _need(gw, "gw", gx.dtype, shape=(N, K))
+    _here(gy, gx, gw)
+    _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("gy_q", "gy_qT"))
+    _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
+    wc, sv = ws.c(), saved.c()
+    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), _ref(wc), _ref(sv), _ptr(gx),
+                                  _ptr(gw), _TYPE[gx.dtype], _stream(stream)), "mxfp4_linear_bwd")
+
+
+def mxfp4_linear_apply(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: Mxfp4, rule: int = MX_FLOOR, stream=None):
+    """y[M,N] = x[M,K] w^T with the weight held as MXFP4 (N x K); ws: scratch (M x K)."""
+    M, K = _matrix(x, "x")
+    if not isinstance(w, Mxfp4):
+        raise TypeError(f"w: expected Mxfp4, got {type(w).__name__}")
+    _need_codes(w, "w", Mxfp4, w.rows, K)
+    _need_codes(ws, "ws", Mxfp4, M, K)
+    _type(y, "y")
+    _need(y, "y", y.dtype, shape=x.shape[:-1] + (w.rows,))
+    _here(x, y, w.q, w.s, ws.q, ws.s)
+    wc, xc = w.c(), ws.c()
+    _check(lib().mxfp4_linear_apply(_ptr(x), _TYPE[x.dtype], _ref(wc), M, w.rows, K, _rule(rule), _ref(xc), _ptr(y),
+                                    _TYPE[y.dtype], _stream(stream)), "mxfp4_linear_apply")
+
+
+# ---------------------------------------------- 8-bit checkpoints, gated activation
+
+def act8_quantize(x: torch.Tensor, c: Act8, stream=None):
+    """The 8-bit checkpoint of x (rows x cols)."""
+    rows, cols = _matrix(x, "x")
+    _need_codes(c, "c", Act8, rows, cols)
+    _here(x, c.q, c.s)
+    p = c.c()
+    _check(lib().act8_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _ref(p), _stream(stream)), "act8_quantize")
+
+
+def act8_dequantize(c: Act8, y: torch.Tensor, stream=None):
+    """The values of a checkpoint into y (rows x cols)."""
+    rows, cols = _matrix(y, "y")
+    _need_codes(c, "c", Act8, rows, cols)
+    _here(y, c.q, c.s)
+    p = c.c()
+    _check(lib().act8_dequantize(_ref(p), rows, cols, _ptr(y), _TYPE[y.dtype], _stream(stream)), "act8_dequantize")
+
+
+def _strided(t, name, like, rows, cols):
+    """Row stride of a matrix whose rows are contiguous (a column range of a
+    wider matrix qualifies); more than two dimensions must be contiguous."""
+    if _type(t, name) != _TYPE[like.dtype]:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype}")
+    if t.shape[-1] != cols or _rows(t) != rows:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {rows} x {cols}")
+    if t.is_contiguous():
+        return cols
+    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _ckpts(cg, cu, rows, cols):
+    if (cg is None) != (cu is None):
+        raise ValueError("both checkpoints are needed, or none")
+    if cg is None:
+        return None, None
+    for c, name in ((cg, "g's checkpoint"), (cu, "u's checkpoint")):
+        _need_codes(c, name, Act8, rows, cols)
+        _here(c.q, c.s)
+    return cg.c(), cu.c()
+
+
+def swiglu_fwd(g: torch.Tensor, u: torch.Tensor, a: torch.Tensor, cg: Act8 = None, cu: Act8 = None, stream=None):
+    """a = silu(g) * u; cg and cu receive 8-bit checkpoints of g and u.  g and u
+    may be column ranges of a wider matrix."""
+    rows, cols = _matrix(a, "a")
+    ldg, ldu = _strided(g, "g", a, rows, cols), _strided(u, "u", a, rows, cols)
+    _here(g, u, a)
+    pg, pu = _ckpts(cg, cu, rows, cols)
+    _check(lib().swiglu_fwd(_ptr(g), ldg, _ptr(u), ldu, _TYPE[a.dtype], rows, cols, _ptr(a), _ref(pg), _ref(pu),
+                            _stream(stream)), "swiglu_fwd")
+
+
+def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, stream=None):
+    """The gradients of swiglu_fwd from da and g, u: the forward's inputs, or
+    their checkpoints (Act8)."""
+    rows, cols = _matrix(da, "da")
+    lddg, lddu = _strided(dg, "dg", da, rows, cols), _strided(du, "du", da, rows, cols)
+    _here(da, dg, du)
+    if isinstance(g, Act8) or isinstance(u, Act8):
+        pg, pu = _ckpts(g, u, rows, cols)
+        args = (None, 0, None, 0, _ref(pg), _ref(pu))
+    else:
+        ldg, ldu = _strided(g, "g", da, rows, cols), _strided(u, "u", da, rows, cols)
+        _here(g, u)
+        args = (_ptr(g), ldg, _ptr(u), ldu, None, None)
+    _check(lib().swiglu_bwd(_ptr(da), *args, _TYPE[da.dtype], rows, cols, _ptr(dg), lddg, _ptr(du), lddu,
+                            _stream(stream)), "swiglu_bwd")
+
+
+# --------------------------------------------------------------------- layer norm
+
+def _params(like, cols, **named):
+    """The parameter dtype: that of the data or float32, the same for all."""
+    dtype = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        _type(t, name)
+        if t.dtype not in (like.dtype, torch.float32) or (dtype is not None and t.dtype != dtype):
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or like.dtype} (or float32 for all parameters)")
+        dtype = t.dtype
+        _need(t, name, dtype, shape=(cols,))
+        _here(t)
+    return _TYPE[dtype or like.dtype]
+
+
+def _stats(mean, rstd, rows):
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _need(t, name, torch.float32, numel=rows)
+        _here(t)
+
+
+def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None, rstd=None, ckpt: Act8 = None,
+                   stream=None):
+    """y = (x - mean) * rstd * w + b over the last dimension; w and b may be None.
+    mean and rstd (float32, one per row) and ckpt (an 8-bit copy of x) are
+    written for the backward."""
+    rows, cols = _matrix(x, "x")
+    _need(y, "y", x.dtype, shape=x.shape)
+    _here(x, y)
+    pt = _params(x, cols, w=w, b=b)
+    if mean is not None or rstd is not None:
+        _stats(mean, rstd, rows)
+    p = None
+    if ckpt is not None:
+        _need_codes(ckpt, "ckpt", Act8, rows, cols)
+        _here(ckpt.q, ckpt.s)
+        p = ckpt.c()
+    _check(lib().layer_norm_fwd(_ptr(x), _TYPE[x.dtype], _ptr(w), _ptr(b), pt, rows, cols, eps, _ptr(y), _ptr(mean),
+                                _ptr(rstd), _ref(p), _stream(stream)), "layer_norm_fwd")
+
+
+def layer_norm_workspace_len(rows: int, cols: int) -> int:
+    """Floats of workspace that layer_norm_bwd needs."""
+    return _bytes(rows, cols, "layer_norm_workspace_len", lib().layer_norm_workspace_len)
+
+
+def layer_norm_bwd(dy: torch.Tensor, x, w, mean, rstd, dx=None, dw=None, db=None, ws=None, stream=None):
+    """dx, dw and db (each may be None) from dy, the forward's x or its
+    checkpoint (Act8), and the forward's mean and rstd."""
+    rows, cols = _matrix(dy, "dy")
+    _here(dy)
+    xp = cp = None
+    if isinstance(x, Act8):
+        _need_codes(x, "x", Act8, rows, cols)
+        _here(x.q, x.s)
+        cp = x.c()
+    else:
+        _need(x, "x", dy.dtype, shape=dy.shape)
+        _here(x)
+        xp = _ptr(x)
+    pt = _params(dy, cols, w=w, dw=dw, db=db)
+    _stats(mean, rstd, rows)
+    if dx is not None:
+        _need(dx, "dx", dy.dtype, shape=dy.shape)
+    if ws is not None:
+        _need(ws, "ws", torch.float32)
+    _here(dx, ws)
+    _check(lib().layer_norm_bwd(_ptr(dy), xp, _ref(cp), _TYPE[dy.dtype], _ptr(w), pt, _ptr(mean), _ptr(rstd), rows,
+                                cols, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
+                                _stream(stream)), "layer_norm_bwd")

@@ -589,6 +589,211 @@ FP8SG_API fp8sg_status amp_update_scale(float* scale, int32_t* growth_tracker, i
                               float growth_factor, float backoff_factor,
                               int32_t growth_interval, fp8sg_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4), 8-bit activation checkpoints,
+ * gated activation, layer norm.
+ *
+ * Formulas of this section are those of the OCP Microscaling Formats (MX)
+ * specification v1.0 for the block formats; [FP8-TRAIN §4, §6] for the three
+ * products of a linear layer and for saving codes instead of 16-bit inputs.
+ *
+ * Element types are passed as fp8sg_out values (bf16, fp16, fp32).  Input and
+ * output matrices of this section need the alignment of their element type
+ * only (2 or 4 bytes) and any row length; 16-byte aligned tensors whose rows
+ * keep that alignment take the fast paths.  Codes and scales need 16 bytes.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * MXFP4 matrix: rows x k values of 4 bits (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives, code 8 = the sign), with one power-of-two scale
+ * 2^(s - 127) (s: one byte) for each block of 32 consecutive values along k,
+ * the dimension its products contract.  A value is e2m1(code) * 2^(s - 127).
+ *   q: codes; row r starts at byte r * 128 * ceil(k / 256); value i of a row is
+ *      in byte i / 2 of it, in the low half for even i.  Values past k are 0.
+ *   s: scales, in groups of 128 rows x 256 values, 1024 bytes each, in the
+ *      order the matrix products read them (one 16-byte load of a lane holds
+ *      the scales it feeds to its matrix instructions).  Block b of row r:
+ *        nk = ceil(k / 256)
+ *        byte (((r / 128) * nk + b / 8) * 64 + ((b % 8) / 2) * 16 + r % 16) * 16
+ *             + ((r % 128) / 16) * 2 + b % 2
+ *      s = 255 is NaN: all 32 values of the block are NaN.  Blocks past k hold
+ *      s = 127; scales of rows past the last are left as they are.
+ * mxfp4_code_bytes and mxfp4_scale_bytes give the sizes of the two buffers in
+ * bytes (-1 for a negative or too large size).
+ */
+typedef struct mxfp4_operand {
+  uint8_t* q;
+  uint8_t* s;
+} mxfp4_operand;
+
+/* How a block's scale 2^e follows from amax, the largest magnitude in it. */
+typedef enum {
+  FP8SG_MX_FLOOR = 0, /* e = floor(log2 amax) - 2, the MX specification's rule: magnitudes in
+                         (6, 8) * 2^e saturate at 6 * 2^e                                   */
+  FP8SG_MX_FIT = 1    /* the smallest e with amax <= 6 * 2^e: nothing saturates (e is at
+                         most 125, so that 6 * 2^e is finite in fp32)                       */
+} fp8sg_mx_rule;
+
+FP8SG_API int64_t mxfp4_code_bytes(int64_t rows, int64_t k);
+FP8SG_API int64_t mxfp4_scale_bytes(int64_t rows, int64_t k);
+
+/*
+ * Quantises a matrix to MXFP4 along its rows and / or along its columns.
+ *   x:  rows x cols of `type`, row-major, contiguous.
+ *   q:  codes and scales of x (rows x cols, blocks along cols), or NULL.
+ *   qT: codes and scales of x transposed (cols x rows, blocks along rows), or
+ *       NULL; at least one of the two is wanted.  The two are different
+ *       roundings of x: their blocks differ.
+ * Elements are rounded to nearest even and saturate at 6 * 2^e; e is never
+ * below -127 (a block of zeros has e = -127).  A block that holds an inf or
+ * a NaN gets s = 255 and codes 0.
+ */
+FP8SG_API fp8sg_status mxfp4_quantize(const void* x, fp8sg_out type, int64_t rows, int64_t cols,
+                                      fp8sg_mx_rule rule, const mxfp4_operand* q,
+                                      const mxfp4_operand* qT, fp8sg_stream stream);
+
+/* The values of an MXFP4 matrix (rows x k), as `type`, row-major, contiguous. */
+FP8SG_API fp8sg_status mxfp4_dequantize(const mxfp4_operand* m, int64_t rows, int64_t k, void* y,
+                                        fp8sg_out type, fp8sg_stream stream);
+
+/*
+ * Product of two MXFP4 matrices: C[M,N] = out(sum_k A[m,k] * B[n,k]), the sum
+ * in fp32 (any order), rounded once to `out`.  A: M x Kc, B: N x Kc, both
+ * quantised along Kc.  M, N, Kc >= 0, any size; Kc == 0 gives zeros.
+ * C: row-major, contiguous, aligned to its element type.
+ */
+FP8SG_API fp8sg_status mxfp4_gemm(const mxfp4_operand* A, const mxfp4_operand* B, void* C,
+                                  fp8sg_out out, int64_t M, int64_t N, int64_t Kc,
+                                  fp8sg_stream stream);
+
+/*
+ * Training linear in MXFP4 [FP8-TRAIN §4, §6]: the forward, input-gradient and
+ * weight-gradient products of y = x W^T, every operand quantised along the
+ * dimension its product contracts.
+ *   saved: what the forward leaves for the backward: W^T (K x N, along N) and
+ *          x^T (K x M, along M).
+ *   ws:    operands that live within one call (x_q: M x K, w_q: N x K for the
+ *          forward; gy_q: M x N, gy_qT: N x M for the backward).  Two calls
+ *          that may overlap in time need a workspace each.
+ */
+typedef struct mxfp4_linear_saved {
+  mxfp4_operand x_qT;
+  mxfp4_operand w_qT;
+} mxfp4_linear_saved;
+typedef struct mxfp4_linear_ws {
+  mxfp4_operand x_q;
+  mxfp4_operand w_q;
+  mxfp4_operand gy_q;
+  mxfp4_operand gy_qT;
+} mxfp4_linear_ws;
+
+/* y[M,N] (type `out`) = x[M,K] W[N,K]^T; x, W of `type`.  saved may be NULL
+ * (no backward follows); only x_q and w_q of ws are used. */
+FP8SG_API fp8sg_status mxfp4_linear_fwd(const void* x, const void* w, fp8sg_out type, int64_t M,
+                                        int64_t N, int64_t K, fp8sg_mx_rule rule,
+                                        const mxfp4_linear_ws* ws, const mxfp4_linear_saved* saved,
+                                        void* y, fp8sg_out out, fp8sg_stream stream);
+
+/* gx[M,K] = gy[M,N] W and gw[N,K] = gy^T x, of type `out`, from what the forward
+ * of the same sizes saved; only gy_q and gy_qT of ws are used. */
+FP8SG_API fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t N,
+                                        int64_t K, fp8sg_mx_rule rule, const mxfp4_linear_ws* ws,
+                                        const mxfp4_linear_saved* saved, void* gx, void* gw,
+                                        fp8sg_out out, fp8sg_stream stream);
+
+/*
+ * Serving linear: y[M,N] = x[M,K] W^T with the weight held as MXFP4 (w: N x K,
+ * quantised once).  x (of `type`) is quantised along K as mxfp4_quantize does;
+ * the result is that of mxfp4_quantize and mxfp4_gemm up to the order of the
+ * fp32 sums.  x_ws (M x K) is scratch, written or not.
+ */
+FP8SG_API fp8sg_status mxfp4_linear_apply(const void* x, fp8sg_out type, const mxfp4_operand* w,
+                                          int64_t M, int64_t N, int64_t K, fp8sg_mx_rule rule,
+                                          const mxfp4_operand* x_ws, void* y, fp8sg_out out,
+                                          fp8sg_stream stream);
+
+/*
+ * 8-bit activation checkpoint: a rows x cols activation kept for the backward
+ * pass as e4m3 codes with one power-of-two scale per block of 32 along a row,
+ * 33/32 bytes per value [FP8-TRAIN §6: save codes, not 16-bit inputs].  The
+ * scale is 2^e with the smallest e such that amax <= 448 * 2^e (-127 <= e <=
+ * 119), so a kept value is within 2^-4 of its own magnitude or 2^-10 * 2^e,
+ * whichever is more.
+ *   q: rows x p codes, p = 32 * ceil(cols / 32); codes past cols are 0.
+ *   s: rows x (p / 32) bytes, value 2^(s - 127); 255 = NaN: the block held an
+ *      inf or a NaN, and all its values are NaN (its codes are 0).
+ */
+typedef struct fp8sg_act8 {
+  uint8_t* q;
+  uint8_t* s;
+} fp8sg_act8;
+
+FP8SG_API fp8sg_status act8_quantize(const void* x, fp8sg_out type, int64_t rows, int64_t cols,
+                                     const fp8sg_act8* c, fp8sg_stream stream);
+FP8SG_API fp8sg_status act8_dequantize(const fp8sg_act8* c, int64_t rows, int64_t cols, void* y,
+                                       fp8sg_out type, fp8sg_stream stream);
+
+/*
+ * Gated activation a = silu(g) * u, silu(g) = g / (1 + exp(-g)), computed in fp32
+ * and rounded once.
+ *   g, u: rows x cols of `type`, rows ldg and ldu elements apart (>= cols), so
+ *         that they may be the two halves of one matrix.
+ *   a:    rows x cols, contiguous.
+ *   cg, cu: checkpoints of g and u written by the same pass, or both NULL.
+ */
+FP8SG_API fp8sg_status swiglu_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                  fp8sg_out type, int64_t rows, int64_t cols, void* a,
+                                  const fp8sg_act8* cg, const fp8sg_act8* cu, fp8sg_stream stream);
+
+/*
+ * Its backward pass: with sg = 1 / (1 + exp(-g)),
+ *   dg = da * u * sg * (1 + g * (1 - sg)),   du = da * g * sg,
+ * from g and u themselves (cg and cu NULL) or from their checkpoints (g and u
+ * NULL, ldg and ldu not read).
+ *   da: rows x cols, contiguous; dg, du: rows lddg and lddu elements apart.
+ *   dg and du may be g and u (each element is read before it is written), but
+ *   no output may otherwise overlap an input.
+ */
+FP8SG_API fp8sg_status swiglu_bwd(const void* da, const void* g, int64_t ldg, const void* u,
+                                  int64_t ldu, const fp8sg_act8* cg, const fp8sg_act8* cu,
+                                  fp8sg_out type, int64_t rows, int64_t cols, void* dg,
+                                  int64_t lddg, void* du, int64_t lddu, fp8sg_stream stream);
+
+/*
+ * Layer norm over the last dimension: y = (x - mean) * rstd * w + b with mean and
+ * rstd = 1 / sqrt(var + eps) of each row (var: the mean squared deviation),
+ * statistics in fp32.
+ *   x, y: rows x cols of `type`, contiguous; cols > 0 where rows > 0.
+ *   w, b: cols values of `ptype` (`type` or FP8SG_OUT_F32), each may be NULL
+ *         (1 and 0).
+ *   mean, rstd: float[rows], written; or both NULL (no backward follows).
+ *   ckpt: an 8-bit checkpoint of x written by the same pass, or NULL.
+ *   eps >= 0.
+ */
+FP8SG_API fp8sg_status layer_norm_fwd(const void* x, fp8sg_out type, const void* w, const void* b,
+                                      fp8sg_out ptype, int64_t rows, int64_t cols, float eps,
+                                      void* y, float* mean, float* rstd, const fp8sg_act8* ckpt,
+                                      fp8sg_stream stream);
+
+/*
+ * Its backward pass: with xh = (x - mean) * rstd and q = dy * w,
+ *   dx = rstd * (q - mean_row(q) - xh * mean_row(q * xh)),
+ *   dw = sum_rows dy * xh,  db = sum_rows dy   (fp32 sums, rounded once; the
+ * order of the sums depends on the sizes only, so a repeated call gives the
+ * same bits).
+ *   x or ckpt: the forward's input or its checkpoint, the other one NULL.
+ *   dx: rows x cols; dw, db: cols values of `ptype`; each of the three may be
+ *   NULL (not wanted).  rows == 0 gives dw = db = 0.
+ *   ws: float[ws_len], ws_len >= layer_norm_workspace_len(rows, cols); not read
+ *   before it is written; may be NULL where dw and db are.
+ */
+FP8SG_API int64_t layer_norm_workspace_len(int64_t rows, int64_t cols);
+FP8SG_API fp8sg_status layer_norm_bwd(const void* dy, const void* x, const fp8sg_act8* ckpt,
+                                      fp8sg_out type, const void* w, fp8sg_out ptype,
+                                      const float* mean, const float* rstd, int64_t rows,
+                                      int64_t cols, void* dx, void* dw, void* db, float* ws,
+                                      int64_t ws_len, fp8sg_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
