@@ -4,16 +4,32 @@
 // l % 16 of a fragment and the 32 consecutive k of block l / 16, and one scale
 // byte for that block; products and the sums inside a block are exact, sums
 // over blocks are fp32.
+#include <utility>
+
+#include "gemm_kernels.hpp"  // LDS staging, tile order
 #include "mx.hpp"
 
 namespace fp8sg {
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
+// f(integral constants 0 .. N - 1): a loop whose index is a constant expression
+template <int... I, class F>
+__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for_(std::make_integer_sequence<int, N>{}, f);
+}
 
-__device__ __forceinline__ v8i frag4(uint4 v) {
-  return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+// One 16 x 16 x 128 product of e2m1 fragments; SA / SB: which byte of sa / sb is
+// the lane's scale.  The first operand's rows become the lane's four
+// accumulators, so it is the one whose rows are C's columns.
+template <int SB, int SA>
+__device__ __forceinline__ v4f mfma4(uint4 b, uint4 a, v4f c, uint32_t sb, uint32_t sa) {
+  const v8i vb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  const v8i va = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 4, 4, SB, (int)sb, SA, (int)sa);
 }
 
 // One wave per 16 x 16 block of C, fragments straight from memory.
@@ -31,8 +47,8 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
       const int64_t b = kt * 8 + 2 * g + j;
       const uint4 a = *reinterpret_cast<const uint4*>(p.A.q + m * nk * 128 + b * 16);
       const uint4 w = *reinterpret_cast<const uint4*>(p.B.q + n * nk * 128 + b * 16);
-      const int sa = p.A.s[mx_scale_off(m, b, nk)], sb = p.B.s[mx_scale_off(n, b, nk)];
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag4(w), frag4(a), acc, 4, 4, 0, sb, 0, sa);
+      const uint32_t sa = p.A.s[mx_scale_off(m, b, nk)], sb = p.B.s[mx_scale_off(n, b, nk)];
+      acc = mfma4<0, 0>(w, a, acc, sb, sa);
     }
   }
   if (bm + r >= p.M) return;
@@ -42,12 +58,228 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
     if (bn + 4 * g + e < p.N) c[bn + 4 * g + e] = from_f32<OUT>(acc[e]);
 }
 
+// Large-tile kernel: a 256 x 256 tile of C per workgroup, K consumed 256 values
+// (128 bytes) at a time, 8 waves in two groups of four, one wave of each group
+// per SIMD.  Group g owns rows [128 g, 128 g + 128), wave q of a group columns
+// [64 q, 64 q + 64): 8 x 4 blocks of 16 x 16.
+//
+// The groups run half a k-tile apart and alternate, meeting at a barrier at
+// every swap, between
+//   - a memory phase: all fragments of the next k-tile from LDS (8 A, 4 B, two
+//     128-deep halves each: 96 VGPRs) and their scales (6 VGPRs), and
+//   - a compute phase: 64 products of 16 cycles on registers only.
+// In phases of half a k-tile, group 0 reads tile t in phase 2 t and computes in
+// 2 t + 1, group 1 a phase later.
+//
+// LDS (136 KB): two slots of A and of B (32 KB each) and of their scales (2 KB
+// each).  Group 0 loads A of t + 1 at the start of its memory phase for t (that
+// slot's tile t - 1 was last read in phase 2 t - 1).  Group 1 loads B of t + 2
+// into B's slot of t during its compute phase for t (last read in phase 2 t + 1,
+// by group 1 itself), one load between every few products, so that the issue
+// hides behind the matrix pipe.  Either way a load has two phases to land; it is
+// waited for by the wave that issued it before the swap ahead of its first read.
+template <int OUT>
+__global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
+  constexpr int BM = 256, BN = 256, kTM = 8, kTN = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[256 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sA1[256 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[256 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB1[256 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sS[4 * 2048];  // scales: A0, A1, B0, B1
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int grp = wave >> 2, wq = wave & 3;
+  const int64_t M = p.M, N = p.N;
+  const int nk = (int)mx_ktiles(p.K);
+  const int pitch = nk * 128;
+  const int nbm = (int)((M + BM - 1) / BM), nbn = (int)((N + BN - 1) / BN);
+  int tm, tn;
+  tile_of(nbm, nbn, tm, tn);
+  const int64_t bm = (int64_t)tm * BM, bn = (int64_t)tn * BN;
+
+  // This group's operand: group 0 stages A, group 1 stages B.  The descriptors
+  // span the rows (and 128-row scale groups) that exist: the rest reads as zero.
+  const int64_t row0 = grp ? bn : bm, rows = (grp ? N : M) - row0;
+  const uint8_t* q0 = (grp ? p.B.q : p.A.q) + row0 * pitch;
+  const uint8_t* s0 = (grp ? p.B.s : p.A.s) + (row0 >> 7) * (int64_t)nk * 1024;
+  const i32x4 rq = make_rsrc(q0, (rows < 256 ? rows : 256) * (int64_t)pitch);
+  const i32x4 rs = make_rsrc(s0, (rows > 128 ? 2 : 1) * (int64_t)nk * 1024);
+  // Load i of wave q: rows 64 q + 8 i + lane / 8, one 16-byte chunk a lane; the
+  // row's swizzle takes two values, for even and odd i.
+  const int lr = lane >> 3;
+  const uint32_t vo0 = (uint32_t)((64 * wq + lr) * pitch + 16 * ((lane & 7) ^ swz16(lr)));
+  const uint32_t vo1 = (uint32_t)((64 * wq + lr) * pitch + 16 * ((lane & 7) ^ swz16(8 + lr)));
+  auto issue = [&](int i, int kt, uint32_t dst) {
+    const uint32_t sb = kt < nk ? (uint32_t)(8 * i * pitch + kt * 128) : kOob;
+    lds_dma16_split(dst + (wq * 8 + i) * 1024, (i & 1) ? vo1 : vo0, sb, rq);
+  };
+  auto issue_scales = [&](int kt, uint32_t dst) {  // waves 0 and 1: one 128-row group each
+    if (wq < 2)
+      lds_dma16_split(dst + wq * 1024, (uint32_t)(lane * 16), kt < nk ? (uint32_t)((wq * nk + kt) * 1024) : kOob, rs);
+  };
+  auto barrier = [&]() {
+    __builtin_amdgcn_s_barrier();
+    compiler_fence();
+  };
+
+  v4f acc[kTM][kTN];
+#pragma unroll
+  for (int i = 0; i < kTM; ++i)
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  uint4 af[kTM][2], bf[kTN][2], sa;
+  uint2 sb;
+
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, 0, lds_u32(sA0));
+    issue_scales(0, lds_u32(sS));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, 0, lds_u32(sB0));
+    issue_scales(0, lds_u32(sS) + 4096);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, 1, lds_u32(sB1));
+    issue_scales(1, lds_u32(sS) + 6144);
+  }
+  wait_vmcnt<0>();
+  barrier();
+  if (grp == 1) barrier();  // group 1 starts half a k-tile later
+
+  const int frow = lane & 15, fchunk = 2 * (lane >> 4);
+  auto step = [&](auto pc, int t) {
+    constexpr int P = decltype(pc)::value;  // t % 2
+    const uint8_t* a = P ? sA1 : sA0;
+    const uint8_t* b = P ? sB1 : sB0;
+    if (grp == 0) {
+      const uint32_t d = lds_u32(P ? sA0 : sA1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) issue(i, t + 1, d);
+      issue_scales(t + 1, lds_u32(sS) + (P ? 0 : 2048));
+    }
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) {
+      const int r = 16 * (4 * wq + j) + frow;
+      bf[j][0] = *reinterpret_cast<const uint4*>(b + lds_off2(r, fchunk));
+      bf[j][1] = *reinterpret_cast<const uint4*>(b + lds_off2(r, fchunk + 1));
+    }
+    sb = *reinterpret_cast<const uint2*>(sS + 4096 + 2048 * P + 1024 * (wq >> 1) + 16 * lane + 8 * (wq & 1));
+    sa = *reinterpret_cast<const uint4*>(sS + 2048 * P + 1024 * grp + 16 * lane);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int r = 16 * (8 * grp + i) + frow;
+      af[i][0] = *reinterpret_cast<const uint4*>(a + lds_off2(r, fchunk));
+      af[i][1] = *reinterpret_cast<const uint4*>(a + lds_off2(r, fchunk + 1));
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    if (grp == 1) wait_vmcnt<0>();       // B of t + 1 has landed
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t sav[4] = {sa.x, sa.y, sa.z, sa.w}, sbv[2] = {sb.x, sb.y};
+    static_for<2>([&](auto kk) {
+      constexpr int KK = decltype(kk)::value;
+      static_for<kTM>([&](auto ic) {
+        constexpr int I = decltype(ic)::value;
+        static_for<kTN>([&](auto jc) {
+          constexpr int J = decltype(jc)::value;
+          acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J][KK], af[I][KK], acc[I][J], sbv[J / 2], sav[I / 2]);
+        });
+        if constexpr (KK == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (grp == 1) issue(I, t + 2, lds_u32(P ? sB1 : sB0));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+    });
+    if (grp == 1) issue_scales(t + 2, lds_u32(sS) + 4096 + 2048 * P);
+    __builtin_amdgcn_sched_barrier(0);
+    if (grp == 0) wait_vmcnt<0>();  // A of t + 1 has landed
+    barrier();
+  };
+  for (int t = 0;;) {
+    step(std::integral_constant<int, 0>{}, t);
+    if (++t >= nk) break;
+    step(std::integral_constant<int, 1>{}, t);
+    if (++t >= nk) break;
+  }
+  if (grp == 0) barrier();
+
+  // Lane: rows wr0 + 16 i + lane % 16, columns wc0 + 16 j + 4 (lane / 16) .. + 3.
+  const int wr0 = grp * 128 + (lane & 15), wc0 = wq * 64 + 4 * (lane >> 4);
+  if constexpr (OUT == FP8SG_OUT_F32) {
+    float* C = reinterpret_cast<float*>(p.C);
+    const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(C) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int64_t m = bm + wr0 + 16 * i;
+      if (m >= M) continue;
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        const int64_t n = bn + wc0 + 16 * j;
+        if (wide) {
+          if (n < N) store4<OUT>(C, m * N + n, acc[i][j]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) C[m * N + n + e] = acc[i][j][e];
+        }
+      }
+    }
+  } else {
+    // the tile through LDS (64 rows of 512 bytes per slot), out in 16-byte chunks
+    auto crow = [&](int r) -> uint8_t* {
+      uint8_t* base = r < 64 ? sA0 : r < 128 ? sA1 : r < 192 ? sB0 : sB1;
+      return base + (r & 63) * 512;
+    };
+    __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing a slot
+    barrier();
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        const int r = wr0 + 16 * i, col = wc0 + 16 * j;
+        store4<OUT>(crow(r) + ((((col >> 3) ^ (r & 31)) << 4) + (col & 7) * 2), 0, acc[i][j]);
+      }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    barrier();
+    uint16_t* C = reinterpret_cast<uint16_t*>(p.C);
+    const bool wide = N % 8 == 0 && (reinterpret_cast<uintptr_t>(C) & 15u) == 0;
+    auto write_tile = [&](auto nt) {
+#pragma unroll 4
+      for (int pass = 0; pass < 16; ++pass) {
+        const int id = pass * 512 + (int)threadIdx.x, r = id >> 5, cc = id & 31;
+        const uint4 v = *reinterpret_cast<const uint4*>(crow(r) + ((cc ^ (r & 31)) << 4));
+        const int64_t m = bm + r, n = bn + 8 * cc;
+        if (m >= M || n >= N) continue;
+        if (wide) {
+          st16<decltype(nt)::value>(C + m * N + n, v);
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) C[m * N + n + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+        }
+      }
+    };
+    if (2 * M * N >= kStreamOutBytes) write_tile(std::true_type{});
+    else write_tile(std::false_type{});
+  }
+}
+
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
   return by_type(out, [&](auto t) {
     constexpr int T = decltype(t)::value;
+    // The large-tile kernel where its tiles fill the chip; its 32-bit offsets
+    // span 256 rows.
+    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+    if (tiles >= 128 && p.K > 0 && mx_pitch(p.K) * 256 < (1ll << 31) - 256) {
+      hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles), dim3(512), 0, stream, p);
+      return hipGetLastError();
+    }
     const int64_t nb = ((p.M + 15) / 16) * ((p.N + 15) / 16);
     hipLaunchKernelGGL((k_mx_gemm_plain<T>), dim3((unsigned)nb), dim3(64), 0, stream, p);
     return hipGetLastError();
