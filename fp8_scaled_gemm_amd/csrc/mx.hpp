@@ -9,10 +9,22 @@
 // scales from 2^-127 to 2^125 against the definition).
 #pragma once
 
+#include <utility>
+
 #include "common.hpp"
 #include "launch_mx.hpp"
 
 namespace fp8sg {
+
+// f(integral constants 0 .. N - 1): a loop whose index is a constant expression
+template <int... I, class F>
+__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for_(std::make_integer_sequence<int, N>{}, f);
+}
 
 // ---- element types (fp8sg_out values): one element as fp32, exactly
 template <int T>

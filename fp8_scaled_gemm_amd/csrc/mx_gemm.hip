@@ -4,23 +4,11 @@
 // l % 16 of a fragment and the 32 consecutive k of block l / 16, and one scale
 // byte for that block; products and the sums inside a block are exact, sums
 // over blocks are fp32.
-#include <utility>
-
 #include "gemm_kernels.hpp"  // LDS staging, tile order
 #include "mx.hpp"
 
 namespace fp8sg {
 namespace {
-
-// f(integral constants 0 .. N - 1): a loop whose index is a constant expression
-template <int... I, class F>
-__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F f) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void static_for(F f) {
-  static_for_(std::make_integer_sequence<int, N>{}, f);
-}
 
 // One 16 x 16 x 128 product of e2m1 fragments; SA / SB: which byte of sa / sb is
 // the lane's scale.  The first operand's rows become the lane's four

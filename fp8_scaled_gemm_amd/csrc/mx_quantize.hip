@@ -8,73 +8,264 @@
 namespace fp8sg {
 namespace {
 
-// One thread per block of 32 along a row (blockIdx.y walks rows), padding
-// blocks up to the last k-tile's end included.
+// Eight 16-bit elements (4 dwords) or eight fp32 (8 dwords) of a row in
+// registers, as loaded.
 template <int T>
-__global__ __launch_bounds__(256) void k_mxq_rows(MxQuantJob j, bool fit) {
+struct Row8 {
+  static constexpr int kW = T == FP8SG_OUT_F32 ? 8 : 4;
+  uint32_t w[kW];
+};
+// 16 bytes at an address aligned to 2 (the hardware takes any; the type tells
+// the compiler).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// p: the row's first element; elements c .. c + 7, those at or past `cols`
+// read as zero (cols > 0).
+template <int T, bool S>
+__device__ __forceinline__ Row8<T> load_row8(const Elem<T>* p, int64_t c, int64_t cols) {
+  Row8<T> r;
+  if (c + 8 <= cols) {
+#pragma unroll
+    for (int h = 0; h < Row8<T>::kW / 4; ++h) {
+      const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p + c + 4 * h);
+      const u32x4_any v = S ? __builtin_nontemporal_load(q) : *q;
+      r.w[4 * h] = v.x;
+      r.w[4 * h + 1] = v.y;
+      r.w[4 * h + 2] = v.z;
+      r.w[4 * h + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t at = c + e < cols ? c + e : cols - 1;
+      const Elem<T> v = p[at];
+      const bool in = c + e < cols;
+      if constexpr (T == FP8SG_OUT_F32) {
+        r.w[e] = in ? __float_as_uint(v) : 0u;
+      } else {
+        const uint32_t b = in ? (uint32_t)v : 0u;
+        if (e & 1) r.w[e / 2] |= b << 16;
+        else r.w[e / 2] = b;
+      }
+    }
+  }
+  return r;
+}
+
+// Running largest magnitudes as bit patterns: two 16-bit ones a dword, or fp32.
+template <int T>
+__device__ __forceinline__ uint32_t mag_max(uint32_t m, uint32_t w) {
+  if constexpr (T == FP8SG_OUT_F32) {
+    w &= 0x7FFFFFFFu;
+    return w > m ? w : m;
+  } else {
+    return pmax(m, w & 0x7FFF7FFFu);
+  }
+}
+// A 16-bit magnitude's fp32 bits (inf and NaN stay above every finite value).
+template <int T>
+__device__ __forceinline__ uint32_t mag_bits(uint32_t code) {
+  if constexpr (T == FP8SG_OUT_BF16) return code << 16;
+  else if constexpr (T == FP8SG_OUT_F16) return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)code));
+  else return code;
+}
+// Two elements to the byte SEL of a dword of codes.
+template <int T, int SEL>
+__device__ __forceinline__ uint32_t put_pair(uint32_t d, uint32_t pair, float scale) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  if constexpr (T == FP8SG_OUT_BF16)
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(d, __builtin_bit_cast(bf2, pair), scale, SEL);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(d, __builtin_bit_cast(h2, pair), scale, SEL);
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t put_pair32(uint32_t d, uint32_t a, uint32_t b, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, __uint_as_float(a), __uint_as_float(b), scale, SEL);
+}
+// Eight elements of a row to a dword of codes.
+template <int T>
+__device__ __forceinline__ uint32_t row_codes(const Row8<T>& r, uint32_t s) {
+  const float sc = scale_value(s);
+  uint32_t d = 0;
+  if constexpr (T == FP8SG_OUT_F32) {
+    d = put_pair32<0>(d, r.w[0], r.w[1], sc);
+    d = put_pair32<1>(d, r.w[2], r.w[3], sc);
+    d = put_pair32<2>(d, r.w[4], r.w[5], sc);
+    d = put_pair32<3>(d, r.w[6], r.w[7], sc);
+  } else {
+    d = put_pair<T, 0>(d, r.w[0], sc);
+    d = put_pair<T, 1>(d, r.w[1], sc);
+    d = put_pair<T, 2>(d, r.w[2], sc);
+    d = put_pair<T, 3>(d, r.w[3], sc);
+  }
+  return s == 255u ? 0u : d;
+}
+// Column J of rows R .. R + 7 to a dword of codes.
+template <int T, int J, int R>
+__device__ __forceinline__ uint32_t col_codes(const Row8<T> (&v)[16], float sc) {
+  uint32_t d = 0;
+  if constexpr (T == FP8SG_OUT_F32) {
+    d = put_pair32<0>(d, v[R].w[J], v[R + 1].w[J], sc);
+    d = put_pair32<1>(d, v[R + 2].w[J], v[R + 3].w[J], sc);
+    d = put_pair32<2>(d, v[R + 4].w[J], v[R + 5].w[J], sc);
+    d = put_pair32<3>(d, v[R + 6].w[J], v[R + 7].w[J], sc);
+  } else {
+    constexpr uint32_t sel = (J & 1) ? 0x07060302u : 0x05040100u;  // the column's half of two rows
+    d = put_pair<T, 0>(d, __builtin_amdgcn_perm(v[R + 1].w[J / 2], v[R].w[J / 2], sel), sc);
+    d = put_pair<T, 1>(d, __builtin_amdgcn_perm(v[R + 3].w[J / 2], v[R + 2].w[J / 2], sel), sc);
+    d = put_pair<T, 2>(d, __builtin_amdgcn_perm(v[R + 5].w[J / 2], v[R + 4].w[J / 2], sel), sc);
+    d = put_pair<T, 3>(d, __builtin_amdgcn_perm(v[R + 7].w[J / 2], v[R + 6].w[J / 2], sel), sc);
+  }
+  return d;
+}
+
+struct MxQuantArgs {
+  MxQuantJob job[2];
+  uint32_t blocks0;  // blocks of job 0
+  int32_t fit;
+};
+
+// A block of NW waves quantises 32 NW rows x 256 columns, read once; wave w
+// holds rows 32 w .. + 31, lane l rows 16 (l / 32) .. + 15 of them and 8
+// columns from 8 (l % 32).  Then
+//   - a block along a row lies in four neighbouring lanes (two DPP steps give
+//     its amax) and 32 lanes write a row's 128 bytes of codes;
+//   - a block along a column lies in lanes l and l ^ 32; the codes of a lane's
+//     8 columns x 16 rows go through LDS, so that the columns' codes leave in
+//     runs of 16 NW bytes.
+// Scales of both directions are gathered in LDS in their stored order.
+// Memory bound: the wider tile (NW = 8) writes whole 128-byte lines; NW = 2
+// gives small matrices more blocks.
+template <int T, int NW, bool S>
+__global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQuantArgs args) {
+  constexpr int kRows = 32 * NW;
+  // column c's codes start at tcol(c); the 16-byte pieces (NW = 8) or the
+  // columns (NW = 2) are shifted so that lanes 8 columns apart write to
+  // different banks
+  auto tcol = [](int c) { return NW == 8 ? c * 128 : c * 32 + (c >> 3) * 16; };
+  __shared__ __attribute__((aligned(16))) uint8_t tq[NW == 8 ? 256 * 128 : 256 * 32 + 32 * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t rs[NW * 256];  // row scales, [row group][g][r % 16][piece]
+  __shared__ __attribute__((aligned(16))) uint8_t ts[NW * 256];  // column scales, [column group][g][c % 16][16]
+
+  const bool second = blockIdx.x >= args.blocks0;
+  const MxQuantJob& j = args.job[second];
+  const uint32_t blk = blockIdx.x - (second ? args.blocks0 : 0u);
+  const int64_t nkc = mx_ktiles(j.cols), nkr = mx_ktiles(j.rows);
+  const int64_t rt = blk / (uint32_t)nkc, ct = blk % (uint32_t)nkc;  // tile
+  const int64_t r0 = rt * kRows, c0 = ct * 256;
+  const bool fit = args.fit != 0;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, cc = lane & 31;
+  const int64_t c = c0 + 8 * cc, rw = r0 + 32 * wave + 16 * half;
   const Elem<T>* x = reinterpret_cast<const Elem<T>*>(j.x);
-  const int64_t nk = mx_ktiles(j.cols), nb = nk * 8, total = j.rows * nb;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / nb, b = i % nb;
-    float v[32];
-    uint32_t amax = 0;
+  Row8<T> v[16];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int64_t c = b * 32 + e;
-      v[e] = c < j.cols ? to_f32<T>(x[r * j.cols + c]) : 0.f;
-      const uint32_t a = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-      amax = a > amax ? a : amax;
-    }
-    const uint32_t s = b * 32 < j.cols ? fp4_scale(amax, fit) : 127u;
-    const float sc = s == 255u ? 1.f : scale_value(s);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (s != 255u) {
+  for (int i = 0; i < 16; ++i) {
+    if (rw + i < j.rows && c < j.cols) {
+      v[i] = load_row8<T, S>(x + (rw + i) * j.cols, c, j.cols);
+    } else {
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) w[e / 8] |= fp4_pair(v[e], v[e + 1], sc) << (8 * ((e / 2) % 4));
+      for (int e = 0; e < Row8<T>::kW; ++e) v[i].w[e] = 0u;
     }
-    *reinterpret_cast<uint4*>(j.q.q + r * nk * 128 + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    j.q.s[mx_scale_off(r, b, nk)] = (uint8_t)s;
+  }
+
+  if (j.q.q) {
+    const bool blk_in = (c & ~31) < j.cols;  // this lane's block of 32 exists
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < Row8<T>::kW; ++e) m = mag_max<T>(m, v[i].w[e]);
+      if constexpr (T != FP8SG_OUT_F32) m = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
+      uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false);
+      m = o > m ? o : m;
+      o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false);
+      m = o > m ? o : m;
+      const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(m), fit) : 127u;
+      if (rw + i < j.rows) *reinterpret_cast<uint32_t*>(j.q.q + ((rw + i) * nkc + ct) * 128 + 4 * cc) = row_codes<T>(v[i], s);
+      if ((lane & 3) == 0) {  // block b = cc / 4 of row rl
+        const int rl = 32 * wave + 16 * half + i, b = cc >> 2;
+        constexpr int kPiece = NW == 8 ? 16 : 8;  // bytes of a 16-byte scale granule that this tile's rows fill
+        rs[(rl >> 7) * 1024 + ((b >> 1) * 16 + (rl & 15)) * kPiece + ((rl & 127) >> 4) * 2 + (b & 1)] = (uint8_t)s;
+      }
+    }
+  }
+  if (j.t.q) {
+    constexpr int kM = Row8<T>::kW;
+    uint32_t m[kM];
+#pragma unroll
+    for (int e = 0; e < kM; ++e) m[e] = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < kM; ++e) m[e] = mag_max<T>(m[e], v[i].w[e]);
+#pragma unroll
+    for (int e = 0; e < kM; ++e) m[e] = mag_max<T>(m[e], (uint32_t)__shfl_xor((int)m[e], 32, kWave));
+    const bool blk_in = r0 + 32 * wave < j.rows;
+    static_for<8>([&](auto jc) {
+      constexpr int J = decltype(jc)::value;
+      const uint32_t code = T == FP8SG_OUT_F32 ? m[J % kM] : ((J & 1) ? m[J / 2] >> 16 : m[J / 2] & 0xFFFFu);
+      const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(code), fit) : 127u;
+      const float sc = scale_value(s);
+      uint2 d = make_uint2(col_codes<T, J, 0>(v, sc), col_codes<T, J, 8>(v, sc));
+      if (s == 255u) d = make_uint2(0, 0);
+      const int cl = 8 * cc + J;
+      const int piece = NW == 8 ? (wave ^ (cc & 7)) : wave;
+      *reinterpret_cast<uint2*>(tq + tcol(cl) + piece * 16 + half * 8) = d;
+      if (half == 0)
+        ts[(cl >> 7) * (NW * 128) + ((wave >> 1) * 16 + (cl & 15)) * 16 + ((cl & 127) >> 4) * 2 + (wave & 1)] = (uint8_t)s;
+    });
+  }
+  __syncthreads();
+  if (j.q.q) {
+    if constexpr (NW == 8) {  // two row groups of 1 KB
+      if (tid < 128 && r0 + (tid >> 6) * 128 < j.rows)
+        *reinterpret_cast<uint4*>(j.q.s + ((r0 / 128 + (tid >> 6)) * nkc + ct) * 1024 + (tid & 63) * 16) =
+            *reinterpret_cast<const uint4*>(rs + tid * 16);
+    } else if (tid < 64 && r0 < j.rows) {  // 64 rows: one half of each granule
+      *reinterpret_cast<uint2*>(j.q.s + ((r0 / 128) * nkc + ct) * 1024 + tid * 16 + ((r0 & 127) ? 8 : 0)) =
+          *reinterpret_cast<const uint2*>(rs + tid * 8);
+    }
+  }
+  if (j.t.q) {
+    // k-tile r0 / 256 of the transposed matrix, from byte (r0 % 256) / 2 on
+    const int64_t kt = r0 >> 8, sub = (r0 & 255) >> 1;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {  // 256 columns x NW pieces of 16 bytes
+      const int id = p * 64 * NW + tid, cl = id / NW, k = id % NW;
+      const int piece = NW == 8 ? (k ^ ((cl >> 3) & 7)) : k;
+      if (c0 + cl < j.cols)
+        st16<S>(j.t.q + ((c0 + cl) * nkr + kt) * 128 + sub + k * 16, *reinterpret_cast<const uint4*>(tq + tcol(cl) + piece * 16));
+    }
+    // whole granules: NW / 2 block pairs of 16 columns, two column groups
+    if (tid < NW * 16) {
+      const int grp = tid / (NW * 8), w = tid % (NW * 8);  // w: [block pair][c % 16]
+      const int64_t g0 = (r0 & 255) >> 6;                  // block pair of the tile's first row
+      if (c0 + grp * 128 < j.cols)
+        *reinterpret_cast<uint4*>(j.t.s + (((c0 >> 7) + grp) * nkr + kt) * 1024 + (g0 * 16 + w) * 16) =
+            *reinterpret_cast<const uint4*>(ts + tid * 16);
+    }
   }
 }
 
-// One thread per block of 32 along a column.
-template <int T>
-__global__ __launch_bounds__(256) void k_mxq_cols(MxQuantJob j, bool fit) {
-  const Elem<T>* x = reinterpret_cast<const Elem<T>*>(j.x);
-  const int64_t nk = mx_ktiles(j.rows), nb = nk * 8, total = j.cols * nb;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t b = i / j.cols, c = i % j.cols;
-    float v[32];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int64_t r = b * 32 + e;
-      v[e] = r < j.rows ? to_f32<T>(x[r * j.cols + c]) : 0.f;
-      const uint32_t a = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-      amax = a > amax ? a : amax;
-    }
-    const uint32_t s = b * 32 < j.rows ? fp4_scale(amax, fit) : 127u;
-    const float sc = s == 255u ? 1.f : scale_value(s);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (s != 255u) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) w[e / 8] |= fp4_pair(v[e], v[e + 1], sc) << (8 * ((e / 2) % 4));
-    }
-    *reinterpret_cast<uint4*>(j.t.q + c * nk * 128 + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    j.t.s[mx_scale_off(c, b, nk)] = (uint8_t)s;
-  }
-}
-
-// One thread per byte of codes (two values).
+// One thread per 8 values: 4 bytes of codes, their block's scale.
 template <int T>
 __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t rows, int64_t k, Elem<T>* y) {
-  const int64_t nk = mx_ktiles(k), pairs = (k + 1) / 2, total = rows * pairs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / pairs, p = i % pairs;
-    const float sc = scale_value(m.s[mx_scale_off(r, p / 16, nk)]);
-    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(m.q[r * nk * 128 + p], 1.f, 0);
-    y[r * k + 2 * p] = from_f32<T>(v[0] * sc);
-    if (2 * p + 1 < k) y[r * k + 2 * p + 1] = from_f32<T>(v[1] * sc);
+  const int64_t nk = mx_ktiles(k), upr = (k + 7) / 8, total = rows * upr;
+  const bool vec = (k * sizeof(Elem<T>)) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < total; i0 += (int64_t)gridDim.x * 256) {
+    const int64_t rb = i0 / upr;  // uniform
+    const uint32_t t = (uint32_t)(i0 - rb * upr) + threadIdx.x, dr = t / (uint32_t)upr;
+    const int64_t r = rb + dr, u = t - dr * (uint32_t)upr;
+    if (r >= rows) continue;
+    const float sc = scale_value(m.s[mx_scale_off(r, u / 4, nk)]);
+    const uint32_t q = *reinterpret_cast<const uint32_t*>(m.q + r * nk * 128 + 4 * u);
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+    const float v[8] = {a[0] * sc, a[1] * sc, b[0] * sc, b[1] * sc, c[0] * sc, c[1] * sc, d[0] * sc, d[1] * sc};
+    if (vec) store8<T, true, false>(y + r * k + 8 * u, 8, v);
+    else store8<T, false, false>(y + r * k + 8 * u, (int)(k - 8 * u < 8 ? k - 8 * u : 8), v);
   }
 }
 
@@ -83,23 +274,41 @@ unsigned grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (unsigned)(b < (1 << 20) ? b : (1 << 20));
 }
+// Tiles of a job: column tiles cover the padded columns; the row tiles the
+// rows, and with a transposed copy the padding of its last k-tile too.
+template <int NW>
+int64_t tiles_of(const MxQuantJob& j) {
+  if (j.rows == 0 || j.cols == 0) return 0;
+  const int64_t rt = j.t.q ? mx_ktiles(j.rows) * (8 / NW) : (j.rows + 32 * NW - 1) / (32 * NW);
+  return rt * mx_ktiles(j.cols);
+}
 
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit, hipStream_t stream) {
-  if (n > 1) {
-    const hipError_t e = launch_mx_quantize(jobs + 1, n - 1, type, fit, stream);
-    if (e != hipSuccess) return e;
+  MxQuantArgs a{};
+  int64_t bytes = 0, wide = 0;
+  for (int i = 0; i < n; ++i) {
+    a.job[i] = jobs[i];
+    wide += tiles_of<8>(jobs[i]);
+    bytes += jobs[i].rows * jobs[i].cols * (type == FP8SG_OUT_F32 ? 5 : 3);
   }
-  const MxQuantJob& j = jobs[0];
-  if (j.rows == 0 || j.cols == 0) return hipSuccess;
+  a.fit = fit;
+  const int cus = device_cus();
   return by_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    if (j.q.q)
-      hipLaunchKernelGGL((k_mxq_rows<T>), dim3(grid_for(j.rows * mx_ktiles(j.cols) * 8)), dim3(256), 0, stream, j, fit);
-    if (j.t.q)
-      hipLaunchKernelGGL((k_mxq_cols<T>), dim3(grid_for(j.cols * mx_ktiles(j.rows) * 8)), dim3(256), 0, stream, j, fit);
-    return hipGetLastError();
+    auto launch = [&](auto nw, auto st) {
+      constexpr int NW = decltype(nw)::value;
+      const int64_t b0 = tiles_of<NW>(a.job[0]), b1 = n > 1 ? tiles_of<NW>(a.job[1]) : 0;
+      if (b0 + b1 == 0) return hipSuccess;
+      a.blocks0 = (uint32_t)b0;
+      hipLaunchKernelGGL((k_mxq<T, NW, decltype(st)::value>), dim3((unsigned)(b0 + b1)), dim3(64 * NW), 0, stream, a);
+      return hipGetLastError();
+    };
+    // a wide tile per compute unit, or the narrow ones
+    if (wide < cus) return launch(std::integral_constant<int, 2>{}, std::false_type{});
+    if (bytes >= kStreamBytes) return launch(std::integral_constant<int, 8>{}, std::true_type{});
+    return launch(std::integral_constant<int, 8>{}, std::false_type{});
   });
 }
 
@@ -107,7 +316,7 @@ hipError_t launch_mx_dequantize(const mxfp4_operand& m, int64_t rows, int64_t k,
   if (rows == 0 || k == 0) return hipSuccess;
   return by_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    hipLaunchKernelGGL((k_mx_dequant<T>), dim3(grid_for(rows * ((k + 1) / 2))), dim3(256), 0, stream, m, rows, k,
+    hipLaunchKernelGGL((k_mx_dequant<T>), dim3(grid_for(rows * ((k + 7) / 8))), dim3(256), 0, stream, m, rows, k,
                        reinterpret_cast<Elem<T>*>(y));
     return hipGetLastError();
   });

@@ -617,7 +617,7 @@ FP8SG_API fp8sg_status amp_update_scale(float* scale, int32_t* growth_tracker, i
  *        byte (((r / 128) * nk + b / 8) * 64 + ((b % 8) / 2) * 16 + r % 16) * 16
  *             + ((r % 128) / 16) * 2 + b % 2
  *      s = 255 is NaN: all 32 values of the block are NaN.  Blocks past k hold
- *      s = 127; scales of rows past the last are left as they are.
+ *      s = 127; what stands for rows past the last is unspecified and not used.
  * mxfp4_code_bytes and mxfp4_scale_bytes give the sizes of the two buffers in
  * bytes (-1 for a negative or too large size).
  */
