@@ -1,48 +1,334 @@
 // Layer norm, forward and backward, with the reduction of the weight's and the
 // bias's gradients over the rows.
+//
+// Bound by memory: the forward reads a row once and writes it once, the
+// backward reads dy and x (or x's 8-bit checkpoint) once and writes dx.  A row
+// stays in registers between the passes over it (mean, squared deviations,
+// result), 8 to 32 elements a thread, so a row takes 1 to 16 waves by its
+// length; rows past kMaxCols are re-read instead (k_*_long).
+//
+// Gradients of the weight and the bias: each block walks its share of the rows
+// with its columns' sums in registers and leaves one partial row of each in
+// the workspace; a second kernel adds the partial rows.  Every sum's order
+// follows from the sizes alone, so results repeat bit for bit.
 #include "mx.hpp"
 
 namespace fp8sg {
 namespace {
 
-template <int NT>
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float red[NT / kWave];
+constexpr int64_t kMaxCols = 16384;  // 16 waves x 64 lanes x 16 elements
+
+__device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = v;
+  return v;
+}
+// Sum over the NW waves of a row, the same in every lane.  `red`: NW floats of
+// the row's own, not in use before the last barrier; buffers alternate between
+// consecutive calls, so one barrier a call is enough.
+template <int NW>
+__device__ __forceinline__ float row_sum(float v, float* red, int wave) {
+  v = wave_sum(v);
+  if constexpr (NW == 1) return v;
+  red[wave] = v;  // every lane holds the sum: a write of one value to one address
   __syncthreads();
-  float r = 0.f;
+  v = red[0];
 #pragma unroll
-  for (int w = 0; w < NT / kWave; ++w) r += red[w];
-  __syncthreads();
-  return r;
+  for (int w = 1; w < NW; ++w) v += red[w];
+  return v;
 }
 
 template <int P>
-__device__ __forceinline__ float param(const void* w, int64_t c, float none) {
-  return w ? to_f32<P>(reinterpret_cast<const Elem<P>*>(w)[c]) : none;
+__device__ __forceinline__ void load_params(const void* w, int64_t c, int n, float none, float (&v)[8]) {
+  if (w && n > 0) {
+    load8<P, false>(reinterpret_cast<const Elem<P>*>(w) + c, n, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = none;
+  }
 }
 
-// One block per row (rows strided by the grid); the row is read once for the
-// mean, once for the squared deviations, once for y.
-template <int T, int P>
-__global__ __launch_bounds__(256) void k_ln_fwd(LayerNormArgs p) {
+// A row per NW waves, R rows a block; V groups of 8 elements a thread: group k
+// of a row's thread t is elements 8 (t + 64 NW k) .. + 7.
+template <int T, int P, int NW, int V>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArgs p) {
+  constexpr int R = NW == 1 ? 4 : 1;
+  __shared__ float red[2][NW];
+  const int lane = threadIdx.x & 63, wave = NW == 1 ? 0 : threadIdx.x >> 6;
+  const int t = wave * 64 + lane;
   const float inv_n = 1.0f / (float)p.cols;
+  float w[V][8], b[V][8];
+  int64_t c[V];
+  int n[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    c[k] = 8 * (t + 64 * NW * k);
+    n[k] = left8(p.cols, c[k]);
+    load_params<P>(p.w, c[k], n[k], 1.f, w[k]);
+    load_params<P>(p.b, c[k], n[k], 0.f, b[k]);
+  }
+  const int64_t pitch = act8_pitch(p.cols);
+  // (a wave past the last row still runs: its neighbours in the block do)
+  for (int64_t r = (int64_t)blockIdx.x * R + (NW == 1 ? threadIdx.x >> 6 : 0); r < p.rows; r += (int64_t)gridDim.x * R) {
+    const Elem<T>* x = reinterpret_cast<const Elem<T>*>(p.x) + r * p.cols;
+    float v[V][8], s = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) load8<T, false>(x + c[k], n[k], v[k]);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[k][e];
+    const float mean = row_sum<NW>(s, red[0], wave) * inv_n;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = v[k][e] - mean;
+        s += e < n[k] ? d * d : 0.f;
+      }
+    const float rstd = 1.0f / sqrtf(row_sum<NW>(s, red[1], wave) * inv_n + p.eps);
+    Elem<T>* y = reinterpret_cast<Elem<T>*>(p.y) + r * p.cols;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (v[k][e] - mean) * rstd * w[k][e] + b[k][e];
+      store8<T, false>(y + c[k], n[k], o);
+    }
+    if (p.ckpt.q) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const uint32_t sc = act8_scale(quad_amax(v[k]));
+        if (c[k] < pitch) {
+          *reinterpret_cast<uint2*>(p.ckpt.q + r * pitch + c[k]) = act8_codes(v[k], sc);
+          if ((lane & 3) == 0) p.ckpt.s[(r * pitch + c[k]) >> 5] = (uint8_t)sc;
+        }
+      }
+    }
+    if (t == 0 && p.mean) {
+      p.mean[r] = mean;
+      p.rstd[r] = rstd;
+    }
+  }
+}
+
+// The backward's x: 8 elements of the input, or of its checkpoint.
+template <int T, bool CKPT>
+struct XRow {
+  Row8<T> x;
+  __device__ __forceinline__ void load(const LayerNormArgs& p, int64_t r, int64_t c, int n) {
+    x = load_row8<T, false>(reinterpret_cast<const Elem<T>*>(p.x) + r * p.cols + c, n);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const { x.values(v); }
+};
+template <int T>
+struct XRow<T, true> {
+  uint2 q;
+  uint32_t s;
+  __device__ __forceinline__ void load(const LayerNormArgs& p, int64_t r, int64_t c, int n) {
+    q = make_uint2(0, 0);
+    s = 127u;
+    if (n > 0) {
+      const int64_t at = r * act8_pitch(p.cols) + c;
+      q = *reinterpret_cast<const uint2*>(p.ckpt.q + at);
+      s = p.ckpt.s[at >> 5];
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const { act8_values(q, s, v); }
+};
+
+// dx of a row, and the block's partial rows of dw and db.  The next row's loads
+// are issued before this row's sums, whose barrier they then hide behind.
+template <int T, int P, int NW, int V, bool CKPT>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_bwd(LayerNormArgs p, int direct) {
+  constexpr int R = NW == 1 ? 4 : 1;
+  __shared__ float red[2][2 * NW];
+  extern __shared__ float part[];  // NW == 1: three waves' partial rows
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rw = NW == 1 ? 0 : wave;
+  const int t = rw * 64 + lane;
+  const float inv_n = 1.0f / (float)p.cols;
+  float w[V][8], dw[V][8], db[V][8];
+  int64_t c[V];
+  int n[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    c[k] = 8 * (t + 64 * NW * k);
+    n[k] = left8(p.cols, c[k]);
+    load_params<P>(p.w, c[k], n[k], 1.f, w[k]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[k][e] = db[k][e] = 0.f;
+  }
+  const Elem<T>* dyp = reinterpret_cast<const Elem<T>*>(p.dy);
+  Row8<T> ndy[V];
+  XRow<T, CKPT> nx[V];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int64_t r) {
+    if (r >= p.rows) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      ndy[k] = load_row8<T, false>(dyp + r * p.cols + c[k], n[k]);
+      nx[k].load(p, r, c[k], n[k]);
+    }
+    nmean = p.mean[r];
+    nrstd = p.rstd[r];
+  };
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t r = (int64_t)blockIdx.x * R + (NW == 1 ? wave : 0);
+  constexpr bool kAhead = !(T == FP8SG_OUT_F32 && V == 4);  // (there the registers are all in use)
+  if constexpr (kAhead) fetch(r);
+#pragma unroll 1
+  for (int it = 0; r < p.rows; r += step, it ^= 1) {
+    float dy[V][8], xh[V][8];
+    if constexpr (!kAhead) fetch(r);
+    const float mean = nmean, rstd = nrstd;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      ndy[k].values(dy[k]);
+      nx[k].values(xh[k]);
+    }
+    if constexpr (kAhead) fetch(r + step);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[k][e] = (xh[k][e] - mean) * rstd;
+        dw[k][e] += dy[k][e] * xh[k][e];  // (elements past the row's end have dy = 0)
+        db[k][e] += dy[k][e];
+        dy[k][e] *= w[k][e];
+        s1 += dy[k][e];
+        s2 += dy[k][e] * xh[k][e];
+      }
+    if (p.dx) {
+      s1 = wave_sum(s1);
+      s2 = wave_sum(s2);
+      if constexpr (NW > 1) {
+        float* buf = red[it];
+        buf[rw] = s1;
+        buf[NW + rw] = s2;
+        __syncthreads();
+        s1 = buf[0];
+        s2 = buf[NW];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) {
+          s1 += buf[i];
+          s2 += buf[NW + i];
+        }
+      }
+      const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+      Elem<T>* dx = reinterpret_cast<Elem<T>*>(p.dx) + r * p.cols;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = rstd * (dy[k][e] - c1 - xh[k][e] * c2);
+        store8<T, false>(dx + c[k], n[k], o);
+      }
+    }
+  }
+  if (!p.dw && !p.db) return;
+  if constexpr (NW == 1) {  // the block's four waves hold the same columns
+    if (wave > 0) {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          part[((wave - 1) * 2 * V + k) * 512 + 64 * e + lane] = dw[k][e];
+          part[((wave - 1) * 2 * V + V + k) * 512 + 64 * e + lane] = db[k][e];
+        }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[k][e] += part[(i * 2 * V + k) * 512 + 64 * e + lane];
+          db[k][e] += part[(i * 2 * V + V + k) * 512 + 64 * e + lane];
+        }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    if (direct) {  // one block: these are the gradients
+      if (p.dw) store8<P, false>(reinterpret_cast<Elem<P>*>(p.dw) + c[k], n[k], dw[k]);
+      if (p.db) store8<P, false>(reinterpret_cast<Elem<P>*>(p.db) + c[k], n[k], db[k]);
+    } else {
+      float* o = p.ws + (int64_t)blockIdx.x * 2 * p.cols + c[k];
+      store8<FP8SG_OUT_F32, false>(o, n[k], dw[k]);
+      store8<FP8SG_OUT_F32, false>(o + p.cols, n[k], db[k]);
+    }
+  }
+}
+
+// The sum of `parts` partial rows: 32 columns a block, 32 threads down each
+// column, then a tree.
+template <int P>
+__global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
+  __shared__ float red[32][33];
+  const int cl = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const bool bias = blockIdx.y != 0;
+  void* out = bias ? p.db : p.dw;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  float s = 0.f;
+  if (out && c < p.cols)
+    for (int i = k; i < parts; i += 32) s += p.ws[((int64_t)i * 2 + bias) * p.cols + c];
+  red[k][cl] = s;
+  __syncthreads();
+#pragma unroll
+  for (int h = 16; h > 0; h >>= 1) {
+    if (k < h) red[k][cl] += red[k + h][cl];
+    __syncthreads();
+  }
+  if (k == 0 && out && c < p.cols) reinterpret_cast<Elem<P>*>(out)[c] = from_f32<P>(red[0][cl]);
+}
+
+// ---- rows past kMaxCols: the same sums, the row read again for each
+template <int T, int P>
+__global__ __launch_bounds__(1024) void k_ln_fwd_long(LayerNormArgs p) {
+  __shared__ float red[2][16];
+  const int wave = threadIdx.x >> 6;
+  const float inv_n = 1.0f / (float)p.cols;
+  const int64_t pitch = act8_pitch(p.cols);
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const Elem<T>* x = reinterpret_cast<const Elem<T>*>(p.x) + r * p.cols;
     Elem<T>* y = reinterpret_cast<Elem<T>*>(p.y) + r * p.cols;
-    float s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) s += to_f32<T>(x[c]);
-    const float mean = block_sum<256>(s) * inv_n;
-    s = 0.f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) {
-      const float d = to_f32<T>(x[c]) - mean;
-      s += d * d;
+    float s = 0.f, v[8];
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
+      load8<T, false>(x + c, left8(p.cols, c), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[e];
     }
-    const float rstd = 1.0f / sqrtf(block_sum<256>(s) * inv_n + p.eps);
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256)
-      y[c] = from_f32<T>((to_f32<T>(x[c]) - mean) * rstd * param<P>(p.w, c, 1.f) + param<P>(p.b, c, 0.f));
+    const float mean = row_sum<16>(s, red[0], wave) * inv_n;
+    s = 0.f;
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
+      const int n = left8(p.cols, c);
+      load8<T, false>(x + c, n, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += e < n ? (v[e] - mean) * (v[e] - mean) : 0.f;
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<16>(s, red[1], wave) * inv_n + p.eps);
+    // whole waves walk the last round: the checkpoint's blocks span lanes
+    for (int64_t c0 = 0; c0 < p.cols; c0 += 8192) {
+      const int64_t c = c0 + 8 * (int64_t)threadIdx.x;
+      const int n = left8(p.cols, c);
+      load8<T, false>(x + c, n, v);
+      if (p.ckpt.q) {
+        const uint32_t sc = act8_scale(quad_amax(v));
+        if (c < pitch) {
+          *reinterpret_cast<uint2*>(p.ckpt.q + r * pitch + c) = act8_codes(v, sc);
+          if ((threadIdx.x & 3) == 0) p.ckpt.s[(r * pitch + c) >> 5] = (uint8_t)sc;
+        }
+      }
+      float w[8], b[8];
+      load_params<P>(p.w, c, n, 1.f, w);
+      load_params<P>(p.b, c, n, 0.f, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd * w[e] + b[e];
+      store8<T, false>(y + c, n, v);
+    }
     if (threadIdx.x == 0 && p.mean) {
       p.mean[r] = mean;
       p.rstd[r] = rstd;
@@ -50,67 +336,73 @@ __global__ __launch_bounds__(256) void k_ln_fwd(LayerNormArgs p) {
   }
 }
 
-// the forward's input, or its checkpoint's value
-template <int T>
-__device__ __forceinline__ float x_at(const LayerNormArgs& p, int64_t r, int64_t c) {
-  if (p.x) return to_f32<T>(reinterpret_cast<const Elem<T>*>(p.x)[r * p.cols + c]);
-  const int64_t at = r * act8_pitch(p.cols) + c;
-  return __builtin_amdgcn_cvt_f32_fp8((int)p.ckpt.q[at], 0) * scale_value(p.ckpt.s[at >> 5]);
-}
-
-template <int T, int P>
-__global__ __launch_bounds__(256) void k_ln_dx(LayerNormArgs p) {
+template <int T, int P, bool CKPT>
+__global__ __launch_bounds__(1024) void k_ln_dx_long(LayerNormArgs p) {
+  __shared__ float red[2][2][16];
+  const int wave = threadIdx.x >> 6;
   const float inv_n = 1.0f / (float)p.cols;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+  int it = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, it ^= 1) {
     const Elem<T>* dy = reinterpret_cast<const Elem<T>*>(p.dy) + r * p.cols;
     const float mean = p.mean[r], rstd = p.rstd[r];
-    float s1 = 0.f, s2 = 0.f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) {
-      const float q = to_f32<T>(dy[c]) * param<P>(p.w, c, 1.f);
-      s1 += q;
-      s2 += q * ((x_at<T>(p, r, c) - mean) * rstd);
+    float s1 = 0.f, s2 = 0.f, q[8], xh[8], w[8];
+    auto load = [&](int64_t c, int n) {
+      XRow<T, CKPT> x;
+      x.load(p, r, c, n);
+      x.values(xh);
+      load8<T, false>(dy + c, n, q);
+      load_params<P>(p.w, c, n, 1.f, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[e] = (xh[e] - mean) * rstd;
+        q[e] *= w[e];
+      }
+    };
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
+      load(c, left8(p.cols, c));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s1 += q[e];
+        s2 += q[e] * xh[e];
+      }
     }
-    const float c1 = block_sum<256>(s1) * inv_n, c2 = block_sum<256>(s2) * inv_n;
+    const float c1 = row_sum<16>(s1, red[it][0], wave) * inv_n, c2 = row_sum<16>(s2, red[it][1], wave) * inv_n;
     Elem<T>* dx = reinterpret_cast<Elem<T>*>(p.dx) + r * p.cols;
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) {
-      const float q = to_f32<T>(dy[c]) * param<P>(p.w, c, 1.f), xh = (x_at<T>(p, r, c) - mean) * rstd;
-      dx[c] = from_f32<T>(rstd * (q - c1 - xh * c2));
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
+      const int n = left8(p.cols, c);
+      load(c, n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = rstd * (q[e] - c1 - xh[e] * c2);
+      store8<T, false>(dx + c, n, q);
     }
   }
 }
 
-constexpr int kParts = 64;  // row chunks of the weight gradient's reduction
-
-// Column sums over one chunk of rows (blockIdx.y) into the workspace.
-template <int T>
-__global__ __launch_bounds__(256) void k_ln_dwb_part(LayerNormArgs p) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// Partial rows of dw and db: 8 columns a thread, the rows of chunk blockIdx.y.
+template <int T, bool CKPT>
+__global__ __launch_bounds__(64) void k_ln_dwb_long(LayerNormArgs p) {
+  const int64_t c = ((int64_t)blockIdx.x * 64 + threadIdx.x) * 8;
   if (c >= p.cols) return;
-  const int64_t per = (p.rows + kParts - 1) / kParts, r0 = blockIdx.y * per;
+  const int n = left8(p.cols, c);
+  const int64_t per = (p.rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * per;
   const int64_t r1 = r0 + per < p.rows ? r0 + per : p.rows;
-  float dw = 0.f, db = 0.f;
+  float dw[8] = {}, db[8] = {}, x[8], dy[8];
   for (int64_t r = r0; r < r1; ++r) {
-    const float dy = to_f32<T>(reinterpret_cast<const Elem<T>*>(p.dy)[r * p.cols + c]);
-    dw += dy * ((x_at<T>(p, r, c) - p.mean[r]) * p.rstd[r]);
-    db += dy;
+    XRow<T, CKPT> xr;
+    xr.load(p, r, c, n);
+    xr.values(x);
+    load8<T, false>(reinterpret_cast<const Elem<T>*>(p.dy) + r * p.cols + c, n, dy);
+    const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dw[e] += dy[e] * ((x[e] - mean) * rstd);
+      db[e] += dy[e];
+    }
   }
-  p.ws[(int64_t)blockIdx.y * 2 * p.cols + c] = dw;
-  p.ws[(int64_t)blockIdx.y * 2 * p.cols + p.cols + c] = db;
+  float* o = p.ws + (int64_t)blockIdx.y * 2 * p.cols + c;
+  store8<FP8SG_OUT_F32, false>(o, n, dw);
+  store8<FP8SG_OUT_F32, false>(o + p.cols, n, db);
 }
-template <int P>
-__global__ __launch_bounds__(256) void k_ln_dwb_join(LayerNormArgs p) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.cols) return;
-  float dw = 0.f, db = 0.f;
-  for (int k = 0; k < kParts; ++k) {
-    dw += p.ws[(int64_t)k * 2 * p.cols + c];
-    db += p.ws[(int64_t)k * 2 * p.cols + p.cols + c];
-  }
-  if (p.dw) reinterpret_cast<Elem<P>*>(p.dw)[c] = from_f32<P>(dw);
-  if (p.db) reinterpret_cast<Elem<P>*>(p.db)[c] = from_f32<P>(db);
-}
-
-unsigned row_blocks(int64_t rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
 
 template <class F>
 hipError_t by_types(int type, int ptype, F f) {
@@ -120,37 +412,86 @@ hipError_t by_types(int type, int ptype, F f) {
     return hipGetLastError();
   });
 }
+// f(waves per row, groups of 8 per thread) for a row of up to kMaxCols.  The
+// backward keeps five fp32 values an element: past 8192 columns it takes more
+// registers a thread (8 waves x 4 groups) rather than 16 waves, whose 128
+// registers a thread it would overrun.
+template <bool BWD, class F>
+void by_width(int64_t cols, F f) {
+  typedef std::integral_constant<int, 1> C1;
+  typedef std::integral_constant<int, 2> C2;
+  if (cols <= 512) f(C1{}, C1{});
+  else if (cols <= 1024) f(C1{}, C2{});
+  else if (cols <= 2048) f(std::integral_constant<int, 4>{}, C1{});
+  else if (cols <= 4096) f(std::integral_constant<int, 4>{}, C2{});
+  else if (cols <= 8192) f(std::integral_constant<int, 8>{}, C2{});
+  else if constexpr (BWD) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, 16>{}, C2{});
+}
+
+// Partial rows of the weight gradients: a block each, enough of them to fill
+// the chip, few enough that writing and adding them stays small next to the
+// rows themselves (8 bytes a column and part against 4 to 12 a column and
+// row).  One, when the rows are few: the block then writes the gradients.
+constexpr int64_t kDirectRows = 8;
+int64_t parts_of(int64_t rows, int64_t cols) {
+  if (cols > kMaxCols) return 64;
+  const int64_t per_block = cols <= 1024 ? 4 : 1;
+  if (rows <= kDirectRows * per_block) return 1;
+  const int64_t n = (rows + 4 * per_block - 1) / (4 * per_block);
+  return n < 512 ? n : 512;
+}
+
+unsigned cap(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
 
 }  // namespace
 
-int64_t layer_norm_ws_len(int64_t rows, int64_t cols) {
-  (void)rows;
-  return 2 * kParts * cols;
-}
+int64_t layer_norm_ws_len(int64_t rows, int64_t cols) { return 2 * parts_of(rows, cols) * cols; }
 
 hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, int type, int ptype, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  if (a.ckpt.q) {
-    const hipError_t e = launch_act8_quantize(a.x, type, a.rows, a.cols, a.ckpt, stream);
-    if (e != hipSuccess) return e;
-  }
   return by_types(type, ptype, [&](auto t, auto p) {
-    hipLaunchKernelGGL((k_ln_fwd<decltype(t)::value, decltype(p)::value>), dim3(row_blocks(a.rows)), dim3(256), 0,
-                       stream, a);
+    constexpr int T = decltype(t)::value, P = decltype(p)::value;
+    if (a.cols > kMaxCols) {
+      hipLaunchKernelGGL((k_ln_fwd_long<T, P>), dim3(cap(a.rows, 1 << 16)), dim3(1024), 0, stream, a);
+      return;
+    }
+    by_width<false>(a.cols, [&](auto nw, auto v) {
+      constexpr int NW = decltype(nw)::value, V = decltype(v)::value, R = NW == 1 ? 4 : 1;
+      // a few rows a block, so that the parameters are loaded once for them
+      const unsigned grid = cap((a.rows + R - 1) / R, 4096);
+      hipLaunchKernelGGL((k_ln_fwd<T, P, NW, V>), dim3(grid), dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
+    });
   });
 }
 
 hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, int type, int ptype, hipStream_t stream) {
-  if (a.cols == 0) return hipSuccess;
+  if (a.cols == 0 || (a.rows == 0 && !a.dw && !a.db)) return hipSuccess;
+  const int parts = (int)parts_of(a.rows, a.cols);
+  const bool wb = a.dw || a.db;
   return by_types(type, ptype, [&](auto t, auto p) {
     constexpr int T = decltype(t)::value, P = decltype(p)::value;
-    if (a.dx && a.rows > 0)
-      hipLaunchKernelGGL((k_ln_dx<T, P>), dim3(row_blocks(a.rows)), dim3(256), 0, stream, a);
-    if (a.dw || a.db) {
-      const unsigned gx = (unsigned)((a.cols + 255) / 256);
-      hipLaunchKernelGGL((k_ln_dwb_part<T>), dim3(gx, kParts), dim3(256), 0, stream, a);
-      hipLaunchKernelGGL((k_ln_dwb_join<P>), dim3(gx), dim3(256), 0, stream, a);
-    }
+    auto run = [&](auto ck) {
+      constexpr bool CK = decltype(ck)::value;
+      if (a.cols > kMaxCols) {
+        if (a.dx && a.rows > 0)
+          hipLaunchKernelGGL((k_ln_dx_long<T, P, CK>), dim3(cap(a.rows, 1 << 16)), dim3(1024), 0, stream, a);
+        if (wb)
+          hipLaunchKernelGGL((k_ln_dwb_long<T, CK>), dim3((unsigned)((a.cols + 511) / 512), parts), dim3(64), 0, stream, a);
+        return;
+      }
+      by_width<true>(a.cols, [&](auto nw, auto v) {
+        constexpr int NW = decltype(nw)::value, V = decltype(v)::value, R = NW == 1 ? 4 : 1;
+        const unsigned grid = wb ? (unsigned)parts : cap((a.rows + R - 1) / R, 2048);
+        const size_t lds = NW == 1 ? 3 * 2 * V * 512 * sizeof(float) : 0;
+        hipLaunchKernelGGL((k_ln_bwd<T, P, NW, V, CK>), dim3(grid), dim3(NW == 1 ? 256 : 64 * NW), lds, stream, a,
+                           parts == 1 ? 1 : 0);
+      });
+    };
+    if (a.ckpt.q) run(std::true_type{});
+    else run(std::false_type{});
+    if (wb && (a.cols > kMaxCols || parts > 1))
+      hipLaunchKernelGGL((k_ln_join<P>), dim3((unsigned)((a.cols + 31) / 32), 2), dim3(1024), 0, stream, a, parts);
   });
 }
 

@@ -125,39 +125,82 @@ __device__ __forceinline__ uint32_t quad_amax(const float (&v)[8]) {
   return o > m ? o : m;
 }
 
-// ---- eight consecutive elements of a row.  VEC: the address is 16-byte
-// aligned and all eight are in range; otherwise element by element, those at
-// or past `n` reading 0 and not written.  S: non-temporal.
-template <int T, bool VEC, bool S>
-__device__ __forceinline__ void load8(const Elem<T>* p, int n, float (&v)[8]) {
-  if constexpr (VEC) {
-    if constexpr (T == FP8SG_OUT_F32) {
-      const uint4 a = ld16<S>(p), b = ld16<S>(p + 4);
-      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-    } else {
-      constexpr bool H = T == FP8SG_OUT_F16;
-      const uint4 a = ld16<S>(p);
-      v[0] = in_lo<H>(a.x); v[1] = in_hi<H>(a.x); v[2] = in_lo<H>(a.y); v[3] = in_hi<H>(a.y);
-      v[4] = in_lo<H>(a.z); v[5] = in_hi<H>(a.z); v[6] = in_lo<H>(a.w); v[7] = in_hi<H>(a.w);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? to_f32<T>(p[e]) : 0.f;
-  }
+// ---- eight consecutive elements of a row, p[0 .. 7], of which n are in range
+// (the rest read as 0 and are not written).  Whole groups move as 16-byte
+// accesses at whatever address the row has: the hardware takes any, and the
+// type tells the compiler.  S: non-temporal.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <bool S>
+__device__ __forceinline__ u32x4 ld_any(const void* p) {
+  const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
+  const u32x4_any v = S ? __builtin_nontemporal_load(q) : *q;
+  return u32x4{v.x, v.y, v.z, v.w};
 }
-template <int T, bool VEC, bool S>
+template <bool S>
+__device__ __forceinline__ void st_any(void* p, u32x4 v) {
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
+  const u32x4_any w = {v.x, v.y, v.z, v.w};
+  if constexpr (S) __builtin_nontemporal_store(w, q);
+  else *q = w;
+}
+
+// As loaded: 4 dwords of 16-bit elements or 8 of fp32.
+template <int T>
+struct Row8 {
+  static constexpr int kW = T == FP8SG_OUT_F32 ? 8 : 4;
+  uint32_t w[kW];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (T == FP8SG_OUT_F32) v[e] = __uint_as_float(w[e]);
+      else v[e] = (e & 1) ? in_hi<T == FP8SG_OUT_F16>(w[e / 2]) : in_lo<T == FP8SG_OUT_F16>(w[e / 2]);
+    }
+  }
+};
+template <int T, bool S>
+__device__ __forceinline__ Row8<T> load_row8(const Elem<T>* p, int n) {
+  Row8<T> r;
+  if (n >= 8) {
+#pragma unroll
+    for (int h = 0; h < Row8<T>::kW / 4; ++h) {
+      const u32x4 v = ld_any<S>(p + 4 * h);
+      r.w[4 * h] = v.x;
+      r.w[4 * h + 1] = v.y;
+      r.w[4 * h + 2] = v.z;
+      r.w[4 * h + 3] = v.w;
+    }
+  } else {  // the row's end, element by element (constant offsets: nothing for a loop around it to keep)
+    r.zero();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e < n) {
+        if constexpr (T == FP8SG_OUT_F32) r.w[e] = __float_as_uint(p[e]);
+        else r.w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+      }
+    }
+  }
+  return r;
+}
+template <int T, bool S>
+__device__ __forceinline__ void load8(const Elem<T>* p, int n, float (&v)[8]) {
+  load_row8<T, S>(p, n).values(v);
+}
+template <int T, bool S>
 __device__ __forceinline__ void store8(Elem<T>* p, int n, const float (&v)[8]) {
-  if constexpr (VEC) {
+  if (n >= 8) {
     if constexpr (T == FP8SG_OUT_F32) {
-      st16<S>(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-      st16<S>(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+      st_any<S>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+      st_any<S>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
     } else {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = (uint32_t)from_f32<T>(v[2 * e]) | ((uint32_t)from_f32<T>(v[2 * e + 1]) << 16);
-      st16<S>(p, make_uint4(w[0], w[1], w[2], w[3]));
+      st_any<S>(p, u32x4{w[0], w[1], w[2], w[3]});
     }
   } else {
 #pragma unroll
@@ -165,5 +208,7 @@ __device__ __forceinline__ void store8(Elem<T>* p, int n, const float (&v)[8]) {
       if (e < n) p[e] = from_f32<T>(v[e]);
   }
 }
+// elements of the 8 from c on that a row of `cols` has
+__device__ __forceinline__ int left8(int64_t cols, int64_t c) { return cols - c < 8 ? (int)(cols - c) : 8; }
 
 }  // namespace fp8sg

@@ -8,50 +8,6 @@
 namespace fp8sg {
 namespace {
 
-// Eight 16-bit elements (4 dwords) or eight fp32 (8 dwords) of a row in
-// registers, as loaded.
-template <int T>
-struct Row8 {
-  static constexpr int kW = T == FP8SG_OUT_F32 ? 8 : 4;
-  uint32_t w[kW];
-};
-// 16 bytes at an address aligned to 2 (the hardware takes any; the type tells
-// the compiler).
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-
-// p: the row's first element; elements c .. c + 7, those at or past `cols`
-// read as zero (cols > 0).
-template <int T, bool S>
-__device__ __forceinline__ Row8<T> load_row8(const Elem<T>* p, int64_t c, int64_t cols) {
-  Row8<T> r;
-  if (c + 8 <= cols) {
-#pragma unroll
-    for (int h = 0; h < Row8<T>::kW / 4; ++h) {
-      const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p + c + 4 * h);
-      const u32x4_any v = S ? __builtin_nontemporal_load(q) : *q;
-      r.w[4 * h] = v.x;
-      r.w[4 * h + 1] = v.y;
-      r.w[4 * h + 2] = v.z;
-      r.w[4 * h + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t at = c + e < cols ? c + e : cols - 1;
-      const Elem<T> v = p[at];
-      const bool in = c + e < cols;
-      if constexpr (T == FP8SG_OUT_F32) {
-        r.w[e] = in ? __float_as_uint(v) : 0u;
-      } else {
-        const uint32_t b = in ? (uint32_t)v : 0u;
-        if (e & 1) r.w[e / 2] |= b << 16;
-        else r.w[e / 2] = b;
-      }
-    }
-  }
-  return r;
-}
-
 // Running largest magnitudes as bit patterns: two 16-bit ones a dword, or fp32.
 template <int T>
 __device__ __forceinline__ uint32_t mag_max(uint32_t m, uint32_t w) {
@@ -163,10 +119,9 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if (rw + i < j.rows && c < j.cols) {
-      v[i] = load_row8<T, S>(x + (rw + i) * j.cols, c, j.cols);
+      v[i] = load_row8<T, S>(x + (rw + i) * j.cols + c, left8(j.cols, c));
     } else {
-#pragma unroll
-      for (int e = 0; e < Row8<T>::kW; ++e) v[i].w[e] = 0u;
+      v[i].zero();
     }
   }
 
@@ -250,10 +205,9 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
 }
 
 // One thread per 8 values: 4 bytes of codes, their block's scale.
-template <int T>
+template <int T, bool S>
 __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t rows, int64_t k, Elem<T>* y) {
   const int64_t nk = mx_ktiles(k), upr = (k + 7) / 8, total = rows * upr;
-  const bool vec = (k * sizeof(Elem<T>)) % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
   for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < total; i0 += (int64_t)gridDim.x * 256) {
     const int64_t rb = i0 / upr;  // uniform
     const uint32_t t = (uint32_t)(i0 - rb * upr) + threadIdx.x, dr = t / (uint32_t)upr;
@@ -264,8 +218,7 @@ __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t row
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
     const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
     const float v[8] = {a[0] * sc, a[1] * sc, b[0] * sc, b[1] * sc, c[0] * sc, c[1] * sc, d[0] * sc, d[1] * sc};
-    if (vec) store8<T, true, false>(y + r * k + 8 * u, 8, v);
-    else store8<T, false, false>(y + r * k + 8 * u, (int)(k - 8 * u < 8 ? k - 8 * u : 8), v);
+    store8<T, S>(y + r * k + 8 * u, left8(k, 8 * u), v);
   }
 }
 
@@ -316,8 +269,11 @@ hipError_t launch_mx_dequantize(const mxfp4_operand& m, int64_t rows, int64_t k,
   if (rows == 0 || k == 0) return hipSuccess;
   return by_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    hipLaunchKernelGGL((k_mx_dequant<T>), dim3(grid_for(rows * ((k + 7) / 8))), dim3(256), 0, stream, m, rows, k,
-                       reinterpret_cast<Elem<T>*>(y));
+    const dim3 grid(grid_for(rows * ((k + 7) / 8)));
+    if (rows * k * (int64_t)sizeof(Elem<T>) >= kStreamBytes)
+      hipLaunchKernelGGL((k_mx_dequant<T, true>), grid, dim3(256), 0, stream, m, rows, k, reinterpret_cast<Elem<T>*>(y));
+    else
+      hipLaunchKernelGGL((k_mx_dequant<T, false>), grid, dim3(256), 0, stream, m, rows, k, reinterpret_cast<Elem<T>*>(y));
     return hipGetLastError();
   });
 }

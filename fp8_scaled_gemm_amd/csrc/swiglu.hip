@@ -11,123 +11,133 @@
 namespace fp8sg {
 namespace {
 
-// Item (8 elements) t of this block -> row and unit of the row: items are
-// numbered row after row, `upr` units a row.  One 64-bit division a block
-// (uniform), one 32-bit division a thread.
+// Unit (8 elements) of this thread in group `blk` of 256: units are numbered row
+// after row, `upr` a row.  One 64-bit division a block (uniform), one 32-bit
+// division a thread.
 struct Unit {
   int64_t row;
   int64_t u;
 };
-__device__ __forceinline__ Unit unit_of(int64_t upr) {
-  const int64_t i0 = (int64_t)blockIdx.x * 256, r0 = i0 / upr;
+__device__ __forceinline__ Unit unit_of(int64_t blk, int64_t upr) {
+  const int64_t i0 = blk * 256, r0 = i0 / upr;
   const int64_t t = i0 - r0 * upr + threadIdx.x;  // < upr + 256, and upr <= 2^26
   const uint32_t d = (uint32_t)t / (uint32_t)upr;
   return Unit{r0 + d, t - (int64_t)d * upr};
 }
 
+// Groups of 256 units of a rows x cols matrix, and the grid that walks them (a
+// launch holds fewer than 2^32 threads).
+__host__ __device__ inline int64_t groups_of(int64_t rows, int64_t cols) {
+  return (rows * (act8_pitch(cols) / 8) + 255) / 256;
+}
+unsigned grid_of(int64_t rows, int64_t cols) {
+  const int64_t n = groups_of(rows, cols);
+  return (unsigned)(n < (1 << 22) ? n : (1 << 22));
+}
+
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 
-template <int T, bool VEC, bool S, bool CKPT>
+template <int T, bool S, bool CKPT>
 __global__ __launch_bounds__(256) void k_swiglu_fwd(SwigluArgs p) {
   const int64_t pitch = act8_pitch(p.cols);
-  const Unit w = unit_of(pitch / 8);
-  const bool in = w.row < p.rows;
-  const int64_t c = w.u * 8;
-  const int n = in && c < p.cols ? (int)(p.cols - c < 8 ? p.cols - c : 8) : 0;
-  float g[8] = {}, u[8] = {}, a[8];
-  if (n > 0) {
-    load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(p.g) + w.row * p.ldg + c, n, g);
-    load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(p.u) + w.row * p.ldu + c, n, u);
+  for (int64_t blk = blockIdx.x; blk < groups_of(p.rows, p.cols); blk += gridDim.x) {
+    const Unit w = unit_of(blk, pitch / 8);
+    const bool in = w.row < p.rows;
+    const int64_t c = w.u * 8;
+    const int n = in && c < p.cols ? left8(p.cols, c) : 0;
+    float g[8] = {}, u[8] = {}, a[8];
+    if (n > 0) {
+      load8<T, S>(reinterpret_cast<const Elem<T>*>(p.g) + w.row * p.ldg + c, n, g);
+      load8<T, S>(reinterpret_cast<const Elem<T>*>(p.u) + w.row * p.ldu + c, n, u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = g[e] * sigmoid(g[e]) * u[e];
-    store8<T, VEC, S>(reinterpret_cast<Elem<T>*>(p.a) + w.row * p.cols + c, n, a);
-  }
-  if constexpr (CKPT) {
-    const uint32_t sg = act8_scale(quad_amax(g)), su = act8_scale(quad_amax(u));
-    if (in) {
-      const int64_t at = w.row * pitch + c;
-      st8<S>(p.cg.q + at, act8_codes(g, sg));
-      st8<S>(p.cu.q + at, act8_codes(u, su));
-      if ((w.u & 3) == 0) {
-        p.cg.s[at >> 5] = (uint8_t)sg;
-        p.cu.s[at >> 5] = (uint8_t)su;
+      for (int e = 0; e < 8; ++e) a[e] = g[e] * sigmoid(g[e]) * u[e];
+      store8<T, S>(reinterpret_cast<Elem<T>*>(p.a) + w.row * p.cols + c, n, a);
+    }
+    if constexpr (CKPT) {
+      const uint32_t sg = act8_scale(quad_amax(g)), su = act8_scale(quad_amax(u));
+      if (in) {
+        const int64_t at = w.row * pitch + c;
+        st8<S>(p.cg.q + at, act8_codes(g, sg));
+        st8<S>(p.cu.q + at, act8_codes(u, su));
+        if ((w.u & 3) == 0) {
+          p.cg.s[at >> 5] = (uint8_t)sg;
+          p.cu.s[at >> 5] = (uint8_t)su;
+        }
       }
     }
   }
 }
 
-template <int T, bool VEC, bool S, bool CKPT>
+template <int T, bool S, bool CKPT>
 __global__ __launch_bounds__(256) void k_swiglu_bwd(SwigluArgs p) {
   const int64_t pitch = act8_pitch(p.cols);
-  const Unit w = unit_of(pitch / 8);
-  const int64_t c = w.u * 8;
-  if (w.row >= p.rows || c >= p.cols) return;
-  const int n = (int)(p.cols - c < 8 ? p.cols - c : 8);
-  float g[8], u[8], da[8], dg[8], du[8];
-  load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(p.da) + w.row * p.cols + c, n, da);
-  if constexpr (CKPT) {
-    const int64_t at = w.row * pitch + c;
-    act8_values(*reinterpret_cast<const uint2*>(p.cg.q + at), p.cg.s[at >> 5], g);
-    act8_values(*reinterpret_cast<const uint2*>(p.cu.q + at), p.cu.s[at >> 5], u);
-  } else {
-    load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(p.g) + w.row * p.ldg + c, n, g);
-    load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(p.u) + w.row * p.ldu + c, n, u);
-  }
+  for (int64_t blk = blockIdx.x; blk < groups_of(p.rows, p.cols); blk += gridDim.x) {
+    const Unit w = unit_of(blk, pitch / 8);
+    const int64_t c = w.u * 8;
+    if (w.row >= p.rows || c >= p.cols) continue;
+    const int n = left8(p.cols, c);
+    float g[8], u[8], da[8], dg[8], du[8];
+    load8<T, S>(reinterpret_cast<const Elem<T>*>(p.da) + w.row * p.cols + c, n, da);
+    if constexpr (CKPT) {
+      const int64_t at = w.row * pitch + c;
+      act8_values(*reinterpret_cast<const uint2*>(p.cg.q + at), p.cg.s[at >> 5], g);
+      act8_values(*reinterpret_cast<const uint2*>(p.cu.q + at), p.cu.s[at >> 5], u);
+    } else {
+      load8<T, S>(reinterpret_cast<const Elem<T>*>(p.g) + w.row * p.ldg + c, n, g);
+      load8<T, S>(reinterpret_cast<const Elem<T>*>(p.u) + w.row * p.ldu + c, n, u);
+    }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float sg = sigmoid(g[e]), d = da[e] * sg;
-    du[e] = d * g[e];
-    dg[e] = d * u[e] * (1.0f + g[e] * (1.0f - sg));
+    for (int e = 0; e < 8; ++e) {
+      const float sg = sigmoid(g[e]), d = da[e] * sg;
+      du[e] = d * g[e];
+      dg[e] = d * u[e] * (1.0f + g[e] * (1.0f - sg));
+    }
+    store8<T, S>(reinterpret_cast<Elem<T>*>(p.dg) + w.row * p.lddg + c, n, dg);
+    store8<T, S>(reinterpret_cast<Elem<T>*>(p.du) + w.row * p.lddu + c, n, du);
   }
-  store8<T, VEC, S>(reinterpret_cast<Elem<T>*>(p.dg) + w.row * p.lddg + c, n, dg);
-  store8<T, VEC, S>(reinterpret_cast<Elem<T>*>(p.du) + w.row * p.lddu + c, n, du);
 }
 
-template <int T, bool VEC, bool S>
+template <int T, bool S>
 __global__ __launch_bounds__(256) void k_act8_quant(const void* x, int64_t rows, int64_t cols, fp8sg_act8 q) {
   const int64_t pitch = act8_pitch(cols);
-  const Unit w = unit_of(pitch / 8);
-  const bool in = w.row < rows;
-  const int64_t c = w.u * 8;
-  const int n = in && c < cols ? (int)(cols - c < 8 ? cols - c : 8) : 0;
-  float v[8] = {};
-  if (n > 0) load8<T, VEC, S>(reinterpret_cast<const Elem<T>*>(x) + w.row * cols + c, n, v);
-  const uint32_t s = act8_scale(quad_amax(v));
-  if (!in) return;
-  const int64_t at = w.row * pitch + c;
-  st8<S>(q.q + at, act8_codes(v, s));
-  if ((w.u & 3) == 0) q.s[at >> 5] = (uint8_t)s;
+  for (int64_t blk = blockIdx.x; blk < groups_of(rows, cols); blk += gridDim.x) {
+    const Unit w = unit_of(blk, pitch / 8);
+    const bool in = w.row < rows;
+    const int64_t c = w.u * 8;
+    const int n = in && c < cols ? left8(cols, c) : 0;
+    float v[8] = {};
+    if (n > 0) load8<T, S>(reinterpret_cast<const Elem<T>*>(x) + w.row * cols + c, n, v);
+    const uint32_t s = act8_scale(quad_amax(v));
+    if (!in) continue;
+    const int64_t at = w.row * pitch + c;
+    st8<S>(q.q + at, act8_codes(v, s));
+    if ((w.u & 3) == 0) q.s[at >> 5] = (uint8_t)s;
+  }
 }
 
-template <int T, bool VEC, bool S>
+template <int T, bool S>
 __global__ __launch_bounds__(256) void k_act8_dequant(fp8sg_act8 q, int64_t rows, int64_t cols, void* y) {
   const int64_t pitch = act8_pitch(cols);
-  const Unit w = unit_of(pitch / 8);
-  const int64_t c = w.u * 8;
-  if (w.row >= rows || c >= cols) return;
-  const int n = (int)(cols - c < 8 ? cols - c : 8);
-  const int64_t at = w.row * pitch + c;
-  float v[8];
-  act8_values(*reinterpret_cast<const uint2*>(q.q + at), q.s[at >> 5], v);
-  store8<T, VEC, S>(reinterpret_cast<Elem<T>*>(y) + w.row * cols + c, n, v);
+  for (int64_t blk = blockIdx.x; blk < groups_of(rows, cols); blk += gridDim.x) {
+    const Unit w = unit_of(blk, pitch / 8);
+    const int64_t c = w.u * 8;
+    if (w.row >= rows || c >= cols) continue;
+    const int n = left8(cols, c);
+    const int64_t at = w.row * pitch + c;
+    float v[8];
+    act8_values(*reinterpret_cast<const uint2*>(q.q + at), q.s[at >> 5], v);
+    store8<T, S>(reinterpret_cast<Elem<T>*>(y) + w.row * cols + c, n, v);
+  }
 }
 
-unsigned blocks_of(int64_t rows, int64_t cols) { return (unsigned)((rows * (act8_pitch(cols) / 8) + 255) / 256); }
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int64_t esize(int type) { return type == FP8SG_OUT_F32 ? 4 : 2; }
-// rows of `ld` elements that all start 16-byte aligned
-bool rows16(const void* p, int64_t ld, int type) { return al16(p) && ld * esize(type) % 16 == 0; }
 
-// f(type, vector, streaming) as compile-time constants
+// f(type, streaming) as compile-time constants
 template <class F>
-hipError_t pick(int type, bool vec, bool stream, F f) {
+hipError_t pick(int type, bool stream, F f) {
   return by_type(type, [&](auto t) {
-    if (vec) {
-      if (stream) f(t, std::true_type{}, std::true_type{});
-      else f(t, std::true_type{}, std::false_type{});
-    } else {
-      f(t, std::false_type{}, std::false_type{});
-    }
+    if (stream) f(t, std::true_type{});
+    else f(t, std::false_type{});
     return hipGetLastError();
   });
 }
@@ -136,47 +146,43 @@ hipError_t pick(int type, bool vec, bool stream, F f) {
 
 hipError_t launch_swiglu_fwd(const SwigluArgs& a, int type, hipStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return hipSuccess;
-  const bool vec = a.cols % 8 == 0 && rows16(a.g, a.ldg, type) && rows16(a.u, a.ldu, type) && rows16(a.a, a.cols, type);
   const bool big = a.rows * a.cols * (3 * esize(type) + (a.cg.q ? 2 : 0)) >= kStreamBytes;
-  const dim3 grid(blocks_of(a.rows, a.cols));
-  return pick(type, vec, big, [&](auto t, auto v, auto s) {
+  const dim3 grid(grid_of(a.rows, a.cols));
+  return pick(type, big, [&](auto t, auto s) {
     constexpr int T = decltype(t)::value;
-    constexpr bool V = decltype(v)::value, St = decltype(s)::value;
-    if (a.cg.q) hipLaunchKernelGGL((k_swiglu_fwd<T, V, St, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((k_swiglu_fwd<T, V, St, false>), grid, dim3(256), 0, stream, a);
+    constexpr bool St = decltype(s)::value;
+    if (a.cg.q) hipLaunchKernelGGL((k_swiglu_fwd<T, St, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_swiglu_fwd<T, St, false>), grid, dim3(256), 0, stream, a);
   });
 }
 
 hipError_t launch_swiglu_bwd(const SwigluArgs& a, int type, hipStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return hipSuccess;
-  const bool vec = a.cols % 8 == 0 && rows16(a.da, a.cols, type) && rows16(a.dg, a.lddg, type) &&
-                   rows16(a.du, a.lddu, type) &&
-                   (a.cg.q || (rows16(a.g, a.ldg, type) && rows16(a.u, a.ldu, type)));
   const bool big = a.rows * a.cols * (3 * esize(type) + 2 * (a.cg.q ? 1 : esize(type))) >= kStreamBytes;
-  const dim3 grid(blocks_of(a.rows, a.cols));
-  return pick(type, vec, big, [&](auto t, auto v, auto s) {
+  const dim3 grid(grid_of(a.rows, a.cols));
+  return pick(type, big, [&](auto t, auto s) {
     constexpr int T = decltype(t)::value;
-    constexpr bool V = decltype(v)::value, St = decltype(s)::value;
-    if (a.cg.q) hipLaunchKernelGGL((k_swiglu_bwd<T, V, St, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((k_swiglu_bwd<T, V, St, false>), grid, dim3(256), 0, stream, a);
+    constexpr bool St = decltype(s)::value;
+    if (a.cg.q) hipLaunchKernelGGL((k_swiglu_bwd<T, St, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_swiglu_bwd<T, St, false>), grid, dim3(256), 0, stream, a);
   });
 }
 
 hipError_t launch_act8_quantize(const void* x, int type, int64_t rows, int64_t cols, fp8sg_act8 c, hipStream_t stream) {
   if (rows == 0 || cols == 0) return hipSuccess;
-  const bool vec = cols % 8 == 0 && rows16(x, cols, type), big = rows * cols * (esize(type) + 1) >= kStreamBytes;
-  return pick(type, vec, big, [&](auto t, auto v, auto s) {
-    hipLaunchKernelGGL((k_act8_quant<decltype(t)::value, decltype(v)::value, decltype(s)::value>),
-                       dim3(blocks_of(rows, cols)), dim3(256), 0, stream, x, rows, cols, c);
+  const bool big = rows * cols * (esize(type) + 1) >= kStreamBytes;
+  return pick(type, big, [&](auto t, auto s) {
+    hipLaunchKernelGGL((k_act8_quant<decltype(t)::value, decltype(s)::value>),
+                       dim3(grid_of(rows, cols)), dim3(256), 0, stream, x, rows, cols, c);
   });
 }
 
 hipError_t launch_act8_dequantize(fp8sg_act8 c, int64_t rows, int64_t cols, void* y, int type, hipStream_t stream) {
   if (rows == 0 || cols == 0) return hipSuccess;
-  const bool vec = cols % 8 == 0 && rows16(y, cols, type), big = rows * cols * (esize(type) + 1) >= kStreamBytes;
-  return pick(type, vec, big, [&](auto t, auto v, auto s) {
-    hipLaunchKernelGGL((k_act8_dequant<decltype(t)::value, decltype(v)::value, decltype(s)::value>),
-                       dim3(blocks_of(rows, cols)), dim3(256), 0, stream, c, rows, cols, y);
+  const bool big = rows * cols * (esize(type) + 1) >= kStreamBytes;
+  return pick(type, big, [&](auto t, auto s) {
+    hipLaunchKernelGGL((k_act8_dequant<decltype(t)::value, decltype(s)::value>),
+                       dim3(grid_of(rows, cols)), dim3(256), 0, stream, c, rows, cols, y);
   });
 }
 
