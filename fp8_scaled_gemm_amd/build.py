@@ -11,6 +11,11 @@ The compiler's per-kernel resource report is read on every build: a kernel
 that spills more than MAX_SPILL_VGPRS registers to scratch fails the build (a
 change to the GEMM's loop shape once spilled its accumulators and ran 30x
 slower with correct results).
+
+The assembly of IN_PLACE's files is read as well: every matrix instruction
+there has to add into the registers it writes.  For these kernels the compiler
+once gave a product's result registers that still held another accumulator,
+which cannot happen to a product whose result and addend are the same.
 """
 import concurrent.futures as cf
 import glob
@@ -30,6 +35,7 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=h
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-command-line-argument"]
 MAX_SPILL_VGPRS = 64
+IN_PLACE = ("mx_gemm.hip",)
 
 
 def spills(stderr: str) -> dict:
@@ -45,13 +51,29 @@ def spills(stderr: str) -> dict:
     return out
 
 
+def moved_products(asm: str) -> dict:
+    """{kernel: matrix instructions whose result and addend registers differ}."""
+    out, name = {}, None
+    for line in asm.splitlines():
+        m = re.match(r"(\w+):", line)
+        if m and not line.startswith(".L"):
+            name = m.group(1)
+        m = re.match(r"\s+v_mfma\S* ([^,]+), [^,]+, [^,]+, ([^,\s]+)", line)
+        if m and m.group(1).strip() != m.group(2).strip():
+            out[name] = out.get(name, 0) + 1
+    return out
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
 def _compile(src, verbose):
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
+    guarded = os.path.basename(src) in IN_PLACE
     cmd = [HIPCC, *FLAGS, "-Rpass-analysis=kernel-resource-usage", "-c", src, "-o", obj]
+    if guarded:
+        cmd.append("-save-temps=obj")
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -60,6 +82,14 @@ def _compile(src, verbose):
     bad = {k: v for k, v in spills(r.stderr or "").items() if v > MAX_SPILL_VGPRS}
     if bad:
         raise RuntimeError(f"{src}: kernels spill registers to scratch: {bad}")
+    if guarded:
+        stem = os.path.splitext(os.path.basename(src))[0]
+        with open(os.path.join(OBJDIR, f"{stem}-hip-amdgcn-amd-amdhsa-{ARCH}.s")) as f:
+            moved = moved_products(f.read())
+        for temp in glob.glob(os.path.join(OBJDIR, f"{stem}-h*")) + glob.glob(os.path.join(OBJDIR, f"{stem}.hip-h*")):
+            os.remove(temp)
+        if moved:
+            raise RuntimeError(f"{src}: products that do not add in place: {moved}")
     # the host pass does not know the packed-fp32 feature and says so; drop that
     # noise, and the resource remarks
     noise = "is not a recognized feature for this target"

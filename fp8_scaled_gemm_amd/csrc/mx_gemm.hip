@@ -20,7 +20,8 @@ __device__ __forceinline__ v4f mfma4(uint4 b, uint4 a, v4f c, uint32_t sb, uint3
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 4, 4, SB, (int)sb, SA, (int)sa);
 }
 
-// One wave per 16 x 16 block of C, fragments straight from memory.
+// One wave per 16 x 16 block of C, fragments straight from memory, in 64-bit
+// addresses: for contractions too long for the other kernels' offsets.
 template <int OUT>
 __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
@@ -255,22 +256,310 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   }
 }
 
+
+// Medium kernel: a 128 x 128 tile per workgroup of four waves (64 x 64 each), two
+// LDS stages of 256 values of K (34 KB each with the scales), so that two
+// workgroups share a compute unit and cover each other's barriers.  Its LDS
+// reads (8 fragments per 16 products) bound it at about half the matrix rate.
+template <int OUT>
+__global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
+  constexpr int kStage = 2 * 128 * 128 + 2048;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];  // A, B, scales of A, of B
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t M = p.M, N = p.N;
+  const int nk = (int)mx_ktiles(p.K), pitch = nk * 128;
+  const int nbm = (int)((M + 127) / 128), nbn = (int)((N + 127) / 128);
+  int tm, tn;
+  tile_of(nbm, nbn, tm, tn);
+  const int64_t bm = (int64_t)tm * 128, bn = (int64_t)tn * 128;
+  const i32x4 ra = make_rsrc(p.A.q + bm * pitch, (M - bm < 128 ? M - bm : 128) * (int64_t)pitch);
+  const i32x4 rb = make_rsrc(p.B.q + bn * pitch, (N - bn < 128 ? N - bn : 128) * (int64_t)pitch);
+  const i32x4 rs = wave ? make_rsrc(p.B.s + (int64_t)tn * nk * 1024, (int64_t)nk * 1024)
+                        : make_rsrc(p.A.s + (int64_t)tm * nk * 1024, (int64_t)nk * 1024);
+  // load i of a wave: rows 32 wave + 8 i + lane / 8 of either operand
+  const int lr = lane >> 3;
+  const uint32_t vo0 = (uint32_t)((32 * wave + lr) * pitch + 16 * ((lane & 7) ^ swz16(lr)));
+  const uint32_t vo1 = (uint32_t)((32 * wave + lr) * pitch + 16 * ((lane & 7) ^ swz16(8 + lr)));
+  auto issue = [&](int kt) {
+    const uint32_t d = lds_u32(lds) + (kt & 1) * kStage + wave * 4096;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sb = (uint32_t)(8 * i * pitch + kt * 128);
+      lds_dma16_split(d + i * 1024, (i & 1) ? vo1 : vo0, sb, ra);
+      lds_dma16_split(d + 16384 + i * 1024, (i & 1) ? vo1 : vo0, sb, rb);
+    }
+    if (wave < 2)
+      lds_dma16_split(lds_u32(lds) + (kt & 1) * kStage + 32768 + wave * 1024, (uint32_t)(lane * 16), (uint32_t)kt * 1024, rs);
+  };
+  v4f acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int frow = lane & 15, fchunk = 2 * (lane >> 4);
+  issue(0);
+  for (int t = 0; t < nk; ++t) {
+    if (t + 1 < nk) {
+      issue(t + 1);
+      if (wave < 2) wait_vmcnt<9>();
+      else wait_vmcnt<8>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    __builtin_amdgcn_s_barrier();
+    compiler_fence();
+    const uint8_t* a = lds + (t & 1) * kStage;
+    const uint8_t* b = a + 16384;
+    const uint2 sa = *reinterpret_cast<const uint2*>(a + 32768 + 16 * lane + 8 * wm);
+    const uint2 sb = *reinterpret_cast<const uint2*>(a + 33792 + 16 * lane + 8 * wn);
+    const uint32_t sav[2] = {sa.x, sa.y}, sbv[2] = {sb.x, sb.y};
+    static_for<2>([&](auto kk) {
+      constexpr int KK = decltype(kk)::value;
+      uint4 af[4], bf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        af[i] = *reinterpret_cast<const uint4*>(a + lds_off2(64 * wm + 16 * i + frow, fchunk + KK));
+        bf[i] = *reinterpret_cast<const uint4*>(b + lds_off2(64 * wn + 16 * i + frow, fchunk + KK));
+      }
+      static_for<4>([&](auto ic) {
+        constexpr int I = decltype(ic)::value;
+        static_for<4>([&](auto jc) {
+          constexpr int J = decltype(jc)::value;
+          acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J], af[I], acc[I][J], sbv[J / 2], sav[I / 2]);
+        });
+      });
+    });
+    // this stage is loaded again two k-tiles on: every wave has read it by then
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    compiler_fence();
+  }
+  Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
+  const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(C) & (4 * sizeof(Elem<OUT>) - 1)) == 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = bm + 64 * wm + 16 * i + frow;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = bn + 64 * wn + 16 * j + 4 * (lane >> 4);
+      if (wide) {
+        if (n < N) store4<OUT>(C, m * N + n, acc[i][j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) C[m * N + n + e] = from_f32<OUT>(acc[i][j][e]);
+      }
+    }
+  }
+}
+
+// Few rows or few tiles: a 16 TM x 16 TN tile per workgroup, whose waves split K
+// (wave w takes k-tiles w, w + W, ...) and join their sums through LDS.  Each
+// wave reads its fragments from memory into registers, one k-tile ahead: with
+// a single row block the weight streams through once and nothing is staged.
+// SWAP: the operands have changed places (few columns): C is written
+// transposed, element (m, n) of the product at C[n * M + m].
+// FT >= 0: operand A is not quantised yet (its rows, of element type FT, are x):
+// a wave quantises the part of x that its k-tile needs into LDS itself.
+// Consecutive tiles go to one XCD: 8 of them share each 1 KB of scales.
+struct MxApply {
+  const void* x;
+  int32_t fit;
+};
+template <int TM, int TN, int OUT, bool SWAP, int FT>
+__global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmProblem p, MxApply ap) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), W = blockDim.x / kWave;
+  const int64_t M = p.M, N = p.N;
+  const int nk = (int)mx_ktiles(p.K), pitch = nk * 128;
+  const int64_t nbm = (M + 16 * TM - 1) / (16 * TM);
+  const int64_t b = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int64_t bm = b % nbm * (16 * TM), bn = b / nbm * (16 * TN);
+  // the tile's first row and scale group (uniform), a lane's 32-bit offsets
+  // from them; rows past the end read the last one (never stored)
+  const uint8_t *qa = p.A.q + bm * pitch, *qb = p.B.q + bn * pitch;
+  const uint8_t *ga = p.A.s + (bm >> 7) * (int64_t)nk * 1024, *gb = p.B.s + (bn >> 7) * (int64_t)nk * 1024;
+  uint32_t oa[TM], ob[TN], ua[TM], ub[TN];
+  auto offsets = [&](int64_t row0, int64_t rows, int i, uint32_t& o, uint32_t& u) {
+    const int64_t row = row0 + 16 * i + r < rows ? row0 + 16 * i + r : rows - 1;
+    o = (uint32_t)((row - row0) * pitch + 32 * g);
+    u = (uint32_t)(((row >> 7) - (row0 >> 7)) * nk * 1024 + (g * 16 + (row & 15)) * 16 + ((row & 127) >> 4) * 2);
+  };
+#pragma unroll
+  for (int i = 0; i < TM; ++i) offsets(bm, M, i, oa[i], ua[i]);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) offsets(bn, N, j, ob[j], ub[j]);
+
+  struct Stage {
+    uint4 a[TM][2], b[TN][2];
+    uint32_t sa[TM], sb[TN];
+  };
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto load = [&](Stage& s, int kt) {
+    const int64_t k0 = (int64_t)kt * 128, s0 = (int64_t)kt * 1024;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      s.b[j][0] = *reinterpret_cast<const uint4*>(qb + k0 + ob[j]);
+      s.b[j][1] = *reinterpret_cast<const uint4*>(qb + k0 + ob[j] + 16);
+      s.sb[j] = *reinterpret_cast<const uint16_t*>(gb + s0 + ub[j]);
+    }
+    if constexpr (FT < 0) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        s.a[i][0] = *reinterpret_cast<const uint4*>(qa + k0 + oa[i]);
+        s.a[i][1] = *reinterpret_cast<const uint4*>(qa + k0 + oa[i] + 16);
+        s.sa[i] = *reinterpret_cast<const uint16_t*>(ga + s0 + ua[i]);
+      }
+    }
+  };
+  auto compute = [&](Stage& s, int kt) {
+    if constexpr (FT >= 0) {  // x's k-tile, two rows at a time, through this wave's LDS
+      typedef Elem<FT> E;
+      uint8_t* my = lds + wave * (16 * 136);  // 16 rows of 128 bytes of codes and 8 of scales
+      const int half = lane >> 5, cc = lane & 31;
+      const int64_t c = (int64_t)kt * 256 + 8 * cc;
+      const int n = left8(p.K, c);
+      for (int m0 = 0; m0 < (int)M; m0 += 2) {
+        const int m = m0 + half;
+        float v[8] = {};
+        if (m < M && n > 0) load8<FT, false>(reinterpret_cast<const E*>(ap.x) + m * p.K + c, n, v);
+        const uint32_t sc = fp4_scale(quad_amax(v), ap.fit != 0);
+        const float f = scale_value(sc);
+        uint32_t d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], f, 0);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[2], v[3], f, 1);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[4], v[5], f, 2);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[6], v[7], f, 3);
+        if (m < M) {
+          *reinterpret_cast<uint32_t*>(my + m * 136 + 4 * cc) = sc == 255u ? 0u : d;
+          if ((lane & 3) == 0) my[m * 136 + 128 + (cc >> 2)] = (uint8_t)sc;
+        }
+      }
+      // rows past M repeat the last one
+      const uint8_t* row = my + (r < M ? r : (int)M - 1) * 136;
+      const uint2 lo0 = *reinterpret_cast<const uint2*>(row + 32 * g), lo1 = *reinterpret_cast<const uint2*>(row + 32 * g + 8);
+      const uint2 hi0 = *reinterpret_cast<const uint2*>(row + 32 * g + 16), hi1 = *reinterpret_cast<const uint2*>(row + 32 * g + 24);
+      s.a[0][0] = make_uint4(lo0.x, lo0.y, lo1.x, lo1.y);
+      s.a[0][1] = make_uint4(hi0.x, hi0.y, hi1.x, hi1.y);
+      s.sa[0] = *reinterpret_cast<const uint16_t*>(row + 128 + 2 * g);
+    }
+    if constexpr (FT >= 0) {  // one product in the body (see below)
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        acc[0][0] = mfma4<0, 0>(s.b[0][0], s.a[0][0], acc[0][0], s.sb[0], s.sa[0]);
+        s.b[0][0] = s.b[0][1];
+        s.a[0][0] = s.a[0][1];
+        s.sb[0] >>= 8;
+        s.sa[0] >>= 8;
+      }
+    } else {
+      static_for<2>([&](auto kk) {
+        constexpr int KK = decltype(kk)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = mfma4<KK, KK>(s.b[j][KK], s.a[i][KK], acc[i][j], s.sb[j], s.sa[i]);
+      });
+    }
+  };
+  // One product per (i, j) and half in the loop's body, so that every
+  // accumulator is updated in place: with two copies of the body the compiler
+  // (clang 22 of ROCm 7.2) gave a product's result registers that still held
+  // another accumulator.  The build checks that each product's result and
+  // addend are the same registers.
+  Stage cur;
+  int kt = wave;
+  if (kt < nk) load(cur, kt);
+#pragma unroll 1
+  for (; kt < nk; kt += W) {
+    if constexpr (TM * TN < 16) {
+      Stage next = cur;
+      if (kt + W < nk) load(next, kt + W);
+      compute(cur, kt);
+      cur = next;
+    } else {  // (no registers for a second stage)
+      compute(cur, kt);
+      if (kt + W < nk) load(cur, kt + W);
+    }
+  }
+
+  // join: a row of blocks at a time, [wave][j][lane] in LDS
+  Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
+  float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    if (i > 0 || FT >= 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < TN; ++j) *reinterpret_cast<v4f*>(red + ((wave * TN + j) * 64 + lane) * 4) = acc[i][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 256 * TN; e += blockDim.x) {
+      const int ml = SWAP ? e % 16 : e / (16 * TN), nl = SWAP ? e / 16 : e % (16 * TN);
+      const int64_t m = bm + 16 * i + ml, n = bn + nl;
+      if (m >= M || n >= N) continue;
+      const float* src = red + ((nl >> 4) * 64 + ((nl & 15) >> 2) * 16 + ml) * 4 + (nl & 3);
+      float v = 0.f;
+      for (int w = 0; w < W; ++w) v += src[w * TN * 256];
+      C[SWAP ? n * M + m : m * N + n] = from_f32<OUT>(v);
+    }
+  }
+}
+
+// Waves that split nk k-tiles: as many as give each the same number of them.
+int split_waves(int64_t nk, int most) {
+  if (nk < 1) return 1;
+  const int64_t per = (nk + most - 1) / most;
+  return (int)((nk + per - 1) / per);
+}
+template <int TM, int TN, int OUT, bool SWAP, int FT>
+hipError_t launch_splitk(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
+  const int W = split_waves(mx_ktiles(p.K), TM * TN > 2 ? 8 : 16);
+  const int64_t blocks = ((p.M + 16 * TM - 1) / (16 * TM)) * ((p.N + 16 * TN - 1) / (16 * TN));
+  const size_t join = (size_t)W * TN * 1024, own = FT >= 0 ? (size_t)W * 16 * 136 : 0;
+  hipLaunchKernelGGL((k_mx_splitk<TM, TN, OUT, SWAP, FT>), dim3((unsigned)blocks), dim3(64 * W), join > own ? join : own,
+                     stream, p, ap);
+  return hipGetLastError();
+}
+template <int OUT, bool SWAP>
+hipError_t launch_few(const MxGemmProblem& p, hipStream_t stream) {
+  const int cus = device_cus();
+  if (p.M <= 16) return launch_splitk<1, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
+  // two column blocks a tile halve the reads of A, where enough tiles are left
+  const bool pairs = (p.N + 31) / 32 >= cus;
+  if (p.M <= 32) return pairs ? launch_splitk<2, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<2, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
+  return pairs ? launch_splitk<4, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<4, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
+}
+
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
   return by_type(out, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    // The large-tile kernel where its tiles fill the chip; its 32-bit offsets
-    // span 256 rows.
-    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-    if (tiles >= 128 && p.K > 0 && mx_pitch(p.K) * 256 < (1ll << 31) - 256) {
-      hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles), dim3(512), 0, stream, p);
+    auto tiles = [&](int64_t e) { return ((p.M + e - 1) / e) * ((p.N + e - 1) / e); };
+    // The tiled kernels' 32-bit offsets span 256 rows: K below 2^24.
+    if (mx_pitch(p.K) * 256 >= (1ll << 31) - 256) {
+      hipLaunchKernelGGL((k_mx_gemm_plain<T>), dim3((unsigned)tiles(16)), dim3(64), 0, stream, p);
       return hipGetLastError();
     }
-    const int64_t nb = ((p.M + 15) / 16) * ((p.N + 15) / 16);
-    hipLaunchKernelGGL((k_mx_gemm_plain<T>), dim3((unsigned)nb), dim3(64), 0, stream, p);
-    return hipGetLastError();
+    const int cus = device_cus();
+    if (p.M <= 64 && p.M <= p.N) return launch_few<T, false>(p, stream);
+    if (p.N <= 64) return launch_few<T, true>(MxGemmProblem{p.B, p.A, p.C, p.N, p.M, p.K}, stream);
+    if (p.K > 0 && tiles(256) * 2 >= cus) {
+      hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
+      return hipGetLastError();
+    }
+    if (p.K > 0 && tiles(64) > 2 * cus) {
+      hipLaunchKernelGGL((k_mx_mid<T>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
+      return hipGetLastError();
+    }
+    return launch_splitk<4, 4, T, false, -1>(p, MxApply{}, stream);
   });
 }
 
@@ -281,6 +570,16 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
 
 hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemmProblem& p, int out,
                            hipStream_t stream) {
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  // Every 16 columns' workgroup would quantise x again: in the product's own
+  // launch only while that is little work in all.
+  constexpr int64_t kFusedWork = 1ll << 28;
+  if (p.M <= 16 && p.K > 0 && p.M * p.N * p.K <= kFusedWork && mx_pitch(p.K) * 256 < (1ll << 31) - 256)
+    return by_type(out, [&](auto t) {
+      return by_type(type, [&](auto f) {
+        return launch_splitk<1, 1, decltype(t)::value, false, decltype(f)::value>(p, MxApply{j.x, fit}, stream);
+      });
+    });
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
   return e != hipSuccess ? e : launch_mx_gemm(p, out, stream);
 }

@@ -142,6 +142,28 @@ def test_large_product(M, N, K, out):
     product(M, N, K, out, M + N + K)
 
 
+@pytest.mark.parametrize("M,N,K", [(200, 300, 3000), (1000, 40, 700), (500, 64, 260), (2500, 1500, 600), (1500, 1400, 130),
+                                   (70, 14336, 256), (40, 14000, 512), (20, 9000, 300), (15, 20, 20000)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product_of_every_shape_of_tile(M, N, K, out):
+    product(M, N, K, out, M + N + K, spread=2)
+
+
+def test_a_contraction_past_the_tiled_kernels_offsets():
+    """K above 2^24: sparse operands, so that the sum is known."""
+    M, N, K = 2, 3, (1 << 24) + 300
+    a, b = torch.zeros(M, K), torch.zeros(N, K)
+    at = torch.tensor([0, 1, 255, 256, 1 << 23, (1 << 24) - 1, 1 << 24, K - 1])
+    a[:, at] = torch.tensor([[1.0], [2.0]]) * torch.tensor([1.0, .5, 3, 1, 2, 1, 4, 6])
+    b[:, at] = torch.tensor([[1.0], [-1.0], [3.0]])
+    A, B, C = F.Mxfp4(M, K), F.Mxfp4(N, K), torch.empty(M, N, device=DEV)
+    F.mxfp4_quantize(a.to(DEV), A)
+    F.mxfp4_quantize(b.to(DEV), B)
+    F.mxfp4_gemm(A, B, C)
+    torch.cuda.synchronize()
+    assert torch.equal(C.cpu(), torch.tensor([[18.5], [37.0]]) * torch.tensor([1.0, -1.0, 3.0]))
+
+
 @pytest.mark.parametrize("M,N", [(1, 5), (40, 300), (200, 200)])
 def test_empty_contraction_gives_zeros(M, N):
     A, B = F.Mxfp4(M, 0), F.Mxfp4(N, 0)

@@ -174,6 +174,19 @@ def test_strided_rows():
         mx._strided(like.half(), "g", like, 6, 16)
 
 
+def test_build_reads_where_products_add():
+    """The build's guard on the matrix instructions sees a result that moves."""
+    from fp8_scaled_gemm_amd.build import moved_products
+    asm = """_Zkern:
+\tv_mfma_scale_f32_16x16x128_f8f6f4 v[4:7], v[14:17], v[50:53], v[4:7], v1, v136 op_sel_hi:[0,0,0] cbsz:4 blgp:4
+.LBB0_1:
+\tv_mfma_scale_f32_16x16x128_f8f6f4 v[4:7], v[14:17], v[50:53], v[6:9], v1, v136 op_sel_hi:[0,0,0] cbsz:4 blgp:4
+_Zother:
+\tv_mfma_f32_16x16x32_bf16 v[0:3], v[4:7], v[8:11], 0
+"""
+    assert moved_products(asm) == {"_Zkern": 1, "_Zother": 1}
+
+
 def test_reference_rounding():
     """Known roundings of the reference the GPU tests compare with."""
     v = np.zeros((1, 32))
