@@ -52,7 +52,7 @@ extern "C" {
 int64_t mxfp4_code_bytes(int64_t rows, int64_t k) { return mat_ok(rows, k) ? rows * mx_pitch(k) : -1; }
 
 int64_t mxfp4_scale_bytes(int64_t rows, int64_t k) {
-  return mat_ok(rows, k) ? (rows + 127) / 128 * mx_ktiles(k) * 1024 : -1;
+  return mat_ok(rows, k) ? (rows + 31) / 32 * mx_ktiles(k) * 256 : -1;
 }
 
 fp8sg_status mxfp4_quantize(const void* x, fp8sg_out type, int64_t rows, int64_t cols, fp8sg_mx_rule rule,

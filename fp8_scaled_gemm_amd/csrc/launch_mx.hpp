@@ -14,9 +14,9 @@ namespace fp8sg {
 // ---- MXFP4 layout (mxfp4_operand)
 __host__ __device__ inline int64_t mx_ktiles(int64_t k) { return (k + 255) >> 8; }
 __host__ __device__ inline int64_t mx_pitch(int64_t k) { return mx_ktiles(k) * 128; }
+// scale bytes: groups of 32 rows x 256 values, 256 bytes each
 __host__ __device__ inline int64_t mx_scale_off(int64_t r, int64_t b, int64_t nk) {
-  return (((r >> 7) * nk + (b >> 3)) * 64 + ((b & 7) >> 1) * 16 + (r & 15)) * 16 +
-         ((r & 127) >> 4) * 2 + (b & 1);
+  return ((r >> 5) * nk + (b >> 3)) * 256 + (((b & 7) >> 1) * 16 + (r & 15)) * 4 + ((r & 31) >> 4) * 2 + (b & 1);
 }
 
 // One matrix to quantise: x rows x cols; q and / or t may have null pointers.

@@ -91,9 +91,9 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   // span the rows (and 128-row scale groups) that exist: the rest reads as zero.
   const int64_t row0 = grp ? bn : bm, rows = (grp ? N : M) - row0;
   const uint8_t* q0 = (grp ? p.B.q : p.A.q) + row0 * pitch;
-  const uint8_t* s0 = (grp ? p.B.s : p.A.s) + (row0 >> 7) * (int64_t)nk * 1024;
+  const uint8_t* s0 = (grp ? p.B.s : p.A.s) + (row0 >> 5) * (int64_t)nk * 256;
   const i32x4 rq = make_rsrc(q0, (rows < 256 ? rows : 256) * (int64_t)pitch);
-  const i32x4 rs = make_rsrc(s0, (rows > 128 ? 2 : 1) * (int64_t)nk * 1024);
+  const i32x4 rs = make_rsrc(s0, (rows < 256 ? (rows + 31) / 32 : 8) * (int64_t)nk * 256);
   // Load i of wave q: rows 64 q + 8 i + lane / 8, one 16-byte chunk a lane; the
   // row's swizzle takes two values, for even and odd i.
   const int lr = lane >> 3;
@@ -103,9 +103,10 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
     const uint32_t sb = kt < nk ? (uint32_t)(8 * i * pitch + kt * 128) : kOob;
     lds_dma16_split(dst + (wq * 8 + i) * 1024, (i & 1) ? vo1 : vo0, sb, rq);
   };
-  auto issue_scales = [&](int kt, uint32_t dst) {  // waves 0 and 1: one 128-row group each
-    if (wq < 2)
-      lds_dma16_split(dst + wq * 1024, (uint32_t)(lane * 16), kt < nk ? (uint32_t)((wq * nk + kt) * 1024) : kOob, rs);
+  // waves 0 and 1: four groups of 32 rows each, 256 bytes apiece
+  const uint32_t vos = (uint32_t)((4 * wq + (lane >> 4)) * nk * 256 + (lane & 15) * 16);
+  auto issue_scales = [&](int kt, uint32_t dst) {
+    if (wq < 2) lds_dma16_split(dst + wq * 1024, vos, kt < nk ? (uint32_t)kt * 256 : kOob, rs);
   };
   auto barrier = [&]() {
     __builtin_amdgcn_s_barrier();
@@ -117,8 +118,8 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   for (int i = 0; i < kTM; ++i)
 #pragma unroll
     for (int j = 0; j < kTN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  uint4 af[kTM][2], bf[kTN][2], sa;
-  uint2 sb;
+  uint4 af[kTM][2], bf[kTN][2];
+  uint32_t sa[4], sb[2];
 
   if (grp == 0) {
 #pragma unroll
@@ -153,8 +154,10 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
       bf[j][0] = *reinterpret_cast<const uint4*>(b + lds_off2(r, fchunk));
       bf[j][1] = *reinterpret_cast<const uint4*>(b + lds_off2(r, fchunk + 1));
     }
-    sb = *reinterpret_cast<const uint2*>(sS + 4096 + 2048 * P + 1024 * (wq >> 1) + 16 * lane + 8 * (wq & 1));
-    sa = *reinterpret_cast<const uint4*>(sS + 2048 * P + 1024 * grp + 16 * lane);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(sS + 4096 + 2048 * P + 256 * (2 * wq + j) + 4 * lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(sS + 2048 * P + 256 * (4 * grp + i) + 4 * lane);
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
       const int r = 16 * (8 * grp + i) + frow;
@@ -165,14 +168,13 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
     if (grp == 1) wait_vmcnt<0>();       // B of t + 1 has landed
     barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const uint32_t sav[4] = {sa.x, sa.y, sa.z, sa.w}, sbv[2] = {sb.x, sb.y};
     static_for<2>([&](auto kk) {
       constexpr int KK = decltype(kk)::value;
       static_for<kTM>([&](auto ic) {
         constexpr int I = decltype(ic)::value;
         static_for<kTN>([&](auto jc) {
           constexpr int J = decltype(jc)::value;
-          acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J][KK], af[I][KK], acc[I][J], sbv[J / 2], sav[I / 2]);
+          acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J][KK], af[I][KK], acc[I][J], sb[J / 2], sa[I / 2]);
         });
         if constexpr (KK == 0) {
           __builtin_amdgcn_sched_barrier(0);
@@ -276,8 +278,11 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
   const int64_t bm = (int64_t)tm * 128, bn = (int64_t)tn * 128;
   const i32x4 ra = make_rsrc(p.A.q + bm * pitch, (M - bm < 128 ? M - bm : 128) * (int64_t)pitch);
   const i32x4 rb = make_rsrc(p.B.q + bn * pitch, (N - bn < 128 ? N - bn : 128) * (int64_t)pitch);
-  const i32x4 rs = wave ? make_rsrc(p.B.s + (int64_t)tn * nk * 1024, (int64_t)nk * 1024)
-                        : make_rsrc(p.A.s + (int64_t)tm * nk * 1024, (int64_t)nk * 1024);
+  // scales: wave 0 A's, wave 1 B's, four groups of 32 rows (those that exist)
+  const int64_t left = wave ? N - bn : M - bm;
+  const i32x4 rs = make_rsrc(wave ? p.B.s + (bn >> 5) * nk * 256 : p.A.s + (bm >> 5) * nk * 256,
+                             (left < 128 ? (left + 31) / 32 : 4) * (int64_t)nk * 256);
+  const uint32_t vos = (uint32_t)((lane >> 4) * nk * 256 + (lane & 15) * 16);
   // load i of a wave: rows 32 wave + 8 i + lane / 8 of either operand
   const int lr = lane >> 3;
   const uint32_t vo0 = (uint32_t)((32 * wave + lr) * pitch + 16 * ((lane & 7) ^ swz16(lr)));
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
       lds_dma16_split(d + 16384 + i * 1024, (i & 1) ? vo1 : vo0, sb, rb);
     }
     if (wave < 2)
-      lds_dma16_split(lds_u32(lds) + (kt & 1) * kStage + 32768 + wave * 1024, (uint32_t)(lane * 16), (uint32_t)kt * 1024, rs);
+      lds_dma16_split(lds_u32(lds) + (kt & 1) * kStage + 32768 + wave * 1024, vos, (uint32_t)kt * 256, rs);
   };
   v4f acc[4][4];
 #pragma unroll
@@ -312,9 +317,12 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
     compiler_fence();
     const uint8_t* a = lds + (t & 1) * kStage;
     const uint8_t* b = a + 16384;
-    const uint2 sa = *reinterpret_cast<const uint2*>(a + 32768 + 16 * lane + 8 * wm);
-    const uint2 sb = *reinterpret_cast<const uint2*>(a + 33792 + 16 * lane + 8 * wn);
-    const uint32_t sav[2] = {sa.x, sa.y}, sbv[2] = {sb.x, sb.y};
+    uint32_t sav[2], sbv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sav[i] = *reinterpret_cast<const uint32_t*>(a + 32768 + 256 * (2 * wm + i) + 4 * lane);
+      sbv[i] = *reinterpret_cast<const uint32_t*>(a + 33792 + 256 * (2 * wn + i) + 4 * lane);
+    }
     static_for<2>([&](auto kk) {
       constexpr int KK = decltype(kk)::value;
       uint4 af[4], bf[4];
@@ -364,7 +372,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
 // transposed, element (m, n) of the product at C[n * M + m].
 // FT >= 0: operand A is not quantised yet (its rows, of element type FT, are x):
 // a wave quantises the part of x that its k-tile needs into LDS itself.
-// Consecutive tiles go to one XCD: 8 of them share each 1 KB of scales.
+// Consecutive tiles go to one XCD: two of them share a row group's scales.
+constexpr int kFusedRows = 4;
 struct MxApply {
   const void* x;
   int32_t fit;
@@ -382,12 +391,12 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   // the tile's first row and scale group (uniform), a lane's 32-bit offsets
   // from them; rows past the end read the last one (never stored)
   const uint8_t *qa = p.A.q + bm * pitch, *qb = p.B.q + bn * pitch;
-  const uint8_t *ga = p.A.s + (bm >> 7) * (int64_t)nk * 1024, *gb = p.B.s + (bn >> 7) * (int64_t)nk * 1024;
+  const uint8_t *ga = p.A.s + (bm >> 5) * (int64_t)nk * 256, *gb = p.B.s + (bn >> 5) * (int64_t)nk * 256;
   uint32_t oa[TM], ob[TN], ua[TM], ub[TN];
   auto offsets = [&](int64_t row0, int64_t rows, int i, uint32_t& o, uint32_t& u) {
     const int64_t row = row0 + 16 * i + r < rows ? row0 + 16 * i + r : rows - 1;
     o = (uint32_t)((row - row0) * pitch + 32 * g);
-    u = (uint32_t)(((row >> 7) - (row0 >> 7)) * nk * 1024 + (g * 16 + (row & 15)) * 16 + ((row & 127) >> 4) * 2);
+    u = (uint32_t)(((row >> 5) - (row0 >> 5)) * nk * 256 + (g * 16 + (row & 15)) * 4 + ((row & 31) >> 4) * 2);
   };
 #pragma unroll
   for (int i = 0; i < TM; ++i) offsets(bm, M, i, oa[i], ua[i]);
@@ -397,6 +406,7 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   struct Stage {
     uint4 a[TM][2], b[TN][2];
     uint32_t sa[TM], sb[TN];
+    Row8<FT < 0 ? 0 : FT> x[FT < 0 ? 1 : kFusedRows / 2];  // rows 2 i + lane / 32 of x
   };
   v4f acc[TM][TN];
 #pragma unroll
@@ -404,7 +414,7 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   auto load = [&](Stage& s, int kt) {
-    const int64_t k0 = (int64_t)kt * 128, s0 = (int64_t)kt * 1024;
+    const int64_t k0 = (int64_t)kt * 128, s0 = (int64_t)kt * 256;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       s.b[j][0] = *reinterpret_cast<const uint4*>(qb + k0 + ob[j]);
@@ -418,29 +428,33 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
         s.a[i][1] = *reinterpret_cast<const uint4*>(qa + k0 + oa[i] + 16);
         s.sa[i] = *reinterpret_cast<const uint16_t*>(ga + s0 + ua[i]);
       }
+    } else {
+      const int64_t c = (int64_t)kt * 256 + 8 * (lane & 31);
+      const int n = left8(p.K, c);
+#pragma unroll
+      for (int i = 0; i < kFusedRows / 2; ++i) {
+        const int m = 2 * i + (lane >> 5);
+        s.x[i] = load_row8<FT, false>(reinterpret_cast<const Elem<FT>*>(ap.x) + (m < M ? m : 0) * p.K + c, n);
+      }
     }
   };
   auto compute = [&](Stage& s, int kt) {
-    if constexpr (FT >= 0) {  // x's k-tile, two rows at a time, through this wave's LDS
-      typedef Elem<FT> E;
-      uint8_t* my = lds + wave * (16 * 136);  // 16 rows of 128 bytes of codes and 8 of scales
-      const int half = lane >> 5, cc = lane & 31;
-      const int64_t c = (int64_t)kt * 256 + 8 * cc;
-      const int n = left8(p.K, c);
-      for (int m0 = 0; m0 < (int)M; m0 += 2) {
-        const int m = m0 + half;
-        float v[8] = {};
-        if (m < M && n > 0) load8<FT, false>(reinterpret_cast<const E*>(ap.x) + m * p.K + c, n, v);
+    if constexpr (FT >= 0) {  // x's k-tile to codes, through this wave's LDS
+      uint8_t* my = lds + wave * (kFusedRows * 136);  // rows of 128 bytes of codes and 8 of scales
+      const int cc = lane & 31;
+#pragma unroll
+      for (int i = 0; i < kFusedRows / 2; ++i) {
+        const int m = 2 * i + (lane >> 5);
+        float v[8];
+        s.x[i].values(v);
         const uint32_t sc = fp4_scale(quad_amax(v), ap.fit != 0);
         const float f = scale_value(sc);
         uint32_t d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], f, 0);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[2], v[3], f, 1);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[4], v[5], f, 2);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[6], v[7], f, 3);
-        if (m < M) {
-          *reinterpret_cast<uint32_t*>(my + m * 136 + 4 * cc) = sc == 255u ? 0u : d;
-          if ((lane & 3) == 0) my[m * 136 + 128 + (cc >> 2)] = (uint8_t)sc;
-        }
+        *reinterpret_cast<uint32_t*>(my + m * 136 + 4 * cc) = sc == 255u ? 0u : d;
+        if ((lane & 3) == 0) my[m * 136 + 128 + (cc >> 2)] = (uint8_t)sc;
       }
       // rows past M repeat the last one
       const uint8_t* row = my + (r < M ? r : (int)M - 1) * 136;
@@ -450,7 +464,7 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
       s.a[0][1] = make_uint4(hi0.x, hi0.y, hi1.x, hi1.y);
       s.sa[0] = *reinterpret_cast<const uint16_t*>(row + 128 + 2 * g);
     }
-    if constexpr (FT >= 0) {  // one product in the body (see below)
+    if constexpr (FT >= 0) {  // (the two halves in a loop: see below)
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         acc[0][0] = mfma4<0, 0>(s.b[0][0], s.a[0][0], acc[0][0], s.sb[0], s.sa[0]);
@@ -467,6 +481,15 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
 #pragma unroll
           for (int j = 0; j < TN; ++j) acc[i][j] = mfma4<KK, KK>(s.b[j][KK], s.a[i][KK], acc[i][j], s.sb[j], s.sa[i]);
       });
+    }
+    // the operands stay in use past the products, so that no product's result
+    // can take their registers (see the loop below)
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) keep_loaded(s.a[i][kk]);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) keep_loaded(s.b[j][kk]);
     }
   };
   // One product per (i, j) and half in the loop's body, so that every
@@ -511,17 +534,21 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   }
 }
 
-// Waves that split nk k-tiles: as many as give each the same number of them.
-int split_waves(int64_t nk, int most) {
+// Waves that split nk k-tiles: as many as give each the same number of them,
+// few enough that all workgroups are resident at once (32 waves a compute
+// unit; one token, 14336 x 4096: 8 waves 8.4 us, 16 waves 9.9 us).
+int split_waves(int64_t nk, int64_t blocks, int most) {
   if (nk < 1) return 1;
+  const int64_t room = (int64_t)device_cus() * 32 / blocks;
+  if (room < most) most = room < 4 ? 4 : (int)room;
   const int64_t per = (nk + most - 1) / most;
   return (int)((nk + per - 1) / per);
 }
 template <int TM, int TN, int OUT, bool SWAP, int FT>
 hipError_t launch_splitk(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
-  const int W = split_waves(mx_ktiles(p.K), TM * TN > 2 ? 8 : 16);
   const int64_t blocks = ((p.M + 16 * TM - 1) / (16 * TM)) * ((p.N + 16 * TN - 1) / (16 * TN));
-  const size_t join = (size_t)W * TN * 1024, own = FT >= 0 ? (size_t)W * 16 * 136 : 0;
+  const int W = split_waves(mx_ktiles(p.K), blocks, TM * TN > 2 ? 8 : 16);
+  const size_t join = (size_t)W * TN * 1024, own = FT >= 0 ? (size_t)W * kFusedRows * 136 : 0;
   hipLaunchKernelGGL((k_mx_splitk<TM, TN, OUT, SWAP, FT>), dim3((unsigned)blocks), dim3(64 * W), join > own ? join : own,
                      stream, p, ap);
   return hipGetLastError();
@@ -529,9 +556,9 @@ hipError_t launch_splitk(const MxGemmProblem& p, const MxApply& ap, hipStream_t 
 template <int OUT, bool SWAP>
 hipError_t launch_few(const MxGemmProblem& p, hipStream_t stream) {
   const int cus = device_cus();
-  if (p.M <= 16) return launch_splitk<1, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
   // two column blocks a tile halve the reads of A, where enough tiles are left
   const bool pairs = (p.N + 31) / 32 >= cus;
+  if (p.M <= 16) return pairs ? launch_splitk<1, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<1, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
   if (p.M <= 32) return pairs ? launch_splitk<2, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<2, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
   return pairs ? launch_splitk<4, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<4, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
 }
@@ -571,10 +598,9 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
 hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemmProblem& p, int out,
                            hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  // Every 16 columns' workgroup would quantise x again: in the product's own
-  // launch only while that is little work in all.
-  constexpr int64_t kFusedWork = 1ll << 28;
-  if (p.M <= 16 && p.K > 0 && p.M * p.N * p.K <= kFusedWork && mx_pitch(p.K) * 256 < (1ll << 31) - 256)
+  // Every 16 columns' workgroup quantises x again, so in the product's own
+  // launch only for as few rows as one pair of loads holds.
+  if (p.M <= kFusedRows && p.K > 0 && mx_pitch(p.K) * 256 < (1ll << 31) - 256)
     return by_type(out, [&](auto t) {
       return by_type(type, [&](auto f) {
         return launch_splitk<1, 1, decltype(t)::value, false, decltype(f)::value>(p, MxApply{j.x, fit}, stream);

@@ -101,8 +101,8 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
   // different banks
   auto tcol = [](int c) { return NW == 8 ? c * 128 : c * 32 + (c >> 3) * 16; };
   __shared__ __attribute__((aligned(16))) uint8_t tq[NW == 8 ? 256 * 128 : 256 * 32 + 32 * 16];
-  __shared__ __attribute__((aligned(16))) uint8_t rs[NW * 256];  // row scales, [row group][g][r % 16][piece]
-  __shared__ __attribute__((aligned(16))) uint8_t ts[NW * 256];  // column scales, [column group][g][c % 16][16]
+  __shared__ __attribute__((aligned(16))) uint8_t rs[NW * 256];  // row scales: NW groups of 256 bytes
+  __shared__ __attribute__((aligned(16))) uint8_t ts[NW * 256];  // column scales: 8 groups of 32 NW bytes
 
   const bool second = blockIdx.x >= args.blocks0;
   const MxQuantJob& j = args.job[second];
@@ -139,11 +139,8 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
       m = o > m ? o : m;
       const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(m), fit) : 127u;
       if (rw + i < j.rows) *reinterpret_cast<uint32_t*>(j.q.q + ((rw + i) * nkc + ct) * 128 + 4 * cc) = row_codes<T>(v[i], s);
-      if ((lane & 3) == 0) {  // block b = cc / 4 of row rl
-        const int rl = 32 * wave + 16 * half + i, b = cc >> 2;
-        constexpr int kPiece = NW == 8 ? 16 : 8;  // bytes of a 16-byte scale granule that this tile's rows fill
-        rs[(rl >> 7) * 1024 + ((b >> 1) * 16 + (rl & 15)) * kPiece + ((rl & 127) >> 4) * 2 + (b & 1)] = (uint8_t)s;
-      }
+      if ((lane & 3) == 0)  // block cc / 4 of row 16 half + i of the wave's group
+        rs[wave * 256 + ((cc >> 3) * 16 + i) * 4 + half * 2 + ((cc >> 2) & 1)] = (uint8_t)s;
     }
   }
   if (j.t.q) {
@@ -168,21 +165,14 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
       const int cl = 8 * cc + J;
       const int piece = NW == 8 ? (wave ^ (cc & 7)) : wave;
       *reinterpret_cast<uint2*>(tq + tcol(cl) + piece * 16 + half * 8) = d;
-      if (half == 0)
-        ts[(cl >> 7) * (NW * 128) + ((wave >> 1) * 16 + (cl & 15)) * 16 + ((cl & 127) >> 4) * 2 + (wave & 1)] = (uint8_t)s;
+      if (half == 0)  // block `wave` of column cl: the tile's blocks are pairs 0 .. NW / 2 - 1 here
+        ts[(cl >> 5) * (NW * 32) + ((wave >> 1) * 16 + (cl & 15)) * 4 + ((cl & 31) >> 4) * 2 + (wave & 1)] = (uint8_t)s;
     });
   }
   __syncthreads();
-  if (j.q.q) {
-    if constexpr (NW == 8) {  // two row groups of 1 KB
-      if (tid < 128 && r0 + (tid >> 6) * 128 < j.rows)
-        *reinterpret_cast<uint4*>(j.q.s + ((r0 / 128 + (tid >> 6)) * nkc + ct) * 1024 + (tid & 63) * 16) =
-            *reinterpret_cast<const uint4*>(rs + tid * 16);
-    } else if (tid < 64 && r0 < j.rows) {  // 64 rows: one half of each granule
-      *reinterpret_cast<uint2*>(j.q.s + ((r0 / 128) * nkc + ct) * 1024 + tid * 16 + ((r0 & 127) ? 8 : 0)) =
-          *reinterpret_cast<const uint2*>(rs + tid * 8);
-    }
-  }
+  if (j.q.q && tid < 16 * NW && r0 + (tid >> 4) * 32 < j.rows)
+    *reinterpret_cast<uint4*>(j.q.s + ((r0 / 32 + (tid >> 4)) * nkc + ct) * 256 + (tid & 15) * 16) =
+        *reinterpret_cast<const uint4*>(rs + tid * 16);
   if (j.t.q) {
     // k-tile r0 / 256 of the transposed matrix, from byte (r0 % 256) / 2 on
     const int64_t kt = r0 >> 8, sub = (r0 & 255) >> 1;
@@ -193,12 +183,11 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
       if (c0 + cl < j.cols)
         st16<S>(j.t.q + ((c0 + cl) * nkr + kt) * 128 + sub + k * 16, *reinterpret_cast<const uint4*>(tq + tcol(cl) + piece * 16));
     }
-    // whole granules: NW / 2 block pairs of 16 columns, two column groups
-    if (tid < NW * 16) {
-      const int grp = tid / (NW * 8), w = tid % (NW * 8);  // w: [block pair][c % 16]
-      const int64_t g0 = (r0 & 255) >> 6;                  // block pair of the tile's first row
-      if (c0 + grp * 128 < j.cols)
-        *reinterpret_cast<uint4*>(j.t.s + (((c0 >> 7) + grp) * nkr + kt) * 1024 + (g0 * 16 + w) * 16) =
+    // 8 groups of 32 columns, of each the bytes of the tile's block pairs
+    if (tid < 16 * NW) {
+      const int grp = tid / (2 * NW), w = tid % (2 * NW);
+      if (c0 + grp * 32 < j.cols)
+        *reinterpret_cast<uint4*>(j.t.s + (((c0 >> 5) + grp) * nkr + kt) * 256 + ((r0 & 255) >> 6) * 64 + w * 16) =
             *reinterpret_cast<const uint4*>(ts + tid * 16);
     }
   }

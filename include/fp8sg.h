@@ -610,12 +610,11 @@ FP8SG_API fp8sg_status amp_update_scale(float* scale, int32_t* growth_tracker, i
  * the dimension its products contract.  A value is e2m1(code) * 2^(s - 127).
  *   q: codes; row r starts at byte r * 128 * ceil(k / 256); value i of a row is
  *      in byte i / 2 of it, in the low half for even i.  Values past k are 0.
- *   s: scales, in groups of 128 rows x 256 values, 1024 bytes each, in the
- *      order the matrix products read them (one 16-byte load of a lane holds
- *      the scales it feeds to its matrix instructions).  Block b of row r:
- *        nk = ceil(k / 256)
- *        byte (((r / 128) * nk + b / 8) * 64 + ((b % 8) / 2) * 16 + r % 16) * 16
- *             + ((r % 128) / 16) * 2 + b % 2
+ *   s: scales, in groups of 32 rows x 256 values, 256 bytes each, in the order
+ *      the matrix products read them (4 bytes a lane are the scales of two row
+ *      blocks and two blocks along k).  Block b of row r, with nk = ceil(k / 256):
+ *        byte ((r / 32) * nk + b / 8) * 256 + (((b % 8) / 2) * 16 + r % 16) * 4
+ *             + ((r % 32) / 16) * 2 + b % 2
  *      s = 255 is NaN: all 32 values of the block are NaN.  Blocks past k hold
  *      s = 127; what stands for rows past the last is unspecified and not used.
  * mxfp4_code_bytes and mxfp4_scale_bytes give the sizes of the two buffers in

@@ -71,7 +71,7 @@ def fp4_unpack(m):
     codes = np.stack([q & 15, q >> 4], axis=-1).reshape(rows, 8 * nk, 32).astype(np.int64)
     s = m.s.cpu().numpy()
     r, b = np.meshgrid(np.arange(rows), np.arange(8 * nk), indexing="ij")
-    at = ((r // 128 * nk + b // 8) * 64 + (b % 8) // 2 * 16 + r % 16) * 16 + (r % 128) // 16 * 2 + b % 2
+    at = (r // 32 * nk + b // 8) * 256 + ((b % 8) // 2 * 16 + r % 16) * 4 + (r % 32) // 16 * 2 + b % 2
     return codes, s[at].astype(np.int64)
 
 

@@ -27,7 +27,7 @@ def test_sizes():
     for rows, k in ((0, 0), (1, 1), (1, 256), (3, 257), (128, 512), (129, 100), (14336, 4096)):
         nk = -(-k // 256)
         assert L.mxfp4_code_bytes(rows, k) == rows * 128 * nk
-        assert L.mxfp4_scale_bytes(rows, k) == -(-rows // 128) * nk * 1024
+        assert L.mxfp4_scale_bytes(rows, k) == -(-rows // 32) * nk * 256
     for bad in ((-1, 4), (4, -1), (BIG, 1), (1, BIG), (1 << 20, 1 << 20)):
         assert L.mxfp4_code_bytes(*bad) == -1 and L.mxfp4_scale_bytes(*bad) == -1
         assert L.layer_norm_workspace_len(*bad) == -1
@@ -145,7 +145,7 @@ def test_binding_refuses_mismatches_before_any_call():
     with pytest.raises(ValueError, match="shape"):
         F.Act8(4, 40, tensors=(torch.zeros(4, 40, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)))
     with pytest.raises(ValueError, match="elements"):
-        F.Mxfp4(4, 40, tensors=(torch.zeros(4, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8)))
+        F.Mxfp4(4, 40, tensors=(torch.zeros(4, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)))
 
 
 @pytest.mark.parametrize("call", [
