@@ -110,8 +110,16 @@ __device__ __forceinline__ void act8_values(uint2 q, uint32_t s, float (&v)[8]) 
     v[4 * h + 3] = hi[1] * sc;
   }
 }
+// Largest of four neighbouring lanes' values, in each of them (two DPP steps;
+// all four lanes active).
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false);
+  m = o > m ? o : m;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false);
+  return o > m ? o : m;
+}
 // Largest magnitude (fp32 bits) of the 32 values that four neighbouring lanes
-// hold eight each of; every lane of the four gets it.  All lanes active.
+// hold eight each of; every lane of the four gets it.
 __device__ __forceinline__ uint32_t quad_amax(const float (&v)[8]) {
   uint32_t m = 0;
 #pragma unroll
@@ -119,10 +127,7 @@ __device__ __forceinline__ uint32_t quad_amax(const float (&v)[8]) {
     const uint32_t a = __float_as_uint(v[e]) & 0x7FFFFFFFu;
     m = a > m ? a : m;
   }
-  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false);
-  m = o > m ? o : m;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false);
-  return o > m ? o : m;
+  return quad_max(m);
 }
 
 // ---- eight consecutive elements of a row, p[0 .. 7], of which n are in range

@@ -535,11 +535,12 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
 }
 
 // Waves that split nk k-tiles: as many as give each the same number of them,
-// few enough that all workgroups are resident at once (32 waves a compute
-// unit; one token, 14336 x 4096: 8 waves 8.4 us, 16 waves 9.9 us).
-int split_waves(int64_t nk, int64_t blocks, int most) {
+// few enough that all workgroups are resident at once, `resident` waves a
+// compute unit (one token, 14336 x 4096: 8 waves 8.4 us, 16 waves 9.9 us; 64
+// tokens: 4 waves 18.9 us, 8 waves 22.8 us).
+int split_waves(int64_t nk, int64_t blocks, int most, int resident) {
   if (nk < 1) return 1;
-  const int64_t room = (int64_t)device_cus() * 32 / blocks;
+  const int64_t room = (int64_t)device_cus() * resident / blocks;
   if (room < most) most = room < 4 ? 4 : (int)room;
   const int64_t per = (nk + most - 1) / most;
   return (int)((nk + per - 1) / per);
@@ -547,7 +548,9 @@ int split_waves(int64_t nk, int64_t blocks, int most) {
 template <int TM, int TN, int OUT, bool SWAP, int FT>
 hipError_t launch_splitk(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
   const int64_t blocks = ((p.M + 16 * TM - 1) / (16 * TM)) * ((p.N + 16 * TN - 1) / (16 * TN));
-  const int W = split_waves(mx_ktiles(p.K), blocks, TM * TN > 2 ? 8 : 16);
+  // waves that a compute unit's registers hold
+  constexpr int kResident = TM * TN == 1 ? 32 : TM * TN == 2 ? 20 : TM * TN == 4 ? 16 : 12;
+  const int W = split_waves(mx_ktiles(p.K), blocks, TM * TN > 2 ? 8 : 16, kResident);
   const size_t join = (size_t)W * TN * 1024, own = FT >= 0 ? (size_t)W * kFusedRows * 136 : 0;
   hipLaunchKernelGGL((k_mx_splitk<TM, TN, OUT, SWAP, FT>), dim3((unsigned)blocks), dim3(64 * W), join > own ? join : own,
                      stream, p, ap);

@@ -133,10 +133,7 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
 #pragma unroll
       for (int e = 0; e < Row8<T>::kW; ++e) m = mag_max<T>(m, v[i].w[e]);
       if constexpr (T != FP8SG_OUT_F32) m = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
-      uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false);
-      m = o > m ? o : m;
-      o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false);
-      m = o > m ? o : m;
+      m = quad_max(m);
       const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(m), fit) : 127u;
       if (rw + i < j.rows) *reinterpret_cast<uint32_t*>(j.q.q + ((rw + i) * nkc + ct) * 128 + 4 * cc) = row_codes<T>(v[i], s);
       if ((lane & 3) == 0)  // block cc / 4 of row 16 half + i of the wave's group
@@ -193,8 +190,30 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
   }
 }
 
+// Rows only, for matrices too small for k_mxq's tiles to fill the chip: 8
+// elements a thread, 8 rows x 256 columns a block (16 x 4096: 6.1 us with the
+// tiles' 16 rows a lane, 2.4 us so).
+template <int T>
+__global__ __launch_bounds__(256) void k_mxq_rows(MxQuantArgs args) {
+  const MxQuantJob& j = args.job[0];
+  const int64_t nk = mx_ktiles(j.cols);
+  const int64_t r = (blockIdx.x / (uint32_t)nk) * 8ll + (threadIdx.x >> 5), ct = blockIdx.x % (uint32_t)nk;
+  if (r >= j.rows) return;  // a half wave: its lanes' groups of four stay whole
+  const int cc = threadIdx.x & 31;
+  const int64_t c = ct * 256 + 8 * cc;
+  const Row8<T> v = load_row8<T, false>(reinterpret_cast<const Elem<T>*>(j.x) + r * j.cols + c, left8(j.cols, c));
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < Row8<T>::kW; ++e) m = mag_max<T>(m, v.w[e]);
+  if constexpr (T != FP8SG_OUT_F32) m = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
+  m = quad_max(m);
+  const uint32_t s = (c & ~31) < j.cols ? fp4_scale(mag_bits<T>(m), args.fit != 0) : 127u;
+  *reinterpret_cast<uint32_t*>(j.q.q + (r * nk + ct) * 128 + 4 * cc) = row_codes<T>(v, s);
+  if ((cc & 3) == 0) j.q.s[mx_scale_off(r, ct * 8 + (cc >> 2), nk)] = (uint8_t)s;
+}
+
 // One thread per 8 values: 4 bytes of codes, their block's scale.
-template <int T, bool S>
+template <int T>
 __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t rows, int64_t k, Elem<T>* y) {
   const int64_t nk = mx_ktiles(k), upr = (k + 7) / 8, total = rows * upr;
   for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < total; i0 += (int64_t)gridDim.x * 256) {
@@ -207,7 +226,7 @@ __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t row
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
     const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
     const float v[8] = {a[0] * sc, a[1] * sc, b[0] * sc, b[1] * sc, c[0] * sc, c[1] * sc, d[0] * sc, d[1] * sc};
-    store8<T, S>(y + r * k + 8 * u, left8(k, 8 * u), v);
+    store8<T, false>(y + r * k + 8 * u, left8(k, 8 * u), v);
   }
 }
 
@@ -247,6 +266,12 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
       hipLaunchKernelGGL((k_mxq<T, NW, decltype(st)::value>), dim3((unsigned)(b0 + b1)), dim3(64 * NW), 0, stream, a);
       return hipGetLastError();
     };
+    if (wide < cus && n == 1 && !a.job[0].t.q) {
+      const int64_t blocks = (a.job[0].rows + 7) / 8 * mx_ktiles(a.job[0].cols);
+      if (a.job[0].rows == 0 || a.job[0].cols == 0) return hipSuccess;
+      hipLaunchKernelGGL((k_mxq_rows<T>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+      return hipGetLastError();
+    }
     // a wide tile per compute unit, or the narrow ones
     if (wide < cus) return launch(std::integral_constant<int, 2>{}, std::false_type{});
     if (bytes >= kStreamBytes) return launch(std::integral_constant<int, 8>{}, std::true_type{});
@@ -259,10 +284,7 @@ hipError_t launch_mx_dequantize(const mxfp4_operand& m, int64_t rows, int64_t k,
   return by_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     const dim3 grid(grid_for(rows * ((k + 7) / 8)));
-    if (rows * k * (int64_t)sizeof(Elem<T>) >= kStreamBytes)
-      hipLaunchKernelGGL((k_mx_dequant<T, true>), grid, dim3(256), 0, stream, m, rows, k, reinterpret_cast<Elem<T>*>(y));
-    else
-      hipLaunchKernelGGL((k_mx_dequant<T, false>), grid, dim3(256), 0, stream, m, rows, k, reinterpret_cast<Elem<T>*>(y));
+    hipLaunchKernelGGL((k_mx_dequant<T>), grid, dim3(256), 0, stream, m, rows, k, reinterpret_cast<Elem<T>*>(y));
     return hipGetLastError();
   });
 }
