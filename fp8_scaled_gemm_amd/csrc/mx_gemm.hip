@@ -364,22 +364,54 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
   }
 }
 
+// 4 bytes per lane from buffer offset `voff` into LDS at lds + 4 * lane (as
+// lds_dma16).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_dma4(uint32_t lds, uint32_t voff, i32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // Few rows or few tiles: a 16 TM x 16 TN tile per workgroup, whose waves split K
 // (wave w takes k-tiles w, w + W, ...) and join their sums through LDS.  Each
-// wave reads its fragments from memory into registers, one k-tile ahead: with
-// a single row block the weight streams through once and nothing is staged.
+// wave streams its k-tiles of both operands into LDS stages of its own, two in
+// flight, so nothing waits for another wave before the join.  (Fragments loaded
+// straight into registers put 16 rows in 16 neighbouring lanes, which the
+// address coalescer takes one at a time: 24 tokens, 4096 x 14336, 12.8 us; with
+// 8 lanes a row through LDS 7.9 us.)
 // SWAP: the operands have changed places (few columns): C is written
 // transposed, element (m, n) of the product at C[n * M + m].
-// FT >= 0: operand A is not quantised yet (its rows, of element type FT, are x):
-// a wave quantises the part of x that its k-tile needs into LDS itself.
-// Consecutive tiles go to one XCD: two of them share a row group's scales.
-constexpr int kFusedRows = 4;
+// FT >= 0: operand A is not quantised yet (its up to kFusedRows rows, of element
+// type FT, are x): a wave first quantises what its k-tiles need of x into LDS.
+// Consecutive tiles go to one XCD: two of them may share a row group's scales.
+constexpr int kFusedRows = 4, kFusedTiles = 8;  // rows of x, k-tiles a wave
 struct MxApply {
   const void* x;
   int32_t fit;
 };
+// Bytes of a wave's stage: codes of TM + TN fragments, the 32-row groups' scales.
+constexpr int few_stage(int tm, int tn, bool fused) {
+  return (fused ? 0 : tm * 2048 + (tm + 1) / 2 * 256) + tn * 2048 + (tn + 1) / 2 * 256;
+}
+constexpr int few_own(bool fused) { return fused ? kFusedTiles * kFusedRows * 136 : 0; }
+
+constexpr int64_t kLds = 160 * 1024;  // of a compute unit
+constexpr int few_wave_bytes(int tm, int tn, bool fused) { return 2 * few_stage(tm, tn, fused) + few_own(fused); }
+// Waves a workgroup can have: what LDS holds.
+constexpr int few_waves(int tm, int tn, bool fused) {
+  return (int)kLds / few_wave_bytes(tm, tn, fused) < 16 ? (int)kLds / few_wave_bytes(tm, tn, fused) : 16;
+}
+
 template <int TM, int TN, int OUT, bool SWAP, int FT>
-__global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmProblem p, MxApply ap) {
+__global__ __launch_bounds__(64 * few_waves(TM, TN, (FT >= 0))) void k_mx_few(MxGemmProblem p, MxApply ap) {
+  constexpr bool kFused = FT >= 0;
+  constexpr int kStage = few_stage(TM, TN, kFused), kOwn = few_own(kFused);
+  // loads of a stage (a wave's count of vmcnt)
+  constexpr int kLoads = (kFused ? 0 : 2 * TM + (TM + 1) / 2) + 2 * TN + (TN + 1) / 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), W = blockDim.x / kWave;
@@ -388,128 +420,143 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   const int64_t nbm = (M + 16 * TM - 1) / (16 * TM);
   const int64_t b = xcd_contiguous(blockIdx.x, gridDim.x);
   const int64_t bm = b % nbm * (16 * TM), bn = b / nbm * (16 * TN);
-  // the tile's first row and scale group (uniform), a lane's 32-bit offsets
-  // from them; rows past the end read the last one (never stored)
-  const uint8_t *qa = p.A.q + bm * pitch, *qb = p.B.q + bn * pitch;
-  const uint8_t *ga = p.A.s + (bm >> 5) * (int64_t)nk * 256, *gb = p.B.s + (bn >> 5) * (int64_t)nk * 256;
-  uint32_t oa[TM], ob[TN], ua[TM], ub[TN];
-  auto offsets = [&](int64_t row0, int64_t rows, int i, uint32_t& o, uint32_t& u) {
-    const int64_t row = row0 + 16 * i + r < rows ? row0 + 16 * i + r : rows - 1;
-    o = (uint32_t)((row - row0) * pitch + 32 * g);
-    u = (uint32_t)(((row >> 5) - (row0 >> 5)) * nk * 256 + (g * 16 + (row & 15)) * 4 + ((row & 31) >> 4) * 2);
-  };
-#pragma unroll
-  for (int i = 0; i < TM; ++i) offsets(bm, M, i, oa[i], ua[i]);
-#pragma unroll
-  for (int j = 0; j < TN; ++j) offsets(bn, N, j, ob[j], ub[j]);
+  uint8_t* my = lds + wave * (2 * kStage + kOwn);
 
-  struct Stage {
-    uint4 a[TM][2], b[TN][2];
-    uint32_t sa[TM], sb[TN];
-    Row8<FT < 0 ? 0 : FT> x[FT < 0 ? 1 : kFusedRows / 2];  // rows 2 i + lane / 32 of x
+  // descriptors over the tile's rows (and 32-row scale groups) that exist
+  const int64_t lm = M - bm < 16 * TM ? M - bm : 16 * TM, ln = N - bn < 16 * TN ? N - bn : 16 * TN;
+  const i32x4 ra = make_rsrc(p.A.q + bm * pitch, kFused ? 0 : lm * pitch);
+  const i32x4 rb = make_rsrc(p.B.q + bn * pitch, ln * pitch);
+  auto groups = [&](int64_t row0, int64_t rows) { return ((row0 + rows + 31) >> 5) - (row0 >> 5); };
+  const i32x4 sa = make_rsrc(p.A.s + (bm >> 5) * (int64_t)nk * 256, kFused ? 0 : groups(bm, lm) * nk * 256);
+  const i32x4 sb = make_rsrc(p.B.s + (bn >> 5) * (int64_t)nk * 256, groups(bn, ln) * nk * 256);
+  // a load: 8 rows of 128 bytes, 8 lanes a row, chunks swizzled by the row
+  const int lr = lane >> 3;
+  const uint32_t vo0 = (uint32_t)(lr * pitch + 16 * ((lane & 7) ^ swz16(lr)));
+  const uint32_t vo1 = (uint32_t)((8 + lr) * pitch + 16 * ((lane & 7) ^ swz16(8 + lr)));
+  auto issue = [&](int kt, uint32_t dst) {
+    const uint32_t k0 = (uint32_t)kt * 128, s0 = (uint32_t)kt * 256 + 4 * lane;
+    if constexpr (!kFused) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        lds_dma16_split(dst + i * 2048, vo0, k0 + 16 * i * pitch, ra);
+        lds_dma16_split(dst + i * 2048 + 1024, vo1, k0 + 16 * i * pitch, ra);
+      }
+      dst += TM * 2048;
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      lds_dma16_split(dst + j * 2048, vo0, k0 + 16 * j * pitch, rb);
+      lds_dma16_split(dst + j * 2048 + 1024, vo1, k0 + 16 * j * pitch, rb);
+    }
+    dst += TN * 2048;
+    if constexpr (!kFused) {
+#pragma unroll
+      for (int i = 0; i < (TM + 1) / 2; ++i) lds_dma4(dst + i * 256, s0 + i * nk * 256, sa);
+      dst += (TM + 1) / 2 * 256;
+    }
+#pragma unroll
+    for (int j = 0; j < (TN + 1) / 2; ++j) lds_dma4(dst + j * 256, s0 + j * nk * 256, sb);
   };
   v4f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto load = [&](Stage& s, int kt) {
-    const int64_t k0 = (int64_t)kt * 128, s0 = (int64_t)kt * 256;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      s.b[j][0] = *reinterpret_cast<const uint4*>(qb + k0 + ob[j]);
-      s.b[j][1] = *reinterpret_cast<const uint4*>(qb + k0 + ob[j] + 16);
-      s.sb[j] = *reinterpret_cast<const uint16_t*>(gb + s0 + ub[j]);
-    }
-    if constexpr (FT < 0) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        s.a[i][0] = *reinterpret_cast<const uint4*>(qa + k0 + oa[i]);
-        s.a[i][1] = *reinterpret_cast<const uint4*>(qa + k0 + oa[i] + 16);
-        s.sa[i] = *reinterpret_cast<const uint16_t*>(ga + s0 + ua[i]);
-      }
-    } else {
-      const int64_t c = (int64_t)kt * 256 + 8 * (lane & 31);
-      const int n = left8(p.K, c);
-#pragma unroll
-      for (int i = 0; i < kFusedRows / 2; ++i) {
-        const int m = 2 * i + (lane >> 5);
-        s.x[i] = load_row8<FT, false>(reinterpret_cast<const Elem<FT>*>(ap.x) + (m < M ? m : 0) * p.K + c, n);
-      }
-    }
-  };
-  auto compute = [&](Stage& s, int kt) {
-    if constexpr (FT >= 0) {  // x's k-tile to codes, through this wave's LDS
-      uint8_t* my = lds + wave * (kFusedRows * 136);  // rows of 128 bytes of codes and 8 of scales
-      const int cc = lane & 31;
+  // a 16-row tile starts in the middle of its 32-row scale group where its
+  // first row is odd in 16s
+  const int odd_a = TM == 1 ? (int)(bm >> 4) & 1 : 0, odd_b = TN == 1 ? (int)(bn >> 4) & 1 : 0;
+
+  const uint32_t d0 = lds_u32(my), d1 = d0 + kStage;
+  if (wave < nk) issue(wave, d0);
+  if (wave + W < nk) issue(wave + W, d1);
+  // x to codes: k-tile kt of row m at own + ((kt - wave) / W * kFusedRows + m) * 136
+  if constexpr (kFused) {
+    const int cc = lane & 31;
+    int t = 0;
+    for (int kt = wave; kt < nk; kt += W, ++t) {
+      const int64_t c = (int64_t)kt * 256 + 8 * cc;
 #pragma unroll
       for (int i = 0; i < kFusedRows / 2; ++i) {
         const int m = 2 * i + (lane >> 5);
         float v[8];
-        s.x[i].values(v);
+        load8<FT, false>(reinterpret_cast<const Elem<FT>*>(ap.x) + (m < M ? m : 0) * p.K + c, left8(p.K, c), v);
         const uint32_t sc = fp4_scale(quad_amax(v), ap.fit != 0);
         const float f = scale_value(sc);
         uint32_t d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], f, 0);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[2], v[3], f, 1);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[4], v[5], f, 2);
         d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[6], v[7], f, 3);
-        *reinterpret_cast<uint32_t*>(my + m * 136 + 4 * cc) = sc == 255u ? 0u : d;
-        if ((lane & 3) == 0) my[m * 136 + 128 + (cc >> 2)] = (uint8_t)sc;
+        uint8_t* row = my + 2 * kStage + (t * kFusedRows + m) * 136;
+        *reinterpret_cast<uint32_t*>(row + 4 * cc) = sc == 255u ? 0u : d;
+        if ((lane & 3) == 0) row[128 + (cc >> 2)] = (uint8_t)sc;
       }
-      // rows past M repeat the last one
-      const uint8_t* row = my + (r < M ? r : (int)M - 1) * 136;
-      const uint2 lo0 = *reinterpret_cast<const uint2*>(row + 32 * g), lo1 = *reinterpret_cast<const uint2*>(row + 32 * g + 8);
-      const uint2 hi0 = *reinterpret_cast<const uint2*>(row + 32 * g + 16), hi1 = *reinterpret_cast<const uint2*>(row + 32 * g + 24);
-      s.a[0][0] = make_uint4(lo0.x, lo0.y, lo1.x, lo1.y);
-      s.a[0][1] = make_uint4(hi0.x, hi0.y, hi1.x, hi1.y);
-      s.sa[0] = *reinterpret_cast<const uint16_t*>(row + 128 + 2 * g);
     }
-    if constexpr (FT >= 0) {  // (the two halves in a loop: see below)
+  }
+
+  int t = 0;
 #pragma unroll 1
+  for (int kt = wave; kt < nk; kt += W, ++t) {
+    const uint8_t* st = my + (t & 1) * kStage;
+    if (kt + W < nk) wait_vmcnt<kLoads>();
+    else wait_vmcnt<0>();
+    compiler_fence();
+    uint4 a[TM][2], w[TN][2];
+    uint32_t ua[TM], ub[TN];
+    const uint8_t* q = st;
+    if constexpr (kFused) {  // rows past M repeat the last one
+      const uint8_t* row = my + 2 * kStage + (t * kFusedRows + (r < M ? r : (int)M - 1)) * 136;
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        acc[0][0] = mfma4<0, 0>(s.b[0][0], s.a[0][0], acc[0][0], s.sb[0], s.sa[0]);
-        s.b[0][0] = s.b[0][1];
-        s.a[0][0] = s.a[0][1];
-        s.sb[0] >>= 8;
-        s.sa[0] >>= 8;
+        const uint2 lo = *reinterpret_cast<const uint2*>(row + 32 * g + 16 * h);
+        const uint2 hi = *reinterpret_cast<const uint2*>(row + 32 * g + 16 * h + 8);
+        a[0][h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
+      ua[0] = *reinterpret_cast<const uint16_t*>(row + 128 + 2 * g);
     } else {
-      static_for<2>([&](auto kk) {
-        constexpr int KK = decltype(kk)::value;
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = mfma4<KK, KK>(s.b[j][KK], s.a[i][KK], acc[i][j], s.sb[j], s.sa[i]);
-      });
+        for (int h = 0; h < 2; ++h) a[i][h] = *reinterpret_cast<const uint4*>(q + i * 2048 + lds_off2(r, 2 * g + h));
+      q += TM * 2048;
     }
-    // the operands stay in use past the products, so that no product's result
-    // can take their registers (see the loop below)
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int i = 0; i < TM; ++i) keep_loaded(s.a[i][kk]);
+      for (int h = 0; h < 2; ++h) w[j][h] = *reinterpret_cast<const uint4*>(q + j * 2048 + lds_off2(r, 2 * g + h));
+    q += TN * 2048;
+    if constexpr (!kFused) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) keep_loaded(s.b[j][kk]);
+      for (int i = 0; i < TM; ++i) ua[i] = *reinterpret_cast<const uint32_t*>(q + i / 2 * 256 + 4 * lane) >> (16 * (TM == 1 ? odd_a : i & 1));
+      q += (TM + 1) / 2 * 256;
     }
-  };
-  // One product per (i, j) and half in the loop's body, so that every
-  // accumulator is updated in place: with two copies of the body the compiler
-  // (clang 22 of ROCm 7.2) gave a product's result registers that still held
-  // another accumulator.  The build checks that each product's result and
-  // addend are the same registers.
-  Stage cur;
-  int kt = wave;
-  if (kt < nk) load(cur, kt);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ub[j] = *reinterpret_cast<const uint32_t*>(q + j / 2 * 256 + 4 * lane) >> (16 * (TN == 1 ? odd_b : j & 1));
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the stage is in registers: load it again
+    compiler_fence();
+    if (kt + 2 * W < nk) issue(kt + 2 * W, (t & 1) ? d1 : d0);
+    // One product per accumulator in the loop's body, so that each is updated
+    // in place: otherwise the compiler (clang 22 of ROCm 7.2) once gave a
+    // product's result registers that still held another accumulator.  The
+    // build checks that every product's result and addend are the same
+    // registers.
 #pragma unroll 1
-  for (; kt < nk; kt += W) {
-    if constexpr (TM * TN < 16) {
-      Stage next = cur;
-      if (kt + W < nk) load(next, kt + W);
-      compute(cur, kt);
-      cur = next;
-    } else {  // (no registers for a second stage)
-      compute(cur, kt);
-      if (kt + W < nk) load(cur, kt + W);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma4<0, 0>(w[j][0], a[i][0], acc[i][j], ub[j], ua[i]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        keep_loaded(a[i][0]);
+        a[i][0] = a[i][1];
+        ua[i] >>= 8;
+      }
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        keep_loaded(w[j][0]);
+        w[j][0] = w[j][1];
+        ub[j] >>= 8;
+      }
     }
   }
 
@@ -518,7 +565,7 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    if (i > 0 || FT >= 0) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < TN; ++j) *reinterpret_cast<v4f*>(red + ((wave * TN + j) * 64 + lane) * 4) = acc[i][j];
     __syncthreads();
@@ -534,36 +581,38 @@ __global__ __launch_bounds__(TM * TN > 2 ? 512 : 1024) void k_mx_splitk(MxGemmPr
   }
 }
 
-// Waves that split nk k-tiles: as many as give each the same number of them,
-// few enough that all workgroups are resident at once, `resident` waves a
-// compute unit (one token, 14336 x 4096: 8 waves 8.4 us, 16 waves 9.9 us; 64
-// tokens: 4 waves 18.9 us, 8 waves 22.8 us).
-int split_waves(int64_t nk, int64_t blocks, int most, int resident) {
+// Waves that split nk k-tiles: as many (at most `most`) as give each the same
+// number of them, and few enough that all workgroups
+// are resident at once.
+int split_waves(int64_t nk, int64_t blocks, int64_t per_wave, int64_t most) {
   if (nk < 1) return 1;
-  const int64_t room = (int64_t)device_cus() * resident / blocks;
-  if (room < most) most = room < 4 ? 4 : (int)room;
+  const int64_t room = (int64_t)device_cus() * kLds / (blocks * per_wave);
+  if (room < most) most = room < 4 ? 4 : room;
   const int64_t per = (nk + most - 1) / most;
   return (int)((nk + per - 1) / per);
 }
 template <int TM, int TN, int OUT, bool SWAP, int FT>
-hipError_t launch_splitk(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
+hipError_t launch_few(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
+  auto kern = k_mx_few<TM, TN, OUT, SWAP, FT>;
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  if (attr != hipSuccess) return attr;
+  constexpr int64_t kWaveBytes = few_wave_bytes(TM, TN, FT >= 0);
+  static_assert(kWaveBytes >= TN * 1024, "the join fits a wave's stages");
   const int64_t blocks = ((p.M + 16 * TM - 1) / (16 * TM)) * ((p.N + 16 * TN - 1) / (16 * TN));
-  // waves that a compute unit's registers hold
-  constexpr int kResident = TM * TN == 1 ? 32 : TM * TN == 2 ? 20 : TM * TN == 4 ? 16 : 12;
-  const int W = split_waves(mx_ktiles(p.K), blocks, TM * TN > 2 ? 8 : 16, kResident);
-  const size_t join = (size_t)W * TN * 1024, own = FT >= 0 ? (size_t)W * kFusedRows * 136 : 0;
-  hipLaunchKernelGGL((k_mx_splitk<TM, TN, OUT, SWAP, FT>), dim3((unsigned)blocks), dim3(64 * W), join > own ? join : own,
-                     stream, p, ap);
+  const int W = split_waves(mx_ktiles(p.K), blocks, kWaveBytes, few_waves(TM, TN, FT >= 0));
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), W * kWaveBytes, stream, p, ap);
   return hipGetLastError();
 }
+// At most 64 rows: as many row blocks as there are; two column blocks a tile
+// (each fragment of A then serves two) where enough tiles are left.
 template <int OUT, bool SWAP>
-hipError_t launch_few(const MxGemmProblem& p, hipStream_t stream) {
-  const int cus = device_cus();
-  // two column blocks a tile halve the reads of A, where enough tiles are left
-  const bool pairs = (p.N + 31) / 32 >= cus;
-  if (p.M <= 16) return pairs ? launch_splitk<1, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<1, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
-  if (p.M <= 32) return pairs ? launch_splitk<2, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<2, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
-  return pairs ? launch_splitk<4, 2, OUT, SWAP, -1>(p, MxApply{}, stream) : launch_splitk<4, 1, OUT, SWAP, -1>(p, MxApply{}, stream);
+hipError_t launch_rows(const MxGemmProblem& p, hipStream_t stream) {
+  const bool pairs = (p.N + 31) / 32 >= device_cus();
+  const MxApply none{};
+  if (p.M <= 16) return pairs ? launch_few<1, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<1, 1, OUT, SWAP, -1>(p, none, stream);
+  if (p.M <= 32) return pairs ? launch_few<2, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<2, 1, OUT, SWAP, -1>(p, none, stream);
+  return pairs ? launch_few<4, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<4, 1, OUT, SWAP, -1>(p, none, stream);
 }
 
 }  // namespace
@@ -579,17 +628,25 @@ hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
       return hipGetLastError();
     }
     const int cus = device_cus();
-    if (p.M <= 64 && p.M <= p.N) return launch_few<T, false>(p, stream);
-    if (p.N <= 64) return launch_few<T, true>(MxGemmProblem{p.B, p.A, p.C, p.N, p.M, p.K}, stream);
-    if (p.K > 0 && tiles(256) * 2 >= cus) {
+    if (p.M <= 64 && p.M <= p.N) return launch_rows<T, false>(p, stream);
+    if (p.N <= 64) return launch_rows<T, true>(MxGemmProblem{p.B, p.A, p.C, p.N, p.M, p.K}, stream);
+    // The large tiles where they occupy most of the chip (2048 x 4096 x 4096, 128
+    // tiles on 256 units: 33.9 us, 24.4 us in tiles of 128; 4096^3, 256 tiles:
+    // 37.1 against 43.3 us).
+    if (p.K > 0 && tiles(256) * 8 >= 5 * cus) {
       hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
       return hipGetLastError();
     }
-    if (p.K > 0 && tiles(64) > 2 * cus) {
+    // Tiles of 128, or of 64 with K split over a workgroup's waves: by the
+    // rounds over the chip and what a round was measured to take (us / 10):
+    // about 20 + 9 a k-tile, and 60 + 3 a k-tile (512 x 4096 x 4096: 14.3
+    // against 22.5 us; 128 x 4096 x 14336: 19.7 us in tiles of 64).
+    const int64_t nk = mx_ktiles(p.K), r128 = (tiles(128) + 2 * cus - 1) / (2 * cus), r64 = (tiles(64) + cus - 1) / cus;
+    if (p.K > 0 && 20 + 9 * nk * r128 <= r64 * (60 + 3 * nk)) {
       hipLaunchKernelGGL((k_mx_mid<T>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
       return hipGetLastError();
     }
-    return launch_splitk<4, 4, T, false, -1>(p, MxApply{}, stream);
+    return launch_few<4, 4, T, false, -1>(p, MxApply{}, stream);
   });
 }
 
@@ -601,12 +658,15 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
 hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemmProblem& p, int out,
                            hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  // Every 16 columns' workgroup quantises x again, so in the product's own
-  // launch only for as few rows as one pair of loads holds.
-  if (p.M <= kFusedRows && p.K > 0 && mx_pitch(p.K) * 256 < (1ll << 31) - 256)
+  // Every workgroup quantises x again, so in the product's own launch only for
+  // a few rows, and only k-tiles that fit its LDS.
+  if (p.M <= kFusedRows && p.K > 0 && mx_ktiles(p.K) <= 4 * kFusedTiles)
     return by_type(out, [&](auto t) {
       return by_type(type, [&](auto f) {
-        return launch_splitk<1, 1, decltype(t)::value, false, decltype(f)::value>(p, MxApply{j.x, fit}, stream);
+        constexpr int T = decltype(t)::value, X = decltype(f)::value;
+        const MxApply ap{j.x, fit};
+        return (p.N + 31) / 32 >= device_cus() ? launch_few<1, 2, T, false, X>(p, ap, stream)
+                                               : launch_few<1, 1, T, false, X>(p, ap, stream);
       });
     });
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
