@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import _check, _need, _ptr, _stream, lib
+from . import _check, _cur_device, _need, _raw_stream, lib
 
 MX_FLOOR, MX_FIT = 0, 1
 
@@ -52,7 +52,7 @@ def bind(L):
 
 def _here(*tensors):
     """Every tensor is on the current device, whose stream the call uses."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             if not t.is_cuda:
@@ -61,10 +61,26 @@ def _here(*tensors):
                              "call under torch.cuda.device(...)")
 
 
+# The calls are short: their host time is kept down by passing addresses as
+# plain integers and by one struct per buffer pair, filled again on each call.
+_device = _cur_device if _cur_device is not None else torch.cuda.current_device
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(stream):
+    """hipStream_t of `stream`, or of torch's current stream on the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(_device()) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _type(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    ty = _TYPE.get(t.dtype)
+    ty = _TYPE.get(t.dtype)  # (c_int of the C ABI's fp8sg_out)
     if ty is None:
         raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16, float16 or float32")
     return ty
@@ -79,11 +95,14 @@ def _rule(rule):
 def _matrix(t, name):
     """(rows, cols) of a contiguous matrix; leading dimensions count as rows."""
     _type(t, name)
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name}: expected at least one dimension")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    cols = t.shape[-1]
+    if len(shape) == 2:
+        return shape
+    cols = shape[-1]
     return (t.numel() // cols if cols else _rows(t)), cols
 
 
@@ -118,11 +137,17 @@ class Mxfp4:
             _need(self.q, "q", torch.uint8, numel=nq)
             _need(self.s, "s", torch.uint8, numel=ns)
 
+        self._pair = _Pair()
+        self._at = ctypes.addressof(self._pair)
+
     def tensors(self):
         return self.q, self.s
 
     def c(self):
-        return _Pair(self.q.data_ptr(), self.s.data_ptr())
+        """Address of the C struct, holding the buffers' present addresses."""
+        p = self._pair
+        p.q, p.s = self.q.data_ptr(), self.s.data_ptr()
+        return self._at
 
 
 class Act8:
@@ -141,11 +166,17 @@ class Act8:
             _need(self.q, "q", torch.uint8, shape=(rows, 32 * blocks))
             _need(self.s, "s", torch.uint8, shape=(rows, blocks))
 
+        self._pair = _Pair()
+        self._at = ctypes.addressof(self._pair)
+
     def tensors(self):
         return self.q, self.s
 
     def c(self):
-        return _Pair(self.q.data_ptr(), self.s.data_ptr())
+        """Address of the C struct, holding the buffers' present addresses."""
+        p = self._pair
+        p.q, p.s = self.q.data_ptr(), self.s.data_ptr()
+        return self._at
 
 
 def _need_codes(m, name, kind, rows, cols):
@@ -154,10 +185,6 @@ def _need_codes(m, name, kind, rows, cols):
     got = (m.rows, m.k) if kind is Mxfp4 else (m.rows, m.cols)
     if got != (rows, cols):
         raise ValueError(f"{name}: {got[0]} x {got[1]}, expected {rows} x {cols}")
-
-
-def _ref(pair):
-    return ctypes.addressof(pair) if pair is not None else None
 
 
 # ------------------------------------------------------------------- MXFP4
@@ -175,7 +202,7 @@ def mxfp4_quantize(x: torch.Tensor, q: Mxfp4 = None, qT: Mxfp4 = None, rule: int
             _here(m.q, m.s)
         args.append(m.c() if m is not None else None)
     _here(x)
-    _check(lib().mxfp4_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _rule(rule), _ref(args[0]), _ref(args[1]),
+    _check(lib().mxfp4_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _rule(rule), args[0], args[1],
                                 _stream(stream)), "mxfp4_quantize")
 
 
@@ -185,7 +212,7 @@ def mxfp4_dequantize(m: Mxfp4, y: torch.Tensor, stream=None):
     _need_codes(m, "m", Mxfp4, rows, k)
     _here(y, m.q, m.s)
     c = m.c()
-    _check(lib().mxfp4_dequantize(_ref(c), rows, k, _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_dequantize")
+    _check(lib().mxfp4_dequantize(c, rows, k, _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_dequantize")
 
 
 def mxfp4_gemm(A: Mxfp4, B: Mxfp4, C: torch.Tensor, stream=None):
@@ -198,7 +225,7 @@ def mxfp4_gemm(A: Mxfp4, B: Mxfp4, C: torch.Tensor, stream=None):
     _need_codes(B, "B", Mxfp4, N, A.k)
     _here(C, A.q, A.s, B.q, B.s)
     a, b = A.c(), B.c()
-    _check(lib().mxfp4_gemm(_ref(a), _ref(b), _ptr(C), _TYPE[C.dtype], M, N, A.k, _stream(stream)), "mxfp4_gemm")
+    _check(lib().mxfp4_gemm(a, b, _ptr(C), _TYPE[C.dtype], M, N, A.k, _stream(stream)), "mxfp4_gemm")
 
 
 class Mxfp4LinearSaved:
@@ -214,7 +241,10 @@ class Mxfp4LinearSaved:
         return self.x_qT.tensors() + self.w_qT.tensors()
 
     def c(self):
-        return _LinSaved(self.x_qT.c(), self.w_qT.c())
+        self.x_qT.c()
+        self.w_qT.c()
+        self._all = _LinSaved(self.x_qT._pair, self.w_qT._pair)
+        return ctypes.addressof(self._all)
 
 
 class Mxfp4LinearWs:
@@ -229,7 +259,13 @@ class Mxfp4LinearWs:
         self.gy_qT = Mxfp4(N, M, device) if backward else None
 
     def c(self):
-        return _LinWs(*[m.c() if m is not None else _Pair() for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT)])
+        pairs = []
+        for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT):
+            if m is not None:
+                m.c()
+            pairs.append(m._pair if m is not None else _Pair())
+        self._all = _LinWs(*pairs)
+        return ctypes.addressof(self._all)
 
 
 def _linear(obj, kind, name, dims, fields):
@@ -263,7 +299,7 @@ def mxfp4_linear_fwd(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearWs, saved:
         _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
         sv = saved.c()
     wc = ws.c()
-    _check(lib().mxfp4_linear_fwd(_ptr(x), _ptr(w), _TYPE[x.dtype], M, N, K, _rule(rule), _ref(wc), _ref(sv),
+    _check(lib().mxfp4_linear_fwd(_ptr(x), _ptr(w), _TYPE[x.dtype], M, N, K, _rule(rule), wc, sv,
                                   _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_linear_fwd")
 
 
@@ -279,7 +315,7 @@ def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSave
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("gy_q", "gy_qT"))
     _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
     wc, sv = ws.c(), saved.c()
-    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), _ref(wc), _ref(sv), _ptr(gx),
+    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), wc, sv, _ptr(gx),
                                   _ptr(gw), _TYPE[gx.dtype], _stream(stream)), "mxfp4_linear_bwd")
 
 
@@ -294,7 +330,7 @@ def mxfp4_linear_apply(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: Mxfp4, ru
     _need(y, "y", y.dtype, shape=x.shape[:-1] + (w.rows,))
     _here(x, y, w.q, w.s, ws.q, ws.s)
     wc, xc = w.c(), ws.c()
-    _check(lib().mxfp4_linear_apply(_ptr(x), _TYPE[x.dtype], _ref(wc), M, w.rows, K, _rule(rule), _ref(xc), _ptr(y),
+    _check(lib().mxfp4_linear_apply(_ptr(x), _TYPE[x.dtype], wc, M, w.rows, K, _rule(rule), xc, _ptr(y),
                                     _TYPE[y.dtype], _stream(stream)), "mxfp4_linear_apply")
 
 
@@ -306,7 +342,7 @@ def act8_quantize(x: torch.Tensor, c: Act8, stream=None):
     _need_codes(c, "c", Act8, rows, cols)
     _here(x, c.q, c.s)
     p = c.c()
-    _check(lib().act8_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _ref(p), _stream(stream)), "act8_quantize")
+    _check(lib().act8_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, p, _stream(stream)), "act8_quantize")
 
 
 def act8_dequantize(c: Act8, y: torch.Tensor, stream=None):
@@ -315,7 +351,7 @@ def act8_dequantize(c: Act8, y: torch.Tensor, stream=None):
     _need_codes(c, "c", Act8, rows, cols)
     _here(y, c.q, c.s)
     p = c.c()
-    _check(lib().act8_dequantize(_ref(p), rows, cols, _ptr(y), _TYPE[y.dtype], _stream(stream)), "act8_dequantize")
+    _check(lib().act8_dequantize(p, rows, cols, _ptr(y), _TYPE[y.dtype], _stream(stream)), "act8_dequantize")
 
 
 def _strided(t, name, like, rows, cols):
@@ -350,7 +386,7 @@ def swiglu_fwd(g: torch.Tensor, u: torch.Tensor, a: torch.Tensor, cg: Act8 = Non
     ldg, ldu = _strided(g, "g", a, rows, cols), _strided(u, "u", a, rows, cols)
     _here(g, u, a)
     pg, pu = _ckpts(cg, cu, rows, cols)
-    _check(lib().swiglu_fwd(_ptr(g), ldg, _ptr(u), ldu, _TYPE[a.dtype], rows, cols, _ptr(a), _ref(pg), _ref(pu),
+    _check(lib().swiglu_fwd(_ptr(g), ldg, _ptr(u), ldu, _TYPE[a.dtype], rows, cols, _ptr(a), pg, pu,
                             _stream(stream)), "swiglu_fwd")
 
 
@@ -362,7 +398,7 @@ def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, strea
     _here(da, dg, du)
     if isinstance(g, Act8) or isinstance(u, Act8):
         pg, pu = _ckpts(g, u, rows, cols)
-        args = (None, 0, None, 0, _ref(pg), _ref(pu))
+        args = (None, 0, None, 0, pg, pu)
     else:
         ldg, ldu = _strided(g, "g", da, rows, cols), _strided(u, "u", da, rows, cols)
         _here(g, u)
@@ -411,7 +447,7 @@ def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None
         _here(ckpt.q, ckpt.s)
         p = ckpt.c()
     _check(lib().layer_norm_fwd(_ptr(x), _TYPE[x.dtype], _ptr(w), _ptr(b), pt, rows, cols, eps, _ptr(y), _ptr(mean),
-                                _ptr(rstd), _ref(p), _stream(stream)), "layer_norm_fwd")
+                                _ptr(rstd), p, _stream(stream)), "layer_norm_fwd")
 
 
 def layer_norm_workspace_len(rows: int, cols: int) -> int:
@@ -440,6 +476,6 @@ def layer_norm_bwd(dy: torch.Tensor, x, w, mean, rstd, dx=None, dw=None, db=None
     if ws is not None:
         _need(ws, "ws", torch.float32)
     _here(dx, ws)
-    _check(lib().layer_norm_bwd(_ptr(dy), xp, _ref(cp), _TYPE[dy.dtype], _ptr(w), pt, _ptr(mean), _ptr(rstd), rows,
+    _check(lib().layer_norm_bwd(_ptr(dy), xp, cp, _TYPE[dy.dtype], _ptr(w), pt, _ptr(mean), _ptr(rstd), rows,
                                 cols, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
                                 _stream(stream)), "layer_norm_bwd")
