@@ -126,18 +126,27 @@ fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t
   if (!ws || !saved) return FP8SG_ERR_NULL;
   if (!type_ok(type) || !type_ok(out) || !rule_ok(rule)) return FP8SG_ERR_FORMAT;
   if (!mat_ok(M, K) || !mat_ok(N, K) || !mat_ok(M, N)) return FP8SG_ERR_SHAPE;
+  if (!gx && !gw && (M * K > 0 || N * K > 0)) return FP8SG_ERR_NULL;
   FP8SG_TRY(check_tensor(gy, M * N, type));
-  FP8SG_TRY(check_codes(ws->gy_q, M * N));
-  FP8SG_TRY(check_codes(ws->gy_qT, M * N));
-  FP8SG_TRY(check_codes(saved->x_qT, M * K));
-  FP8SG_TRY(check_codes(saved->w_qT, N * K));
-  FP8SG_TRY(check_tensor(gx, M * K, out));
-  FP8SG_TRY(check_tensor(gw, N * K, out));
-  const MxQuantJob j{gy, M, N, ws->gy_q, ws->gy_qT};
-  const hipError_t e = launch_mx_quantize(&j, 1, type, rule == FP8SG_MX_FIT, S(stream));
+  MxQuantJob j{gy, M, N, {}, {}};
+  if (gx) {
+    FP8SG_TRY(check_codes(ws->gy_q, M * N));
+    FP8SG_TRY(check_codes(saved->w_qT, N * K));
+    FP8SG_TRY(check_tensor(gx, M * K, out));
+    j.q = ws->gy_q;
+  }
+  if (gw) {
+    FP8SG_TRY(check_codes(ws->gy_qT, M * N));
+    FP8SG_TRY(check_codes(saved->x_qT, M * K));
+    FP8SG_TRY(check_tensor(gw, N * K, out));
+    j.t = ws->gy_qT;
+  }
+  hipError_t e = launch_mx_quantize(&j, 1, type, rule == FP8SG_MX_FIT, S(stream));
   if (e != hipSuccess) return FP8SG_ERR_HIP;
-  return hip_status(launch_mx_gemm_pair(MxGemmProblem{ws->gy_q, saved->w_qT, gx, M, K, N},
-                                        MxGemmProblem{ws->gy_qT, saved->x_qT, gw, N, K, M}, out, S(stream)));
+  const MxGemmProblem dgrad{ws->gy_q, saved->w_qT, gx, M, K, N}, wgrad{ws->gy_qT, saved->x_qT, gw, N, K, M};
+  if (gx && gw) e = launch_mx_gemm_pair(dgrad, wgrad, out, S(stream));
+  else if (gx || gw) e = launch_mx_gemm(gx ? dgrad : wgrad, out, S(stream));
+  return hip_status(e);
 }
 
 fp8sg_status mxfp4_linear_apply(const void* x, fp8sg_out type, const mxfp4_operand* w, int64_t M, int64_t N,

@@ -239,7 +239,7 @@ unsigned grid_for(int64_t n) {
 // rows, and with a transposed copy the padding of its last k-tile too.
 template <int NW>
 int64_t tiles_of(const MxQuantJob& j) {
-  if (j.rows == 0 || j.cols == 0) return 0;
+  if (j.rows == 0 || j.cols == 0 || (!j.q.q && !j.t.q)) return 0;
   const int64_t rt = j.t.q ? mx_ktiles(j.rows) * (8 / NW) : (j.rows + 32 * NW - 1) / (32 * NW);
   return rt * mx_ktiles(j.cols);
 }

@@ -303,20 +303,31 @@ def mxfp4_linear_fwd(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearWs, saved:
                                   _ptr(y), _TYPE[y.dtype], _stream(stream)), "mxfp4_linear_fwd")
 
 
-def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSaved, gx: torch.Tensor,
-                     gw: torch.Tensor, rule: int = MX_FLOOR, stream=None):
-    """gx[M,K] = gy[M,N] W and gw[N,K] = gy^T x from what the forward saved."""
+def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSaved, gx, gw, rule: int = MX_FLOOR,
+                     stream=None):
+    """gx[M,K] = gy[M,N] W and gw[N,K] = gy^T x from what the forward saved; either
+    may be None."""
     M, N = _matrix(gy, "gy")
-    M2, K = _matrix(gx, "gx")
-    if M2 != M:
-        raise ValueError(f"gx: {M2} rows, expected {M}")
-    _need(gw, "gw", gx.dtype, shape=(N, K))
+    if not isinstance(saved, Mxfp4LinearSaved):
+        raise TypeError(f"saved: expected Mxfp4LinearSaved, got {type(saved).__name__}")
+    K = saved.dims[2]
+    if gx is None and gw is None:
+        raise ValueError("mxfp4_linear_bwd: gx or gw is needed")
+    out = gw if gx is None else gx
+    _type(out, "gw" if gx is None else "gx")
+    need = ()
+    if gx is not None:
+        _need(gx, "gx", out.dtype, shape=gy.shape[:-1] + (K,))
+        need += ("gy_q",)
+    if gw is not None:
+        _need(gw, "gw", out.dtype, shape=(N, K))
+        need += ("gy_qT",)
     _here(gy, gx, gw)
-    _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("gy_q", "gy_qT"))
+    _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), need)
     _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
     wc, sv = ws.c(), saved.c()
-    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), wc, sv, _ptr(gx),
-                                  _ptr(gw), _TYPE[gx.dtype], _stream(stream)), "mxfp4_linear_bwd")
+    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), wc, sv, _ptr(gx), _ptr(gw),
+                                  _TYPE[out.dtype], _stream(stream)), "mxfp4_linear_bwd")
 
 
 def mxfp4_linear_apply(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: Mxfp4, rule: int = MX_FLOOR, stream=None):

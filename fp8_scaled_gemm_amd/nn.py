@@ -31,7 +31,12 @@ weight gradient leaves the wgrad GEMM unscaled and checked (the scaler's
 unscale_ then skips it); the input gradient keeps the loss scale for the layers
 below.
 
-Limits of this layer: inputs and weights are bf16 or fp16; Float8Linear has no bias (the method's linear has none; the default
+  - MXFP4Linear, PackedMXFP4Linear, convert_to_mxfp4_training / _serving: the
+    same layer with 4-bit microscaled operands, for training and for serving.
+  - SwiGLU, LayerNorm: the gated activation and the norm around those linears,
+    which may keep what their backward pass needs in 8 bits.
+
+Limits of Float8Linear: inputs and weights are bf16 or fp16; Float8Linear has no bias (the method's linear has none; the default
 filter leaves biased layers alone); leading dimensions of the input are
 flattened into M; M, N, K must be multiples of 16.
 """
@@ -48,6 +53,9 @@ from . import (E4M3FN, E5M2, LinearBwdWs, LinearBwdWsRW, LinearSaved, LinearSave
                fp8_quantize_f16, fp8_scaled_linear_bwd, fp8_scaled_linear_bwd_delayed,
                fp8_scaled_linear_bwd_rowwise, fp8_scaled_linear_fwd, fp8_scaled_linear_fwd_delayed,
                fp8_scaled_linear_fwd_rowwise)
+from . import (MX_FIT, MX_FLOOR, Act8, Mxfp4, Mxfp4LinearSaved, Mxfp4LinearWs, layer_norm_bwd,
+               layer_norm_fwd, layer_norm_workspace_len, mxfp4_linear_apply, mxfp4_linear_bwd,
+               mxfp4_linear_fwd, mxfp4_quantize, swiglu_bwd, swiglu_fwd)
 
 SCALINGS = ("dynamic", "delayed", "rowwise")
 
@@ -468,3 +476,387 @@ class GradScaler:
     def state(self):
         """(scale, growth tracker, non-finite flag), read from the device."""
         return self.get_scale(), int(self._tracker.item()), int(self._found.item())
+
+
+# ------------------------------------------- MXFP4 linears, gated activation, norm
+# Each as a pair of registered operators, forward and backward, with fresh
+# outputs (torch.compile keeps them as opaque calls).  Workspaces are taken from
+# torch's allocator on the current stream, so calls on several streams share
+# nothing.
+
+MX_RULES = {"floor": MX_FLOOR, "fit": MX_FIT}
+_MX_DTYPES = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _u8(like, n):
+    return like.new_empty(n, dtype=torch.uint8)
+
+
+def _mx_bytes(rows, k):
+    nk = -(-k // 256)
+    return rows * 128 * nk, -(-rows // 32) * 256 * nk
+
+
+@torch.library.custom_op("fp8sg::mxfp4_linear_fwd", mutates_args=())
+def _op_mx_fwd(x: torch.Tensor, w: torch.Tensor, rule: int, save: bool) -> tuple[
+        torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    M, K = x.shape
+    N = w.shape[0]
+    y = x.new_empty((M, N))
+    saved = Mxfp4LinearSaved(M, N, K, x.device) if save else None
+    mxfp4_linear_fwd(x, w, Mxfp4LinearWs(M, N, K, x.device, backward=False), saved, y, rule)
+    return (y,) + (saved.tensors() if save else tuple(_u8(x, 0) for _ in range(4)))
+
+
+@_op_mx_fwd.register_fake
+def _op_mx_fwd_fake(x, w, rule, save):
+    M, K = x.shape
+    N = w.shape[0]
+    sizes = _mx_bytes(K, M) + _mx_bytes(K, N) if save else (0, 0, 0, 0)
+    return (x.new_empty((M, N)),) + tuple(_u8(x, n) for n in sizes)
+
+
+@torch.library.custom_op("fp8sg::mxfp4_linear_bwd", mutates_args=())
+def _op_mx_bwd(gy: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, K: int,
+               rule: int, need_x: bool, need_w: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    M, N = gy.shape
+    saved = Mxfp4LinearSaved(M, N, K, gy.device, tensors=(xq, xs, wq, ws))
+    gx = gy.new_empty((M, K) if need_x else (0,))
+    gw = gy.new_empty((N, K) if need_w else (0,))
+    mxfp4_linear_bwd(gy, Mxfp4LinearWs(M, N, K, gy.device, forward=False), saved, gx if need_x else None,
+                     gw if need_w else None, rule)
+    return gx, gw
+
+
+@_op_mx_bwd.register_fake
+def _op_mx_bwd_fake(gy, xq, xs, wq, ws, K, rule, need_x, need_w):
+    M, N = gy.shape
+    return gy.new_empty((M, K) if need_x else (0,)), gy.new_empty((N, K) if need_w else (0,))
+
+
+def _mx_setup(ctx, inputs, output):
+    x, _w, rule, save = inputs
+    ctx.dims, ctx.rule, ctx.saved = (x.shape[1],), rule, save
+    ctx.save_for_backward(*output[1:])
+    ctx.set_materialize_grads(False)
+
+
+def _mx_backward(ctx, gy, *_unused):
+    need_x, need_w = ctx.needs_input_grad[:2]
+    if gy is None or not (need_x or need_w):
+        return None, None, None, None
+    if not ctx.saved:
+        raise RuntimeError("this MXFP4 linear ran without saving for a backward pass")
+    gx, gw = torch.ops.fp8sg.mxfp4_linear_bwd(gy.contiguous(), *ctx.saved_tensors, ctx.dims[0], ctx.rule, need_x, need_w)
+    return gx if need_x else None, gw if need_w else None, None, None
+
+
+_op_mx_fwd.register_autograd(_mx_backward, setup_context=_mx_setup)
+
+
+def _mx_rule(rule):
+    if rule not in MX_RULES:
+        raise ValueError(f"rule must be one of {tuple(MX_RULES)}, not {rule!r}")
+    return rule
+
+
+class MXFP4Linear(nn.Module):
+    """nn.Linear (no bias) whose forward, input-gradient and weight-gradient
+    products run in MXFP4: every operand is quantised in blocks of 32 along the
+    dimension its product contracts.  Kept for the backward pass are the 4-bit
+    x^T and W^T, not the inputs.  Weights, inputs and gradients share one dtype
+    (bf16, fp16 or fp32); any sizes.
+
+    rule: how a block's scale follows from its largest value, "floor" (the MX
+    specification's, which saturates the top of some blocks) or "fit" (no
+    saturation)."""
+
+    def __init__(self, in_features: int, out_features: int, rule: str = "floor", device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if dtype not in _MX_DTYPES:
+            raise TypeError(f"MXFP4Linear takes bf16, fp16 or fp32, not {dtype}")
+        self.in_features, self.out_features, self.rule = in_features, out_features, _mx_rule(rule)
+        self.weight = nn.Parameter(torch.empty((out_features, in_features), dtype=dtype, device=device))
+
+    @classmethod
+    def from_float(cls, lin: nn.Linear, rule: str = "floor") -> "MXFP4Linear":
+        """An MXFP4Linear sharing lin's weight tensor (no copy)."""
+        if lin.bias is not None:
+            raise ValueError("MXFP4Linear has no bias")
+        if lin.weight.dtype not in _MX_DTYPES:
+            raise TypeError(f"MXFP4Linear needs a bf16, fp16 or fp32 weight, got {lin.weight.dtype}")
+        with torch.device("meta"):
+            new = cls(lin.in_features, lin.out_features, rule, dtype=lin.weight.dtype)
+        new.weight = lin.weight
+        return new
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dtype != self.weight.dtype:
+            raise TypeError(f"MXFP4Linear takes inputs of its weight's dtype {self.weight.dtype}")
+        x2d = x.reshape(-1, self.in_features).contiguous()
+        save = torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad)
+        y = torch.ops.fp8sg.mxfp4_linear_fwd(x2d, self.weight.contiguous(), MX_RULES[self.rule], save)[0]
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, out_features={self.out_features}, rule={self.rule}"
+
+
+class PackedMXFP4Linear(nn.Module):
+    """A linear for serving: the weight is held as MXFP4 (17/32 byte a value) and
+    only inputs are quantised, for a few tokens in the product's own launch.
+    No gradients."""
+
+    def __init__(self, in_features: int, out_features: int, rule: str = "floor", device=None):
+        super().__init__()
+        self.in_features, self.out_features, self.rule = in_features, out_features, _mx_rule(rule)
+        nq, ns = _mx_bytes(out_features, in_features)
+        self.register_buffer("weight_q", torch.zeros(nq, dtype=torch.uint8, device=device))
+        self.register_buffer("weight_s", torch.zeros(ns, dtype=torch.uint8, device=device))
+
+    @classmethod
+    def from_float(cls, lin: nn.Module, rule: str = "floor") -> "PackedMXFP4Linear":
+        """The packed form of an nn.Linear's or MXFP4Linear's weight."""
+        if getattr(lin, "bias", None) is not None:
+            raise ValueError("PackedMXFP4Linear has no bias")
+        w = lin.weight.detach()
+        new = cls(w.shape[1], w.shape[0], rule, device=w.device)
+        mxfp4_quantize(w.contiguous(), new._packed(), rule=MX_RULES[new.rule])
+        return new
+
+    def _packed(self):
+        return Mxfp4(self.out_features, self.in_features, tensors=(self.weight_q, self.weight_s))
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        x2d = x.reshape(-1, self.in_features).contiguous()
+        y = x2d.new_empty((x2d.shape[0], self.out_features))
+        mxfp4_linear_apply(x2d, self._packed(), y, Mxfp4(x2d.shape[0], self.in_features, x.device),
+                           MX_RULES[self.rule])
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, out_features={self.out_features}, rule={self.rule}"
+
+
+def _mx_filter(mod: nn.Linear, fqn: str) -> bool:
+    """As default_module_filter, without its rules on sizes (MXFP4 takes any)."""
+    return (mod.bias is None and mod.weight.dtype in _MX_DTYPES and
+            fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES)
+
+
+def _replace_linears(model, accept, make):
+    for parent, attr, child, path in list(_descendants_post_order(model, ())):
+        if type(child) in (nn.Linear, MXFP4Linear) and accept(child, ".".join(path)):
+            setattr(parent, attr, make(child))
+    return model
+
+
+def convert_to_mxfp4_training(model: nn.Module,
+                              module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
+                              rule: str = "floor") -> nn.Module:
+    """convert_to_float8_training's walk with MXFP4Linear: every nn.Linear child
+    that module_filter_fn accepts (default: no bias, not an output head or a
+    router by name) is replaced in place by one that shares its weight."""
+    accept = module_filter_fn or _mx_filter
+    return _replace_linears(model, lambda m, fqn: type(m) is nn.Linear and accept(m, fqn),
+                            lambda m: MXFP4Linear.from_float(m, rule))
+
+
+def convert_to_mxfp4_serving(model: nn.Module,
+                             module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
+                             rule: str = "floor") -> nn.Module:
+    """Replace, in place, every nn.Linear and MXFP4Linear child that the filter
+    accepts by a PackedMXFP4Linear holding its quantised weight."""
+    return _replace_linears(model, module_filter_fn or
+                            (lambda m, fqn: fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES and
+                             getattr(m, "bias", None) is None),
+                            lambda m: PackedMXFP4Linear.from_float(m, rule))
+
+
+# ---- gated activation
+
+def _rows_of(t):
+    """t with contiguous rows that may be apart, as the kernels read them (a
+    column range of a matrix stays as it is)."""
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t
+    return t.contiguous()
+
+
+@torch.library.custom_op("fp8sg::swiglu_fwd", mutates_args=())
+def _op_swiglu_fwd(g: torch.Tensor, u: torch.Tensor, save: bool) -> tuple[
+        torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    rows, cols = g.shape
+    a = g.new_empty((rows, cols))
+    c = [Act8(rows, cols, g.device) for _ in range(2)] if save else [None, None]
+    swiglu_fwd(g, u, a, *c)
+    return (a,) + (c[0].tensors() + c[1].tensors() if save else tuple(_u8(g, 0) for _ in range(4)))
+
+
+@_op_swiglu_fwd.register_fake
+def _op_swiglu_fwd_fake(g, u, save):
+    rows, cols = g.shape
+    n = -(-cols // 32)
+    shapes = ((rows, 32 * n), (rows, n)) * 2 if save else ((0,),) * 4
+    return (g.new_empty((rows, cols)),) + tuple(_u8(g, s) for s in shapes)
+
+
+@torch.library.custom_op("fp8sg::swiglu_bwd", mutates_args=())
+def _op_swiglu_bwd(da: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, uq: torch.Tensor,
+                   us: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    rows, cols = da.shape
+    dg, du = torch.empty_like(da), torch.empty_like(da)
+    swiglu_bwd(da, Act8(rows, cols, tensors=(gq, gs)), Act8(rows, cols, tensors=(uq, us)), dg, du)
+    return dg, du
+
+
+@_op_swiglu_bwd.register_fake
+def _op_swiglu_bwd_fake(da, gq, gs, uq, us):
+    return torch.empty_like(da), torch.empty_like(da)
+
+
+@torch.library.custom_op("fp8sg::swiglu_bwd_plain", mutates_args=())
+def _op_swiglu_bwd_plain(da: torch.Tensor, g: torch.Tensor, u: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    dg, du = torch.empty_like(da), torch.empty_like(da)
+    swiglu_bwd(da, g, u, dg, du)
+    return dg, du
+
+
+@_op_swiglu_bwd_plain.register_fake
+def _op_swiglu_bwd_plain_fake(da, g, u):
+    return torch.empty_like(da), torch.empty_like(da)
+
+
+def _swiglu_setup(ctx, inputs, output):
+    g, u, save = inputs
+    ctx.save_for_backward(*(output[1:] if save else (g, u)))
+    ctx.set_materialize_grads(False)
+
+
+def _swiglu_backward(ctx, da, *_unused):
+    if da is None:
+        return None, None, None
+    op = torch.ops.fp8sg.swiglu_bwd if len(ctx.saved_tensors) == 4 else torch.ops.fp8sg.swiglu_bwd_plain
+    return (*op(da.contiguous(), *ctx.saved_tensors), None)
+
+
+_op_swiglu_fwd.register_autograd(_swiglu_backward, setup_context=_swiglu_setup)
+
+
+class SwiGLU(nn.Module):
+    """silu(gate) * up.  checkpoint: keep both for the backward pass as 8-bit
+    blocks (33/32 bytes a value) instead of themselves; the result is the same,
+    the gradients are those at the kept values.  gate and up may be the two
+    halves of one projection's output."""
+
+    def __init__(self, checkpoint: bool = True):
+        super().__init__()
+        self.checkpoint = checkpoint
+
+    def forward(self, gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
+        if gate.shape != up.shape or gate.dtype != up.dtype:
+            raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype} and up {tuple(up.shape)} {up.dtype} differ")
+        if gate.dim() < 1:
+            raise ValueError("SwiGLU takes at least one dimension")
+        cols = gate.shape[-1]
+        g, u = (_rows_of(t if t.dim() == 2 else t.reshape(-1, cols) if t.numel() else t.reshape(0, cols))
+                for t in (gate, up))
+        save = self.checkpoint and torch.is_grad_enabled() and (gate.requires_grad or up.requires_grad)
+        return torch.ops.fp8sg.swiglu_fwd(g, u, save)[0].reshape(gate.shape)
+
+    def extra_repr(self):
+        return f"checkpoint={self.checkpoint}"
+
+
+# ---- layer norm
+
+@torch.library.custom_op("fp8sg::layer_norm_fwd", mutates_args=())
+def _op_ln_fwd(x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor], eps: float, save: bool) -> tuple[
+        torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    rows, cols = x.shape
+    y = torch.empty_like(x)
+    mean, rstd = (x.new_empty(rows, dtype=torch.float32) for _ in range(2))
+    c = Act8(rows, cols, x.device) if save else None
+    layer_norm_fwd(x, w, b, eps, y, mean, rstd, c)
+    return (y, mean, rstd) + (c.tensors() if save else (_u8(x, 0), _u8(x, 0)))
+
+
+@_op_ln_fwd.register_fake
+def _op_ln_fwd_fake(x, w, b, eps, save):
+    rows, cols = x.shape
+    n = -(-cols // 32)
+    st = x.new_empty(rows, dtype=torch.float32)
+    shapes = ((rows, 32 * n), (rows, n)) if save else ((0,), (0,))
+    return (torch.empty_like(x), st, torch.empty_like(st)) + tuple(_u8(x, s) for s in shapes)
+
+
+@torch.library.custom_op("fp8sg::layer_norm_bwd", mutates_args=())
+def _op_ln_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], xq: Optional[torch.Tensor], xs: Optional[torch.Tensor],
+               w: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor, need: int,
+               pdtype: torch.dtype) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    rows, cols = dy.shape
+    dx = torch.empty_like(dy) if need & 1 else dy.new_empty(0)
+    dw, db = (dy.new_empty(cols if need & m else 0, dtype=pdtype) for m in (2, 4))
+    ws = dy.new_empty(layer_norm_workspace_len(rows, cols), dtype=torch.float32) if need & 6 else None
+    layer_norm_bwd(dy, Act8(rows, cols, tensors=(xq, xs)) if x is None else x, w, mean, rstd,
+                   dx if need & 1 else None, dw if need & 2 else None, db if need & 4 else None, ws)
+    return dx, dw, db
+
+
+@_op_ln_bwd.register_fake
+def _op_ln_bwd_fake(dy, x, xq, xs, w, mean, rstd, need, pdtype):
+    cols = dy.shape[1]
+    return (torch.empty_like(dy) if need & 1 else dy.new_empty(0),
+            dy.new_empty(cols if need & 2 else 0, dtype=pdtype), dy.new_empty(cols if need & 4 else 0, dtype=pdtype))
+
+
+def _ln_setup(ctx, inputs, output):
+    x, w, b, _eps, save = inputs
+    _y, mean, rstd, xq, xs = output
+    ctx.kept = save
+    ctx.pdtype = w.dtype if w is not None else b.dtype if b is not None else x.dtype
+    ctx.save_for_backward(w, mean, rstd, *((xq, xs) if save else (x,)))
+    ctx.mark_non_differentiable(mean, rstd, xq, xs)
+    ctx.set_materialize_grads(False)
+
+
+def _ln_backward(ctx, dy, *_unused):
+    need = sum(m for m, f in zip((1, 2, 4), ctx.needs_input_grad) if f)
+    if dy is None or not need:
+        return None, None, None, None, None
+    w, mean, rstd, *kept = ctx.saved_tensors
+    x, xq, xs = (None, *kept) if ctx.kept else (kept[0], None, None)
+    got = torch.ops.fp8sg.layer_norm_bwd(dy.contiguous(), x, xq, xs, w, mean, rstd, need, ctx.pdtype)
+    return (*(t if need & m else None for t, m in zip(got, (1, 2, 4))), None, None)
+
+
+_op_ln_fwd.register_autograd(_ln_backward, setup_context=_ln_setup)
+
+
+class LayerNorm(nn.Module):
+    """Layer norm over the last dimension, with its own forward and backward
+    kernels.  Parameters are of the data's dtype or fp32.  checkpoint: keep the
+    input for the backward pass as 8-bit blocks instead of itself (mean and rstd
+    are kept in fp32 either way)."""
+
+    def __init__(self, normalized_shape: int, eps: float = 1e-5, elementwise_affine: bool = True, bias: bool = True,
+                 checkpoint: bool = False, device=None, dtype=torch.float32):
+        super().__init__()
+        if normalized_shape < 1:
+            raise ValueError(f"normalized_shape must be at least 1, not {normalized_shape}")
+        self.normalized_shape, self.eps, self.checkpoint = normalized_shape, eps, checkpoint
+        kw = dict(device=device, dtype=dtype)
+        self.weight = nn.Parameter(torch.ones(normalized_shape, **kw)) if elementwise_affine else None
+        self.bias = nn.Parameter(torch.zeros(normalized_shape, **kw)) if elementwise_affine and bias else None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[-1:] != (self.normalized_shape,):
+            raise ValueError(f"LayerNorm over {self.normalized_shape} values got {tuple(x.shape)}")
+        x2d = x.reshape(-1, self.normalized_shape).contiguous()
+        needs = any(t is not None and t.requires_grad for t in (x, self.weight, self.bias))
+        save = self.checkpoint and torch.is_grad_enabled() and needs
+        return torch.ops.fp8sg.layer_norm_fwd(x2d, self.weight, self.bias, self.eps, save)[0].reshape(x.shape)
+
+    def extra_repr(self):
+        return f"{self.normalized_shape}, eps={self.eps}, checkpoint={self.checkpoint}"

@@ -76,7 +76,7 @@ def test_linear_validation():
     assert L.mxfp4_linear_fwd(A, A, 0, 4, 4, 64, 0, P(mx._LinWs(OFFPAIR, PAIR, PAIR, PAIR)), None, A, 0, None) == EALIGN
     assert L.mxfp4_linear_fwd(A, A, 0, 4, 4, 64, 0, P(ws), P(sv), None, 0, None) == ENULL
     assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), None, A, A, 0, None) == ENULL
-    assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), P(sv), None, A, 0, None) == ENULL
+    assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), P(sv), None, None, 0, None) == ENULL
     assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), P(sv), A, A + 1, 0, None) == EALIGN
     assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(mx._LinWs(PAIR, PAIR, PAIR, NOPAIR)), P(sv), A, A, 0, None) == ENULL
     assert L.mxfp4_linear_bwd(A, 0, -4, 4, 64, 0, P(ws), P(sv), A, A, 0, None) == ESHAPE

@@ -1,0 +1,64 @@
+"""Module conversion for the MXFP4 layers, on the CPU (no kernel runs here)."""
+import pytest
+import torch
+from torch import nn
+
+from fp8_scaled_gemm_amd.nn import (LayerNorm, MXFP4Linear, PackedMXFP4Linear, SwiGLU,
+                                    convert_to_mxfp4_training)
+
+
+class Block(nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.norm = LayerNorm(40, dtype=torch.bfloat16)
+        self.gate = nn.Linear(40, 72, bias=False, dtype=torch.bfloat16)
+        self.up = nn.Linear(40, 72, bias=False, dtype=torch.bfloat16)
+        self.down = nn.Linear(72, 40, bias=False, dtype=torch.bfloat16)
+        self.lm_head = nn.Linear(40, 11, bias=False, dtype=torch.bfloat16)
+        self.biased = nn.Linear(40, 8, dtype=torch.bfloat16)
+
+
+def test_training_conversion_shares_weights_and_keeps_heads():
+    m = nn.ModuleDict({"a": Block(), "b": Block()})
+    before = {n: p for n, p in m.named_parameters()}
+    convert_to_mxfp4_training(m, rule="fit")
+    for blk in m.values():
+        assert all(type(getattr(blk, n)) is MXFP4Linear for n in ("gate", "up", "down"))
+        assert type(blk.lm_head) is nn.Linear and type(blk.biased) is nn.Linear
+        assert blk.gate.rule == "fit"
+    after = {n: p for n, p in m.named_parameters()}
+    assert before.keys() == after.keys() and all(before[n] is after[n] for n in before)
+
+
+def test_filter_is_asked_with_the_full_name():
+    m = nn.ModuleDict({"a": Block(), "b": Block()})
+    seen = []
+    convert_to_mxfp4_training(m, lambda mod, fqn: seen.append(fqn) or fqn == "a.gate")
+    assert type(m["a"].gate) is MXFP4Linear and type(m["b"].gate) is nn.Linear
+    assert "b.lm_head" in seen and len(seen) == 10
+
+
+def test_packed_buffers_are_in_the_state():
+    p = PackedMXFP4Linear(300, 40)
+    sd = p.state_dict()
+    assert sd["weight_q"].shape == (40 * 256,) and sd["weight_s"].shape == (2 * 2 * 256,)
+    PackedMXFP4Linear(300, 40).load_state_dict(sd)
+
+
+def test_refusals():
+    with pytest.raises(ValueError, match="bias"):
+        MXFP4Linear.from_float(nn.Linear(4, 4, dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="weight"):
+        MXFP4Linear.from_float(nn.Linear(4, 4, bias=False, dtype=torch.float64))
+    with pytest.raises(ValueError, match="rule"):
+        MXFP4Linear(4, 4, rule="ceil")
+    with pytest.raises(TypeError, match="dtype"):
+        MXFP4Linear(4, 4)(torch.zeros(2, 4))
+    with pytest.raises(ValueError, match="differ"):
+        SwiGLU()(torch.zeros(2, 4), torch.zeros(2, 5))
+    with pytest.raises(ValueError, match="at least 1"):
+        LayerNorm(0)
+    with pytest.raises(ValueError, match="over 8"):
+        LayerNorm(8)(torch.zeros(2, 4))
+    with pytest.raises(ValueError, match="bias"):
+        PackedMXFP4Linear.from_float(nn.Linear(4, 4))
