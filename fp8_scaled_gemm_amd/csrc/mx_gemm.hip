@@ -61,12 +61,16 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
 // 2 t + 1, group 1 a phase later.
 //
 // LDS (136 KB): two slots of A and of B (32 KB each) and of their scales (2 KB
-// each).  Group 0 loads A of t + 1 at the start of its memory phase for t (that
-// slot's tile t - 1 was last read in phase 2 t - 1).  Group 1 loads B of t + 2
-// into B's slot of t during its compute phase for t (last read in phase 2 t + 1,
-// by group 1 itself), one load between every few products, so that the issue
-// hides behind the matrix pipe.  Either way a load has two phases to land; it is
-// waited for by the wave that issued it before the swap ahead of its first read.
+// each).  Loads are issued in memory phases only (issued between products they
+// held the products up: a k-tile took 3400 cycles, 2x00 so).  In its memory
+// phase for t,
+//   - group 0 loads B and all scales of t + 1: that slot's t - 1 was last read
+//     in phase 2 t - 1, by group 1;
+//   - group 1 loads its own half of A of t + 1, whose slot it last read in phase
+//     2 t - 1, and group 0's half of A of t + 2, whose slot (that of t) group 0
+//     last read in phase 2 t.
+// Each has two phases or more to land; the wave that issued a load waits for it
+// before the swap ahead of its first read.
 template <int OUT>
 __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   constexpr int BM = 256, BN = 256, kTM = 8, kTN = 4;
@@ -87,26 +91,39 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   tile_of(nbm, nbn, tm, tn);
   const int64_t bm = (int64_t)tm * BM, bn = (int64_t)tn * BN;
 
-  // This group's operand: group 0 stages A, group 1 stages B.  The descriptors
-  // span the rows (and 128-row scale groups) that exist: the rest reads as zero.
-  const int64_t row0 = grp ? bn : bm, rows = (grp ? N : M) - row0;
-  const uint8_t* q0 = (grp ? p.B.q : p.A.q) + row0 * pitch;
-  const uint8_t* s0 = (grp ? p.B.s : p.A.s) + (row0 >> 5) * (int64_t)nk * 256;
-  const i32x4 rq = make_rsrc(q0, (rows < 256 ? rows : 256) * (int64_t)pitch);
-  const i32x4 rs = make_rsrc(s0, (rows < 256 ? (rows + 31) / 32 : 8) * (int64_t)nk * 256);
-  // Load i of wave q: rows 64 q + 8 i + lane / 8, one 16-byte chunk a lane; the
-  // row's swizzle takes two values, for even and odd i.
-  const int lr = lane >> 3;
-  const uint32_t vo0 = (uint32_t)((64 * wq + lr) * pitch + 16 * ((lane & 7) ^ swz16(lr)));
-  const uint32_t vo1 = (uint32_t)((64 * wq + lr) * pitch + 16 * ((lane & 7) ^ swz16(8 + lr)));
-  auto issue = [&](int i, int kt, uint32_t dst) {
-    const uint32_t sb = kt < nk ? (uint32_t)(8 * i * pitch + kt * 128) : kOob;
-    lds_dma16_split(dst + (wq * 8 + i) * 1024, (i & 1) ? vo1 : vo0, sb, rq);
+  // This group's operand: group 0 stages B, group 1 stages A.  The descriptors
+  // span the rows (and 32-row scale groups) that exist: the rest reads as zero.
+  const int64_t row0 = grp ? bm : bn, rows = (grp ? M : N) - row0;
+  const i32x4 rq = make_rsrc((grp ? p.A.q : p.B.q) + row0 * pitch, (rows < 256 ? rows : 256) * (int64_t)pitch);
+  // scales, by group 0: A's by waves 0 and 1, B's by waves 2 and 3, four groups
+  // of 32 rows (256 bytes each) a wave
+  const bool of_a = wq < 2;
+  const int64_t srow = of_a ? bm : bn, sleft = (of_a ? M : N) - srow;
+  const i32x4 rs = make_rsrc((of_a ? p.A.s : p.B.s) + (srow >> 5) * (int64_t)nk * 256,
+                             (sleft < 256 ? (sleft + 31) / 32 : 8) * (int64_t)nk * 256);
+  const uint32_t vos = (uint32_t)((4 * (wq & 1) + (lane >> 4)) * nk * 256 + (lane & 15) * 16);
+  // A load moves 8 rows, one 16-byte chunk a lane; the row's swizzle takes two
+  // values, for even and odd multiples of 8.  Wave q starts at row 64 q of B's
+  // 256, or at row 32 q of each half of A.
+  const int lr = lane >> 3, r0 = (grp ? 32 : 64) * wq + lr;
+  const uint32_t vo0 = (uint32_t)(r0 * pitch + 16 * ((lane & 7) ^ swz16(lr)));
+  const uint32_t vo1 = (uint32_t)(r0 * pitch + 16 * ((lane & 7) ^ swz16(8 + lr)));
+  // rows from 8 i (+ 128 h): loads [wave][i] of a slot; past the last k-tile, zeros
+  auto issue = [&](int i, int h, int kt, uint32_t dst) {
+    const uint32_t sb = kt < nk ? (uint32_t)((8 * i + 128 * h) * pitch + kt * 128) : kOob;
+    lds_dma16_split(dst, (i & 1) ? vo1 : vo0, sb, rq);
   };
-  // waves 0 and 1: four groups of 32 rows each, 256 bytes apiece
-  const uint32_t vos = (uint32_t)((4 * wq + (lane >> 4)) * nk * 256 + (lane & 15) * 16);
-  auto issue_scales = [&](int kt, uint32_t dst) {
-    if (wq < 2) lds_dma16_split(dst + wq * 1024, vos, kt < nk ? (uint32_t)kt * 256 : kOob, rs);
+  auto issue_b = [&](int kt, uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(i, 0, kt, slot + (wq * 8 + i) * 1024);
+  };
+  auto issue_a = [&](int h, int kt, uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) issue(i, h, kt, slot + (16 * h + wq * 4 + i) * 1024);
+  };
+  auto issue_scales = [&](int kt, int slot) {  // sS: A0, A1, B0, B1
+    lds_dma16_split(lds_u32(sS) + (of_a ? 0 : 4096) + slot * 2048 + (wq & 1) * 1024, vos,
+                    kt < nk ? (uint32_t)kt * 256 : kOob, rs);
   };
   auto barrier = [&]() {
     __builtin_amdgcn_s_barrier();
@@ -122,16 +139,12 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   uint32_t sa[4], sb[2];
 
   if (grp == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) issue(i, 0, lds_u32(sA0));
-    issue_scales(0, lds_u32(sS));
+    issue_b(0, lds_u32(sB0));
+    issue_scales(0, 0);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) issue(i, 0, lds_u32(sB0));
-    issue_scales(0, lds_u32(sS) + 4096);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) issue(i, 1, lds_u32(sB1));
-    issue_scales(1, lds_u32(sS) + 6144);
+    issue_a(0, 0, lds_u32(sA0));
+    issue_a(1, 0, lds_u32(sA0));
+    issue_a(0, 1, lds_u32(sA1));
   }
   wait_vmcnt<0>();
   barrier();
@@ -143,10 +156,11 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
     const uint8_t* a = P ? sA1 : sA0;
     const uint8_t* b = P ? sB1 : sB0;
     if (grp == 0) {
-      const uint32_t d = lds_u32(P ? sA0 : sA1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) issue(i, t + 1, d);
-      issue_scales(t + 1, lds_u32(sS) + (P ? 0 : 2048));
+      issue_b(t + 1, lds_u32(P ? sB0 : sB1));
+      issue_scales(t + 1, 1 - P);
+    } else {
+      issue_a(1, t + 1, lds_u32(P ? sA0 : sA1));
+      issue_a(0, t + 2, lds_u32(P ? sA1 : sA0));
     }
 #pragma unroll
     for (int j = 0; j < kTN; ++j) {
@@ -165,7 +179,7 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
       af[i][1] = *reinterpret_cast<const uint4*>(a + lds_off2(r, fchunk + 1));
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    if (grp == 1) wait_vmcnt<0>();       // B of t + 1 has landed
+    if (grp == 1) wait_vmcnt<8>();       // group 0's half of A of t + 1 has landed
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     static_for<2>([&](auto kk) {
@@ -176,16 +190,17 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
           constexpr int J = decltype(jc)::value;
           acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J][KK], af[I][KK], acc[I][J], sb[J / 2], sa[I / 2]);
         });
-        if constexpr (KK == 0) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (grp == 1) issue(I, t + 2, lds_u32(P ? sB1 : sB0));
-          __builtin_amdgcn_sched_barrier(0);
-        }
       });
     });
-    if (grp == 1) issue_scales(t + 2, lds_u32(sS) + 4096 + 2048 * P);
+    // The products stay in this phase: without this use of their results (no
+    // instruction) the compiler sank them past the swap below, where both
+    // groups then computed at once.
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
     __builtin_amdgcn_sched_barrier(0);
-    if (grp == 0) wait_vmcnt<0>();  // A of t + 1 has landed
+    if (grp == 0) wait_vmcnt<0>();  // B and the scales of t + 1 have landed
+    else wait_vmcnt<4>();           // so has group 1's half of A of t + 1
     barrier();
   };
   for (int t = 0;;) {
