@@ -86,6 +86,16 @@ def _type(t, name):
     return ty
 
 
+def _same(t, name, dtype, shape):
+    """t is a contiguous tensor of this dtype and shape (_need names what differs)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape=shape)
+
+
 def _rule(rule):
     if rule not in (MX_FLOOR, MX_FIT):
         raise ValueError(f"rule must be MX_FLOOR or MX_FIT, not {rule!r}")
@@ -420,25 +430,20 @@ def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, strea
 
 # --------------------------------------------------------------------- layer norm
 
-def _params(like, cols, **named):
-    """The parameter dtype: that of the data or float32, the same for all."""
-    dtype = None
-    for name, t in named.items():
+def _params(like, cols, *named):
+    """Type code of the parameters (name, tensor): the data's dtype or float32,
+    the same for all that are given."""
+    dtype, shape = None, (cols,)
+    for name, t in named:
         if t is None:
             continue
-        _type(t, name)
-        if t.dtype not in (like.dtype, torch.float32) or (dtype is not None and t.dtype != dtype):
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or like.dtype} (or float32 for all parameters)")
-        dtype = t.dtype
-        _need(t, name, dtype, shape=(cols,))
-        _here(t)
+        if dtype is None:
+            _type(t, name)
+            dtype = t.dtype
+        if dtype is not like.dtype and dtype is not torch.float32 or t.dtype is not dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype} (or float32 for all parameters)")
+        _same(t, name, dtype, shape)
     return _TYPE[dtype or like.dtype]
-
-
-def _stats(mean, rstd, rows):
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _need(t, name, torch.float32, numel=rows)
-        _here(t)
 
 
 def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None, rstd=None, ckpt: Act8 = None,
@@ -447,18 +452,19 @@ def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None
     mean and rstd (float32, one per row) and ckpt (an 8-bit copy of x) are
     written for the backward."""
     rows, cols = _matrix(x, "x")
-    _need(y, "y", x.dtype, shape=x.shape)
-    _here(x, y)
-    pt = _params(x, cols, w=w, b=b)
+    _same(y, "y", x.dtype, x.shape)
+    pt = _params(x, cols, ("w", w), ("b", b))
     if mean is not None or rstd is not None:
-        _stats(mean, rstd, rows)
+        _same(mean, "mean", torch.float32, (rows,))
+        _same(rstd, "rstd", torch.float32, (rows,))
     p = None
     if ckpt is not None:
         _need_codes(ckpt, "ckpt", Act8, rows, cols)
         _here(ckpt.q, ckpt.s)
         p = ckpt.c()
-    _check(lib().layer_norm_fwd(_ptr(x), _TYPE[x.dtype], _ptr(w), _ptr(b), pt, rows, cols, eps, _ptr(y), _ptr(mean),
-                                _ptr(rstd), p, _stream(stream)), "layer_norm_fwd")
+    _here(x, y, w, b, mean, rstd)
+    _check(lib().layer_norm_fwd(x.data_ptr(), _TYPE[x.dtype], _ptr(w), _ptr(b), pt, rows, cols, eps, y.data_ptr(),
+                                _ptr(mean), _ptr(rstd), p, _stream(stream)), "layer_norm_fwd")
 
 
 def layer_norm_workspace_len(rows: int, cols: int) -> int:
@@ -470,23 +476,25 @@ def layer_norm_bwd(dy: torch.Tensor, x, w, mean, rstd, dx=None, dw=None, db=None
     """dx, dw and db (each may be None) from dy, the forward's x or its
     checkpoint (Act8), and the forward's mean and rstd."""
     rows, cols = _matrix(dy, "dy")
-    _here(dy)
     xp = cp = None
     if isinstance(x, Act8):
         _need_codes(x, "x", Act8, rows, cols)
         _here(x.q, x.s)
         cp = x.c()
     else:
-        _need(x, "x", dy.dtype, shape=dy.shape)
+        _same(x, "x", dy.dtype, dy.shape)
         _here(x)
-        xp = _ptr(x)
-    pt = _params(dy, cols, w=w, dw=dw, db=db)
-    _stats(mean, rstd, rows)
+        xp = x.data_ptr()
+    pt = _params(dy, cols, ("w", w), ("dw", dw), ("db", db))
+    _same(mean, "mean", torch.float32, (rows,))
+    _same(rstd, "rstd", torch.float32, (rows,))
     if dx is not None:
-        _need(dx, "dx", dy.dtype, shape=dy.shape)
+        _same(dx, "dx", dy.dtype, dy.shape)
+    n = 0
     if ws is not None:
+        n = ws.numel()
         _need(ws, "ws", torch.float32)
-    _here(dx, ws)
-    _check(lib().layer_norm_bwd(_ptr(dy), xp, cp, _TYPE[dy.dtype], _ptr(w), pt, _ptr(mean), _ptr(rstd), rows,
-                                cols, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
-                                _stream(stream)), "layer_norm_bwd")
+    _here(dy, w, mean, rstd, dx, dw, db, ws)
+    _check(lib().layer_norm_bwd(dy.data_ptr(), xp, cp, _TYPE[dy.dtype], _ptr(w), pt, mean.data_ptr(), rstd.data_ptr(),
+                                rows, cols, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), n, _stream(stream)),
+           "layer_norm_bwd")
