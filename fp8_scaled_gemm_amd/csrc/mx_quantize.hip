@@ -57,22 +57,19 @@ __device__ __forceinline__ uint32_t row_codes(const Row8<T>& r, uint32_t s) {
   }
   return s == 255u ? 0u : d;
 }
-// Column J of rows R .. R + 7 to a dword of codes.
-template <int T, int J, int R>
-__device__ __forceinline__ uint32_t col_codes(const Row8<T> (&v)[16], float sc) {
+// Column J of rows R .. R + 2 L - 1 to L bytes of codes (L = 2 or 4).
+template <int T, int J, int R, int L, int N>
+__device__ __forceinline__ uint32_t col_codes(const Row8<T> (&v)[N], float sc) {
   uint32_t d = 0;
-  if constexpr (T == FP8SG_OUT_F32) {
-    d = put_pair32<0>(d, v[R].w[J], v[R + 1].w[J], sc);
-    d = put_pair32<1>(d, v[R + 2].w[J], v[R + 3].w[J], sc);
-    d = put_pair32<2>(d, v[R + 4].w[J], v[R + 5].w[J], sc);
-    d = put_pair32<3>(d, v[R + 6].w[J], v[R + 7].w[J], sc);
-  } else {
-    constexpr uint32_t sel = (J & 1) ? 0x07060302u : 0x05040100u;  // the column's half of two rows
-    d = put_pair<T, 0>(d, __builtin_amdgcn_perm(v[R + 1].w[J / 2], v[R].w[J / 2], sel), sc);
-    d = put_pair<T, 1>(d, __builtin_amdgcn_perm(v[R + 3].w[J / 2], v[R + 2].w[J / 2], sel), sc);
-    d = put_pair<T, 2>(d, __builtin_amdgcn_perm(v[R + 5].w[J / 2], v[R + 4].w[J / 2], sel), sc);
-    d = put_pair<T, 3>(d, __builtin_amdgcn_perm(v[R + 7].w[J / 2], v[R + 6].w[J / 2], sel), sc);
-  }
+  static_for<L>([&](auto bc) {
+    constexpr int B = decltype(bc)::value, r = R + 2 * B;
+    if constexpr (T == FP8SG_OUT_F32) {
+      d = put_pair32<B>(d, v[r].w[J], v[r + 1].w[J], sc);
+    } else {
+      constexpr uint32_t sel = (J & 1) ? 0x07060302u : 0x05040100u;  // the column's half of two rows
+      d = put_pair<T, B>(d, __builtin_amdgcn_perm(v[r + 1].w[J / 2], v[r].w[J / 2], sel), sc);
+    }
+  });
   return d;
 }
 
@@ -82,27 +79,28 @@ struct MxQuantArgs {
   int32_t fit;
 };
 
-// A block of NW waves quantises 32 NW rows x 256 columns, read once; wave w
-// holds rows 32 w .. + 31, lane l rows 16 (l / 32) .. + 15 of them and 8
-// columns from 8 (l % 32).  Then
+// A block quantises 32 G rows x 256 columns, read once: a wave holds 32 rows x
+// 8 C columns, C = 2 RL lanes across, each with RL rows x 8 columns (RL = 16: one
+// wave spans the 256 columns; RL = 4: four do).  Then
 //   - a block along a row lies in four neighbouring lanes (two DPP steps give
 //     its amax) and 32 lanes write a row's 128 bytes of codes;
-//   - a block along a column lies in lanes l and l ^ 32; the codes of a lane's
-//     8 columns x 16 rows go through LDS, so that the columns' codes leave in
-//     runs of 16 NW bytes.
+//   - a block along a column lies in lanes C apart; a lane's codes go through
+//     LDS, so that the columns' codes leave in runs of 16 G bytes.
 // Scales of both directions are gathered in LDS in their stored order.
-// Memory bound: the wider tile (NW = 8) writes whole 128-byte lines; NW = 2
-// gives small matrices more blocks.
-template <int T, int NW, bool S>
-__global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQuantArgs args) {
-  constexpr int kRows = 32 * NW;
-  // column c's codes start at tcol(c); the 16-byte pieces (NW = 8) or the
-  // columns (NW = 2) are shifted so that lanes 8 columns apart write to
+// Memory bound.  G = 8, RL = 16 writes whole 128-byte lines with the fewest
+// instructions; G = 2, RL = 4 gives small matrices four times the blocks and
+// 16 times the waves (37 x 1001 fp32, both ways: 9.2 us with RL = 16; so, less than
+// the call's 6.1 us on the host).
+template <int T, int G, int RL, bool S>
+__global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 ? 2 : 4) void k_mxq(MxQuantArgs args) {
+  constexpr int kRows = 32 * G, C = 2 * RL, kAcross = 32 / C, kThreads = 64 * G * kAcross;
+  // column c's codes start at tcol(c); the 16-byte pieces (G = 8) or the
+  // columns (G = 2) are shifted so that lanes 8 columns apart write to
   // different banks
-  auto tcol = [](int c) { return NW == 8 ? c * 128 : c * 32 + (c >> 3) * 16; };
-  __shared__ __attribute__((aligned(16))) uint8_t tq[NW == 8 ? 256 * 128 : 256 * 32 + 32 * 16];
-  __shared__ __attribute__((aligned(16))) uint8_t rs[NW * 256];  // row scales: NW groups of 256 bytes
-  __shared__ __attribute__((aligned(16))) uint8_t ts[NW * 256];  // column scales: 8 groups of 32 NW bytes
+  auto tcol = [](int c) { return G == 8 ? c * 128 : c * 32 + (c >> 3) * 16; };
+  __shared__ __attribute__((aligned(16))) uint8_t tq[G == 8 ? 256 * 128 : 256 * 32 + 32 * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t rs[G * 256];  // row scales: G groups of 256 bytes
+  __shared__ __attribute__((aligned(16))) uint8_t ts[G * 256];  // column scales: 8 groups of 32 G bytes
 
   const bool second = blockIdx.x >= args.blocks0;
   const MxQuantJob& j = args.job[second];
@@ -112,12 +110,14 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
   const int64_t r0 = rt * kRows, c0 = ct * 256;
   const bool fit = args.fit != 0;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, cc = lane & 31;
-  const int64_t c = c0 + 8 * cc, rw = r0 + 32 * wave + 16 * half;
+  // group wg of 32 rows; rows RL rg .. of it; columns 8 cc .. of the tile
+  const int tid = threadIdx.x, lane = tid & 63, wg = (tid >> 6) / kAcross, rg = lane / C;
+  const int cc = (tid >> 6) % kAcross * C + lane % C;
+  const int64_t c = c0 + 8 * cc, rw = r0 + 32 * wg + RL * rg;
   const Elem<T>* x = reinterpret_cast<const Elem<T>*>(j.x);
-  Row8<T> v[16];
+  Row8<T> v[RL];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < RL; ++i) {
     if (rw + i < j.rows && c < j.cols) {
       v[i] = load_row8<T, S>(x + (rw + i) * j.cols + c, left8(j.cols, c));
     } else {
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
   if (j.q.q) {
     const bool blk_in = (c & ~31) < j.cols;  // this lane's block of 32 exists
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < RL; ++i) {
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < Row8<T>::kW; ++e) m = mag_max<T>(m, v[i].w[e]);
@@ -136,8 +136,9 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
       m = quad_max(m);
       const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(m), fit) : 127u;
       if (rw + i < j.rows) *reinterpret_cast<uint32_t*>(j.q.q + ((rw + i) * nkc + ct) * 128 + 4 * cc) = row_codes<T>(v[i], s);
-      if ((lane & 3) == 0)  // block cc / 4 of row 16 half + i of the wave's group
-        rs[wave * 256 + ((cc >> 3) * 16 + i) * 4 + half * 2 + ((cc >> 2) & 1)] = (uint8_t)s;
+      const int row = RL * rg + i;  // of the group
+      if ((lane & 3) == 0)          // block cc / 4
+        rs[wg * 256 + ((cc >> 3) * 16 + (row & 15)) * 4 + (row >> 4) * 2 + ((cc >> 2) & 1)] = (uint8_t)s;
     }
   }
   if (j.t.q) {
@@ -146,43 +147,49 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
 #pragma unroll
     for (int e = 0; e < kM; ++e) m[e] = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < RL; ++i)
 #pragma unroll
       for (int e = 0; e < kM; ++e) m[e] = mag_max<T>(m[e], v[i].w[e]);
 #pragma unroll
-    for (int e = 0; e < kM; ++e) m[e] = mag_max<T>(m[e], (uint32_t)__shfl_xor((int)m[e], 32, kWave));
-    const bool blk_in = r0 + 32 * wave < j.rows;
+    for (int d = C; d < 64; d *= 2)
+#pragma unroll
+      for (int e = 0; e < kM; ++e) m[e] = mag_max<T>(m[e], (uint32_t)__shfl_xor((int)m[e], d, kWave));
+    const bool blk_in = r0 + 32 * wg < j.rows;
     static_for<8>([&](auto jc) {
       constexpr int J = decltype(jc)::value;
       const uint32_t code = T == FP8SG_OUT_F32 ? m[J % kM] : ((J & 1) ? m[J / 2] >> 16 : m[J / 2] & 0xFFFFu);
       const uint32_t s = blk_in ? fp4_scale(mag_bits<T>(code), fit) : 127u;
       const float sc = scale_value(s);
-      uint2 d = make_uint2(col_codes<T, J, 0>(v, sc), col_codes<T, J, 8>(v, sc));
-      if (s == 255u) d = make_uint2(0, 0);
       const int cl = 8 * cc + J;
-      const int piece = NW == 8 ? (wave ^ (cc & 7)) : wave;
-      *reinterpret_cast<uint2*>(tq + tcol(cl) + piece * 16 + half * 8) = d;
-      if (half == 0)  // block `wave` of column cl: the tile's blocks are pairs 0 .. NW / 2 - 1 here
-        ts[(cl >> 5) * (NW * 32) + ((wave >> 1) * 16 + (cl & 15)) * 4 + ((cl & 31) >> 4) * 2 + (wave & 1)] = (uint8_t)s;
+      const int piece = G == 8 ? (wg ^ (cc & 7)) : wg;
+      uint8_t* at = tq + tcol(cl) + piece * 16 + rg * (RL / 2);
+      if constexpr (RL == 16) {
+        const uint2 d = make_uint2(col_codes<T, J, 0, 4>(v, sc), col_codes<T, J, 8, 4>(v, sc));
+        *reinterpret_cast<uint2*>(at) = s == 255u ? make_uint2(0, 0) : d;
+      } else {
+        *reinterpret_cast<uint16_t*>(at) = s == 255u ? (uint16_t)0 : (uint16_t)col_codes<T, J, 0, 2>(v, sc);
+      }
+      if (rg == 0)  // block wg of column cl: the tile's blocks are pairs 0 .. G / 2 - 1 here
+        ts[(cl >> 5) * (G * 32) + ((wg >> 1) * 16 + (cl & 15)) * 4 + ((cl & 31) >> 4) * 2 + (wg & 1)] = (uint8_t)s;
     });
   }
   __syncthreads();
-  if (j.q.q && tid < 16 * NW && r0 + (tid >> 4) * 32 < j.rows)
+  if (j.q.q && tid < 16 * G && r0 + (tid >> 4) * 32 < j.rows)
     *reinterpret_cast<uint4*>(j.q.s + ((r0 / 32 + (tid >> 4)) * nkc + ct) * 256 + (tid & 15) * 16) =
         *reinterpret_cast<const uint4*>(rs + tid * 16);
   if (j.t.q) {
     // k-tile r0 / 256 of the transposed matrix, from byte (r0 % 256) / 2 on
     const int64_t kt = r0 >> 8, sub = (r0 & 255) >> 1;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {  // 256 columns x NW pieces of 16 bytes
-      const int id = p * 64 * NW + tid, cl = id / NW, k = id % NW;
-      const int piece = NW == 8 ? (k ^ ((cl >> 3) & 7)) : k;
+    for (int p = 0; p < 256 * G / kThreads; ++p) {  // 256 columns x G pieces of 16 bytes
+      const int id = p * kThreads + tid, cl = id / G, k = id % G;
+      const int piece = G == 8 ? (k ^ ((cl >> 3) & 7)) : k;
       if (c0 + cl < j.cols)
         st16<S>(j.t.q + ((c0 + cl) * nkr + kt) * 128 + sub + k * 16, *reinterpret_cast<const uint4*>(tq + tcol(cl) + piece * 16));
     }
     // 8 groups of 32 columns, of each the bytes of the tile's block pairs
-    if (tid < 16 * NW) {
-      const int grp = tid / (2 * NW), w = tid % (2 * NW);
+    if (tid < 16 * G) {
+      const int grp = tid / (2 * G), w = tid % (2 * G);
       if (c0 + grp * 32 < j.cols)
         *reinterpret_cast<uint4*>(j.t.s + (((c0 >> 5) + grp) * nkr + kt) * 256 + ((r0 & 255) >> 6) * 64 + w * 16) =
             *reinterpret_cast<const uint4*>(ts + tid * 16);
@@ -190,9 +197,9 @@ __global__ __launch_bounds__(64 * NW, T == FP8SG_OUT_F32 ? 2 : 4) void k_mxq(MxQ
   }
 }
 
-// Rows only, for matrices too small for k_mxq's tiles to fill the chip: 8
-// elements a thread, 8 rows x 256 columns a block (16 x 4096: 6.1 us with the
-// tiles' 16 rows a lane, 2.4 us so).
+// Rows only, for matrices too small for k_mxq's wide tiles to fill the chip: 8
+// elements a thread, 8 rows x 256 columns a block (16 x 4096: 6.1 us in tiles of
+// 16 rows a lane, 2.4 us so).
 template <int T>
 __global__ __launch_bounds__(256) void k_mxq_rows(MxQuantArgs args) {
   const MxQuantJob& j = args.job[0];
@@ -237,10 +244,10 @@ unsigned grid_for(int64_t n) {
 }
 // Tiles of a job: column tiles cover the padded columns; the row tiles the
 // rows, and with a transposed copy the padding of its last k-tile too.
-template <int NW>
+template <int G>
 int64_t tiles_of(const MxQuantJob& j) {
   if (j.rows == 0 || j.cols == 0 || (!j.q.q && !j.t.q)) return 0;
-  const int64_t rt = j.t.q ? mx_ktiles(j.rows) * (8 / NW) : (j.rows + 32 * NW - 1) / (32 * NW);
+  const int64_t rt = j.t.q ? mx_ktiles(j.rows) * (8 / G) : (j.rows + 32 * G - 1) / (32 * G);
   return rt * mx_ktiles(j.cols);
 }
 
@@ -258,12 +265,13 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
   const int cus = device_cus();
   return by_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    auto launch = [&](auto nw, auto st) {
-      constexpr int NW = decltype(nw)::value;
-      const int64_t b0 = tiles_of<NW>(a.job[0]), b1 = n > 1 ? tiles_of<NW>(a.job[1]) : 0;
+    auto launch = [&](auto gc, auto rl, auto st) {
+      constexpr int G = decltype(gc)::value, RL = decltype(rl)::value;
+      const int64_t b0 = tiles_of<G>(a.job[0]), b1 = n > 1 ? tiles_of<G>(a.job[1]) : 0;
       if (b0 + b1 == 0) return hipSuccess;
       a.blocks0 = (uint32_t)b0;
-      hipLaunchKernelGGL((k_mxq<T, NW, decltype(st)::value>), dim3((unsigned)(b0 + b1)), dim3(64 * NW), 0, stream, a);
+      hipLaunchKernelGGL((k_mxq<T, G, RL, decltype(st)::value>), dim3((unsigned)(b0 + b1)), dim3(64 * G * (16 / RL)), 0,
+                         stream, a);
       return hipGetLastError();
     };
     if (wide < cus && n == 1 && !a.job[0].t.q) {
@@ -273,9 +281,11 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
       return hipGetLastError();
     }
     // a wide tile per compute unit, or the narrow ones
-    if (wide < cus) return launch(std::integral_constant<int, 2>{}, std::false_type{});
-    if (bytes >= kStreamBytes) return launch(std::integral_constant<int, 8>{}, std::true_type{});
-    return launch(std::integral_constant<int, 8>{}, std::false_type{});
+    typedef std::integral_constant<int, 16> C16;
+    typedef std::integral_constant<int, 8> C8;
+    if (wide < cus) return launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{}, std::false_type{});
+    if (bytes >= kStreamBytes) return launch(C8{}, C16{}, std::true_type{});
+    return launch(C8{}, C16{}, std::false_type{});
   });
 }
 

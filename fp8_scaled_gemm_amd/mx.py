@@ -190,6 +190,8 @@ class Act8:
 
 
 def _need_codes(m, name, kind, rows, cols):
+    if m.__class__ is kind and m.rows == rows and (m.k if kind is Mxfp4 else m.cols) == cols:
+        return
     if not isinstance(m, kind):
         raise TypeError(f"{name}: expected {kind.__name__}, got {type(m).__name__}")
     got = (m.rows, m.k) if kind is Mxfp4 else (m.rows, m.cols)
@@ -378,6 +380,8 @@ def act8_dequantize(c: Act8, y: torch.Tensor, stream=None):
 def _strided(t, name, like, rows, cols):
     """Row stride of a matrix whose rows are contiguous (a column range of a
     wider matrix qualifies); more than two dimensions must be contiguous."""
+    if t.__class__ is like.__class__ and t.dtype is like.dtype and t.shape == like.shape and t.is_contiguous():
+        return cols
     if _type(t, name) != _TYPE[like.dtype]:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype}")
     if t.shape[-1] != cols or _rows(t) != rows:
@@ -394,9 +398,9 @@ def _ckpts(cg, cu, rows, cols):
         raise ValueError("both checkpoints are needed, or none")
     if cg is None:
         return None, None
-    for c, name in ((cg, "g's checkpoint"), (cu, "u's checkpoint")):
-        _need_codes(c, name, Act8, rows, cols)
-        _here(c.q, c.s)
+    _need_codes(cg, "g's checkpoint", Act8, rows, cols)
+    _need_codes(cu, "u's checkpoint", Act8, rows, cols)
+    _here(cg.q, cg.s, cu.q, cu.s)
     return cg.c(), cu.c()
 
 
