@@ -80,7 +80,7 @@ const char* fp8sg_status_string(int status) {
   }
 }
 
-int fp8sg_version(void) { return 100; }
+int fp8sg_version(void) { return 200; }
 
 fp8sg_status fp8_linear_copies(int64_t M, int64_t N, int64_t K, int32_t* x_T, int32_t* w_T,
                                int32_t* gy_T) {

@@ -263,7 +263,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_bwd(LayerNormArg
   }
 }
 
-// The sum of `parts` partial rows: 32 columns a block, 32 threads down each
+// The sum of `parts` partial rows: 32 columns at a time, 32 threads down each
 // column, then a tree.
 template <int P>
 __global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
@@ -271,18 +271,22 @@ __global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
   const int cl = threadIdx.x & 31, k = threadIdx.x >> 5;
   const bool bias = blockIdx.y != 0;
   void* out = bias ? p.db : p.dw;
-  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
-  float s = 0.f;
-  if (out && c < p.cols)
-    for (int i = k; i < parts; i += 32) s += p.ws[((int64_t)i * 2 + bias) * p.cols + c];
-  red[k][cl] = s;
-  __syncthreads();
+  if (!out) return;
+  for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < p.cols; c0 += (int64_t)gridDim.x * 32) {
+    const int64_t c = c0 + cl;
+    float s = 0.f;
+    if (c < p.cols)
+      for (int i = k; i < parts; i += 32) s += p.ws[((int64_t)i * 2 + bias) * p.cols + c];
+    red[k][cl] = s;
+    __syncthreads();
 #pragma unroll
-  for (int h = 16; h > 0; h >>= 1) {
-    if (k < h) red[k][cl] += red[k + h][cl];
+    for (int h = 16; h > 0; h >>= 1) {
+      if (k < h) red[k][cl] += red[k + h][cl];
+      __syncthreads();
+    }
+    if (k == 0 && c < p.cols) reinterpret_cast<Elem<P>*>(out)[c] = from_f32<P>(red[0][cl]);
     __syncthreads();
   }
-  if (k == 0 && out && c < p.cols) reinterpret_cast<Elem<P>*>(out)[c] = from_f32<P>(red[0][cl]);
 }
 
 // ---- rows past kMaxCols: the same sums, the row read again for each
@@ -439,7 +443,10 @@ void by_width(int64_t cols, F f) {
 // gradients.
 constexpr int64_t kDirectRows = 8;
 int64_t parts_of(int64_t rows, int64_t cols) {
-  if (cols > kMaxCols) return 64;
+  if (cols > kMaxCols) {
+    const int64_t n = (rows + 7) / 8;
+    return n < 1 ? 1 : n < 64 ? n : 64;
+  }
   const int64_t per_block = cols <= 1024 ? 4 : 1;
   if (rows <= kDirectRows * per_block) return 1;
   const int64_t n = (rows + 4 * per_block - 1) / (4 * per_block);
@@ -496,7 +503,7 @@ hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, int type, int ptype, hi
     if (a.ckpt.q) run(std::true_type{});
     else run(std::false_type{});
     if (wb && (a.cols > kMaxCols || parts > 1))
-      hipLaunchKernelGGL((k_ln_join<P>), dim3((unsigned)((a.cols + 31) / 32), 2), dim3(1024), 0, stream, a, parts);
+      hipLaunchKernelGGL((k_ln_join<P>), dim3(cap((a.cols + 31) / 32, 1 << 16), 2), dim3(1024), 0, stream, a, parts);
   });
 }
 

@@ -4,6 +4,8 @@
 // l % 16 of a fragment and the 32 consecutive k of block l / 16, and one scale
 // byte for that block; products and the sums inside a block are exact, sums
 // over blocks are fp32.
+#include <atomic>
+
 #include "gemm_kernels.hpp"  // LDS staging, tile order
 #include "mx.hpp"
 
@@ -61,9 +63,7 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
 // 2 t + 1, group 1 a phase later.
 //
 // LDS (136 KB): two slots of A and of B (32 KB each) and of their scales (2 KB
-// each).  Loads are issued in memory phases only (issued between products they
-// held the products up: a k-tile took 3400 cycles, 2x00 so).  In its memory
-// phase for t,
+// each).  In its memory phase for t,
 //   - group 0 loads B and all scales of t + 1: that slot's t - 1 was last read
 //     in phase 2 t - 1, by group 1;
 //   - group 1 loads its own half of A of t + 1, whose slot it last read in phase
@@ -625,6 +625,19 @@ __global__ __launch_bounds__(64 * few_waves(4, 4, false)) void k_mx_few_pair(MxG
                                  second ? gridDim.x - blocks0 : blocks0);
 }
 
+// A kernel's dynamic LDS limit, raised once per device.
+template <class K>
+hipError_t allow_lds(K kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Waves that split nk k-tiles: as many (at most `most`) as give each the same
 // number of them, and few enough that all workgroups
 // are resident at once.
@@ -638,8 +651,8 @@ int split_waves(int64_t nk, int64_t blocks, int64_t per_wave, int64_t most) {
 template <int TM, int TN, int OUT, bool SWAP, int FT>
 hipError_t launch_few(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
   auto kern = k_mx_few<TM, TN, OUT, SWAP, FT>;
-  static const hipError_t attr =
-      hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t attr = allow_lds(kern, done);
   if (attr != hipSuccess) return attr;
   constexpr int64_t kWaveBytes = few_wave_bytes(TM, TN, FT >= 0);
   static_assert(kWaveBytes >= TN * 1024, "the join fits a wave's stages");
@@ -703,8 +716,8 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
   if (b0 > 0 && b1 > 0 && b0 + b1 <= kTiles && n0 <= kLong && n1 <= kLong)
     return by_type(out, [&](auto t) {
       auto kern = k_mx_few_pair<decltype(t)::value>;
-      static const hipError_t attr =
-          hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+      static std::atomic<uint64_t> done{0};
+      const hipError_t attr = allow_lds(kern, done);
       if (attr != hipSuccess) return attr;
       const int64_t W = n0 > n1 ? n0 : n1;
       static_assert(kLong <= few_waves(4, 4, false), "a wave a k-tile");

@@ -248,15 +248,18 @@ class Mxfp4LinearSaved:
         t = tensors or (None, None, None, None)
         self.x_qT = Mxfp4(K, M, device, t[0:2] if tensors else None)
         self.w_qT = Mxfp4(K, N, device, t[2:4] if tensors else None)
+        self._all = _LinSaved()
+        self._at = ctypes.addressof(self._all)
 
     def tensors(self):
         return self.x_qT.tensors() + self.w_qT.tensors()
 
     def c(self):
-        self.x_qT.c()
-        self.w_qT.c()
-        self._all = _LinSaved(self.x_qT._pair, self.w_qT._pair)
-        return ctypes.addressof(self._all)
+        for name in ("x_qT", "w_qT"):
+            m = getattr(self, name)
+            m.c()
+            setattr(self._all, name, m._pair)
+        return self._at
 
 
 class Mxfp4LinearWs:
@@ -269,15 +272,16 @@ class Mxfp4LinearWs:
         self.w_q = Mxfp4(N, K, device) if forward else None
         self.gy_q = Mxfp4(M, N, device) if backward else None
         self.gy_qT = Mxfp4(N, M, device) if backward else None
+        self._all = _LinWs()
+        self._at = ctypes.addressof(self._all)
 
     def c(self):
-        pairs = []
-        for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT):
+        for name in ("x_q", "w_q", "gy_q", "gy_qT"):
+            m = getattr(self, name)
             if m is not None:
                 m.c()
-            pairs.append(m._pair if m is not None else _Pair())
-        self._all = _LinWs(*pairs)
-        return ctypes.addressof(self._all)
+                setattr(self._all, name, m._pair)
+        return self._at
 
 
 def _linear(obj, kind, name, dims, fields):
