@@ -4,6 +4,7 @@
 // l % 16 of a fragment and the 32 consecutive k of block l / 16, and one scale
 // byte for that block; products and the sums inside a block are exact, sums
 // over blocks are fp32.
+#include <algorithm>
 #include <atomic>
 
 #include "gemm_kernels.hpp"  // LDS staging, tile order
@@ -398,8 +399,6 @@ __device__ __forceinline__ void lds_dma4(uint32_t lds, uint32_t voff, i32x4 rsrc
 // straight into registers put 16 rows in 16 neighbouring lanes, which the
 // address coalescer takes one at a time: 24 tokens, 4096 x 14336, 12.8 us; with
 // 8 lanes a row through LDS 7.9 us.)
-// SWAP: the operands have changed places (few columns): C is written
-// transposed, element (m, n) of the product at C[n * M + m].
 // FT >= 0: operand A is not quantised yet (its up to kFusedRows rows, of element
 // type FT, are x): a wave first quantises what its k-tiles need of x into LDS.
 // Consecutive tiles go to one XCD: two of them may share a row group's scales.
@@ -422,7 +421,7 @@ constexpr int few_waves(int tm, int tn, bool fused) {
 }
 
 // blk of blocks: this workgroup's place among the problem's.
-template <int TM, int TN, int OUT, bool SWAP, int FT>
+template <int TM, int TN, int OUT, int FT>
 __device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& ap, int64_t blk, int64_t blocks) {
   constexpr bool kFused = FT >= 0;
   constexpr int kStage = few_stage(TM, TN, kFused), kOwn = few_own(kFused);
@@ -587,7 +586,7 @@ __device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t n = bn + 16 * j + 4 * g + e;
-          if (n < N) C[SWAP ? n * M + m : m * N + n] = from_f32<OUT>(acc[i][j][e]);
+          if (n < N) C[m * N + n] = from_f32<OUT>(acc[i][j][e]);
         }
     }
     return;
@@ -601,27 +600,27 @@ __device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& 
     for (int j = 0; j < TN; ++j) *reinterpret_cast<v4f*>(red + ((wave * TN + j) * 64 + lane) * 4) = acc[i][j];
     __syncthreads();
     for (int e = threadIdx.x; e < 256 * TN; e += blockDim.x) {
-      const int ml = SWAP ? e % 16 : e / (16 * TN), nl = SWAP ? e / 16 : e % (16 * TN);
+      const int ml = e / (16 * TN), nl = e % (16 * TN);
       const int64_t m = bm + 16 * i + ml, n = bn + nl;
       if (m >= M || n >= N) continue;
       const float* src = red + ((nl >> 4) * 64 + ((nl & 15) >> 2) * 16 + ml) * 4 + (nl & 3);
       float v = 0.f;
       for (int w = 0; w < W; ++w) v += src[w * TN * 256];
-      C[SWAP ? n * M + m : m * N + n] = from_f32<OUT>(v);
+      C[m * N + n] = from_f32<OUT>(v);
     }
   }
 }
 
-template <int TM, int TN, int OUT, bool SWAP, int FT>
+template <int TM, int TN, int OUT, int FT>
 __global__ __launch_bounds__(64 * few_waves(TM, TN, (FT >= 0))) void k_mx_few(MxGemmProblem p, MxApply ap) {
-  few_tile<TM, TN, OUT, SWAP, FT>(p, ap, blockIdx.x, gridDim.x);
+  few_tile<TM, TN, OUT, FT>(p, ap, blockIdx.x, gridDim.x);
 }
 // Two small products in one launch: the first `blocks0` workgroups' and the rest's.
 template <int OUT>
-__global__ __launch_bounds__(64 * few_waves(4, 4, false)) void k_mx_few_pair(MxGemmProblem p0, MxGemmProblem p1, int blocks0) {
+__global__ __launch_bounds__(64 * few_waves(1, 1, false)) void k_mx_few_pair(MxGemmProblem p0, MxGemmProblem p1, int blocks0) {
   const bool second = (int)blockIdx.x >= blocks0;
   const MxGemmProblem p = second ? p1 : p0;
-  few_tile<4, 4, OUT, false, -1>(p, MxApply{}, second ? blockIdx.x - blocks0 : blockIdx.x,
+  few_tile<1, 1, OUT, -1>(p, MxApply{}, second ? blockIdx.x - blocks0 : blockIdx.x,
                                  second ? gridDim.x - blocks0 : blocks0);
 }
 
@@ -648,9 +647,9 @@ int split_waves(int64_t nk, int64_t blocks, int64_t per_wave, int64_t most) {
   const int64_t per = (nk + most - 1) / most;
   return (int)((nk + per - 1) / per);
 }
-template <int TM, int TN, int OUT, bool SWAP, int FT>
+template <int TM, int TN, int OUT, int FT>
 hipError_t launch_few(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
-  auto kern = k_mx_few<TM, TN, OUT, SWAP, FT>;
+  auto kern = k_mx_few<TM, TN, OUT, FT>;
   static std::atomic<uint64_t> done{0};
   const hipError_t attr = allow_lds(kern, done);
   if (attr != hipSuccess) return attr;
@@ -661,15 +660,32 @@ hipError_t launch_few(const MxGemmProblem& p, const MxApply& ap, hipStream_t str
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), W * kWaveBytes, stream, p, ap);
   return hipGetLastError();
 }
-// At most 64 rows: as many row blocks as there are; two column blocks a tile
-// (each fragment of A then serves two) where enough tiles are left.
-template <int OUT, bool SWAP>
-hipError_t launch_rows(const MxGemmProblem& p, hipStream_t stream) {
-  const bool pairs = (p.N + 31) / 32 >= device_cus();
-  const MxApply none{};
-  if (p.M <= 16) return pairs ? launch_few<1, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<1, 1, OUT, SWAP, -1>(p, none, stream);
-  if (p.M <= 32) return pairs ? launch_few<2, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<2, 1, OUT, SWAP, -1>(p, none, stream);
-  return pairs ? launch_few<4, 2, OUT, SWAP, -1>(p, none, stream) : launch_few<4, 1, OUT, SWAP, -1>(p, none, stream);
+// Estimated time (us) of a product in workgroup tiles of 16 TM x 16 TN whose
+// waves split K: rounds of resident workgroups, each a fixed part (start, join,
+// stores) and one part per k-tile of a wave; or the fixed part and the operands'
+// way through L2, or from memory.  The constants are fits to products of 1 to
+// 1600 rows, 8 to 14336 columns and K of 500 to 14336 in every tile shape (us,
+// measured: 200 x 200 x 14336, tiles of 16 5.5, 32 8.0, 64 19.1, 128 37.7; 128 x
+// 4096 x 14336: 22.8, 15.0, 20.5, 38.8; 1600 x 1600 x 6000: 68, 34, 39.5, 20.1; one
+// token, 14336 x 4096: 7.3, 7.7, 9.2, 12.5).
+struct FewCost {
+  double fixed, step;
+};
+double few_cost(const MxGemmProblem& p, int tm, int tn, FewCost c, int cus) {
+  const int64_t nk = mx_ktiles(p.K), per_wave = few_wave_bytes(tm, tn, false);
+  const int64_t bm = (p.M + 16 * tm - 1) / (16 * tm), bn = (p.N + 16 * tn - 1) / (16 * tn), blocks = bm * bn;
+  const int64_t W = split_waves(nk, blocks, per_wave, few_waves(tm, tn, false)), per = (nk + W - 1) / W;
+  const int64_t resident = kLds / (W * per_wave) * cus, rounds = (blocks + resident - 1) / resident;
+  const double row = (double)nk * 136;  // bytes of an operand's row: codes and scales
+  const double l2 = (double)blocks * 16 * (tm + tn) * row / 20e6, hbm = (double)(p.M + p.N) * row / 5.2e6;
+  const double work = rounds * (c.fixed + per * c.step) - c.fixed;
+  return c.fixed + (work > l2 ? (work > hbm ? work : hbm) : (l2 > hbm ? l2 : hbm));
+}
+// ... and in tiles of 128 x 128, one or two workgroups a compute unit.
+double mid_cost(const MxGemmProblem& p, int cus) {
+  const int64_t nk = mx_ktiles(p.K), tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
+  if (tiles <= cus) return 2.8 + nk * (0.62 + 0.2 * tiles / cus);
+  return 2.8 + nk * 1.35 * ((tiles + 2 * cus - 1) / (2 * cus));
 }
 
 }  // namespace
@@ -685,8 +701,6 @@ hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
       return hipGetLastError();
     }
     const int cus = device_cus();
-    if (p.M <= 64 && p.M <= p.N) return launch_rows<T, false>(p, stream);
-    if (p.N <= 64) return launch_rows<T, true>(MxGemmProblem{p.B, p.A, p.C, p.N, p.M, p.K}, stream);
     // The large tiles where they occupy most of the chip (2048 x 4096 x 4096, 128
     // tiles on 256 units: 33.9 us, 24.4 us in tiles of 128; 4096^3, 256 tiles:
     // 37.1 against 43.3 us).
@@ -694,24 +708,26 @@ hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
       hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
       return hipGetLastError();
     }
-    // Tiles of 128, or of 64 with K split over a workgroup's waves: by the
-    // rounds over the chip and what a round was measured to take (us / 10):
-    // about 20 + 9 a k-tile, and 60 + 3 a k-tile (512 x 4096 x 4096: 14.3
-    // against 22.5 us; 128 x 4096 x 14336: 19.7 us in tiles of 64).
-    const int64_t nk = mx_ktiles(p.K), r128 = (tiles(128) + 2 * cus - 1) / (2 * cus), r64 = (tiles(64) + cus - 1) / cus;
-    if (p.K > 0 && 20 + 9 * nk * r128 <= r64 * (60 + 3 * nk)) {
+    const double c11 = few_cost(p, 1, 1, FewCost{2.0, 0.7}, cus), c12 = few_cost(p, 1, 2, FewCost{2.4, 0.7}, cus);
+    const double c22 = few_cost(p, 2, 2, FewCost{3.5, 0.6}, cus), c44 = few_cost(p, 4, 4, FewCost{8.8, 0.7}, cus);
+    const double few = std::min(std::min(c11, c12), std::min(c22, c44));
+    if (p.K > 0 && mid_cost(p, cus) < few) {
       hipLaunchKernelGGL((k_mx_mid<T>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
       return hipGetLastError();
     }
-    return launch_few<4, 4, T, false, -1>(p, MxApply{}, stream);
+    const MxApply none{};
+    if (few == c11) return launch_few<1, 1, T, -1>(p, none, stream);
+    if (few == c12) return launch_few<1, 2, T, -1>(p, none, stream);
+    if (few == c22) return launch_few<2, 2, T, -1>(p, none, stream);
+    return launch_few<4, 4, T, -1>(p, none, stream);
   });
 }
 
 hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1, int out, hipStream_t stream) {
-  // Where launches dominate (few tiles of 64, short contractions), both in one
+  // Where launches dominate (few tiles of 16, short contractions), both in one
   // launch (64 x 256 x 128 layer, backward call: 16.5 us as two, 13.3 us so).
-  auto tiles = [](const MxGemmProblem& p) { return ((p.M + 63) / 64) * ((p.N + 63) / 64); };
-  constexpr int64_t kTiles = 64, kLong = 4;
+  auto tiles = [](const MxGemmProblem& p) { return ((p.M + 15) / 16) * ((p.N + 15) / 16); };
+  constexpr int64_t kTiles = 512, kLong = 8;
   const int64_t b0 = tiles(p0), b1 = tiles(p1), n0 = mx_ktiles(p0.K), n1 = mx_ktiles(p1.K);
   if (b0 > 0 && b1 > 0 && b0 + b1 <= kTiles && n0 <= kLong && n1 <= kLong)
     return by_type(out, [&](auto t) {
@@ -720,9 +736,9 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
       const hipError_t attr = allow_lds(kern, done);
       if (attr != hipSuccess) return attr;
       const int64_t W = n0 > n1 ? n0 : n1;
-      static_assert(kLong <= few_waves(4, 4, false), "a wave a k-tile");
+      static_assert(kLong <= few_waves(1, 1, false), "a wave a k-tile");
       hipLaunchKernelGGL(kern, dim3((unsigned)(b0 + b1)), dim3(64 * (unsigned)(W > 0 ? W : 1)),
-                         (W > 0 ? W : 1) * few_wave_bytes(4, 4, false), stream, p0, p1, (int)b0);
+                         (W > 0 ? W : 1) * few_wave_bytes(1, 1, false), stream, p0, p1, (int)b0);
       return hipGetLastError();
     });
   const hipError_t e = launch_mx_gemm(p0, out, stream);
@@ -739,8 +755,8 @@ hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemm
       return by_type(type, [&](auto f) {
         constexpr int T = decltype(t)::value, X = decltype(f)::value;
         const MxApply ap{j.x, fit};
-        return (p.N + 31) / 32 >= device_cus() ? launch_few<1, 2, T, false, X>(p, ap, stream)
-                                               : launch_few<1, 1, T, false, X>(p, ap, stream);
+        return (p.N + 31) / 32 >= device_cus() ? launch_few<1, 2, T, X>(p, ap, stream)
+                                               : launch_few<1, 1, T, X>(p, ap, stream);
       });
     });
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
