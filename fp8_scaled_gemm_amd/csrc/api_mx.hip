@@ -141,11 +141,12 @@ fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t
     FP8SG_TRY(check_tensor(gw, N * K, out));
     j.t = ws->gy_qT;
   }
+  if (!gx && !gw) return FP8SG_OK;  // both empty: K == 0, or no rows and no outputs
   hipError_t e = launch_mx_quantize(&j, 1, type, rule == FP8SG_MX_FIT, S(stream));
   if (e != hipSuccess) return FP8SG_ERR_HIP;
   const MxGemmProblem dgrad{ws->gy_q, saved->w_qT, gx, M, K, N}, wgrad{ws->gy_qT, saved->x_qT, gw, N, K, M};
   if (gx && gw) e = launch_mx_gemm_pair(dgrad, wgrad, out, S(stream));
-  else if (gx || gw) e = launch_mx_gemm(gx ? dgrad : wgrad, out, S(stream));
+  else e = launch_mx_gemm(gx ? dgrad : wgrad, out, S(stream));
   return hip_status(e);
 }
 

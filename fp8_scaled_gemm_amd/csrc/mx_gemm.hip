@@ -637,8 +637,7 @@ hipError_t allow_lds(K kern, std::atomic<uint64_t>& done) {
 }
 
 // Waves that split nk k-tiles: as many (at most `most`) as give each the same
-// number of them, and few enough that all workgroups
-// are resident at once.
+// number of them, and few enough that all workgroups are resident at once.
 int split_waves(int64_t nk, int64_t blocks, int64_t per_wave, int64_t most) {
   if (nk < 1) return 1;
   const int64_t room = (int64_t)device_cus() * kLds / (blocks * per_wave);
@@ -699,22 +698,25 @@ hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
       hipLaunchKernelGGL((k_mx_gemm_plain<T>), dim3((unsigned)tiles(16)), dim3(64), 0, stream, p);
       return hipGetLastError();
     }
+    const MxApply none{};
+    // Nothing to add up: zeros, in the fewest workgroups of those kernels that
+    // take an empty contraction.
+    if (p.K == 0) return launch_few<4, 4, T, -1>(p, none, stream);
     const int cus = device_cus();
     // The large tiles where they occupy most of the chip (2048 x 4096 x 4096, 128
     // tiles on 256 units: 33.9 us, 24.4 us in tiles of 128; 4096^3, 256 tiles:
     // 37.1 against 43.3 us).
-    if (p.K > 0 && tiles(256) * 8 >= 5 * cus) {
+    if (tiles(256) * 8 >= 5 * cus) {
       hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
       return hipGetLastError();
     }
     const double c11 = few_cost(p, 1, 1, FewCost{2.0, 0.7}, cus), c12 = few_cost(p, 1, 2, FewCost{2.4, 0.7}, cus);
     const double c22 = few_cost(p, 2, 2, FewCost{3.5, 0.6}, cus), c44 = few_cost(p, 4, 4, FewCost{8.8, 0.7}, cus);
     const double few = std::min(std::min(c11, c12), std::min(c22, c44));
-    if (p.K > 0 && mid_cost(p, cus) < few) {
+    if (mid_cost(p, cus) < few) {
       hipLaunchKernelGGL((k_mx_mid<T>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
       return hipGetLastError();
     }
-    const MxApply none{};
     if (few == c11) return launch_few<1, 1, T, -1>(p, none, stream);
     if (few == c12) return launch_few<1, 2, T, -1>(p, none, stream);
     if (few == c22) return launch_few<2, 2, T, -1>(p, none, stream);

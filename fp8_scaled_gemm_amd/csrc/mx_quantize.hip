@@ -276,7 +276,7 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
     };
     if (wide < cus && n == 1 && !a.job[0].t.q) {
       const int64_t blocks = (a.job[0].rows + 7) / 8 * mx_ktiles(a.job[0].cols);
-      if (a.job[0].rows == 0 || a.job[0].cols == 0) return hipSuccess;
+      if (blocks == 0 || !a.job[0].q.q) return hipSuccess;
       hipLaunchKernelGGL((k_mxq_rows<T>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
       return hipGetLastError();
     }

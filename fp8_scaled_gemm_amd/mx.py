@@ -207,6 +207,8 @@ def mxfp4_quantize(x: torch.Tensor, q: Mxfp4 = None, qT: Mxfp4 = None, rule: int
     rows, cols = _matrix(x, "x")
     if q is None and qT is None:
         raise ValueError("mxfp4_quantize: q or qT is needed")
+    if q is qT:
+        raise ValueError("mxfp4_quantize: q and qT are one object, each needs its own")
     args = []
     for m, name, shape in ((q, "q", (rows, cols)), (qT, "qT", (cols, rows))):
         if m is not None:
@@ -397,11 +399,13 @@ def _strided(t, name, like, rows, cols):
     return t.stride(0) if rows > 1 else cols
 
 
-def _ckpts(cg, cu, rows, cols):
+def _ckpts(cg, cu, rows, cols, written):
     if (cg is None) != (cu is None):
         raise ValueError("both checkpoints are needed, or none")
     if cg is None:
         return None, None
+    if cg is cu and written:
+        raise ValueError("g and u need a checkpoint each")
     _need_codes(cg, "g's checkpoint", Act8, rows, cols)
     _need_codes(cu, "u's checkpoint", Act8, rows, cols)
     _here(cg.q, cg.s, cu.q, cu.s)
@@ -414,7 +418,7 @@ def swiglu_fwd(g: torch.Tensor, u: torch.Tensor, a: torch.Tensor, cg: Act8 = Non
     rows, cols = _matrix(a, "a")
     ldg, ldu = _strided(g, "g", a, rows, cols), _strided(u, "u", a, rows, cols)
     _here(g, u, a)
-    pg, pu = _ckpts(cg, cu, rows, cols)
+    pg, pu = _ckpts(cg, cu, rows, cols, True)
     _check(lib().swiglu_fwd(_ptr(g), ldg, _ptr(u), ldu, _TYPE[a.dtype], rows, cols, _ptr(a), pg, pu,
                             _stream(stream)), "swiglu_fwd")
 
@@ -426,7 +430,7 @@ def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, strea
     lddg, lddu = _strided(dg, "dg", da, rows, cols), _strided(du, "du", da, rows, cols)
     _here(da, dg, du)
     if isinstance(g, Act8) or isinstance(u, Act8):
-        pg, pu = _ckpts(g, u, rows, cols)
+        pg, pu = _ckpts(g, u, rows, cols, False)
         args = (None, 0, None, 0, pg, pu)
     else:
         ldg, ldu = _strided(g, "g", da, rows, cols), _strided(u, "u", da, rows, cols)

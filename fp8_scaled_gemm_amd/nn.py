@@ -40,6 +40,7 @@ Limits of Float8Linear: inputs and weights are bf16 or fp16; Float8Linear has no
 filter leaves biased layers alone); leading dimensions of the input are
 flattened into M; M, N, K must be multiples of 16.
 """
+import math
 from typing import Callable, Optional
 
 import torch
@@ -488,6 +489,13 @@ MX_RULES = {"floor": MX_FLOOR, "fit": MX_FIT}
 _MX_DTYPES = (torch.bfloat16, torch.float16, torch.float32)
 
 
+def _flat(x, cols, who):
+    """x, whose last dimension is cols, as a matrix (leading dimensions are rows)."""
+    if x.dim() < 1 or x.shape[-1] != cols:
+        raise ValueError(f"{who} over {cols} values got {tuple(x.shape)}")
+    return x.reshape(math.prod(x.shape[:-1]), cols)
+
+
 def _u8(like, n):
     return like.new_empty(n, dtype=torch.uint8)
 
@@ -593,7 +601,7 @@ class MXFP4Linear(nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.dtype != self.weight.dtype:
             raise TypeError(f"MXFP4Linear takes inputs of its weight's dtype {self.weight.dtype}")
-        x2d = x.reshape(-1, self.in_features).contiguous()
+        x2d = _flat(x, self.in_features, "MXFP4Linear").contiguous()
         save = torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad)
         y = torch.ops.fp8sg.mxfp4_linear_fwd(x2d, self.weight.contiguous(), MX_RULES[self.rule], save)[0]
         return y.reshape(*x.shape[:-1], self.out_features)
@@ -629,7 +637,7 @@ class PackedMXFP4Linear(nn.Module):
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        x2d = x.reshape(-1, self.in_features).contiguous()
+        x2d = _flat(x, self.in_features, "PackedMXFP4Linear").contiguous()
         y = x2d.new_empty((x2d.shape[0], self.out_features))
         mxfp4_linear_apply(x2d, self._packed(), y, Mxfp4(x2d.shape[0], self.in_features, x.device),
                            MX_RULES[self.rule])
@@ -759,9 +767,7 @@ class SwiGLU(nn.Module):
             raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype} and up {tuple(up.shape)} {up.dtype} differ")
         if gate.dim() < 1:
             raise ValueError("SwiGLU takes at least one dimension")
-        cols = gate.shape[-1]
-        g, u = (_rows_of(t if t.dim() == 2 else t.reshape(-1, cols) if t.numel() else t.reshape(0, cols))
-                for t in (gate, up))
+        g, u = (_rows_of(t if t.dim() == 2 else _flat(t, gate.shape[-1], "SwiGLU")) for t in (gate, up))
         save = self.checkpoint and torch.is_grad_enabled() and (gate.requires_grad or up.requires_grad)
         return torch.ops.fp8sg.swiglu_fwd(g, u, save)[0].reshape(gate.shape)
 
@@ -851,9 +857,7 @@ class LayerNorm(nn.Module):
         self.bias = nn.Parameter(torch.zeros(normalized_shape, **kw)) if elementwise_affine and bias else None
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if x.shape[-1:] != (self.normalized_shape,):
-            raise ValueError(f"LayerNorm over {self.normalized_shape} values got {tuple(x.shape)}")
-        x2d = x.reshape(-1, self.normalized_shape).contiguous()
+        x2d = _flat(x, self.normalized_shape, "LayerNorm").contiguous()
         needs = any(t is not None and t.requires_grad for t in (x, self.weight, self.bias))
         save = self.checkpoint and torch.is_grad_enabled() and needs
         return torch.ops.fp8sg.layer_norm_fwd(x2d, self.weight, self.bias, self.eps, save)[0].reshape(x.shape)

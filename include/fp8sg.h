@@ -1,6 +1,8 @@
 /*
  * fp8sg -- FP8 per-tensor dynamically scaled linear layer and GradScaler step
- * for AMD Instinct MI355X (gfx950).  C ABI.
+ * for AMD Instinct MI355X (gfx950), and the MXFP4 linear layer, the gated
+ * activation and the layer norm of the same transformer block (last section).
+ * C ABI.
  *
  * The operations follow these web pages (cited by title and section):
  *   [FP8-TRAIN]  "FP8训练：量化、自动微分、Torchao" (lzwjava.github.io)
@@ -601,6 +603,7 @@ FP8SG_API fp8sg_status amp_update_scale(float* scale, int32_t* growth_tracker, i
  * output matrices of this section need the alignment of their element type
  * only (2 or 4 bytes) and any row length; 16-byte aligned tensors whose rows
  * keep that alignment take the fast paths.  Codes and scales need 16 bytes.
+ * The buffers of one call do not overlap, except where swiglu_bwd says so.
  * ------------------------------------------------------------------------ */
 
 /*

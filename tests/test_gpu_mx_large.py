@@ -58,6 +58,17 @@ def test_product(M, N, K):
             R.check(C[rows, cols], want, bound, f"{rows} {cols}")
 
 
+def test_empty_contraction_of_many_outputs():
+    """2^34 outputs, all zero."""
+    M, N = 1 << 28, 64
+    C = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    C[:100], C[-100:] = 7, 7
+    F.mxfp4_gemm(F.Mxfp4(M, 0), F.Mxfp4(N, 0), C)
+    torch.cuda.synchronize()
+    for r in range(0, M, 1 << 25):
+        assert not bool(C[r:r + (1 << 25)].any())
+
+
 def test_swiglu():
     rows, cols = 70001, 32768
     g, u = fill(rows, cols, torch.bfloat16, 1), fill(rows, cols, torch.bfloat16, 2)

@@ -146,6 +146,16 @@ def test_strided_inputs_and_expanded_gradients():
     assert act(both[:0, :64], both[:0, 64:]).shape == (0, 64)
 
 
+def test_no_input_features():
+    """A sum over nothing: zeros, and a gradient of nothing."""
+    lin = MXFP4Linear(0, 24, device=DEV)
+    x = torch.zeros(5, 3, 0, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    y = lin(x)
+    assert y.shape == (5, 3, 24) and not bool(y.any())
+    y.sum().backward()
+    assert x.grad.shape == x.shape and lin.weight.grad.shape == (24, 0)
+
+
 def test_empty_batch():
     m = make()
     x = torch.empty(0, 96, device=DEV, dtype=torch.bfloat16, requires_grad=True)

@@ -80,6 +80,8 @@ def test_linear_validation():
     assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), P(sv), A, A + 1, 0, None) == EALIGN
     assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(mx._LinWs(PAIR, PAIR, PAIR, NOPAIR)), P(sv), A, A, 0, None) == ENULL
     assert L.mxfp4_linear_bwd(A, 0, -4, 4, 64, 0, P(ws), P(sv), A, A, 0, None) == ESHAPE
+    # both gradients are empty (and so NULL): nothing is enqueued, gy is not cast either
+    assert L.mxfp4_linear_bwd(A, 0, 4, 4, 0, 0, P(ws), P(sv), None, None, 0, None) == OK
 
 
 def test_swiglu_and_checkpoint_validation():
@@ -146,6 +148,14 @@ def test_binding_refuses_mismatches_before_any_call():
         F.Act8(4, 40, tensors=(torch.zeros(4, 40, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)))
     with pytest.raises(ValueError, match="elements"):
         F.Mxfp4(4, 40, tensors=(torch.zeros(4, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)))
+
+
+def test_outputs_that_would_be_one_buffer_are_refused():
+    x, m, c = torch.zeros(64, 64), F.Mxfp4(64, 64, device="cpu"), F.Act8(64, 64, device="cpu")
+    with pytest.raises(ValueError, match="each needs its own"):
+        F.mxfp4_quantize(x, m, m)
+    with pytest.raises(ValueError, match="a checkpoint each"):
+        mx._ckpts(c, c, 64, 64, True)
 
 
 @pytest.mark.parametrize("call", [

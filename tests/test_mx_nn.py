@@ -62,3 +62,11 @@ def test_refusals():
         LayerNorm(8)(torch.zeros(2, 4))
     with pytest.raises(ValueError, match="bias"):
         PackedMXFP4Linear.from_float(nn.Linear(4, 4))
+
+
+@pytest.mark.parametrize("layer", [MXFP4Linear(16, 4), PackedMXFP4Linear(16, 4)])
+@pytest.mark.parametrize("shape", [(4, 8), (0, 8), (32,), ()])
+def test_inputs_of_another_width_are_refused(layer, shape):
+    """Also where the elements would fill whole rows of the layer's width."""
+    with pytest.raises(ValueError, match="over 16"):
+        layer(torch.zeros(shape, dtype=torch.bfloat16))
