@@ -11,6 +11,11 @@
 // with its columns' sums in registers and leaves one partial row of each in
 // the workspace; a second kernel adds the partial rows.  Every sum's order
 // follows from the sizes alone, so results repeat bit for bit.
+//
+// Measured: 8192 x 4096 bf16 forward 30 us, 35 us with the checkpoint (4.9 TB/s),
+// backward from the checkpoint 38 us and the join 7; 1000 x 14336 fp16 forward 19
+// us, backward 23.5 us and the join 8.5: there the 250 partial rows are as many
+// bytes as dx.
 #include "mx.hpp"
 
 namespace fp8sg {

@@ -45,7 +45,8 @@ __device__ __forceinline__ void put4(Elem<OUT>* row, int64_t n, int64_t N, v4f v
 }
 
 // One wave per 16 x 16 block of C, fragments straight from memory, in 64-bit
-// addresses: for contractions too long for the other kernels' offsets.
+// addresses: for contractions of 2^24 values or more, too long for the other
+// kernels' offsets.  Kept simple: such a matrix has at most 2048 rows.
 template <int OUT>
 __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
@@ -90,6 +91,15 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
 //     last read in phase 2 t.
 // Each has two phases or more to land; the wave that issued a load waits for it
 // before the swap ahead of its first read.
+//
+// Bound by the matrix cores and their clock, which these products pull down to
+// 1.5 - 1.8 GHz: 8192 x 14336 x 4096 237 - 255 us (3.8 - 4.05 PFLOP/s), 8192 x 4096 x
+// 14336 194 - 213 us (4.5 - 4.96), 14336 x 4096 x 8192 212 - 245 us, 4096^3 35 - 37
+// us; the same instructions alone reach 6.3 - 6.8 PFLOP/s.  A k-tile takes about
+// 2650 cycles of which 2150 are products (the swaps and the phases' unequal
+// lengths are the rest), a tile's start and epilogue about 16000 more, a quarter
+// of the tile's time at K = 4096.  256 x 256: halving either side doubles the LDS
+// reads per product (see k_mx_mid).
 template <int OUT>
 __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   constexpr int BM = 256, BN = 256, kTM = 8, kTN = 4;
@@ -285,7 +295,9 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
 // Medium kernel: a 128 x 128 tile per workgroup of four waves (64 x 64 each), two
 // LDS stages of 256 values of K (34 KB each with the scales), so that two
 // workgroups share a compute unit and cover each other's barriers.  Its LDS
-// reads (8 fragments per 16 products) bound it at about half the matrix rate.
+// reads (8 fragments per 16 products) bound it at about half the matrix rate
+// (2048 x 2048 x 4096 16 us, 2.1 PFLOP/s; 256 x 14336 x 4096 15.5 us, 1.9), so it is
+// for products that the large tiles would leave compute units idle for.
 template <int OUT>
 __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
   constexpr int kStage = 2 * 128 * 128 + 2048;
@@ -402,7 +414,9 @@ __device__ __forceinline__ void lds_dma4(uint32_t lds, uint32_t voff, i32x4 rsrc
 // flight, so nothing waits for another wave before the join.  (Fragments loaded
 // straight into registers put 16 rows in 16 neighbouring lanes, which the
 // address coalescer takes one at a time: 24 tokens, 4096 x 14336, 12.8 us; with
-// 8 lanes a row through LDS 7.9 us.)
+// 8 lanes a row through LDS 7.9 us.)  Bound by the weight's bytes and the time to
+// get them moving: one token, 14336 x 4096, 31 MB, 6.9 us (4.5 TB/s), of which the
+// launch and the join are about 2 us.
 // FT >= 0: operand A is not quantised yet (its up to kFusedRows rows, of element
 // type FT, are x): a wave first quantises what its k-tiles need of x into LDS.
 // Consecutive tiles go to one XCD: two of them may share a row group's scales.
