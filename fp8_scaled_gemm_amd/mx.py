@@ -54,7 +54,7 @@ def _here(*tensors):
     """Every tensor is on the current device, whose stream the call uses."""
     dev = _device()
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is not None and t.get_device() != dev:  # (-1: not on a device)
             if not t.is_cuda:
                 raise ValueError("tensor arguments must be device tensors")
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}: "
@@ -242,6 +242,17 @@ def mxfp4_gemm(A: Mxfp4, B: Mxfp4, C: torch.Tensor, stream=None):
     _check(lib().mxfp4_gemm(a, b, _ptr(C), _TYPE[C.dtype], M, N, A.k, _stream(stream)), "mxfp4_gemm")
 
 
+def _inside(owner, struct):
+    """Let owner's operands keep their addresses inside `struct`, whose fields
+    have their names; the struct's address."""
+    for name, _ in struct._fields_:
+        m = getattr(owner, name)
+        if m is not None:
+            m._pair = getattr(struct, name)  # (shares the struct's memory and keeps it alive)
+            m._at = ctypes.addressof(m._pair)
+    return ctypes.addressof(struct)
+
+
 class Mxfp4LinearSaved:
     """What the forward of an M x N x K MXFP4 linear leaves for its backward."""
 
@@ -251,16 +262,14 @@ class Mxfp4LinearSaved:
         self.x_qT = Mxfp4(K, M, device, t[0:2] if tensors else None)
         self.w_qT = Mxfp4(K, N, device, t[2:4] if tensors else None)
         self._all = _LinSaved()
-        self._at = ctypes.addressof(self._all)
+        self._at = _inside(self, self._all)
 
     def tensors(self):
         return self.x_qT.tensors() + self.w_qT.tensors()
 
     def c(self):
-        for name in ("x_qT", "w_qT"):
-            m = getattr(self, name)
-            m.c()
-            setattr(self._all, name, m._pair)
+        self.x_qT.c()
+        self.w_qT.c()
         return self._at
 
 
@@ -275,14 +284,12 @@ class Mxfp4LinearWs:
         self.gy_q = Mxfp4(M, N, device) if backward else None
         self.gy_qT = Mxfp4(N, M, device) if backward else None
         self._all = _LinWs()
-        self._at = ctypes.addressof(self._all)
+        self._at = _inside(self, self._all)
 
     def c(self):
-        for name in ("x_q", "w_q", "gy_q", "gy_qT"):
-            m = getattr(self, name)
+        for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT):
             if m is not None:
                 m.c()
-                setattr(self._all, name, m._pair)
         return self._at
 
 
@@ -291,11 +298,13 @@ def _linear(obj, kind, name, dims, fields):
         raise TypeError(f"{name}: expected {kind.__name__}, got {type(obj).__name__}")
     if obj.dims != dims:
         raise ValueError(f"{name}: made for a layer of {obj.dims}, not {dims}")
+    tensors = ()
     for f in fields:
         m = getattr(obj, f)
         if m is None:
             raise ValueError(f"{name}: made without {f}")
-        _here(m.q, m.s)
+        tensors += (m.q, m.s)
+    _here(*tensors)
 
 
 def mxfp4_linear_fwd(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSaved, y: torch.Tensor,
@@ -309,7 +318,7 @@ def mxfp4_linear_fwd(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearWs, saved:
     if K2 != K:
         raise ValueError(f"w: {K2} columns, expected {K}")
     _type(y, "y")
-    _need(y, "y", y.dtype, shape=x.shape[:-1] + (N,))
+    _same(y, "y", y.dtype, x.shape[:-1] + (N,))
     _here(x, w, y)
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("x_q", "w_q"))
     sv = None
@@ -335,10 +344,10 @@ def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSave
     _type(out, "gw" if gx is None else "gx")
     need = ()
     if gx is not None:
-        _need(gx, "gx", out.dtype, shape=gy.shape[:-1] + (K,))
+        _same(gx, "gx", out.dtype, gy.shape[:-1] + (K,))
         need += ("gy_q",)
     if gw is not None:
-        _need(gw, "gw", out.dtype, shape=(N, K))
+        _same(gw, "gw", out.dtype, (N, K))
         need += ("gy_qT",)
     _here(gy, gx, gw)
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), need)
@@ -356,7 +365,7 @@ def mxfp4_linear_apply(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: Mxfp4, ru
     _need_codes(w, "w", Mxfp4, w.rows, K)
     _need_codes(ws, "ws", Mxfp4, M, K)
     _type(y, "y")
-    _need(y, "y", y.dtype, shape=x.shape[:-1] + (w.rows,))
+    _same(y, "y", y.dtype, x.shape[:-1] + (w.rows,))
     _here(x, y, w.q, w.s, ws.q, ws.s)
     wc, xc = w.c(), ws.c()
     _check(lib().mxfp4_linear_apply(_ptr(x), _TYPE[x.dtype], wc, M, w.rows, K, _rule(rule), xc, _ptr(y),

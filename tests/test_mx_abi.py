@@ -171,6 +171,22 @@ def test_host_tensors_are_refused(call):
         call(torch.zeros(4, 64))
 
 
+def test_operands_of_a_layer_lie_in_its_struct():
+    """A layer's buffers reach the library at their present addresses, also after
+    one was exchanged, and from an operand taken out of its layer."""
+    for obj in (F.Mxfp4LinearSaved(40, 24, 70, "cpu"), F.Mxfp4LinearWs(40, 24, 70, "cpu", backward=False)):
+        names = [n for n, _ in obj._all._fields_ if getattr(obj, n) is not None]
+        getattr(obj, names[0]).q = torch.zeros_like(getattr(obj, names[0]).q)
+        got = type(obj._all).from_address(obj.c())
+        for n in names:
+            m = getattr(obj, n)
+            assert (getattr(got, n).q, getattr(got, n).s) == (m.q.data_ptr(), m.s.data_ptr())
+        m = getattr(obj, names[1])
+        del obj, got
+        pair = mx._Pair.from_address(m.c())
+        assert (pair.q, pair.s) == (m.q.data_ptr(), m.s.data_ptr())
+
+
 def test_strided_rows():
     m = torch.zeros(6, 40)
     like = torch.zeros(6, 16)
