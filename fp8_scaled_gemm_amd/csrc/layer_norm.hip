@@ -12,8 +12,8 @@
 // the workspace; a second kernel adds the partial rows.  Every sum's order
 // follows from the sizes alone, so results repeat bit for bit.
 //
-// Measured: 8192 x 4096 bf16 forward 30 us, 35 us with the checkpoint (4.9 TB/s),
-// backward from the checkpoint 38 us and the join 7; 1000 x 14336 fp16 forward 19
+// Measured: 8192 x 4096 bf16 forward 30 us, 35 us with the checkpoint (4.8 TB/s),
+// backward from the checkpoint 38 us and the join 7; 1000 x 14336 fp16 forward 15.4
 // us, backward 23.5 us and the join 8.5: there the 250 partial rows are as many
 // bytes as dx.
 #include "mx.hpp"
@@ -54,7 +54,11 @@ __device__ __forceinline__ void load_params(const void* w, int64_t c, int n, flo
 }
 
 // A row per NW waves, R rows a block; V groups of 8 elements a thread: group k
-// of a row's thread t is elements 8 (t + 64 NW k) .. + 7.
+// of a row's thread t is elements 8 (t + 64 NW k) .. + 7.  With two groups the next
+// row's loads are issued before this row's sums (4000 x 14336 bf16 with checkpoint:
+// 67 us, 92 us a row at a time; 8192 x 8192: 50, 62 us; 16384 x 1024: 13.6, 17.2); with
+// one, the waves that the registers for it would cost do more (8192 x 2048: 16.3
+// us, without 15.4).
 template <int T, int P, int NW, int V>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArgs p) {
   constexpr int R = NW == 1 ? 4 : 1;
@@ -73,12 +77,24 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArg
     load_params<P>(p.b, c[k], n[k], 0.f, b[k]);
   }
   const int64_t pitch = act8_pitch(p.cols);
-  // (a wave past the last row still runs: its neighbours in the block do)
-  for (int64_t r = (int64_t)blockIdx.x * R + (NW == 1 ? threadIdx.x >> 6 : 0); r < p.rows; r += (int64_t)gridDim.x * R) {
-    const Elem<T>* x = reinterpret_cast<const Elem<T>*>(p.x) + r * p.cols;
-    float v[V][8], s = 0.f;
+  const Elem<T>* xp = reinterpret_cast<const Elem<T>*>(p.x);
+  Row8<T> next[V];
+  auto fetch = [&](int64_t r) {
+    if (r >= p.rows) return;
 #pragma unroll
-    for (int k = 0; k < V; ++k) load8<T, false>(x + c[k], n[k], v[k]);
+    for (int k = 0; k < V; ++k) next[k] = load_row8<T, false>(xp + r * p.cols + c[k], n[k]);
+  };
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t r = (int64_t)blockIdx.x * R + (NW == 1 ? threadIdx.x >> 6 : 0);
+  constexpr bool kAhead = V > 1;
+  if constexpr (kAhead) fetch(r);
+#pragma unroll 1
+  for (; r < p.rows; r += step) {
+    float v[V][8], s = 0.f;
+    if constexpr (!kAhead) fetch(r);
+#pragma unroll
+    for (int k = 0; k < V; ++k) next[k].values(v[k]);
+    if constexpr (kAhead) fetch(r + step);
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -475,8 +491,11 @@ hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, int type, int ptype, hi
     }
     by_width<false>(a.cols, [&](auto nw, auto v) {
       constexpr int NW = decltype(nw)::value, V = decltype(v)::value, R = NW == 1 ? 4 : 1;
-      // a few rows a block, so that the parameters are loaded once for them
-      const unsigned grid = cap((a.rows + R - 1) / R, 4096);
+      // Several rows a block, so that the parameters are loaded once for them:
+      // with the next row's loads ahead, as many blocks as are resident (16 waves
+      // a compute unit); else enough to cover each other's loads.
+      const int64_t most = V > 1 ? (int64_t)device_cus() * 16 / (NW == 1 ? 4 : NW) : 4096;
+      const unsigned grid = cap((a.rows + R - 1) / R, most);
       hipLaunchKernelGGL((k_ln_fwd<T, P, NW, V>), dim3(grid), dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
     });
   });
