@@ -13,8 +13,8 @@
 // follows from the sizes alone, so results repeat bit for bit.
 //
 // Measured: 8192 x 4096 bf16 forward 30 us, 35 us with the checkpoint (4.8 TB/s),
-// backward from the checkpoint 38 us and the join 7; 1000 x 14336 fp16 forward 15.4
-// us, backward 23.5 us and the join 8.5: there the 250 partial rows are as many
+// backward from the checkpoint 38 us and the join 5; 1000 x 14336 fp16 forward 15.4
+// us, backward 23.5 us and the join 7: there the 250 partial rows are as many
 // bytes as dx.
 #include "mx.hpp"
 
@@ -285,7 +285,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_bwd(LayerNormArg
 }
 
 // The sum of `parts` partial rows: 32 columns at a time, 32 threads down each
-// column, then a tree.
+// column with eight loads under way each (one at a time: 8192 x 1024, backward 19.9
+// us, so 16.6), then a tree.
 template <int P>
 __global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
   __shared__ float red[32][33];
@@ -296,8 +297,16 @@ __global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
   for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < p.cols; c0 += (int64_t)gridDim.x * 32) {
     const int64_t c = c0 + cl;
     float s = 0.f;
-    if (c < p.cols)
-      for (int i = k; i < parts; i += 32) s += p.ws[((int64_t)i * 2 + bias) * p.cols + c];
+    if (c < p.cols) {
+      const float* at = p.ws + (int64_t)bias * p.cols + c;
+      for (int i = k; i < parts; i += 256) {
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) v[h] = i + 32 * h < parts ? at[(int64_t)(i + 32 * h) * 2 * p.cols] : 0.f;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) s += v[h];
+      }
+    }
     red[k][cl] = s;
     __syncthreads();
 #pragma unroll
