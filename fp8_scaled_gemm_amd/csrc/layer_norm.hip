@@ -467,9 +467,9 @@ void by_width(int64_t cols, F f) {
 // the chip, few enough that writing and adding them stays small next to the
 // rows themselves (8 bytes a column and part against 4 to 12 a column and
 // row).  At most 512 of up to 4096 columns, 256 of more (backward of 8192 x 4096
-// bf16 from checkpoints: 256 parts 52 us, 512 46 us, 1024 55 us; 8192 x 8192: 82,
-// 88, 104 us), and 4 rows a block at least (1000 x 14336: 2 rows 48 us, 4 rows 34
-// us, 16 rows 54 us).  One, when the rows are few: the block then writes the
+// bf16 from checkpoints: 256 parts 53 us, 512 44 us, 1024 52 us; 8192 x 8192: 83,
+// 89, 100 us), and 4 rows a block at least (1000 x 14336: 2 rows 46 us, 4 rows 32
+// us, 8 rows 38 us).  One, when the rows are few: the block then writes the
 // gradients.
 constexpr int64_t kDirectRows = 8;
 int64_t parts_of(int64_t rows, int64_t cols) {
