@@ -12,7 +12,7 @@
 // the workspace; a second kernel adds the partial rows.  Every sum's order
 // follows from the sizes alone, so results repeat bit for bit.
 //
-// Measured: 8192 x 4096 bf16 forward 30 us, 35 us with the checkpoint (4.8 TB/s),
+// Measured: 8192 x 4096 bf16 forward 30 us, 32 - 35 us with the checkpoint (4.8 - 5.2 TB/s),
 // backward from the checkpoint 38 us and the join 5; 1000 x 14336 fp16 forward 15.4
 // us, backward 23.5 us and the join 7: there the 250 partial rows are as many
 // bytes as dx.
