@@ -242,55 +242,59 @@ def mxfp4_gemm(A: Mxfp4, B: Mxfp4, C: torch.Tensor, stream=None):
     _check(lib().mxfp4_gemm(a, b, _ptr(C), _TYPE[C.dtype], M, N, A.k, _stream(stream)), "mxfp4_gemm")
 
 
-def _inside(owner, struct):
-    """Let owner's operands keep their addresses inside `struct`, whose fields
-    have their names; the struct's address."""
-    for name, _ in struct._fields_:
-        m = getattr(owner, name)
-        if m is not None:
-            m._pair = getattr(struct, name)  # (shares the struct's memory and keeps it alive)
-            m._at = ctypes.addressof(m._pair)
-    return ctypes.addressof(struct)
+class _Operands:
+    """A layer's operands, attributes with the names of a C struct's fields; any
+    may be exchanged for another operand, e.g. for one that two layers share."""
+
+    def __init__(self, dims, struct, *operands):
+        self.__dict__.update(zip(self._names, operands), dims=dims, _all=struct, _at=ctypes.addressof(struct))
+        self._place()
+
+    def _place(self):
+        """The operands with their places in the struct, for c()."""
+        held = []
+        for name in self._names:
+            pair, m = getattr(self._all, name), getattr(self, name)
+            if m is None:
+                pair.q = pair.s = None
+            else:
+                held.append((pair, m))
+        self.__dict__["_held"] = held
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name in self._names:
+            self._place()
+
+    def c(self):
+        """Address of the C struct, holding the present operands' present addresses."""
+        for pair, m in self._held:
+            pair.q, pair.s = m.q.data_ptr(), m.s.data_ptr()
+        return self._at
 
 
-class Mxfp4LinearSaved:
+class Mxfp4LinearSaved(_Operands):
     """What the forward of an M x N x K MXFP4 linear leaves for its backward."""
+    _names = tuple(n for n, _ in _LinSaved._fields_)
 
     def __init__(self, M, N, K, device="cuda", tensors=None):
-        self.dims = (M, N, K)
         t = tensors or (None, None, None, None)
-        self.x_qT = Mxfp4(K, M, device, t[0:2] if tensors else None)
-        self.w_qT = Mxfp4(K, N, device, t[2:4] if tensors else None)
-        self._all = _LinSaved()
-        self._at = _inside(self, self._all)
+        super().__init__((M, N, K), _LinSaved(), Mxfp4(K, M, device, t[0:2] if tensors else None),
+                         Mxfp4(K, N, device, t[2:4] if tensors else None))
 
     def tensors(self):
         return self.x_qT.tensors() + self.w_qT.tensors()
 
-    def c(self):
-        self.x_qT.c()
-        self.w_qT.c()
-        return self._at
 
-
-class Mxfp4LinearWs:
+class Mxfp4LinearWs(_Operands):
     """Operands that live within one forward or backward call.  The two calls
     use different ones; calls that may overlap in time need a workspace each."""
+    _names = tuple(n for n, _ in _LinWs._fields_)
 
     def __init__(self, M, N, K, device="cuda", forward=True, backward=True):
-        self.dims = (M, N, K)
-        self.x_q = Mxfp4(M, K, device) if forward else None
-        self.w_q = Mxfp4(N, K, device) if forward else None
-        self.gy_q = Mxfp4(M, N, device) if backward else None
-        self.gy_qT = Mxfp4(N, M, device) if backward else None
-        self._all = _LinWs()
-        self._at = _inside(self, self._all)
-
-    def c(self):
-        for m in (self.x_q, self.w_q, self.gy_q, self.gy_qT):
-            if m is not None:
-                m.c()
-        return self._at
+        super().__init__((M, N, K), _LinWs(),
+                         Mxfp4(M, K, device) if forward else None, Mxfp4(N, K, device) if forward else None,
+                         Mxfp4(M, N, device) if backward else None, Mxfp4(N, M, device) if backward else None)
 
 
 def _linear(obj, kind, name, dims, fields):
