@@ -4,7 +4,8 @@ points of the same names, on the current torch stream.  Its names are those of
 the package (`import fp8_scaled_gemm_amd as F; F.mxfp4_gemm(...)`).
 
 Argument marshalling only, as in the package itself: every buffer's dtype,
-shape, strides and device are checked here, before the library is called.
+shape, strides and device are checked here, before the library is called (the
+two buffers of an operand where they are put into it, their device on each call).
 """
 import ctypes
 
@@ -130,63 +131,78 @@ def _bytes(rows, k, what, fn):
     return n
 
 
-class Mxfp4:
+class _Codes:
+    """Codes q and scales s of a matrix of fixed size (_fixed).  Either buffer may
+    be exchanged for another that fits."""
+
+    def __setattr__(self, name, value):
+        if name in self._fixed:
+            raise AttributeError(f"{name}: the size of a {type(self).__name__} is fixed")
+        if name in ("q", "s"):
+            self._fits(value, name)
+        super().__setattr__(name, value)
+
+    def tensors(self):
+        return self.q, self.s
+
+    def c(self):
+        """Address of the C struct, holding the buffers' present addresses."""
+        p = self._pair
+        p.q, p.s = self.q.data_ptr(), self.s.data_ptr()
+        return self._at
+
+
+class Mxfp4(_Codes):
     """An MXFP4 matrix, rows x k (mxfp4_operand): codes q and scales s, two
     uint8 device tensors, uninitialised until a call writes them."""
+    _fixed = ("rows", "k")
 
     def __init__(self, rows: int, k: int, device="cuda", tensors=None):
-        self.rows, self.k = rows, k
+        d = self.__dict__  # (past __setattr__: the buffers are checked or made here)
+        d["rows"], d["k"] = rows, k
         L = lib()
         nq = _bytes(rows, k, "Mxfp4", L.mxfp4_code_bytes)
         ns = _bytes(rows, k, "Mxfp4", L.mxfp4_scale_bytes)
         if tensors is None:
-            self.q = torch.empty(nq, dtype=torch.uint8, device=device)
-            self.s = torch.empty(ns, dtype=torch.uint8, device=device)
+            d["q"] = torch.empty(nq, dtype=torch.uint8, device=device)
+            d["s"] = torch.empty(ns, dtype=torch.uint8, device=device)
         else:  # the two buffers of another Mxfp4 of the same size
-            self.q, self.s = tensors
+            d["q"], d["s"] = tensors
             _need(self.q, "q", torch.uint8, numel=nq)
             _need(self.s, "s", torch.uint8, numel=ns)
 
-        self._pair = _Pair()
-        self._at = ctypes.addressof(self._pair)
+        d["_pair"] = _Pair()
+        d["_at"] = ctypes.addressof(self._pair)
 
-    def tensors(self):
-        return self.q, self.s
-
-    def c(self):
-        """Address of the C struct, holding the buffers' present addresses."""
-        p = self._pair
-        p.q, p.s = self.q.data_ptr(), self.s.data_ptr()
-        return self._at
+    def _fits(self, t, name):
+        L = lib()
+        _need(t, name, torch.uint8, numel=(L.mxfp4_code_bytes if name == "q" else L.mxfp4_scale_bytes)(self.rows, self.k))
 
 
-class Act8:
+class Act8(_Codes):
     """An 8-bit checkpoint of a rows x cols activation (fp8sg_act8)."""
+    _fixed = ("rows", "cols")
 
     def __init__(self, rows: int, cols: int, device="cuda", tensors=None):
         if rows < 0 or cols < 0:
             raise ValueError(f"Act8: {rows} x {cols}")
-        self.rows, self.cols = rows, cols
+        d = self.__dict__
+        d["rows"], d["cols"] = rows, cols
         blocks = -(-cols // 32)
         if tensors is None:
-            self.q = torch.empty((rows, 32 * blocks), dtype=torch.uint8, device=device)
-            self.s = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+            d["q"] = torch.empty((rows, 32 * blocks), dtype=torch.uint8, device=device)
+            d["s"] = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
         else:
-            self.q, self.s = tensors
+            d["q"], d["s"] = tensors
             _need(self.q, "q", torch.uint8, shape=(rows, 32 * blocks))
             _need(self.s, "s", torch.uint8, shape=(rows, blocks))
 
-        self._pair = _Pair()
-        self._at = ctypes.addressof(self._pair)
+        d["_pair"] = _Pair()
+        d["_at"] = ctypes.addressof(self._pair)
 
-    def tensors(self):
-        return self.q, self.s
-
-    def c(self):
-        """Address of the C struct, holding the buffers' present addresses."""
-        p = self._pair
-        p.q, p.s = self.q.data_ptr(), self.s.data_ptr()
-        return self._at
+    def _fits(self, t, name):
+        blocks = -(-self.cols // 32)
+        _need(t, name, torch.uint8, shape=(self.rows, 32 * blocks if name == "q" else blocks))
 
 
 def _need_codes(m, name, kind, rows, cols):
@@ -247,24 +263,32 @@ class _Operands:
     may be exchanged for another operand, e.g. for one that two layers share."""
 
     def __init__(self, dims, struct, *operands):
-        self.__dict__.update(zip(self._names, operands), dims=dims, _all=struct, _at=ctypes.addressof(struct))
+        d = self.__dict__
+        d.update(zip(self._names, operands))
+        d["dims"], d["_all"], d["_at"] = dims, struct, ctypes.addressof(struct)
         self._place()
 
     def _place(self):
         """The operands with their places in the struct, for c()."""
-        held = []
+        held = self.__dict__["_held"] = []
         for name in self._names:
             pair, m = getattr(self._all, name), getattr(self, name)
-            if m is None:
-                pair.q = pair.s = None
-            else:
+            if m is not None:
                 held.append((pair, m))
-        self.__dict__["_held"] = held
+            elif pair.q:
+                pair.q = pair.s = None
 
     def __setattr__(self, name, value):
-        super().__setattr__(name, value)
+        if name == "dims":
+            raise AttributeError("dims: the operands were made for these sizes")
         if name in self._names:
+            if value is not None:
+                M, N, K = self.dims
+                _need_codes(value, name, Mxfp4, *self._shapes(M, N, K)[self._names.index(name)])
+            super().__setattr__(name, value)
             self._place()
+        else:
+            super().__setattr__(name, value)
 
     def c(self):
         """Address of the C struct, holding the present operands' present addresses."""
@@ -276,6 +300,10 @@ class _Operands:
 class Mxfp4LinearSaved(_Operands):
     """What the forward of an M x N x K MXFP4 linear leaves for its backward."""
     _names = tuple(n for n, _ in _LinSaved._fields_)
+
+    @staticmethod
+    def _shapes(M, N, K):
+        return (K, M), (K, N)
 
     def __init__(self, M, N, K, device="cuda", tensors=None):
         t = tensors or (None, None, None, None)
@@ -290,6 +318,10 @@ class Mxfp4LinearWs(_Operands):
     """Operands that live within one forward or backward call.  The two calls
     use different ones; calls that may overlap in time need a workspace each."""
     _names = tuple(n for n, _ in _LinWs._fields_)
+
+    @staticmethod
+    def _shapes(M, N, K):
+        return (M, K), (N, K), (M, N), (N, M)
 
     def __init__(self, M, N, K, device="cuda", forward=True, backward=True):
         super().__init__((M, N, K), _LinWs(),
