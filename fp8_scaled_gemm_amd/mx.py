@@ -215,6 +215,37 @@ def _need_codes(m, name, kind, rows, cols):
         raise ValueError(f"{name}: {got[0]} x {got[1]}, expected {rows} x {cols}")
 
 
+def _apart(a, name_a, lda, b, name_b, ldb):
+    """Two outputs of one shape, rows lda and ldb elements apart, share no memory
+    (they may be column ranges of one matrix)."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if pb < pa:
+        pa, pb, lda, ldb = pb, pa, ldb, lda
+    n, cols = a.numel(), a.shape[-1]
+    if n == 0:
+        return
+    rows, at = n // cols, (pb - pa) // a.element_size()
+    if at >= (rows - 1) * lda + cols:
+        return
+    if lda == ldb:
+        clear = cols <= at % lda <= lda - cols
+    else:  # row i of the first against the first row of the second that ends behind its start
+        clear = True
+        for i in range(rows):
+            j = max(0, -(-(i * lda - cols + 1 - at) // ldb))
+            if j < rows and at + j * ldb < i * lda + cols:
+                clear = False
+                break
+    if not clear:
+        raise ValueError(f"{name_a} and {name_b} overlap")
+
+
+def _own_codes(a, name_a, b, name_b):
+    """Two operands that one call writes have buffers of their own."""
+    if a.q is b.q or a.s is b.s:
+        raise ValueError(f"the buffers of {name_a} and {name_b} overlap")
+
+
 # ------------------------------------------------------------------- MXFP4
 
 def mxfp4_quantize(x: torch.Tensor, q: Mxfp4 = None, qT: Mxfp4 = None, rule: int = MX_FLOOR, stream=None):
@@ -231,6 +262,8 @@ def mxfp4_quantize(x: torch.Tensor, q: Mxfp4 = None, qT: Mxfp4 = None, rule: int
             _need_codes(m, name, Mxfp4, *shape)
             _here(m.q, m.s)
         args.append(m.c() if m is not None else None)
+    if q is not None and qT is not None:
+        _own_codes(q, "q", qT, "qT")
     _here(x)
     _check(lib().mxfp4_quantize(_ptr(x), _TYPE[x.dtype], rows, cols, _rule(rule), args[0], args[1],
                                 _stream(stream)), "mxfp4_quantize")
@@ -340,6 +373,8 @@ def _linear(obj, kind, name, dims, fields):
         if m is None:
             raise ValueError(f"{name}: made without {f}")
         tensors += (m.q, m.s)
+    if len(fields) == 2 and (tensors[0] is tensors[2] or tensors[1] is tensors[3]):
+        raise ValueError(f"{name}: the buffers of {fields[0]} and {fields[1]} overlap")
     _here(*tensors)
 
 
@@ -385,11 +420,14 @@ def mxfp4_linear_bwd(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4LinearSave
     if gw is not None:
         _same(gw, "gw", out.dtype, (N, K))
         need += ("gy_qT",)
+    px, pw = _ptr(gx), _ptr(gw)
+    if px and pw and (pw - px < gx.nbytes if px <= pw else px - pw < gw.nbytes):
+        raise ValueError("gx and gw overlap")
     _here(gy, gx, gw)
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), need)
     _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
     wc, sv = ws.c(), saved.c()
-    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), wc, sv, _ptr(gx), _ptr(gw),
+    _check(lib().mxfp4_linear_bwd(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), wc, sv, px, pw,
                                   _TYPE[out.dtype], _stream(stream)), "mxfp4_linear_bwd")
 
 
@@ -453,6 +491,8 @@ def _ckpts(cg, cu, rows, cols, written):
         raise ValueError("g and u need a checkpoint each")
     _need_codes(cg, "g's checkpoint", Act8, rows, cols)
     _need_codes(cu, "u's checkpoint", Act8, rows, cols)
+    if written:
+        _own_codes(cg, "g's checkpoint", cu, "u's checkpoint")
     _here(cg.q, cg.s, cu.q, cu.s)
     return cg.c(), cu.c()
 
@@ -473,6 +513,9 @@ def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, strea
     their checkpoints (Act8)."""
     rows, cols = _matrix(da, "da")
     lddg, lddu = _strided(dg, "dg", da, rows, cols), _strided(du, "du", da, rows, cols)
+    pdg, pdu = dg.data_ptr(), du.data_ptr()
+    if abs(pdu - pdg) < 4 * rows * max(lddg, lddu):  # (farther apart they cannot overlap)
+        _apart(dg, "dg", lddg, du, "du", lddu)
     _here(da, dg, du)
     if isinstance(g, Act8) or isinstance(u, Act8):
         pg, pu = _ckpts(g, u, rows, cols, False)
@@ -481,7 +524,7 @@ def swiglu_bwd(da: torch.Tensor, g, u, dg: torch.Tensor, du: torch.Tensor, strea
         ldg, ldu = _strided(g, "g", da, rows, cols), _strided(u, "u", da, rows, cols)
         _here(g, u)
         args = (_ptr(g), ldg, _ptr(u), ldu, None, None)
-    _check(lib().swiglu_bwd(_ptr(da), *args, _TYPE[da.dtype], rows, cols, _ptr(dg), lddg, _ptr(du), lddu,
+    _check(lib().swiglu_bwd(_ptr(da), *args, _TYPE[da.dtype], rows, cols, pdg, lddg, pdu, lddu,
                             _stream(stream)), "swiglu_bwd")
 
 
@@ -511,9 +554,13 @@ def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None
     rows, cols = _matrix(x, "x")
     _same(y, "y", x.dtype, x.shape)
     pt = _params(x, cols, ("w", w), ("b", b))
+    pm = pr = None
     if mean is not None or rstd is not None:
         _same(mean, "mean", torch.float32, (rows,))
         _same(rstd, "rstd", torch.float32, (rows,))
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+        if abs(pr - pm) < 4 * rows:
+            raise ValueError("mean and rstd overlap")
     p = None
     if ckpt is not None:
         _need_codes(ckpt, "ckpt", Act8, rows, cols)
@@ -521,7 +568,7 @@ def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None
         p = ckpt.c()
     _here(x, y, w, b, mean, rstd)
     _check(lib().layer_norm_fwd(x.data_ptr(), _TYPE[x.dtype], _ptr(w), _ptr(b), pt, rows, cols, eps, y.data_ptr(),
-                                _ptr(mean), _ptr(rstd), p, _stream(stream)), "layer_norm_fwd")
+                                pm, pr, p, _stream(stream)), "layer_norm_fwd")
 
 
 def layer_norm_workspace_len(rows: int, cols: int) -> int:
@@ -547,11 +594,14 @@ def layer_norm_bwd(dy: torch.Tensor, x, w, mean, rstd, dx=None, dw=None, db=None
     _same(rstd, "rstd", torch.float32, (rows,))
     if dx is not None:
         _same(dx, "dx", dy.dtype, dy.shape)
+    pdw, pdb = _ptr(dw), _ptr(db)
+    if pdw and pdb and abs(pdb - pdw) < cols * (4 if pt == 2 else 2):
+        raise ValueError("dw and db overlap")
     n = 0
     if ws is not None:
         n = ws.numel()
         _need(ws, "ws", torch.float32)
     _here(dy, w, mean, rstd, dx, dw, db, ws)
     _check(lib().layer_norm_bwd(dy.data_ptr(), xp, cp, _TYPE[dy.dtype], _ptr(w), pt, mean.data_ptr(), rstd.data_ptr(),
-                                rows, cols, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), n, _stream(stream)),
+                                rows, cols, _ptr(dx), pdw, pdb, _ptr(ws), n, _stream(stream)),
            "layer_norm_bwd")

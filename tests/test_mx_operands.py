@@ -87,3 +87,70 @@ def test_an_exchanged_operand_is_checked():
     for name, bad in (("x_qT", F.Mxfp4(40, 70, "cpu")), ("w_qT", F.Mxfp4(24, 70, "cpu"))):
         with pytest.raises(ValueError, match=f"^{name}: "):
             setattr(saved, name, bad)
+
+
+def on_device(monkeypatch):
+    """Let host tensors through to the last check before the library, which is not reached."""
+    from fp8_scaled_gemm_amd import mx
+    monkeypatch.setattr(mx, "_here", lambda *t: None)
+    monkeypatch.setattr(mx, "_stream", lambda s: pytest.fail("went on to the library"))
+
+
+def test_two_outputs_in_one_buffer_are_refused(monkeypatch):
+    on_device(monkeypatch)
+    x, t = torch.zeros(64, 64), torch.zeros(64, 200)
+    row = torch.zeros(64)
+    one = dict(match="overlap")
+    with pytest.raises(ValueError, **one):
+        F.swiglu_bwd(x, x + 1, x + 2, t[:, :64], t[:, :64])
+    with pytest.raises(ValueError, **one):  # partly
+        F.swiglu_bwd(x, x + 1, x + 2, t[:, :64], t[:, 63:127])
+    with pytest.raises(ValueError, **one):  # the later rows of one among the other's
+        F.swiglu_bwd(x[:32], x[:32] + 1, x[:32] + 2, t[:32, :64], t[5:37, :64])
+    with pytest.raises(ValueError, **one):  # different row lengths
+        F.swiglu_bwd(x, x + 1, x + 2, t[:, :64], t.view(-1)[64 * 5:64 * 69].view(64, 64))
+    with pytest.raises(ValueError, **one):
+        F.layer_norm_bwd(x, x + 1, row, row, row, dw=row, db=row, ws=torch.zeros(1 << 16))
+    with pytest.raises(ValueError, **one):
+        F.layer_norm_fwd(x, row, row, 1e-5, x + 1, mean=row, rstd=row)
+    ws, saved = F.Mxfp4LinearWs(64, 64, 64, "cpu"), F.Mxfp4LinearSaved(64, 64, 64, "cpu")
+    g = torch.zeros(64, 64)
+    with pytest.raises(ValueError, **one):
+        F.mxfp4_linear_bwd(x, ws, saved, g, g)
+    a, b = F.Mxfp4(64, 64, "cpu"), F.Mxfp4(64, 64, "cpu")
+    for which in ("q", "s"):
+        old = getattr(b, which)
+        setattr(b, which, getattr(a, which))
+        with pytest.raises(ValueError, **one):
+            F.mxfp4_quantize(x, a, b)
+        setattr(b, which, old)
+    c, d = F.Act8(64, 64, "cpu"), F.Act8(64, 64, "cpu")
+    d.s = c.s
+    with pytest.raises(ValueError, **one):
+        F.swiglu_fwd(x, x + 1, x + 2, c, d)
+
+
+@pytest.mark.parametrize("fields", [("x_q", "w_q"), ("gy_q", "gy_qT"), ("x_qT", "w_qT")])
+def test_operands_of_one_call_in_one_buffer_are_refused(monkeypatch, fields):
+    """Of equal sizes; operands of the forward may be those of the backward."""
+    on_device(monkeypatch)
+    x = torch.zeros(64, 64)
+    ws, saved = F.Mxfp4LinearWs(64, 64, 64, "cpu"), F.Mxfp4LinearSaved(64, 64, 64, "cpu")
+    obj = saved if "x_qT" in fields else ws
+    setattr(obj, fields[1], getattr(obj, fields[0]))
+    if "gy_q" not in fields:
+        with pytest.raises(ValueError, match="overlap"):
+            F.mxfp4_linear_fwd(x, x + 1, ws, saved, x + 2)
+    if "x_q" not in fields:
+        with pytest.raises(ValueError, match="overlap"):
+            F.mxfp4_linear_bwd(x, ws, saved, x + 1, x + 2)
+
+
+def test_outputs_side_by_side_are_taken(monkeypatch):
+    from fp8_scaled_gemm_amd import mx
+    t = torch.zeros(64, 200)
+    for a, b in ((t[:, :64], t[:, 64:128]), (t[:, 64:128], t[:, :64]), (t[:, 136:], t[:, :64]), (t[:32, :64], t[32:, :64]),
+                 (t[:1, :64], t[:1, 64:128]), (t[:0, :64], t[:0, :64]), (t[:32, :100], t[32:, :100])):
+        mx._apart(a, "dg", a.stride(0), b, "du", b.stride(0))
+    mx._apart(t.view(-1)[:64 * 64].view(64, 64), "dg", 64, t.view(-1)[64 * 64:64 * 128].view(64, 64), "du", 64)
+    mx._apart(t[:0], "dg", 200, t[:0], "du", 200)
