@@ -623,10 +623,13 @@ class PackedMXFP4Linear(nn.Module):
         self.register_buffer("weight_s", torch.zeros(ns, dtype=torch.uint8, device=device))
 
     @classmethod
-    def from_float(cls, lin: nn.Module, rule: str = "floor") -> "PackedMXFP4Linear":
-        """The packed form of an nn.Linear's or MXFP4Linear's weight."""
+    def from_float(cls, lin: nn.Module, rule: Optional[str] = None) -> "PackedMXFP4Linear":
+        """The packed form of an nn.Linear's or MXFP4Linear's weight.  rule None: the
+        one an MXFP4Linear was trained with, "floor" for an nn.Linear."""
         if getattr(lin, "bias", None) is not None:
             raise ValueError("PackedMXFP4Linear has no bias")
+        if rule is None:
+            rule = lin.rule if isinstance(lin, MXFP4Linear) else "floor"
         w = lin.weight.detach()
         new = cls(w.shape[1], w.shape[0], rule, device=w.device)
         mxfp4_quantize(w.contiguous(), new._packed(), rule=MX_RULES[new.rule])
@@ -673,9 +676,10 @@ def convert_to_mxfp4_training(model: nn.Module,
 
 def convert_to_mxfp4_serving(model: nn.Module,
                              module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
-                             rule: str = "floor") -> nn.Module:
+                             rule: Optional[str] = None) -> nn.Module:
     """Replace, in place, every nn.Linear and MXFP4Linear child that the filter
-    accepts by a PackedMXFP4Linear holding its quantised weight."""
+    accepts by a PackedMXFP4Linear holding its quantised weight.  rule None: each
+    layer's own, "floor" for an nn.Linear."""
     return _replace_linears(model, module_filter_fn or
                             (lambda m, fqn: fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES and
                              getattr(m, "bias", None) is None),

@@ -270,3 +270,25 @@ def test_registered_operators_are_well_formed():
     torch.library.opcheck(torch.ops.fp8sg.mxfp4_linear_fwd, (x, w, F.MX_FLOOR, True), test_utils=("test_schema", "test_faketensor"))
     torch.library.opcheck(torch.ops.fp8sg.swiglu_fwd, (x, x + 1, True), test_utils=("test_schema",))
     torch.library.opcheck(torch.ops.fp8sg.layer_norm_fwd, (x, None, None, 1e-5, False), test_utils=("test_schema",))
+
+
+@pytest.mark.parametrize("rule", ["floor", "fit"])
+def test_serving_quantises_as_training_did(rule):
+    """The packed weight has the codes of the training layer's forward, and its
+    inputs are cast by the same rule."""
+    m = make(96, 200, rule=rule, seed=5)
+    w = {n: getattr(m, n).weight.detach() for n in ("gate", "up", "down")}
+    convert_to_mxfp4_serving(m)
+    x = torch.randn(9, 96, device=DEV, dtype=torch.bfloat16)
+    for n, weight in w.items():
+        p = getattr(m, n)
+        want = F.Mxfp4(*weight.shape)
+        F.mxfp4_quantize(weight, want, rule=F.MX_FIT if rule == "fit" else F.MX_FLOOR)
+        torch.cuda.synchronize()
+        rows = p.weight_q.numel()
+        assert torch.equal(p.weight_q, want.q) and rows == want.q.numel()
+        got, need = R.fp4_unpack(p._packed()), R.fp4_unpack(want)  # (scales of rows past the last are anyone's)
+        assert (got[1] == need[1]).all()
+    fit = rule == "fit"
+    y = m.gate(x)
+    R.check(y, *R.dot(R.fp4_values(R.f64(x), fit), R.fp4_values(R.f64(w["gate"]), fit)), "y")

@@ -70,3 +70,28 @@ def test_inputs_of_another_width_are_refused(layer, shape):
     """Also where the elements would fill whole rows of the layer's width."""
     with pytest.raises(ValueError, match="over 16"):
         layer(torch.zeros(shape, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("rule", ["floor", "fit"])
+def test_serving_keeps_the_rule_a_layer_was_trained_with(rule, monkeypatch):
+    """Unless the caller names another; an nn.Linear has none and takes "floor"."""
+    from fp8_scaled_gemm_amd import nn as N
+    used = []
+    monkeypatch.setattr(N, "mxfp4_quantize", lambda w, q, rule: used.append(rule))
+    blk = Block()
+    blk.down = MXFP4Linear.from_float(blk.down, rule)
+    want = {"gate": "floor", "down": rule}
+    N.convert_to_mxfp4_serving(blk)
+    for n in want:
+        layer = getattr(blk, n)
+        assert type(layer) is PackedMXFP4Linear and layer.rule == want[n] and f"rule={want[n]}" in repr(layer)
+    assert used.count(N.MX_FIT) == (rule == "fit")
+    lin = MXFP4Linear(16, 4, rule=rule)
+    assert PackedMXFP4Linear.from_float(lin).rule == rule
+    assert PackedMXFP4Linear.from_float(nn.Linear(16, 4, bias=False)).rule == "floor"
+    for named in ("floor", "fit"):
+        assert PackedMXFP4Linear.from_float(lin, rule=named).rule == named
+        m = nn.Sequential(MXFP4Linear(16, 4, rule=rule), nn.Linear(4, 4, bias=False))
+        assert [layer.rule for layer in N.convert_to_mxfp4_serving(m, rule=named)] == [named, named]
+    with pytest.raises(ValueError, match="rule"):
+        PackedMXFP4Linear.from_float(lin, rule="ceil")
