@@ -126,7 +126,7 @@ fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t
   if (!ws || !saved) return FP8SG_ERR_NULL;
   if (!type_ok(type) || !type_ok(out) || !rule_ok(rule)) return FP8SG_ERR_FORMAT;
   if (!mat_ok(M, K) || !mat_ok(N, K) || !mat_ok(M, N)) return FP8SG_ERR_SHAPE;
-  if (!gx && !gw && (M * K > 0 || N * K > 0)) return FP8SG_ERR_NULL;
+  if (!gx && !gw && M * K > 0 && N * K > 0) return FP8SG_ERR_NULL;  // (an empty gradient may be NULL)
   FP8SG_TRY(check_tensor(gy, M * N, type));
   MxQuantJob j{gy, M, N, {}, {}};
   if (gx) {
@@ -141,7 +141,7 @@ fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t
     FP8SG_TRY(check_tensor(gw, N * K, out));
     j.t = ws->gy_qT;
   }
-  if (!gx && !gw) return FP8SG_OK;  // both empty: K == 0, or no rows and no outputs
+  if (!gx && !gw) return FP8SG_OK;  // what is wanted is empty
   hipError_t e = launch_mx_quantize(&j, 1, type, rule == FP8SG_MX_FIT, S(stream));
   if (e != hipSuccess) return FP8SG_ERR_HIP;
   const MxGemmProblem dgrad{ws->gy_q, saved->w_qT, gx, M, K, N}, wgrad{ws->gy_qT, saved->x_qT, gw, N, K, M};

@@ -697,7 +697,7 @@ FP8SG_API fp8sg_status mxfp4_linear_fwd(const void* x, const void* w, fp8sg_out 
                                         void* y, fp8sg_out out, fp8sg_stream stream);
 
 /* gx[M,K] = gy[M,N] W and gw[N,K] = gy^T x, of type `out`, from what the forward
- * of the same sizes saved.  Either may be NULL (not wanted).  Of ws only gy_q
+ * of the same sizes saved.  Either may be NULL (not wanted, or empty).  Of ws only gy_q
  * (for gx) and gy_qT (for gw) are used. */
 FP8SG_API fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t M, int64_t N,
                                         int64_t K, fp8sg_mx_rule rule, const mxfp4_linear_ws* ws,

@@ -292,3 +292,16 @@ def test_serving_quantises_as_training_did(rule):
     fit = rule == "fit"
     y = m.gate(x)
     R.check(y, *R.dot(R.fp4_values(R.f64(x), fit), R.fp4_values(R.f64(w["gate"]), fit)), "y")
+
+
+def test_empty_batch_with_frozen_weights():
+    m = make()
+    for p in m.parameters():
+        p.requires_grad_(False)
+    x = torch.empty(2, 0, 96, device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    m(x).sum().backward()
+    assert x.grad.shape == (2, 0, 96)
+    lin = MXFP4Linear(64, 0, device=DEV)  # no outputs: the weight's gradient is empty, and the only one wanted
+    y = lin(torch.zeros(5, 64, dtype=torch.bfloat16, device=DEV))
+    y.sum().backward()
+    assert y.shape == (5, 0) and lin.weight.grad.shape == (0, 64)

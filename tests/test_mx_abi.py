@@ -227,3 +227,16 @@ def test_reference_rounding():
     a[0, :4] = [448, 17, 2.0 ** -10, -3 * 2.0 ** -10]
     assert R.act8_values(a)[0, :4].tolist() == [448, 16, 0, -2.0 ** -8]
     assert len(R.E4M3) == 127 and R.E4M3[-1] == 448
+
+
+def test_a_wanted_gradient_that_is_empty():
+    """No rows, only gx wanted, or no outputs, only gw wanted: the gradient is empty
+    and so NULL, which is no missing argument."""
+    L = F.lib()
+    ws, sv = mx._LinWs(PAIR, PAIR, PAIR, PAIR), mx._LinSaved(PAIR, PAIR)
+    assert L.mxfp4_linear_bwd(None, 0, 0, 4, 64, 0, P(ws), P(sv), None, None, 0, None) == OK
+    assert L.mxfp4_linear_bwd(None, 0, 4, 0, 64, 0, P(ws), P(sv), None, None, 0, None) == OK
+    assert L.mxfp4_linear_bwd(A, 0, 4, 4, 64, 0, P(ws), P(sv), None, None, 0, None) == ENULL
+    # the other sizes of such a call are still looked at
+    assert L.mxfp4_linear_bwd(None, 3, 0, 4, 64, 0, P(ws), P(sv), None, None, 0, None) == EFORMAT
+    assert L.mxfp4_linear_bwd(None, 0, 0, -4, 64, 0, P(ws), P(sv), None, None, 0, None) == ESHAPE
