@@ -135,6 +135,19 @@ class _Codes:
     """Codes q and scales s of a matrix of fixed size (_fixed).  Either buffer may
     be exchanged for another that fits."""
 
+    def _place(self):
+        """The C struct, for c()."""
+        d = self.__dict__
+        d["_pair"] = p = _Pair()
+        d["_at"] = ctypes.addressof(p)
+
+    def __getstate__(self):  # for copies and pickles: all but the struct of addresses
+        return {n: self.__dict__[n] for n in self._fixed + ("q", "s")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._place()
+
     def __setattr__(self, name, value):
         if name in self._fixed:
             raise AttributeError(f"{name}: the size of a {type(self).__name__} is fixed")
@@ -171,8 +184,7 @@ class Mxfp4(_Codes):
             _need(self.q, "q", torch.uint8, numel=nq)
             _need(self.s, "s", torch.uint8, numel=ns)
 
-        d["_pair"] = _Pair()
-        d["_at"] = ctypes.addressof(self._pair)
+        self._place()
 
     def _fits(self, t, name):
         L = lib()
@@ -197,8 +209,7 @@ class Act8(_Codes):
             _need(self.q, "q", torch.uint8, shape=(rows, 32 * blocks))
             _need(self.s, "s", torch.uint8, shape=(rows, blocks))
 
-        d["_pair"] = _Pair()
-        d["_at"] = ctypes.addressof(self._pair)
+        self._place()
 
     def _fits(self, t, name):
         blocks = -(-self.cols // 32)
@@ -295,11 +306,18 @@ class _Operands:
     """A layer's operands, attributes with the names of a C struct's fields; any
     may be exchanged for another operand, e.g. for one that two layers share."""
 
-    def __init__(self, dims, struct, *operands):
+    def __init__(self, dims, *operands):
         d = self.__dict__
+        struct = self._struct()
         d.update(zip(self._names, operands))
         d["dims"], d["_all"], d["_at"] = dims, struct, ctypes.addressof(struct)
         self._place()
+
+    def __getstate__(self):  # for copies and pickles: all but the struct of addresses
+        return {n: getattr(self, n) for n in self._names + ("dims",)}
+
+    def __setstate__(self, state):
+        _Operands.__init__(self, state["dims"], *(state[n] for n in self._names))
 
     def _place(self):
         """The operands with their places in the struct, for c()."""
@@ -332,7 +350,7 @@ class _Operands:
 
 class Mxfp4LinearSaved(_Operands):
     """What the forward of an M x N x K MXFP4 linear leaves for its backward."""
-    _names = tuple(n for n, _ in _LinSaved._fields_)
+    _struct, _names = _LinSaved, tuple(n for n, _ in _LinSaved._fields_)
 
     @staticmethod
     def _shapes(M, N, K):
@@ -340,7 +358,7 @@ class Mxfp4LinearSaved(_Operands):
 
     def __init__(self, M, N, K, device="cuda", tensors=None):
         t = tensors or (None, None, None, None)
-        super().__init__((M, N, K), _LinSaved(), Mxfp4(K, M, device, t[0:2] if tensors else None),
+        super().__init__((M, N, K), Mxfp4(K, M, device, t[0:2] if tensors else None),
                          Mxfp4(K, N, device, t[2:4] if tensors else None))
 
     def tensors(self):
@@ -350,14 +368,14 @@ class Mxfp4LinearSaved(_Operands):
 class Mxfp4LinearWs(_Operands):
     """Operands that live within one forward or backward call.  The two calls
     use different ones; calls that may overlap in time need a workspace each."""
-    _names = tuple(n for n, _ in _LinWs._fields_)
+    _struct, _names = _LinWs, tuple(n for n, _ in _LinWs._fields_)
 
     @staticmethod
     def _shapes(M, N, K):
         return (M, K), (N, K), (M, N), (N, M)
 
     def __init__(self, M, N, K, device="cuda", forward=True, backward=True):
-        super().__init__((M, N, K), _LinWs(),
+        super().__init__((M, N, K),
                          Mxfp4(M, K, device) if forward else None, Mxfp4(N, K, device) if forward else None,
                          Mxfp4(M, N, device) if backward else None, Mxfp4(N, M, device) if backward else None)
 

@@ -1,5 +1,9 @@
 """Operands of the MXFP4 layers and checkpoints as Python objects: what a call
 passes on is what its checks saw (no kernel runs here)."""
+import copy
+import io
+import pickle
+
 import pytest
 import torch
 
@@ -154,3 +158,47 @@ def test_outputs_side_by_side_are_taken(monkeypatch):
         mx._apart(a, "dg", a.stride(0), b, "du", b.stride(0))
     mx._apart(t.view(-1)[:64 * 64].view(64, 64), "dg", 64, t.view(-1)[64 * 64:64 * 128].view(64, 64), "du", 64)
     mx._apart(t[:0], "dg", 200, t[:0], "du", 200)
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "copy", "pickle", "save"])
+@pytest.mark.parametrize("make", [
+    lambda: F.Mxfp4(4, 300, "cpu"), lambda: F.Act8(4, 40, "cpu"), lambda: F.Mxfp4LinearSaved(40, 24, 70, "cpu"),
+    lambda: F.Mxfp4LinearWs(40, 24, 70, "cpu", forward=False), lambda: F.Mxfp4LinearWs(40, 24, 70, "cpu")])
+def test_copies_and_pickles(make, how):
+    """A copy has the sizes and the values, buffers of its own (a shallow one: the
+    same buffers) and its own place for their addresses."""
+    obj = make()
+    parts = [obj] if hasattr(obj, "q") else [m for n in obj._names if (m := getattr(obj, n)) is not None]
+    for i, m in enumerate(parts):
+        m.q.fill_(17 + i)
+        m.s.fill_(120 + i)
+    if how == "deepcopy":
+        new = copy.deepcopy(obj)
+    elif how == "copy":
+        new = copy.copy(obj)
+    elif how == "pickle":
+        new = pickle.loads(pickle.dumps(obj))
+    else:
+        f = io.BytesIO()
+        torch.save(obj, f)
+        f.seek(0)
+        new = torch.load(f, weights_only=False)
+    assert type(new) is type(obj)
+    news = [new] if hasattr(new, "q") else [m for n in new._names if (m := getattr(new, n)) is not None]
+    assert len(news) == len(parts) and getattr(new, "dims", None) == getattr(obj, "dims", None)
+    for a, b in zip(parts, news):
+        assert all(getattr(a, n) == getattr(b, n) for n in a._fixed)
+        assert torch.equal(a.q, b.q) and torch.equal(a.s, b.s)
+        assert (a.q.data_ptr() == b.q.data_ptr()) is (how == "copy")
+    assert new.c() != obj.c()
+    if not hasattr(obj, "q"):
+        assert addresses(new) == own_addresses(new) and addresses(obj) == own_addresses(obj)
+    with pytest.raises(AttributeError, match="fixed|made for"):
+        setattr(new, "dims" if hasattr(obj, "dims") else "rows", 3)
+
+
+def test_a_copy_keeps_what_its_operands_share():
+    a = F.Mxfp4LinearWs(64, 64, 64, "cpu")
+    a.gy_q = a.x_q
+    b = copy.deepcopy(a)
+    assert b.gy_q is b.x_q and b.x_q is not a.x_q and addresses(b) == own_addresses(b)
