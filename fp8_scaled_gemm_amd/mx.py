@@ -567,15 +567,15 @@ def _params(like, cols, *named):
 def layer_norm_fwd(x: torch.Tensor, w, b, eps: float, y: torch.Tensor, mean=None, rstd=None, ckpt: Act8 = None,
                    stream=None):
     """y = (x - mean) * rstd * w + b over the last dimension; w and b may be None.
-    mean and rstd (float32, one per row) and ckpt (an 8-bit copy of x) are
+    mean and rstd (float32, one value per row, in any shape) and ckpt (an 8-bit copy of x) are
     written for the backward."""
     rows, cols = _matrix(x, "x")
     _same(y, "y", x.dtype, x.shape)
     pt = _params(x, cols, ("w", w), ("b", b))
     pm = pr = None
     if mean is not None or rstd is not None:
-        _same(mean, "mean", torch.float32, (rows,))
-        _same(rstd, "rstd", torch.float32, (rows,))
+        _need(mean, "mean", torch.float32, numel=rows)
+        _need(rstd, "rstd", torch.float32, numel=rows)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
         if abs(pr - pm) < 4 * rows:
             raise ValueError("mean and rstd overlap")
@@ -608,8 +608,8 @@ def layer_norm_bwd(dy: torch.Tensor, x, w, mean, rstd, dx=None, dw=None, db=None
         _here(x)
         xp = x.data_ptr()
     pt = _params(dy, cols, ("w", w), ("dw", dw), ("db", db))
-    _same(mean, "mean", torch.float32, (rows,))
-    _same(rstd, "rstd", torch.float32, (rows,))
+    _need(mean, "mean", torch.float32, numel=rows)
+    _need(rstd, "rstd", torch.float32, numel=rows)
     if dx is not None:
         _same(dx, "dx", dy.dtype, dy.shape)
     pdw, pdb = _ptr(dw), _ptr(db)

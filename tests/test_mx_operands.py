@@ -202,3 +202,33 @@ def test_a_copy_keeps_what_its_operands_share():
     a.gy_q = a.x_q
     b = copy.deepcopy(a)
     assert b.gy_q is b.x_q and b.x_q is not a.x_q and addresses(b) == own_addresses(b)
+
+
+class Reached(Exception):
+    pass
+
+
+@pytest.mark.parametrize("shape", [(6,), (2, 3), (2, 3, 1), (1, 6)])
+def test_statistics_of_any_shape_with_one_value_a_row(shape, monkeypatch):
+    """As the leading dimensions of x, kept as a last one or not."""
+    from fp8_scaled_gemm_amd import mx
+    monkeypatch.setattr(mx, "_here", lambda *t: None)
+
+    def stream(s):
+        raise Reached
+    monkeypatch.setattr(mx, "_stream", stream)
+    x, w = torch.zeros(2, 3, 40), torch.ones(40)
+    mean, rstd = torch.zeros(shape), torch.zeros(shape)
+    with pytest.raises(Reached):
+        F.layer_norm_fwd(x, w, w, 1e-5, x + 1, mean, rstd)
+    with pytest.raises(Reached):
+        F.layer_norm_bwd(x, x + 1, w, mean, rstd, dx=x + 2)
+    for bad in (torch.zeros(5), torch.zeros(2, 3, 40), torch.zeros(2, 12)[:, ::4]):
+        for m, r in ((bad, rstd), (mean, bad)):
+            with pytest.raises(ValueError, match="^mean: |^rstd: "):
+                F.layer_norm_fwd(x, w, w, 1e-5, x + 1, m, r)
+            with pytest.raises(ValueError, match="^mean: |^rstd: "):
+                F.layer_norm_bwd(x, x + 1, w, m, r, dx=x + 2)
+    for bad in (mean.double(), None, [0.0] * 6):
+        with pytest.raises(TypeError, match="^mean: "):
+            F.layer_norm_bwd(x, x + 1, w, bad, rstd, dx=x + 2)
