@@ -23,11 +23,30 @@ namespace {
 
 constexpr int64_t kMaxCols = 16384;  // 16 waves x 64 lanes x 16 elements
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+// Sum over groups of N neighbouring lanes (N a power of two up to 64), the same in
+// each of them: quads, then mirrored halves and rows of 16, then rows and halves
+// of the wave swapped.  All on the vector unit; all lanes active.
+template <int N>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (N > 1) v = add_dpp<0xB1>(v);   // quad_perm 1 0 3 2
+  if constexpr (N > 2) v = add_dpp<0x4E>(v);   // quad_perm 2 3 0 1
+  if constexpr (N > 4) v = add_dpp<0x141>(v);  // row_half_mirror
+  if constexpr (N > 8) v = add_dpp<0x140>(v);  // row_mirror
+  if constexpr (N > 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (N > 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
   return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return lane_sum<kWave>(v); }
 // Sum over the NW waves of a row, the same in every lane.  `red`: NW floats of
 // the row's own, not in use before the last barrier; buffers alternate between
 // consecutive calls, so one barrier a call is enough.
@@ -37,10 +56,54 @@ __device__ __forceinline__ float row_sum(float v, float* red, int wave) {
   if constexpr (NW == 1) return v;
   red[wave] = v;  // every lane holds the sum: a write of one value to one address
   __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < NW; ++w) v += red[w];
-  return v;
+  return lane_sum<NW>(red[threadIdx.x & (NW - 1)]);
+}
+// The same for two sums at once; `red`: 2 NW floats.
+template <int NW>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int wave) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (NW > 1) {
+    red[wave] = a;
+    red[NW + wave] = b;
+    __syncthreads();
+    a = lane_sum<NW>(red[threadIdx.x & (NW - 1)]);
+    b = lane_sum<NW>(red[NW + (threadIdx.x & (NW - 1))]);
+  }
+}
+
+// s / n as the product with the rounded 1 / n and one correction: within half a
+// step and a little, and exact where n divides s.  (The product alone gives a row
+// of n values 1000 a mean one step off.)
+struct Count {
+  float n, inv;
+  __device__ __forceinline__ explicit Count(int64_t cols) : n((float)cols), inv(1.0f / n) {}
+  __device__ __forceinline__ float mean(float s) const {
+    const float q = s * inv;
+    return fmaf(fmaf(-q, n, s), inv, q);
+  }
+};
+
+// 1 / sqrt(v): the library's estimate (a step or two off) and one Newton step, about
+// a step off at most; as it is for 0, infinity and NaN.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return v > 0.f && v < __builtin_inff() ? fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r) : r;
+}
+
+// A row's statistics from a first mean m0 and the sums s1, s2 of the deviations
+// from it and of their squares: the mean is m0 + shift, the variance s2 / n -
+// shift^2.  A row of one value has deviations of one value, a few steps, whose
+// sum is exact: a variance of exactly 0, however its own sum rounded; and
+// deviations keep their own precision where the mean is far from zero.  The third
+// sum is paid for by adding over lanes on the vector unit (8192 x 4096 bf16 23.7
+// us, 23.9 without it and through LDS permutes; 130000 x 256 36.5 and 35.7).
+struct RowStats {
+  float shift, rstd;
+};
+__device__ __forceinline__ RowStats row_stats(float s1, float s2, const Count& n, float eps) {
+  const float shift = n.mean(s1), var = fmaf(-shift, shift, n.mean(s2));
+  return RowStats{shift, inv_sqrt((var < 0.f ? 0.f : var) + eps)};
 }
 
 template <int P>
@@ -62,10 +125,10 @@ __device__ __forceinline__ void load_params(const void* w, int64_t c, int n, flo
 template <int T, int P, int NW, int V>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArgs p) {
   constexpr int R = NW == 1 ? 4 : 1;
-  __shared__ float red[2][NW];
+  __shared__ float red[3 * NW];
   const int lane = threadIdx.x & 63, wave = NW == 1 ? 0 : threadIdx.x >> 6;
   const int t = wave * 64 + lane;
-  const float inv_n = 1.0f / (float)p.cols;
+  const Count count(p.cols);
   float w[V][8], b[V][8];
   int64_t c[V];
   int n[V];
@@ -87,6 +150,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArg
   const int64_t step = (int64_t)gridDim.x * R;
   int64_t r = (int64_t)blockIdx.x * R + (NW == 1 ? threadIdx.x >> 6 : 0);
   constexpr bool kAhead = V > 1;
+  const bool ragged = (p.cols & 7) != 0;  // (uniform)
   if constexpr (kAhead) fetch(r);
 #pragma unroll 1
   for (; r < p.rows; r += step) {
@@ -99,24 +163,6 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArg
     for (int k = 0; k < V; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[k][e];
-    const float mean = row_sum<NW>(s, red[0], wave) * inv_n;
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = v[k][e] - mean;
-        s += e < n[k] ? d * d : 0.f;
-      }
-    const float rstd = 1.0f / sqrtf(row_sum<NW>(s, red[1], wave) * inv_n + p.eps);
-    Elem<T>* y = reinterpret_cast<Elem<T>*>(p.y) + r * p.cols;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (v[k][e] - mean) * rstd * w[k][e] + b[k][e];
-      store8<T, false>(y + c[k], n[k], o);
-    }
     if (p.ckpt.q) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -127,9 +173,36 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_fwd(LayerNormArg
         }
       }
     }
+    const float m0 = count.mean(row_sum<NW>(s, red, wave));
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float m = n[k] > 0 ? m0 : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] -= m;
+      if (ragged) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] = e < n[k] ? v[k][e] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s1 += v[k][e];
+        s2 = fmaf(v[k][e], v[k][e], s2);
+      }
+    }
+    row_sum2<NW>(s1, s2, red + NW, wave);
+    const RowStats st = row_stats(s1, s2, count, p.eps);
+    Elem<T>* y = reinterpret_cast<Elem<T>*>(p.y) + r * p.cols;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf((v[k][e] - st.shift) * st.rstd, w[k][e], b[k][e]);
+      store8<T, false>(y + c[k], n[k], o);
+    }
     if (t == 0 && p.mean) {
-      p.mean[r] = mean;
-      p.rstd[r] = rstd;
+      p.mean[r] = m0 + st.shift;
+      p.rstd[r] = st.rstd;
     }
   }
 }
@@ -168,7 +241,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_bwd(LayerNormArg
   extern __shared__ float part[];  // NW == 1: three waves' partial rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rw = NW == 1 ? 0 : wave;
   const int t = rw * 64 + lane;
-  const float inv_n = 1.0f / (float)p.cols;
+  const Count count(p.cols);
   float w[V][8], dw[V][8], db[V][8];
   int64_t c[V];
   int n[V];
@@ -237,7 +310,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void k_ln_bwd(LayerNormArg
           s2 += buf[NW + i];
         }
       }
-      const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+      const float c1 = count.mean(s1), c2 = count.mean(s2);
       Elem<T>* dx = reinterpret_cast<Elem<T>*>(p.dx) + r * p.cols;
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -322,9 +395,9 @@ __global__ __launch_bounds__(1024) void k_ln_join(LayerNormArgs p, int parts) {
 // ---- rows past kMaxCols: the same sums, the row read again for each
 template <int T, int P>
 __global__ __launch_bounds__(1024) void k_ln_fwd_long(LayerNormArgs p) {
-  __shared__ float red[2][16];
+  __shared__ float red[3 * 16];
   const int wave = threadIdx.x >> 6;
-  const float inv_n = 1.0f / (float)p.cols;
+  const Count count(p.cols);
   const int64_t pitch = act8_pitch(p.cols);
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const Elem<T>* x = reinterpret_cast<const Elem<T>*>(p.x) + r * p.cols;
@@ -335,15 +408,20 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_long(LayerNormArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[e];
     }
-    const float mean = row_sum<16>(s, red[0], wave) * inv_n;
-    s = 0.f;
+    const float m0 = count.mean(row_sum<16>(s, red, wave));
+    float s1 = 0.f, s2 = 0.f;
     for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
       const int n = left8(p.cols, c);
       load8<T, false>(x + c, n, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += e < n ? (v[e] - mean) * (v[e] - mean) : 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const float d = e < n ? v[e] - m0 : 0.f;
+        s1 += d;
+        s2 = fmaf(d, d, s2);
+      }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<16>(s, red[1], wave) * inv_n + p.eps);
+    row_sum2<16>(s1, s2, red + 16, wave);
+    const RowStats st = row_stats(s1, s2, count, p.eps);
     // whole waves walk the last round: the checkpoint's blocks span lanes
     for (int64_t c0 = 0; c0 < p.cols; c0 += 8192) {
       const int64_t c = c0 + 8 * (int64_t)threadIdx.x;
@@ -360,12 +438,12 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_long(LayerNormArgs p) {
       load_params<P>(p.w, c, n, 1.f, w);
       load_params<P>(p.b, c, n, 0.f, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd * w[e] + b[e];
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(((v[e] - m0) - st.shift) * st.rstd, w[e], b[e]);
       store8<T, false>(y + c, n, v);
     }
     if (threadIdx.x == 0 && p.mean) {
-      p.mean[r] = mean;
-      p.rstd[r] = rstd;
+      p.mean[r] = m0 + st.shift;
+      p.rstd[r] = st.rstd;
     }
   }
 }
@@ -374,7 +452,7 @@ template <int T, int P, bool CKPT>
 __global__ __launch_bounds__(1024) void k_ln_dx_long(LayerNormArgs p) {
   __shared__ float red[2][2][16];
   const int wave = threadIdx.x >> 6;
-  const float inv_n = 1.0f / (float)p.cols;
+  const Count count(p.cols);
   int it = 0;
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, it ^= 1) {
     const Elem<T>* dy = reinterpret_cast<const Elem<T>*>(p.dy) + r * p.cols;
@@ -400,7 +478,7 @@ __global__ __launch_bounds__(1024) void k_ln_dx_long(LayerNormArgs p) {
         s2 += q[e] * xh[e];
       }
     }
-    const float c1 = row_sum<16>(s1, red[it][0], wave) * inv_n, c2 = row_sum<16>(s2, red[it][1], wave) * inv_n;
+    const float c1 = count.mean(row_sum<16>(s1, red[it][0], wave)), c2 = count.mean(row_sum<16>(s2, red[it][1], wave));
     Elem<T>* dx = reinterpret_cast<Elem<T>*>(p.dx) + r * p.cols;
     for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.cols; c += 8192) {
       const int n = left8(p.cols, c);
