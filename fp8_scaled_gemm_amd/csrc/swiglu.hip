@@ -5,9 +5,15 @@
 // Elementwise and bound by memory.  A thread takes 8 consecutive elements of a
 // row, and four neighbouring lanes one block of 32, whose largest magnitude
 // two DPP exchanges give all four; rows are cut into whole blocks, so four
-// lanes never straddle two rows.  8192 x 14336 bf16, checkpoints: forward 161 - 188
-// us, backward 161 - 172 us for 947 MB each (5.0 - 5.9 TB/s; a copy of 1 GiB reaches
-// 5.2), with non-temporal accesses, which tensors past the caches take.
+// lanes never straddle two rows.  8192 x 14336 from a graph, with non-temporal
+// accesses, which tensors past the caches take (a copy of 1 GiB reaches 5.2 TB/s, a
+// streamed read and write 6.3):
+//   bf16, checkpoints  forward 163 us, backward 149 us for 947 MB each (5.8, 6.4 TB/s)
+//   bf16, without      116 us for 705 MB, 188 us for 1174 MB (6.1, 6.2)
+//   fp16, checkpoints  157, 141 us
+//   fp32, 4096 rows    checkpoints 154, 138 us for 826 MB; without 125 us for 705 MB, 214 us for 1174 MB
+// fp32's exponential costs its backward from checkpoints 5% (131 us with the
+// hardware's), the rest nothing.
 #include "mx.hpp"
 
 namespace fp8sg {
@@ -37,7 +43,35 @@ unsigned grid_of(int64_t rows, int64_t cols) {
   return (unsigned)(n < (1 << 22) ? n : (1 << 22));
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+// exp(-x) for x >= 0, within a step of fp32 and a little, subnormal results too: x
+// log2 e = n + f with n whole and f in [-1/2, 1/2], log2 e in two parts, and 2^-f
+// by the hardware.  (From 200 on the result is 0.)
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;
+  x = fminf(x, 200.f);
+  const float n = __builtin_rintf(x * kHi);
+  const float f = fmaf(x, kLo, fmaf(x, kHi, -n));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(-f), -(int)n);
+}
+// Sigmoid of g and of -g (= 1 - sigmoid of g, without the subtraction's loss), from
+// t = exp(-|g|), which cannot overflow: r = 1 / (1 + t) and t r.  fp32 takes the
+// exponential above; the 16-bit types the hardware's alone, whose error grows to 2
+// |g| half steps of fp32 (1e-5 of the value where fp32 ends, a twentieth of fp16's
+// half step).  A NaN reaches the results through g itself.
+struct Sigmoid {
+  float at, neg;
+};
+template <int T>
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+  float t;
+  if constexpr (T == FP8SG_OUT_F32) t = exp_neg(fabsf(g));
+  else t = __expf(-fabsf(g));
+  // (the divisor lies in [1, 2]: the hardware's reciprocal, a step off at most, and
+  // one Newton step give the quotient within half a step and a little)
+  const float d = 1.0f + t, q = __builtin_amdgcn_rcpf(d);
+  const float r = fmaf(q, fmaf(-d, q, 1.0f), q), tr = t * r;
+  return g < 0.f ? Sigmoid{tr, r} : Sigmoid{r, tr};
+}
 
 template <int T, bool S, bool CKPT>
 __global__ __launch_bounds__(256) void k_swiglu_fwd(SwigluArgs p) {
@@ -52,7 +86,7 @@ __global__ __launch_bounds__(256) void k_swiglu_fwd(SwigluArgs p) {
       load8<T, S>(reinterpret_cast<const Elem<T>*>(p.g) + w.row * p.ldg + c, n, g);
       load8<T, S>(reinterpret_cast<const Elem<T>*>(p.u) + w.row * p.ldu + c, n, u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = g[e] * sigmoid(g[e]) * u[e];
+      for (int e = 0; e < 8; ++e) a[e] = g[e] * sigmoid<T>(g[e]).at * u[e];
       store8<T, S>(reinterpret_cast<Elem<T>*>(p.a) + w.row * p.cols + c, n, a);
     }
     if constexpr (CKPT) {
@@ -90,9 +124,9 @@ __global__ __launch_bounds__(256) void k_swiglu_bwd(SwigluArgs p) {
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float sg = sigmoid(g[e]), d = da[e] * sg;
-      du[e] = d * g[e];
-      dg[e] = d * u[e] * (1.0f + g[e] * (1.0f - sg));
+      const Sigmoid sg = sigmoid<T>(g[e]);  // (da, often small, comes last: da sigmoid may lie below fp32's range)
+      du[e] = da[e] * (g[e] * sg.at);
+      dg[e] = da[e] * (u[e] * (sg.at * (1.0f + g[e] * sg.neg)));
     }
     store8<T, S>(reinterpret_cast<Elem<T>*>(p.dg) + w.row * p.lddg + c, n, dg);
     store8<T, S>(reinterpret_cast<Elem<T>*>(p.du) + w.row * p.lddu + c, n, du);

@@ -171,3 +171,53 @@ def test_empty():
         F.swiglu_fwd(t, t, t.clone(), F.Act8(*shape), F.Act8(*shape))
         F.swiglu_bwd(t, F.Act8(*shape), F.Act8(*shape), t.clone(), t.clone())
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_fp32_keeps_its_precision_over_the_whole_range(ckpt):
+    """fp32 values in and out: errors in half steps of fp32 (U), whatever |g|.  t =
+    exp(-|g|) is off by a step (2 U), 1 + t by 2, r = 1 / (1 + t) by 3, t r by 6;
+    sigmoid is one of r and t r, 1 - sigmoid the other.  Two products more each
+    for a and du (8 U); dg's factor 1 + g (1 - sigmoid) is off by 7 U of |g| (1 -
+    sigmoid) and U of itself, and three more products follow (10 U)."""
+    g = torch.linspace(-86, 86, 64 * 500, device=DEV).view(64, 500)
+    u, da = rand((64, 500), "f32", 1), rand((64, 500), "f32", 2)
+    a, dg, du = (torch.empty_like(g) for _ in range(3))
+    cg, cu = (F.Act8(64, 500), F.Act8(64, 500)) if ckpt else (None, None)
+    F.swiglu_fwd(g, u, a, cg, cu)
+    F.swiglu_bwd(da, cg if ckpt else g, cu if ckpt else u, dg, du)
+    torch.cuda.synchronize()
+    vg, vu, vda = R.f64(g), R.f64(u), R.f64(da)
+
+    def parts(v):  # sigmoid(v) and 1 - sigmoid(v), both to 64 bits
+        return 1 / (1 + np.exp(-v)), 1 / (1 + np.exp(v))
+    s, _ = parts(vg)
+    want = vg * s * vu
+    R.check(a, want, 8 * R.U32 * np.abs(want) + np.abs(vu) * 2.0 ** -140, "a")
+    if ckpt:
+        vg, vu = R.act8_values(vg), R.act8_values(vu)
+    s, c = parts(vg)
+    tiny = np.abs(vda) * (1 + np.abs(vu)) * 2.0 ** -140
+    R.check(du, vda * vg * s, 8 * R.U32 * np.abs(vda * vg * s) + tiny, "du")
+    f = 1 + vg * c
+    bound = np.abs(vda * vu) * s * (7 * np.abs(vg) * c + 11 * np.abs(f)) * R.U32 + tiny
+    R.check(dg, vda * vu * s * f, bound, "dg")
+
+
+def test_gates_below_the_exponentials_range():
+    """exp(90) is past fp32, silu(-90) is not: -90 exp(-90) is a normal number."""
+    g = torch.full((1, 8), -87.5, device=DEV) - torch.arange(8, device=DEV) * 0.5
+    u, da = torch.full_like(g, 1e10), torch.full_like(g, 1e10)
+    a, dg, du = (torch.empty_like(g) for _ in range(3))
+    F.swiglu_fwd(g, u, a)
+    F.swiglu_bwd(da, g, u / 1e10, dg, du)
+    torch.cuda.synchronize()
+    v = R.f64(g)
+    s = 1 / (1 + np.exp(-v))
+    # exp(g) is subnormal here: off by half of 2^-149, times what it is multiplied by, and the roundings above
+    step = 2.0 ** -149
+    R.check(a, v * s * R.f64(u), np.abs(v) * R.f64(u) * (step + 8 * R.U32 * s) + R.f64(u) * step, "a")
+    R.check(du, v * s * R.f64(da), np.abs(v) * R.f64(da) * (step + 8 * R.U32 * s) + R.f64(da) * step, "du")
+    want = R.f64(da) * s * (1 + v / (1 + np.exp(v)))
+    R.check(dg, want, np.abs(v) * R.f64(da) * (2 * step + 20 * R.U32 * s), "dg")
+    assert bool((a < 0).all()) and bool((dg < 0).all())
