@@ -13,9 +13,10 @@ change to the GEMM's loop shape once spilled its accumulators and ran 30x
 slower with correct results).
 
 The assembly of IN_PLACE's files is read as well: every matrix instruction
-there has to add into the registers it writes.  For these kernels the compiler
-once gave a product's result registers that still held another accumulator,
-which cannot happen to a product whose result and addend are the same.
+there has to add into the registers it writes.  The compiler once gave the
+result of an MXFP4 product registers that still held another accumulator, which
+cannot happen to a product whose result and addend are the same.  Every file
+with matrix instructions is among them.
 """
 import concurrent.futures as cf
 import glob
@@ -35,7 +36,8 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=h
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-command-line-argument"]
 MAX_SPILL_VGPRS = 64
-IN_PLACE = ("mx_gemm.hip",)
+IN_PLACE = ("gemm.hip", "gemm_km.hip", "gemm_km01.hip", "gemm_km10.hip", "gemm_km11.hip", "gemm_rowwise.hip",
+            "gemm_unscale.hip", "mx_gemm.hip", "small_layer.hip")
 
 
 def spills(stderr: str) -> dict:
@@ -85,9 +87,12 @@ def _compile(src, verbose):
     if guarded:
         stem = os.path.splitext(os.path.basename(src))[0]
         with open(os.path.join(OBJDIR, f"{stem}-hip-amdgcn-amd-amdhsa-{ARCH}.s")) as f:
-            moved = moved_products(f.read())
+            asm = f.read()
+        moved = moved_products(asm)
         for temp in glob.glob(os.path.join(OBJDIR, f"{stem}-h*")) + glob.glob(os.path.join(OBJDIR, f"{stem}.hip-h*")):
             os.remove(temp)
+        if "v_mfma" not in asm:
+            raise RuntimeError(f"{src}: no matrix instructions found in its assembly")
         if moved:
             raise RuntimeError(f"{src}: products that do not add in place: {moved}")
     # the host pass does not know the packed-fp32 feature and says so; drop that
