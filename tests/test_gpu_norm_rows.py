@@ -6,6 +6,7 @@ import torch
 
 import fp8_scaled_gemm_amd as F
 from tests import mx_reference as R
+from tests.test_gpu_layer_norm import rand, run
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -70,3 +71,81 @@ def test_a_mean_far_from_zero(cols):
     R.check(y, want, bound, "y")
     R.check(mean, m[:, 0], mean_err, "mean")
     R.check(rstd, 1 / np.sqrt(var + EPS)[:, 0], rel / np.sqrt(var + EPS)[:, 0], "rstd")
+
+
+UNEVEN = [(1100, 4090), (1300, 8100), (700, 14333), (17000, 2000), (5000, 700), (20001, 300)]
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pdtype,ckpt", [(*s, *t, False) for s in UNEVEN
+                                                         for t in (("bf16", "f32"), ("f16", "f16"), ("f32", "f32"))] +
+                         [(*s, *t, True) for s, t in zip(UNEVEN, [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")] * 2)])
+def test_several_rows_a_block(rows, cols, dtype, pdtype, ckpt):
+    """More rows than blocks, unevenly: statistics of one row after the other in the
+    same block, loads ahead across rows, and hundreds of partial rows of dw and db.
+    The bounds on dw and db are those of the sums' own chains (long ones would
+    hide a missing part)."""
+    x, dy = rand((rows, cols), dtype, 1, 2.0, 0.5), rand((rows, cols), dtype, 2, 0.1)
+    w, b = rand((cols,), pdtype, 3, 0.2, 1.0), rand((cols,), pdtype, 4, 0.2)
+    y, mean, rstd, c, dx, dw, db = run(x, w, b, dy, ckpt, pdtype=R.DTYPES[pdtype])
+    chain = chain_of(rows, cols)
+    assert chain < rows / 20
+    wsum = None
+    for lo in range(0, rows, 2500):  # (in pieces: 64-bit copies of the whole take long)
+        at = slice(lo, min(lo + 2500, rows))
+        ref = R.LayerNorm(R.f64(x[at]), R.f64(w), R.f64(b), EPS)
+        R.check(y[at], ref.y, ref.y_err, "y")
+        R.check(mean[at], ref.mean[:, 0], ref.mean_err[:, 0], "mean")
+        R.check(rstd[at], ref.rstd[:, 0], (ref.rstd * ref.rstd_rel)[:, 0], "rstd")
+        xv, vdy = R.f64(x[at]), R.f64(dy[at])
+        if ckpt:
+            codes, s = R.act8(xv)
+            assert np.array_equal(c.s[at].cpu().numpy().astype(np.int64), s)
+            assert np.array_equal(c.q[at].cpu().numpy().astype(np.int64).reshape(codes.shape), codes)
+            xv = R.act8_values(xv)
+        (want, bound), _, _ = ref.grads(vdy, xv)
+        R.check(dx[at], want, bound, "dx")
+        xh = (xv - ref.mean) * ref.rstd
+        xh_err = ref.rstd * ref.mean_err + np.abs(xh) * (ref.rstd_rel + 3 * R.U32)
+        sums = np.stack([(vdy * xh).sum(0), np.abs(vdy * xh).sum(0), (np.abs(vdy) * xh_err).sum(0), vdy.sum(0), np.abs(vdy).sum(0)])
+        wsum = sums if wsum is None else wsum + sums
+    R.check(dw, wsum[0], chain * R.U32 * wsum[1] + wsum[2], "dw")
+    R.check(db, wsum[3], chain * R.U32 * wsum[4], "db")
+    assert (np.abs(wsum[3]) > 10 * chain * R.U32 * wsum[4]).mean() > 0.9  # (the bounds tell db from 0)
+
+
+def chain_of(rows, cols):
+    """Additions in a chain behind an element of dw or db: a wave's rows, four waves
+    of a block, every 32nd part (eight at a time), a tree of 32, and the product.
+    A block has rows / parts of them or one more; where a row takes one wave, it
+    has four rows at a time."""
+    parts = F.layer_norm_workspace_len(rows, cols) // (2 * cols)
+    return -(-rows // parts) + 4 + -(-parts // 32) + 8 + 5 + 2
+
+
+@pytest.mark.parametrize("rows,cols", [(1500, 2048), (2048, 4096), (5000, 1024), (2100, 5000), (30000, 40), (600, 20000),
+                                       (2200000, 1024), (130000, 16640)])
+def test_parts_add_up(rows, cols):
+    """db of whole numbers is exact whatever the order, every partial row in it (up
+    to 512); dw likewise where xh is made whole: mean 0 and rstd 1 handed in."""
+    g = torch.Generator(DEV).manual_seed(rows)
+    x, dy = (torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    sums = torch.zeros(2, cols, dtype=torch.int64, device=DEV)
+    for r in range(0, rows, 1 << 14):
+        at = slice(r, min(r + (1 << 14), rows))
+        n = at.stop - r
+        vx = torch.randint(-2, 3, (n, cols), generator=g, device=DEV, dtype=torch.int32)
+        vdy = torch.randint(-2, 4, (n, cols), generator=g, device=DEV, dtype=torch.int32)  # (not balanced: db grows)
+        x[at], dy[at] = vx, vdy
+        sums[0] += (vx * vdy).sum(0)
+        sums[1] += vdy.sum(0)
+    assert 6 * rows < 1 << 24  # every partial sum is a whole number below 2^24
+    mean, rstd = torch.zeros(rows, device=DEV), torch.ones(rows, device=DEV)
+    dw, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    n = F.layer_norm_workspace_len(rows, cols)
+    ws = torch.full((n,), float("nan"), device=DEV)
+    F.layer_norm_bwd(dy, x, None, mean, rstd, dw=dw, db=db, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(db.long(), sums[1]) and torch.equal(dw.long(), sums[0])
+    assert torch.equal(db, db.round()) and torch.equal(dw, dw.round())
+    del x, dy
+    torch.cuda.empty_cache()
