@@ -26,7 +26,7 @@ __device__ __forceinline__ void static_for(F f) {
   static_for_(std::make_integer_sequence<int, N>{}, f);
 }
 
-// ---- element types (fp8sg_out values): one element as fp32, exactly
+// ---- element types (fp8sg_out values)
 template <int T>
 struct ElemOf { typedef uint16_t type; };
 template <>
@@ -34,12 +34,6 @@ struct ElemOf<FP8SG_OUT_F32> { typedef float type; };
 template <int T>
 using Elem = typename ElemOf<T>::type;
 
-template <int T>
-__device__ __forceinline__ float to_f32(Elem<T> v) {
-  if constexpr (T == FP8SG_OUT_BF16) return __uint_as_float((uint32_t)v << 16);
-  else if constexpr (T == FP8SG_OUT_F16) return (float)__builtin_bit_cast(_Float16, v);
-  else return v;
-}
 // fp32 -> element, rounded once to nearest even
 template <int T>
 __device__ __forceinline__ Elem<T> from_f32(float v) {
@@ -53,9 +47,9 @@ __device__ __forceinline__ Elem<T> from_f32(float v) {
 // cleared): floor(log2 amax) is the exponent field, so floor(log2 amax) - emax
 // + 127 = field - emax.  `fit` raises it by one where the mantissa exceeds the
 // largest element's (kMant: 1.5 for e2m1's 6, 1.75 for e4m3's 448), up to
-// 254 - emax - 2, where the largest element times the scale is still finite
-// (floor never exceeds that).  Subnormal magnitudes count as field 0: they
-// lie below 2^-126, far under the smallest scale's range.
+// 254 - emax, where the largest element times the scale is still finite
+// (floor never exceeds that).  Subnormal magnitudes count as field 0: both
+// rules give them the smallest scale, 2^-127, of which they are below 2.
 template <int EMAX, uint32_t kMant>
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax, bool fit) {
   if (amax >= 0x7F800000u) return 255u;
@@ -73,11 +67,6 @@ __device__ __forceinline__ uint32_t act8_scale(uint32_t amax) {
 __device__ __forceinline__ float scale_value(uint32_t s) {
   if (s == 255u) return __uint_as_float(0x7FC00000u);
   return __uint_as_float(s ? s << 23 : 0x00400000u);
-}
-
-// Two fp32 values to one byte of e2m1 codes (first value in the low half).
-__device__ __forceinline__ uint32_t fp4_pair(float a, float b, float scale) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a, b, scale, 0) & 0xFFu;
 }
 
 // e4m3 codes of values in a block with scale byte s: v * 2^(127 - s) is exact
