@@ -12,10 +12,11 @@
 // the workspace; a second kernel adds the partial rows.  Every sum's order
 // follows from the sizes alone, so results repeat bit for bit.
 //
-// Measured: 8192 x 4096 bf16 forward 30 us, 32 - 35 us with the checkpoint (4.8 - 5.2 TB/s),
-// backward from the checkpoint 38 us and the join 5; 1000 x 14336 fp16 forward 15.4
-// us, backward 23.5 us and the join 7: there the 250 partial rows are as many
-// bytes as dx.
+// Measured: 8192 x 4096 bf16 forward 24 us from a graph (5.6 TB/s), with the checkpoint
+// 30 there and 32 alone (5.3 TB/s), backward from the checkpoint 35 us and the join
+// 5; fp32 44 and 82 us (6.0, 4.9 TB/s).  1000 x 14336 fp16 forward 15 us, backward 23 us
+// and the join 7: there the 250 partial rows are as many bytes as dx.  Past kMaxCols,
+// 4096 x 20480 bf16: forward 101 us (3.3 TB/s), backward 192 (2.6).
 #include "mx.hpp"
 
 namespace fp8sg {
@@ -525,9 +526,11 @@ hipError_t by_types(int type, int ptype, F f) {
   });
 }
 // f(waves per row, groups of 8 per thread) for a row of up to kMaxCols.  The
-// backward keeps five fp32 values an element: past 8192 columns it takes more
-// registers a thread (8 waves x 4 groups) rather than 16 waves, whose 128
-// registers a thread it would overrun.
+// backward keeps five fp32 values an element: past 8192 columns 8 waves x 4 groups
+// take all 256 registers a thread, and in the 16-bit types 10 more, saved before
+// the loop over the rows and read back after it (40 bytes a thread, 4.9 MiB of
+// writes at 1000 x 14336).  16 waves x 2 groups would have 128 registers for the 139 -
+// 150 that two groups take at 4 waves, inside that loop.
 template <bool BWD, class F>
 void by_width(int64_t cols, F f) {
   typedef std::integral_constant<int, 1> C1;
@@ -544,11 +547,23 @@ void by_width(int64_t cols, F f) {
 // Partial rows of the weight gradients: a block each, enough of them to fill
 // the chip, few enough that writing and adding them stays small next to the
 // rows themselves (8 bytes a column and part against 4 to 12 a column and
-// row).  At most 512 of up to 4096 columns, 256 of more (backward of 8192 x 4096
-// bf16 from checkpoints: 256 parts 53 us, 512 44 us, 1024 52 us; 8192 x 8192: 83,
-// 89, 100 us), and 4 rows a block at least (1000 x 14336: 2 rows 46 us, 4 rows 32
-// us, 8 rows 38 us).  One, when the rows are few: the block then writes the
-// gradients.
+// row).  At most 512 of up to 4096 columns, 256 of more, and 4 rows a block (a
+// wave, where a row takes one) at least.  Backward from a graph, us:
+//   parts            128    256    512   1024
+//   65536 x 512       82     45     37     39
+//   16384 x 1000      47     29     24     27
+//   16384 x 2048     103     56     39     39
+//   4000 x 4096       40     26     25     31
+//   8192 x 4096 ckpt  77     44     36     41
+//   4000 x 5000       49     32     38     48
+//   16384 x 8192     198    167    175    186
+//   4000 x 14336      95     81     92    120
+//   least rows         2      4      8
+//   1000 x 4096     18.3   15.4   16.9
+//   1000 x 2048     12.5   11.4   13.3
+//   1000 x 14336    30.1   30.3   34.1
+//   256 x 1000       9.7   11.7   16.4   (few rows of up to 2048 columns: 2 would be better)
+// One, when the rows are few: the block then writes the gradients.
 constexpr int64_t kDirectRows = 8;
 int64_t parts_of(int64_t rows, int64_t cols) {
   if (cols > kMaxCols) {

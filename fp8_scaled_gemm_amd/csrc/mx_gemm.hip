@@ -92,14 +92,15 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
 // Each has two phases or more to land; the wave that issued a load waits for it
 // before the swap ahead of its first read.
 //
-// Bound by the matrix cores and their clock, which these products pull down to
-// 1.5 - 1.8 GHz: 8192 x 14336 x 4096 237 - 255 us (3.8 - 4.05 PFLOP/s), 8192 x 4096 x
-// 14336 194 - 213 us (4.5 - 4.96), 14336 x 4096 x 8192 212 - 245 us, 4096^3 35 - 37
-// us; the same instructions alone reach 6.3 - 6.8 PFLOP/s.  A k-tile takes about
-// 2650 cycles of which 2150 are products (the swaps and the phases' unequal
-// lengths are the rest), a tile's start and epilogue about 16000 more, a quarter
-// of the tile's time at K = 4096.  256 x 256: halving either side doubles the LDS
-// reads per product (see k_mx_mid).
+// 8192 x 14336 x 4096 230 - 255 us (3.8 - 4.2 PFLOP/s), 8192 x 4096 x 14336 194 - 213
+// us (4.5 - 4.96), 14336 x 4096 x 8192 212 - 245 us, 4096^3 35 - 37 us; the same
+// instructions alone reach 6.3 - 6.8 PFLOP/s, at the 1.5 - 1.8 GHz that such
+// products leave.  The matrix cores are busy 51, 63 and 53 % of the first three's
+// cycles.  Of the first's 64 thousand cycles a tile, 34 are products (16 k-tiles of
+// 2150), 8 the swaps and the phases' unequal lengths (a k-tile takes about 2650),
+// and some 20 the tile's start and its stores: one workgroup fills a unit and all
+// tiles are alike, so all units store at once while none multiplies.  256 x 256:
+// halving either side doubles the LDS reads per product (see k_mx_mid).
 template <int OUT>
 __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
   constexpr int BM = 256, BN = 256, kTM = 8, kTN = 4;
@@ -740,7 +741,11 @@ hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
 
 hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1, int out, hipStream_t stream) {
   // Where launches dominate (few tiles of 16, short contractions), both in one
-  // launch (64 x 256 x 128 layer, backward call: 16.5 us as two, 13.3 us so).
+  // launch, in tiles of 16; as two, each takes the tiles that suit it.  The whole
+  // backward call from a graph, M x N x K, as two / in one (us): 16 x 64 x 64 8.4 / 6.5,
+  // 64 x 256 x 128 9.3 / 7.2, 256^3 9.5 / 7.5, 64 x 1024 x 128 10.0 / 8.2, 2048 x 2048 x 32
+  // (8 k-tiles) 15.0 / 12.8.  The gain ends between 1000 and 4000 tiles: 64 x 2048 x 128
+  // (1056) 10.6 / 10.8, 512^3 (2048) 11.6 / 9.4, 2048 x 2048 x 256 (4096) 21.7 / 27.3.
   auto tiles = [](const MxGemmProblem& p) { return ((p.M + 15) / 16) * ((p.N + 15) / 16); };
   constexpr int64_t kTiles = 512, kLong = 8;
   const int64_t b0 = tiles(p0), b1 = tiles(p1), n0 = mx_ktiles(p0.K), n1 = mx_ktiles(p1.K);

@@ -88,10 +88,11 @@ struct MxQuantArgs {
 //     LDS, so that the columns' codes leave in runs of 16 G bytes.
 // Scales of both directions are gathered in LDS in their stored order.
 // Memory bound (both ways, bf16: 8192 x 14336 71 - 75 us, 4.8 - 5.1 TB/s; 14336 x 4096
-// 45 - 51 us; 8192 x 4096 25 us).  G = 8, RL = 16 writes whole 128-byte lines with the
-// fewest instructions; G = 2, RL = 4 gives small matrices four times the blocks and
-// 16 times the waves (37 x 1001 fp32, both ways: 9.2 us with RL = 16; so, less than
-// the call's 6.1 us on the host).
+// 45 - 52 us; 8192 x 4096 25 us; fp32, whose 128 elements a lane leave half the
+// waves: 147 us, 4.05 TB/s; 80 us; 38 us).  G = 8, RL = 16 writes whole 128-byte lines
+// with the fewest instructions; G = 2, RL = 4 gives small matrices four times the
+// blocks and 16 times the waves (37 x 1001 fp32, both ways: 9.2 us with RL = 16; so,
+// less than the call's 6.1 us on the host).
 template <int T, int G, int RL, bool S>
 __global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 ? 2 : 4) void k_mxq(MxQuantArgs args) {
   constexpr int kRows = 32 * G, C = 2 * RL, kAcross = 32 / C, kThreads = 64 * G * kAcross;
@@ -221,7 +222,8 @@ __global__ __launch_bounds__(256) void k_mxq_rows(MxQuantArgs args) {
 }
 
 // One thread per 8 values: 4 bytes of codes, their block's scale.  Bound by the
-// values' writes (14336 x 4096 to bf16: 26.5 - 28.6 us, 5.2 - 5.6 TB/s).
+// values' writes (14336 x 4096 to bf16: 26.5 - 28.6 us, 5.2 - 5.6 TB/s; to fp32 48 us,
+// 5.5; 8192 x 14336: 68 us, 4.3 TB/s, to fp32 111, 4.8).
 template <int T>
 __global__ __launch_bounds__(256) void k_mx_dequant(mxfp4_operand m, int64_t rows, int64_t k, Elem<T>* y) {
   const int64_t nk = mx_ktiles(k), upr = (k + 7) / 8, total = rows * upr;

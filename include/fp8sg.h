@@ -654,7 +654,10 @@ FP8SG_API fp8sg_status mxfp4_quantize(const void* x, fp8sg_out type, int64_t row
                                       fp8sg_mx_rule rule, const mxfp4_operand* q,
                                       const mxfp4_operand* qT, fp8sg_stream stream);
 
-/* The values of an MXFP4 matrix (rows x k), as `type`, row-major, contiguous. */
+/* The values of an MXFP4 matrix (rows x k), as `type`, row-major, contiguous,
+ * rounded to nearest even.  Codes of fp16 values may stand for more than fp16 holds
+ * (65504 rounds to 4 * 2^14 by FP8SG_MX_FIT): as fp16 that is an infinity.  The same
+ * goes for act8_dequantize. */
 FP8SG_API fp8sg_status mxfp4_dequantize(const mxfp4_operand* m, int64_t rows, int64_t k, void* y,
                                         fp8sg_out type, fp8sg_stream stream);
 

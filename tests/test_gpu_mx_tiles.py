@@ -116,3 +116,22 @@ def test_streaming_cast(rows, cols, dtype):
     torch.cuda.synchronize()
     check_codes(q, x, True, "rows")
     check_codes(qT, x.t(), True, "columns")
+
+
+def test_values_past_fp16():
+    """The largest fp16 value rounds up to 2^16 by FIT and in an 8-bit checkpoint,
+    which is an infinity as fp16 and a number as fp32; FLOOR saturates below."""
+    x = torch.full((3, 40), 65504.0, dtype=torch.float16, device=DEV)
+    m, c = F.Mxfp4(3, 40), F.Act8(3, 40)
+    y16, y32 = torch.empty_like(x), torch.empty(3, 40, device=DEV)
+    for rule, value in ((F.MX_FLOOR, 6 * 2.0 ** 13), (F.MX_FIT, 2.0 ** 16)):
+        F.mxfp4_quantize(x, m, rule=rule)
+        F.mxfp4_dequantize(m, y16)
+        F.mxfp4_dequantize(m, y32)
+        torch.cuda.synchronize()
+        assert (y32 == value).all() and (y16 == (value if value < 65504 else float("inf"))).all()
+    F.act8_quantize(x, c)
+    F.act8_dequantize(c, y16)
+    F.act8_dequantize(c, y32)
+    torch.cuda.synchronize()
+    assert (y32 == 2.0 ** 16).all() and torch.isinf(y16).all()
