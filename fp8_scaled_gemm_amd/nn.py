@@ -650,9 +650,9 @@ class PackedMXFP4Linear(nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, rule={self.rule}"
 
 
-def _mx_filter(mod: nn.Linear, fqn: str) -> bool:
+def _mx_filter(mod: nn.Module, fqn: str) -> bool:
     """As default_module_filter, without its rules on sizes (MXFP4 takes any)."""
-    return (mod.bias is None and mod.weight.dtype in _MX_DTYPES and
+    return (getattr(mod, "bias", None) is None and mod.weight.dtype in _MX_DTYPES and
             fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES)
 
 
@@ -680,10 +680,7 @@ def convert_to_mxfp4_serving(model: nn.Module,
     """Replace, in place, every nn.Linear and MXFP4Linear child that the filter
     accepts by a PackedMXFP4Linear holding its quantised weight.  rule None: each
     layer's own, "floor" for an nn.Linear."""
-    return _replace_linears(model, module_filter_fn or
-                            (lambda m, fqn: fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES and
-                             getattr(m, "bias", None) is None),
-                            lambda m: PackedMXFP4Linear.from_float(m, rule))
+    return _replace_linears(model, module_filter_fn or _mx_filter, lambda m: PackedMXFP4Linear.from_float(m, rule))
 
 
 # ---- gated activation

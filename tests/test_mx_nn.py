@@ -95,3 +95,17 @@ def test_serving_keeps_the_rule_a_layer_was_trained_with(rule, monkeypatch):
         assert [layer.rule for layer in N.convert_to_mxfp4_serving(m, rule=named)] == [named, named]
     with pytest.raises(ValueError, match="rule"):
         PackedMXFP4Linear.from_float(lin, rule="ceil")
+
+
+def test_default_filters_leave_other_types_alone(monkeypatch):
+    """A linear that MXFP4 does not take (float64) stays as it is in both conversions."""
+    from fp8_scaled_gemm_amd import nn as N
+
+    def quantize(w, q, rule):
+        if w.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            raise TypeError(w.dtype)
+    monkeypatch.setattr(N, "mxfp4_quantize", quantize)
+    for convert, kind in ((convert_to_mxfp4_training, MXFP4Linear), (N.convert_to_mxfp4_serving, PackedMXFP4Linear)):
+        m = nn.Sequential(nn.Linear(8, 8, bias=False), nn.Linear(8, 8, bias=False, dtype=torch.float64), nn.Linear(8, 8))
+        convert(m)
+        assert [type(c) for c in m] == [kind, nn.Linear, nn.Linear]
