@@ -33,7 +33,10 @@ EXPORTS = ("fp8sg_status_string", "fp8sg_version", "amp_norm_workspace_len", "fp
            "mxfp4_code_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize",
            "mxfp4_gemm", "mxfp4_linear_fwd", "mxfp4_linear_bwd", "mxfp4_linear_apply",
            "act8_quantize", "act8_dequantize", "swiglu_fwd", "swiglu_bwd", "layer_norm_fwd",
-           "layer_norm_workspace_len", "layer_norm_bwd")
+           "layer_norm_workspace_len", "layer_norm_bwd", "fp8_gemm_epilogue", "fp8_gemm_rowwise_epilogue",
+           "fp8_scaled_linear_fwd_epilogue", "fp8_scaled_linear_bwd_epilogue", "epilogue_workspace_len",
+           "epilogue_bwd", "mxfp4_gemm_epilogue", "mxfp4_linear_fwd_epilogue", "mxfp4_linear_apply_epilogue",
+           "mxfp4_linear_bwd_epilogue", "dropout_fwd", "dropout_bwd")
 MAX_HISTORY = 1024
 MAX_DIM = 1 << 29     # largest matrix dimension an entry point takes
 MAX_ELEMS = 1 << 35   # largest tensor, in elements
@@ -122,6 +125,7 @@ def lib():
     for name in EXPORTS[3:]:
         getattr(L, name).restype = i
     _bind_mx(L)
+    _bind_epilogue(L)
     _lib = L
     return L
 
@@ -803,3 +807,10 @@ from .mx import (MX_FIT, MX_FLOOR, Act8, Mxfp4, Mxfp4LinearSaved, Mxfp4LinearWs,
                  layer_norm_workspace_len, mxfp4_dequantize, mxfp4_gemm, mxfp4_linear_apply,
                  mxfp4_linear_bwd, mxfp4_linear_fwd, mxfp4_quantize, swiglu_bwd, swiglu_fwd)
 from .mx import bind as _bind_mx  # noqa: E402
+# The products with an epilogue and dropout (the module uses both sets of checks).
+from .epilogue import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, dropout_bwd,  # noqa: E402, F401
+                       dropout_fwd, epilogue_bwd, epilogue_workspace_len, fp8_gemm_epilogue,
+                       fp8_gemm_rowwise_epilogue, fp8_scaled_linear_bwd_epilogue,
+                       fp8_scaled_linear_fwd_epilogue, mxfp4_gemm_epilogue, mxfp4_linear_apply_epilogue,
+                       mxfp4_linear_bwd_epilogue, mxfp4_linear_fwd_epilogue)
+from .epilogue import bind as _bind_epilogue  # noqa: E402

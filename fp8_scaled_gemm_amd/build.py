@@ -36,8 +36,8 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=h
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-command-line-argument"]
 MAX_SPILL_VGPRS = 64
-IN_PLACE = ("gemm.hip", "gemm_km.hip", "gemm_km01.hip", "gemm_km10.hip", "gemm_km11.hip", "gemm_rowwise.hip",
-            "gemm_unscale.hip", "mx_gemm.hip", "small_layer.hip")
+IN_PLACE = ("gemm.hip", "gemm_km.hip", "gemm_km01.hip", "gemm_km10.hip", "gemm_km11.hip", "gemm_epilogue.hip",
+            "gemm_rowwise.hip", "gemm_unscale.hip", "mx_gemm.hip", "small_layer.hip")
 
 
 def spills(stderr: str) -> dict:

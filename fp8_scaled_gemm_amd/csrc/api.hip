@@ -267,6 +267,91 @@ fp8sg_status check_saved_rw(const fp8_linear_saved_rw* s, int64_t M, int64_t N, 
   return FP8SG_OK;
 }
 
+}  // namespace
+
+namespace fp8sg {
+
+hipError_t launch_linear_casts(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                               const fp8_linear_saved& saved, float* hist_x, float* hist_w,
+                               int32_t hist_len, bool f16, hipStream_t s) {
+  QuantArgs qa{};
+  qa.job[0] = QuantJob{x, M, K, saved.x_sc, saved.x_q, saved.x_qT, 0, 0, 0, hist_x, hist_len};
+  qa.job[1] = QuantJob{w, N, K, saved.w_sc, saved.w_q, saved.w_qT, 0, 0, 0, hist_w, hist_len};
+  qa.njobs = 2;
+  qa.in_f16 = f16;
+  if (!hist_x && !f16 && self_cast_fits(qa))  // small x and W: amax and cast in one launch
+    return launch_quantize_self(qa, FP8SG_E4M3FN, s);
+  if (!hist_x) {
+    AmaxArgs am{};
+    am.job[0] = AmaxJob{x, M * K, saved.x_sc, 0, amax_blocks_for(M * K)};
+    am.job[1] = AmaxJob{w, N * K, saved.w_sc, 0, amax_blocks_for(N * K)};
+    am.njobs = 2;
+    am.in_f16 = f16;
+    const hipError_t e = launch_amax(am, false, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_quantize(qa, FP8SG_E4M3FN, s);
+}
+
+hipError_t launch_linear_bwd(const uint16_t* gy, const fp8_linear_saved& sv, int64_t M, int64_t N,
+                             int64_t K, const fp8_linear_bwd_ws& w, float* hist_gy, int32_t hist_len,
+                             void* gx, void* gw, int out, const float* amp_scale, int32_t* found_inf,
+                             bool f16, bool have_amax, hipStream_t s) {
+  hipError_t e;
+  // An operand without its transposed copy is read from its row-major codes,
+  // contraction-major: dgrad's W codes [N, K] as B^T, wgrad's gy codes
+  // [M, N] as A^T and x codes [M, K] as B^T.
+  const bool tb_d = !sv.w_qT, ta_w = !w.gy_qT, tb_w = !sv.x_qT;
+  const int o = amp_scale ? kOutF16Unscale : out;
+  if (!hist_gy && !f16 && tb_d && ta_w && tb_w && small_layer_fits(M, N, K)) {
+    // small layer without transposed copies: the cast of gy and both GEMMs
+    // in one launch
+    SmallBwdArgs a{gy, M, N,
+                   GemmProblem{w.gy_q, sv.w_q, gx, nullptr, &sv.w_sc->inv, M, K, N,
+                               amp_scale, found_inf},
+                   GemmProblem{w.gy_q, sv.x_q, gw, nullptr, &sv.x_sc->inv, N, K, M,
+                               amp_scale, found_inf},
+                   w.gy_sc, w.gy_q};
+    return launch_small_bwd(a, o, s);
+  }
+  QuantArgs qa{};
+  qa.job[0] = QuantJob{gy, M, N, w.gy_sc, w.gy_q, w.gy_qT, 0, 0, 0, hist_gy, hist_len};
+  qa.njobs = 1;
+  qa.in_f16 = f16;
+  if (!hist_gy && !f16 && self_cast_fits(qa)) {  // small gy: amax and cast in one launch
+    e = launch_quantize_self(qa, FP8SG_E5M2, s);
+  } else {
+    if (!hist_gy && !have_amax) {
+      AmaxArgs am{};
+      am.job[0] = AmaxJob{gy, M * N, w.gy_sc, 0, amax_blocks_for(M * N)};
+      am.njobs = 1;
+      am.in_f16 = f16;
+      e = launch_amax(am, false, s);
+      if (e != hipSuccess) return e;
+    }
+    e = launch_quantize(qa, FP8SG_E5M2, s);
+  }
+  if (e != hipSuccess) return e;
+
+  GemmProblem dg{w.gy_q, tb_d ? sv.w_q : sv.w_qT, gx, &w.gy_sc->inv, &sv.w_sc->inv,
+                 M, K, N, amp_scale, found_inf};
+  GemmProblem wg{ta_w ? w.gy_q : w.gy_qT, tb_w ? sv.x_q : sv.x_qT, gw, &w.gy_sc->inv,
+                 &sv.x_sc->inv, N, K, M, amp_scale, found_inf};
+  if (tb_d && ta_w && tb_w) return launch_gemm_km_pair(dg, wg, o, s);
+  if (tb_d || ta_w || tb_w) {  // some copies kept: one launch per GEMM
+    e = launch_gemm_km(dg, FP8SG_E5M2, FP8SG_E4M3FN, o, false, tb_d, s);
+    if (e != hipSuccess) return e;
+    return launch_gemm_km(wg, FP8SG_E5M2, FP8SG_E4M3FN, o, ta_w, tb_w, s);
+  }
+  if (amp_scale)  // fp16 gradients unscaled and checked in the GEMM epilogues
+    return launch_gemm_unscale_pair(dg, wg, false, s);
+  return launch_gemm_pair(dg, wg, FP8SG_E5M2, FP8SG_E4M3FN, out, s);
+}
+
+}  // namespace fp8sg
+
+namespace {
+
 // Forward [FP8-TRAIN §4 forward, §6]: codes and transposed copies of x and W
 // (dynamic: one amax launch over both, then one quantize launch; delayed: one
 // quantize launch that also reduces the current amax, then the history push),
@@ -288,31 +373,14 @@ fp8sg_status linear_fwd(const uint16_t* x, const uint16_t* w, int64_t M, int64_t
     if (!hist_ok(hist_x) || !hist_ok(hist_w)) return FP8SG_ERR_ALIGN;
   }
   hipStream_t s = S(stream);
-  hipError_t e;
   if (!delayed && !saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K)) {
     // small layer without transposed copies: casts and GEMM in one launch
     SmallFwdArgs a{x, w, GemmProblem{saved->x_q, saved->w_q, y, nullptr, nullptr, M, N, K},
                    saved->x_sc, saved->w_sc, saved->x_q, saved->w_q};
     return hip_status(launch_small_fwd(a, out, s));
   }
-  QuantArgs qa{};
-  qa.job[0] = QuantJob{x, M, K, saved->x_sc, saved->x_q, saved->x_qT, 0, 0, 0, hist_x, hist_len};
-  qa.job[1] = QuantJob{w, N, K, saved->w_sc, saved->w_q, saved->w_qT, 0, 0, 0, hist_w, hist_len};
-  qa.njobs = 2;
-  if (!delayed && self_cast_fits(qa)) {  // small x and W: amax and cast in one launch
-    e = launch_quantize_self(qa, FP8SG_E4M3FN, s);
-  } else {
-    if (!delayed) {
-      AmaxArgs am{};
-      am.job[0] = AmaxJob{x, M * K, saved->x_sc, 0, amax_blocks_for(M * K)};
-      am.job[1] = AmaxJob{w, N * K, saved->w_sc, 0, amax_blocks_for(N * K)};
-      am.njobs = 2;
-      e = launch_amax(am, false, s);
-      if (e != hipSuccess) return FP8SG_ERR_HIP;
-    }
-    e = launch_quantize(qa, FP8SG_E4M3FN, s);
-  }
-  if (e != hipSuccess) return FP8SG_ERR_HIP;
+  if (launch_linear_casts(x, w, M, N, K, *saved, hist_x, hist_w, hist_len, false, s) != hipSuccess)
+    return FP8SG_ERR_HIP;
 
   GemmProblem p{saved->x_q, saved->w_q, y, &saved->x_sc->inv, &saved->w_sc->inv, M, N, K};
   return hip_status(launch_gemm(p, FP8SG_E4M3FN, FP8SG_E4M3FN, out, s));
@@ -338,54 +406,8 @@ fp8sg_status linear_bwd(const uint16_t* gy, const fp8_linear_saved* saved, int64
     if (!hist_len_ok(hist_len)) return FP8SG_ERR_SHAPE;
     if (!hist_ok(hist_gy)) return FP8SG_ERR_ALIGN;
   }
-  hipStream_t s = S(stream);
-  hipError_t e;
-  // An operand without its transposed copy is read from its row-major codes,
-  // contraction-major: dgrad's W codes [N, K] as B^T, wgrad's gy codes
-  // [M, N] as A^T and x codes [M, K] as B^T.
-  const bool tb_d = !saved->w_qT, ta_w = !ws->gy_qT, tb_w = !saved->x_qT;
-  const int o = amp_scale ? kOutF16Unscale : (int)out;
-  if (!hist_gy && tb_d && ta_w && tb_w && small_layer_fits(M, N, K)) {
-    // small layer without transposed copies: the cast of gy and both GEMMs
-    // in one launch
-    SmallBwdArgs a{gy, M, N,
-                   GemmProblem{ws->gy_q, saved->w_q, gx, nullptr, &saved->w_sc->inv, M, K, N,
-                               amp_scale, found_inf},
-                   GemmProblem{ws->gy_q, saved->x_q, gw, nullptr, &saved->x_sc->inv, N, K, M,
-                               amp_scale, found_inf},
-                   ws->gy_sc, ws->gy_q};
-    return hip_status(launch_small_bwd(a, o, s));
-  }
-  QuantArgs qa{};
-  qa.job[0] = QuantJob{gy, M, N, ws->gy_sc, ws->gy_q, ws->gy_qT, 0, 0, 0, hist_gy, hist_len};
-  qa.njobs = 1;
-  if (!hist_gy && self_cast_fits(qa)) {  // small gy: amax and cast in one launch
-    e = launch_quantize_self(qa, FP8SG_E5M2, s);
-  } else {
-    if (!hist_gy) {
-      AmaxArgs am{};
-      am.job[0] = AmaxJob{gy, M * N, ws->gy_sc, 0, amax_blocks_for(M * N)};
-      am.njobs = 1;
-      e = launch_amax(am, false, s);
-      if (e != hipSuccess) return FP8SG_ERR_HIP;
-    }
-    e = launch_quantize(qa, FP8SG_E5M2, s);
-  }
-  if (e != hipSuccess) return FP8SG_ERR_HIP;
-
-  GemmProblem dg{ws->gy_q, tb_d ? saved->w_q : saved->w_qT, gx, &ws->gy_sc->inv, &saved->w_sc->inv,
-                 M, K, N, amp_scale, found_inf};
-  GemmProblem wg{ta_w ? ws->gy_q : ws->gy_qT, tb_w ? saved->x_q : saved->x_qT, gw, &ws->gy_sc->inv,
-                 &saved->x_sc->inv, N, K, M, amp_scale, found_inf};
-  if (tb_d && ta_w && tb_w) return hip_status(launch_gemm_km_pair(dg, wg, o, s));
-  if (tb_d || ta_w || tb_w) {  // some copies kept: one launch per GEMM
-    e = launch_gemm_km(dg, FP8SG_E5M2, FP8SG_E4M3FN, o, false, tb_d, s);
-    if (e != hipSuccess) return FP8SG_ERR_HIP;
-    return hip_status(launch_gemm_km(wg, FP8SG_E5M2, FP8SG_E4M3FN, o, ta_w, tb_w, s));
-  }
-  if (amp_scale)  // fp16 gradients unscaled and checked in the GEMM epilogues
-    return hip_status(launch_gemm_unscale_pair(dg, wg, false, s));
-  return hip_status(launch_gemm_pair(dg, wg, FP8SG_E5M2, FP8SG_E4M3FN, out, s));
+  return hip_status(launch_linear_bwd(gy, *saved, M, N, K, *ws, hist_gy, hist_len, gx, gw, out, amp_scale, found_inf,
+                                      false, false, S(stream)));
 }
 
 // Row-wise backward [FP8-TRAIN §1, §4 backward]: gy cast by rows and by

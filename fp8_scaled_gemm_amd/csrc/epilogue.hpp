@@ -1,0 +1,348 @@
+// What stands behind a linear layer's product, in the product's own epilogue and
+// in kernels of its own:
+//   h = acc + bias[n],  y = residual + drop(act(h)),
+// and, for the backward pass, gh = drop'(gy) act'(h).  Everything is computed in
+// fp32 from the fp32 accumulator and rounded once, to y (and to the kept h).
+#pragma once
+
+#include "launch_epilogue.hpp"
+#include "mx.hpp"
+
+namespace fp8sg {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// ---- dropout: a counter-based generator, so the mask is computed again wherever
+// it is needed and never stored.  Philox 4x32 with 10 rounds (Salmon, Moraes,
+// Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011).  One call
+// gives 128 bits, 16 for each of eight consecutive columns: p is a multiple of
+// 2^-16, and the 20 products of a call, which the vector unit takes at a quarter
+// of its rate, are shared by eight elements.  (With 32 bits an element the
+// generator alone would take 26 us for 8192 x 4096, longer than the memory needs.)
+__device__ __forceinline__ uint4 philox(uint64_t n, uint64_t offset, uint64_t key) {
+  uint32_t c0 = (uint32_t)n, c1 = (uint32_t)(n >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+  uint32_t k0 = (uint32_t)key, k1 = (uint32_t)(key >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)b;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// The generator's state and the rule of one call.
+struct Drop {
+  uint64_t key, offset;
+  uint32_t t;   // an element is kept where its 16 bits are at least this
+  float scale;  // 65536 / (65536 - t); 0 where nothing is kept
+};
+__device__ __forceinline__ Drop drop_of(const DropArgs& a) {
+  return a.rng ? Drop{a.rng[0], a.rng[1], a.t, a.scale} : Drop{0, 0, 0, 1.f};
+}
+// v[i] (column 8 g + FIRST + i of a row whose groups start at `group`) dropped or
+// scaled; a dropped element is 0 whatever it held.
+template <int N>
+__device__ __forceinline__ void drop_n(const Drop& d, uint64_t group, int first, float (&v)[N]) {
+  const uint4 r = philox(group, d.offset, d.key);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (N == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (w[i / 2] >> (16 * (i & 1)) & 0xFFFFu) >= d.t ? v[i] * d.scale : 0.f;
+  } else if constexpr (N == 4) {
+    const uint32_t a = first ? w[2] : w[0], b = first ? w[3] : w[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ((i < 2 ? a : b) >> (16 * (i & 1)) & 0xFFFFu) >= d.t ? v[i] * d.scale : 0.f;
+  } else {
+    static_assert(N == 1, "1, 4 or 8 columns");
+    const uint32_t lo = first & 2 ? w[1] : w[0], hi = first & 2 ? w[3] : w[2];
+    v[0] = ((first & 4 ? hi : lo) >> (16 * (first & 1)) & 0xFFFFu) >= d.t ? v[0] * d.scale : 0.f;
+  }
+}
+
+// ---- activations.  FAST: for results of 16 bits, exponentials by the hardware's
+// 2^x alone (within 2 |x| half steps of fp32) and a shorter series for the normal
+// distribution; otherwise within about a step of fp32.
+// exp(-x), x >= 0
+template <bool FAST>
+__device__ __forceinline__ float exp_minus(float x) {
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;  // log2 e in two parts
+  if constexpr (FAST) {
+    return __builtin_amdgcn_exp2f(x * -kHi);
+  } else {
+    // 2^-(n + f), n whole: the hardware's 2^-f, f in [-1/2, 1/2]
+    x = fminf(x, 200.f);
+    const float n = __builtin_rintf(x * kHi);
+    const float f = fmaf(x, kLo, fmaf(x, kHi, -n));
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(-f), -(int)n);
+  }
+}
+// 1 / d, d in [1, 2] or larger
+template <bool FAST>
+__device__ __forceinline__ float recip(float d) {
+  const float q = __builtin_amdgcn_rcpf(d);
+  return FAST ? q : fmaf(q, fmaf(-d, q, 1.0f), q);
+}
+// The sigmoid of g and 1 minus it, from t = exp(-|g|).
+struct Sigm {
+  float at, neg;
+};
+template <bool FAST>
+__device__ __forceinline__ Sigm sigm(float g) {
+  const float t = exp_minus<FAST>(fabsf(g)), r = recip<FAST>(1.0f + t), tr = t * r;
+  return g < 0.f ? Sigm{tr, r} : Sigm{r, tr};
+}
+// The normal distribution's upper tail Q(z) = erfc(z / sqrt 2) / 2 and exp(-z^2 / 2)
+// for z >= 0: Q = exp(-z^2 / 2) m(z), where m falls slowly from 1/2 like 1 / z, so
+// m = t P(t) with t = 1 / (1 + c z) and P a polynomial fitted to m for the least
+// relative error on [0, 16] (8.6e-6 with six terms, 4e-8 with nine).  The tail keeps
+// its relative precision, which 1 - erf would lose.
+struct Tail {
+  float q, e;
+};
+template <bool FAST>
+__device__ __forceinline__ Tail tail(float z) {
+  if constexpr (FAST) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.46f, z, 1.0f));
+    const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170367f);
+    const float p = fmaf(fmaf(fmaf(fmaf(fmaf(0.0722274631f, t, -0.236543089f), t, 0.177799612f), t, 0.116107389f), t, 0.18706657f), t, 0.183346346f);
+    return Tail{p * t * e, e};
+  } else {
+    const float t = recip<false>(fmaf(0.26f, z, 1.0f));
+    const float s = z * z, lo = fmaf(z, z, -s);  // z^2 in two parts
+    const float e0 = exp_minus<false>(0.5f * s), e = fmaf(e0, -0.5f * lo, e0);
+    const float p = fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(0.0294354856f, t, -0.147663906f), t, 0.240891442f), t, -0.138905317f), t, 0.152682543f), t, 0.0545273423f), t, 0.102139488f), t, 0.103141129f), t, 0.103751779f);
+    return Tail{p * t * e, e};
+  }
+}
+constexpr float kPhi0 = 0.3989422804014327f;  // 1 / sqrt(2 pi)
+constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.044715f;  // 2 sqrt(2 / pi)
+
+// act(h) and act'(h).  Every one has its limit at h = -inf (0) instead of the
+// formula's NaN, by a bound on h below which the result is 0 in fp32; a NaN stays.
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_of(float h) {
+  if constexpr (ACT == FP8SG_ACT_RELU) {
+    return h <= 0.f ? 0.f : h;
+  } else if constexpr (ACT == FP8SG_ACT_SILU) {
+    return (h < -150.f ? -150.f : h) * sigm<FAST>(h).at;
+  } else if constexpr (ACT == FP8SG_ACT_GELU) {
+    const float z = fminf(fabsf(h), 16.f), zq = z * tail<FAST>(z).q;
+    return h <= 0.f ? -zq : h - zq;
+  } else if constexpr (ACT == FP8SG_ACT_GELU_TANH) {
+    const float c = h < -16.f ? -16.f : h;
+    return c * sigm<FAST>(kTanhA * fmaf(kTanhB * c * c, c, c)).at;
+  } else {
+    return h;
+  }
+}
+template <int ACT, bool FAST>
+__device__ __forceinline__ float slope_of(float h) {
+  if constexpr (ACT == FP8SG_ACT_RELU) {
+    return h <= 0.f ? 0.f : 1.f;
+  } else if constexpr (ACT == FP8SG_ACT_SILU) {
+    const float c = h < -150.f ? -150.f : h > 150.f ? 150.f : h;
+    const Sigm s = sigm<FAST>(c);
+    return s.at * fmaf(c, s.neg, 1.0f);
+  } else if constexpr (ACT == FP8SG_ACT_GELU) {
+    const float z = fminf(fabsf(h), 16.f);
+    const Tail t = tail<FAST>(z);
+    const float d = fmaf(-kPhi0 * z, t.e, t.q);  // at -z; at z it is 1 - d
+    return h != h ? h : h <= 0.f ? d : 1.0f - d;
+  } else if constexpr (ACT == FP8SG_ACT_GELU_TANH) {
+    const float c = h < -16.f ? -16.f : h > 16.f ? 16.f : h;
+    const float cc = c * c;
+    const Sigm s = sigm<FAST>(kTanhA * fmaf(kTanhB * cc, c, c));
+    return s.at * fmaf(s.neg * kTanhA * c, fmaf(3.f * kTanhB, cc, 1.0f), 1.0f);
+  } else {
+    return 1.0f;
+  }
+}
+// f(integral constant of the activation): one branch for a whole group of values
+template <class F>
+__device__ __forceinline__ void by_act(int act, F f) {
+  switch (act) {
+    case FP8SG_ACT_RELU: f(std::integral_constant<int, FP8SG_ACT_RELU>{}); break;
+    case FP8SG_ACT_SILU: f(std::integral_constant<int, FP8SG_ACT_SILU>{}); break;
+    case FP8SG_ACT_GELU: f(std::integral_constant<int, FP8SG_ACT_GELU>{}); break;
+    case FP8SG_ACT_GELU_TANH: f(std::integral_constant<int, FP8SG_ACT_GELU_TANH>{}); break;
+    default: break;
+  }
+}
+
+// ---- elements of a type known at run time (one branch a group)
+template <int N>
+struct Raw {  // N elements as loaded: N dwords of fp32, N / 2 of 16 bits
+  uint32_t w[N];
+};
+// Elements past `n` read as 0.
+template <int N>
+__device__ __forceinline__ Raw<N> load_raw(const void* p, int64_t at, int n, int type) {
+  Raw<N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.w[i] = 0u;
+  if (type == FP8SG_OUT_F32) {
+    const float* q = reinterpret_cast<const float*>(p) + at;
+    if constexpr (N == 8) {
+      if (n >= 8) {
+        const u32x4 a = ld_any<false>(q), b = ld_any<false>(q + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = a[i], r.w[4 + i] = b[i];
+        return r;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) r.w[i] = __float_as_uint(q[i]);
+  } else {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
+    if constexpr (N == 8) {
+      if (n >= 8) {
+        const u32x4 a = ld_any<false>(q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = a[i];
+        return r;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) r.w[i / 2] |= (uint32_t)q[i] << (16 * (i & 1));
+  }
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void raw_values(const Raw<N>& r, int type, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (type == FP8SG_OUT_F32) v[i] = __uint_as_float(r.w[i]);
+    else if (type == FP8SG_OUT_F16) v[i] = (i & 1) ? in_hi<true>(r.w[i / 2]) : in_lo<true>(r.w[i / 2]);
+    else v[i] = (i & 1) ? in_hi<false>(r.w[i / 2]) : in_lo<false>(r.w[i / 2]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const void* p, int64_t at, int n, int type, float (&v)[N]) {
+  raw_values(load_raw<N>(p, at, n, type), type, v);
+}
+template <int N, int T, bool S>
+__device__ __forceinline__ void store_t(void* p, int64_t at, int n, const float (&v)[N]) {
+  Elem<T>* q = reinterpret_cast<Elem<T>*>(p) + at;
+  if constexpr (N == 8) {
+    store8<T, S>(q, n, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) q[i] = from_f32<T>(v[i]);
+  }
+}
+// S: non-temporal
+template <int N, bool S>
+__device__ __forceinline__ void store_n(void* p, int64_t at, int n, int type, const float (&v)[N]) {
+  if (type == FP8SG_OUT_BF16) store_t<N, FP8SG_OUT_BF16, S>(p, at, n, v);
+  else if (type == FP8SG_OUT_F16) store_t<N, FP8SG_OUT_F16, S>(p, at, n, v);
+  else store_t<N, FP8SG_OUT_F32, S>(p, at, n, v);
+}
+
+// ---- the epilogue of N columns from n on (n % N == 0) of row m: acc (the product
+// times its scales), its bias and the residual as loaded
+template <int N, bool FAST>
+__device__ __forceinline__ void epilogue_n(const EpilogueArgs& e, const Drop& d, float (&v)[N], const float (&bias)[N],
+                                           const Raw<N>& res, int64_t m, int64_t n) {
+  const int cnt = e.N - n < N ? (int)(e.N - n) : N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] += bias[i];
+  if (e.pre) {
+    if (e.stream) store_n<N, true>(e.pre, m * e.N + n, cnt, e.type, v);
+    else store_n<N, false>(e.pre, m * e.N + n, cnt, e.type, v);
+  }
+  by_act(e.act, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_of<decltype(a)::value, FAST>(v[i]);
+  });
+  if (e.drop.rng) drop_n<N>(d, (uint64_t)m * (uint64_t)((e.N + 7) >> 3) + (uint64_t)(n >> 3), (int)(n & 7), v);
+  if (e.residual) {
+    float r[N];
+    raw_values(res, e.type, r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += r[i];
+  }
+  if (e.stream) store_n<N, true>(e.C, m * e.ldc + n, cnt, e.type, v);
+  else store_n<N, false>(e.C, m * e.ldc + n, cnt, e.type, v);
+}
+template <int N>
+__device__ __forceinline__ Raw<N> load_residual(const EpilogueArgs& e, int64_t m, int64_t n) {
+  if (e.residual && m < e.M && n < e.N)
+    return load_raw<N>(e.residual, m * e.ldr + n, e.N - n < N ? (int)(e.N - n) : N, e.type);
+  return Raw<N>{};
+}
+template <int N>
+__device__ __forceinline__ void load_bias(const EpilogueArgs& e, int64_t n, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  if (e.bias && n < e.N) load_n<N>(e.bias, n, e.N - n < N ? (int)(e.N - n) : N, e.bias_type, v);
+}
+// N columns whose inputs were not loaded ahead
+template <int N, bool FAST>
+__device__ __forceinline__ void epilogue_at(const EpilogueArgs& e, float (&v)[N], int64_t m, int64_t n) {
+  if (m >= e.M || n >= e.N) return;
+  float b[N];
+  load_bias<N>(e, n, b);
+  epilogue_n<N, FAST>(e, drop_of(e.drop), v, b, load_residual<N>(e, m, n), m, n);
+}
+
+// The epilogue of a wave's 16 TM x 64 sub-tile with origin (m0, n0), held as 16 x 16
+// blocks of the matrix instruction's layout (lane: row lane % 16, columns 4 (lane /
+// 16) .. + 3 of a block).  The accumulators go through 16 KB of LDS that belong to
+// the wave alone, 64 rows at a time in fp32, so no wave waits for another, and a
+// lane gets eight consecutive columns of a row: residual and results then move 16
+// bytes a lane in whole 128-byte lines (in the blocks' own layout a lane's four
+// columns would be 8 bytes of a line that 16 rows share), the generator's eight
+// elements are one lane's, and the activation is code for 8 values in a loop, not
+// for the tile's 128 a lane.  The next row group's residual is loaded ahead.
+// scale(c, i, j): the product's scales on block (i, j).
+constexpr int kWaveEpilogueLds = 64 * 64 * 4;
+template <int TM, bool FAST, class Scale>
+__device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[TM][4], uint8_t* lds, int64_t m0,
+                                              int64_t n0, int lane, Scale scale) {
+  const int cc = lane & 7, lr = lane >> 3;
+  const int64_t n = n0 + 8 * cc;
+  float* tile = reinterpret_cast<float*>(lds);
+  // 16-byte chunk c of row r at c ^ r % 16: the 16 rows that a store writes, and the
+  // even chunks of two rows that a load reads, fall on different banks
+  auto at = [&](int r, int c) { return tile + r * 64 + ((c ^ (r & 15)) << 2); };
+  const Drop d = drop_of(e.drop);
+  float bias[8];
+  load_bias<8>(e, n, bias);
+  Raw<8> next = load_residual<8>(e, m0 + lr, n);
+#pragma unroll
+  for (int h = 0; h < TM; h += 4) {
+#pragma unroll
+    for (int i = h; i < TM && i < h + 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v4f c = acc[i][j];
+        scale(c, i, j);
+        *reinterpret_cast<v4f*>(at(16 * (i - h) + (lane & 15), 4 * j + (lane >> 4))) = c;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int rows = 16 * (TM - h < 4 ? TM - h : 4);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      const int r = r0 + lr;
+      const int64_t m = m0 + 16 * h + r;
+      const Raw<8> res = next;
+      if (r0 + 8 < rows || h + 4 < TM) next = load_residual<8>(e, m + 8, n);
+      const v4f a = *reinterpret_cast<const v4f*>(at(r, 2 * cc)), b = *reinterpret_cast<const v4f*>(at(r, 2 * cc + 1));
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      if (m < e.M && n < e.N) epilogue_n<8, FAST>(e, d, v, bias, res, m, n);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+}  // namespace fp8sg

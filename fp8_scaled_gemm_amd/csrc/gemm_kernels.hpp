@@ -20,12 +20,14 @@
 //   - k_gemm: 128 x 128 tiles with register-staged loads, for smaller problems.
 // Each kernel has a per-tensor epilogue (one alpha) and a row-wise one (RW:
 // inverse-scale vectors along M and N); gemm.hip and gemm_rowwise.hip hold the
-// two sets of instantiations.
+// two sets of instantiations.  A problem with an epilogue behind the product
+// (GemmEpiProblem; gemm_epilogue.hip) takes wave_epilogue in place of the stores.
 #pragma once
 
 #include <type_traits>
 
 #include "common.hpp"
+#include "epilogue.hpp"
 #include "launch.hpp"
 
 namespace fp8sg {
@@ -191,8 +193,8 @@ struct CastSrc {
 // as in the large-tile kernel below.
 // CA / CB: the operand is a bf16 tensor cast on the fly (CastSrc ca / cb).
 template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, bool RW, bool TA = false,
-          bool TB = false, bool CA = false, bool CB = false>
-__device__ __forceinline__ void gemm_small_tile(const GemmProblem& p, int bx, int by,
+          bool TB = false, bool CA = false, bool CB = false, class Prob = GemmProblem>
+__device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
                                                 CastSrc ca = CastSrc{}, CastSrc cb = CastSrc{}) {
   static_assert(!(TA || TB) || (BM == 128 && BN == 128), "contraction-major: 128 x 128 tiles");
   using Cfg = GemmCfg<BM, BN, WM, WN>;
@@ -389,6 +391,12 @@ __device__ __forceinline__ void gemm_small_tile(const GemmProblem& p, int bx, in
       return Alpha<RW, Cfg::kTM, Cfg::kTN>(p, bm + wm * (BM / WM), bn + wn * (BN / WN), lane);
   };
   const Alpha<RW, Cfg::kTM, Cfg::kTN> alpha = make_alpha();
+  if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {  // (the loop ended with a barrier: the tiles are free)
+    static_assert(BN / WN == 64 && (BM / WM) % 64 == 0 && Cfg::kLdsBytes >= WM * WN * kWaveEpilogueLds, "wave sub-tile");
+    wave_epilogue<Cfg::kTM, true>(p.epi, acc, smem + wave * kWaveEpilogueLds, bm + wm * (BM / WM), bn + wn * 64, lane,
+                                  [&](v4f& c, int i, int j) { alpha.apply(c, i, j); });
+    return;
+  }
   Unscale us;
   if constexpr (OUT == kOutF16Unscale) us.load(p);
 #pragma unroll
@@ -411,8 +419,8 @@ __device__ __forceinline__ void gemm_small_tile(const GemmProblem& p, int bx, in
 }
 
 template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, bool RW, bool TA = false,
-          bool TB = false>
-__global__ __launch_bounds__(WM* WN* kWave) void k_gemm(GemmProblem p) {
+          bool TB = false, class Prob = GemmProblem>
+__global__ __launch_bounds__(WM* WN* kWave) void k_gemm(Prob p) {
   gemm_small_tile<BM, BN, WM, WN, FA, FB, OUT, RW, TA, TB>(p, blockIdx.x, blockIdx.y);
 }
 
@@ -589,8 +597,10 @@ __device__ __forceinline__ void tile_of(int nbm, int nbn, int& tm, int& tn) {
 __device__ __forceinline__ int swzT(int r) { return (r & 7) | ((((r >> 5) ^ (r >> 6)) & 1) << 3); }
 
 template <int FA, int FB, int OUT, bool RAGGED_K, bool RW, int BM = 256, bool TR = false,
-          bool TA = false, bool TB = false>
-__global__ __launch_bounds__(512) void k_gemm_pingpong(GemmProblem p) {
+          bool TA = false, bool TB = false, class Prob = GemmProblem>
+__global__ __launch_bounds__(512) void k_gemm_pingpong(Prob p) {
+  constexpr bool kEpi = std::is_same_v<Prob, GemmEpiProblem>;
+  static_assert(!kEpi || !TR, "the epilogue takes C's own rows");
   static_assert(BM == 256 || BM == 224, "tile rows");
   static_assert(!(TR && RW), "transposed roles: per-tensor scaling only");
   static_assert(!(RW && (TA || TB)), "contraction-major operands: per-tensor scaling only");
@@ -843,7 +853,14 @@ __global__ __launch_bounds__(512) void k_gemm_pingpong(GemmProblem p) {
   };
   const int64_t c_rows = TR ? N : M, c_cols = TR ? M : N;
   const int64_t row0 = TR ? bn : bm, col0 = TR ? bm : bn;
-  if constexpr (OUT == FP8SG_OUT_F32) {
+  if constexpr (kEpi) {
+    __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing a slot
+    barrier();
+    static_assert(2 * kWaveEpilogueLds == 256 * kBK, "two waves a slot");
+    uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
+    wave_epilogue<kTM, true>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + wr0, bn + wc0, lane,
+                             [&](v4f& c, int i, int j) { alpha.apply(c, i, j); });
+  } else if constexpr (OUT == FP8SG_OUT_F32) {
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
 #pragma unroll

@@ -117,6 +117,17 @@ struct SmallBwdArgs {
 bool small_layer_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream);
 hipError_t launch_small_bwd(const SmallBwdArgs& a, int out, hipStream_t stream);
+// A linear layer's passes behind the validated entry points (api.hip).  Casts of x
+// and W (dynamic: amax and quantize; delayed: histories given) of bf16 or fp16
+// tensors; and the cast of gy with the two backward GEMMs.  have_amax: gy's
+// per-block maxima are in its record already.
+hipError_t launch_linear_casts(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                               const fp8_linear_saved& saved, float* hist_x, float* hist_w,
+                               int32_t hist_len, bool f16, hipStream_t stream);
+hipError_t launch_linear_bwd(const uint16_t* gy, const fp8_linear_saved& saved, int64_t M, int64_t N,
+                             int64_t K, const fp8_linear_bwd_ws& ws, float* hist_gy, int32_t hist_len,
+                             void* gx, void* gw, int out, const float* amp_scale, int32_t* found_inf,
+                             bool f16, bool have_amax, hipStream_t stream);
 // Row-wise scaling (gemm_rowwise.hip): inv_a points to M doubles, inv_b to N;
 // element (m, n) is scaled by fl32(inv_a[m] * inv_b[n]).
 hipError_t launch_gemm_rowwise(const GemmProblem& p, int fa, int fb, int out, hipStream_t stream);

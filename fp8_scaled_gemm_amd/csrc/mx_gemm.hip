@@ -7,11 +7,19 @@
 #include <algorithm>
 #include <atomic>
 
+#include "epilogue.hpp"
 #include "gemm_kernels.hpp"  // LDS staging, tile order
 #include "mx.hpp"
 
 namespace fp8sg {
 namespace {
+
+// A problem with an epilogue behind the product (epilogue.hpp) has its result's
+// type at run time; OUT then only says whether it is fp32 or has 16 bits.
+template <class Prob>
+constexpr bool kEpi = std::is_same_v<Prob, MxGemmEpiProblem>;
+template <int OUT>
+constexpr bool kFast = OUT != FP8SG_OUT_F32;
 
 // One 16 x 16 x 128 product of e2m1 fragments; SA / SB: which byte of sa / sb is
 // the lane's scale.  The first operand's rows become the lane's four
@@ -47,8 +55,8 @@ __device__ __forceinline__ void put4(Elem<OUT>* row, int64_t n, int64_t N, v4f v
 // One wave per 16 x 16 block of C, fragments straight from memory, in 64-bit
 // addresses: for contractions of 2^24 values or more, too long for the other
 // kernels' offsets.  Kept simple: such a matrix has at most 2048 rows.
-template <int OUT>
-__global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
+template <int OUT, class Prob = MxGemmProblem>
+__global__ __launch_bounds__(64) void k_mx_gemm_plain(Prob p) {
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
   const int64_t nk = mx_ktiles(p.K);
   const int64_t nbn = (p.N + 15) / 16;
@@ -66,6 +74,11 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
     }
   }
   if (bm + r >= p.M) return;
+  if constexpr (kEpi<Prob>) {
+    float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+    epilogue_at<4, kFast<OUT>>(p.epi, v, bm + r, bn + 4 * g);
+    return;
+  }
   put4<OUT, false>(reinterpret_cast<Elem<OUT>*>(p.C) + (bm + r) * p.N, bn + 4 * g, p.N, acc);
 }
 
@@ -101,8 +114,8 @@ __global__ __launch_bounds__(64) void k_mx_gemm_plain(MxGemmProblem p) {
 // and some 20 the tile's start and its stores: one workgroup fills a unit and all
 // tiles are alike, so all units store at once while none multiplies.  256 x 256:
 // halving either side doubles the LDS reads per product (see k_mx_mid).
-template <int OUT>
-__global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
+template <int OUT, class Prob = MxGemmProblem>
+__global__ __launch_bounds__(512) void k_mx_pingpong(Prob p) {
   constexpr int BM = 256, BN = 256, kTM = 8, kTN = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[256 * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t sA1[256 * 128];
@@ -243,7 +256,14 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
 
   // Lane: rows wr0 + 16 i + lane % 16, columns wc0 + 16 j + 4 (lane / 16) .. + 3.
   const int wr0 = grp * 128 + (lane & 15), wc0 = wq * 64 + 4 * (lane >> 4);
-  if constexpr (OUT == FP8SG_OUT_F32) {
+  if constexpr (kEpi<Prob>) {
+    __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing a slot
+    barrier();
+    static_assert(2 * kWaveEpilogueLds == sizeof(sA0), "two waves a slot");
+    uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
+    wave_epilogue<kTM, kFast<OUT>>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + grp * 128, bn + wq * 64, lane,
+                                   [](v4f&, int, int) {});
+  } else if constexpr (OUT == FP8SG_OUT_F32) {
     float* C = reinterpret_cast<float*>(p.C);
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
@@ -299,8 +319,8 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(MxGemmProblem p) {
 // reads (8 fragments per 16 products) bound it at about half the matrix rate
 // (2048 x 2048 x 4096 16 us, 2.1 PFLOP/s; 256 x 14336 x 4096 15.5 us, 1.9), so it is
 // for products that the large tiles would leave compute units idle for.
-template <int OUT>
-__global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
+template <int OUT, class Prob = MxGemmProblem>
+__global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
   constexpr int kStage = 2 * 128 * 128 + 2048;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];  // A, B, scales of A, of B
   const int lane = threadIdx.x & (kWave - 1);
@@ -380,6 +400,12 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(MxGemmProblem p) {
     __builtin_amdgcn_s_barrier();
     compiler_fence();
   }
+  if constexpr (kEpi<Prob>) {  // (every load has landed, every wave has read its last stage)
+    static_assert(4 * kWaveEpilogueLds <= sizeof(lds), "wave sub-tiles");
+    wave_epilogue<4, kFast<OUT>>(p.epi, acc, lds + wave * kWaveEpilogueLds, bm + 64 * wm, bn + 64 * wn, lane,
+                                 [](v4f&, int, int) {});
+    return;
+  }
   Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
   auto write = [&](auto fours) {
 #pragma unroll
@@ -440,8 +466,8 @@ constexpr int few_waves(int tm, int tn, bool fused) {
 }
 
 // blk of blocks: this workgroup's place among the problem's.
-template <int TM, int TN, int OUT, int FT>
-__device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& ap, int64_t blk, int64_t blocks) {
+template <int TM, int TN, int OUT, int FT, class Prob>
+__device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64_t blk, int64_t blocks) {
   constexpr bool kFused = FT >= 0;
   constexpr int kStage = few_stage(TM, TN, kFused), kOwn = few_own(kFused);
   // loads of a stage (a wave's count of vmcnt)
@@ -595,7 +621,7 @@ __device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& 
   }
 
   Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
-  if (W == 1) {  // nothing to join
+  if (!kEpi<Prob> && W == 1) {  // nothing to join (an epilogue takes the join's element order all the same)
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int64_t m = bm + 16 * i + r;
@@ -620,13 +646,18 @@ __device__ __forceinline__ void few_tile(const MxGemmProblem& p, const MxApply& 
       const float* src = red + ((nl >> 4) * 64 + ((nl & 15) >> 2) * 16 + ml) * 4 + (nl & 3);
       float v = 0.f;
       for (int w = 0; w < W; ++w) v += src[w * TN * 256];
-      C[m * N + n] = from_f32<OUT>(v);
+      if constexpr (kEpi<Prob>) {
+        float one[1] = {v};
+        epilogue_at<1, kFast<OUT>>(p.epi, one, m, n);
+      } else {
+        C[m * N + n] = from_f32<OUT>(v);
+      }
     }
   }
 }
 
-template <int TM, int TN, int OUT, int FT>
-__global__ __launch_bounds__(64 * few_waves(TM, TN, (FT >= 0))) void k_mx_few(MxGemmProblem p, MxApply ap) {
+template <int TM, int TN, int OUT, int FT, class Prob>
+__global__ __launch_bounds__(64 * few_waves(TM, TN, (FT >= 0))) void k_mx_few(Prob p, MxApply ap) {
   few_tile<TM, TN, OUT, FT>(p, ap, blockIdx.x, gridDim.x);
 }
 // Two small products in one launch: the first `blocks0` workgroups' and the rest's.
@@ -660,9 +691,9 @@ int split_waves(int64_t nk, int64_t blocks, int64_t per_wave, int64_t most) {
   const int64_t per = (nk + most - 1) / most;
   return (int)((nk + per - 1) / per);
 }
-template <int TM, int TN, int OUT, int FT>
-hipError_t launch_few(const MxGemmProblem& p, const MxApply& ap, hipStream_t stream) {
-  auto kern = k_mx_few<TM, TN, OUT, FT>;
+template <int TM, int TN, int OUT, int FT, class Prob>
+hipError_t launch_few(const Prob& p, const MxApply& ap, hipStream_t stream) {
+  auto kern = k_mx_few<TM, TN, OUT, FT, Prob>;
   static std::atomic<uint64_t> done{0};
   const hipError_t attr = allow_lds(kern, done);
   if (attr != hipSuccess) return attr;
@@ -701,42 +732,51 @@ double mid_cost(const MxGemmProblem& p, int cus) {
   return 2.8 + nk * 1.35 * ((tiles + 2 * cus - 1) / (2 * cus));
 }
 
+// A product with or without an epilogue.
+template <int T, class Prob>
+hipError_t launch_product(const Prob& p, hipStream_t stream) {
+  auto tiles = [&](int64_t e) { return ((p.M + e - 1) / e) * ((p.N + e - 1) / e); };
+  // The tiled kernels' 32-bit offsets span 256 rows: K below 2^24.
+  if (mx_pitch(p.K) * 256 >= (1ll << 31) - 256) {
+    hipLaunchKernelGGL((k_mx_gemm_plain<T, Prob>), dim3((unsigned)tiles(16)), dim3(64), 0, stream, p);
+    return hipGetLastError();
+  }
+  const MxApply none{};
+  // Nothing to add up: zeros, in the fewest workgroups of those kernels that
+  // take an empty contraction.
+  if (p.K == 0) return launch_few<4, 4, T, -1>(p, none, stream);
+  const int cus = device_cus();
+  // The large tiles where they occupy most of the chip (2048 x 4096 x 4096, 128
+  // tiles on 256 units: 33.9 us, 24.4 us in tiles of 128; 4096^3, 256 tiles:
+  // 37.1 against 43.3 us).
+  if (tiles(256) * 8 >= 5 * cus) {
+    hipLaunchKernelGGL((k_mx_pingpong<T, Prob>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
+    return hipGetLastError();
+  }
+  const double c11 = few_cost(p, 1, 1, FewCost{2.0, 0.7}, cus), c12 = few_cost(p, 1, 2, FewCost{2.4, 0.7}, cus);
+  const double c22 = few_cost(p, 2, 2, FewCost{3.5, 0.6}, cus), c44 = few_cost(p, 4, 4, FewCost{8.8, 0.7}, cus);
+  const double few = std::min(std::min(c11, c12), std::min(c22, c44));
+  if (mid_cost(p, cus) < few) {
+    hipLaunchKernelGGL((k_mx_mid<T, Prob>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
+  if (few == c11) return launch_few<1, 1, T, -1>(p, none, stream);
+  if (few == c12) return launch_few<1, 2, T, -1>(p, none, stream);
+  if (few == c22) return launch_few<2, 2, T, -1>(p, none, stream);
+  return launch_few<4, 4, T, -1>(p, none, stream);
+}
+
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmProblem& p, int out, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  return by_type(out, [&](auto t) {
-    constexpr int T = decltype(t)::value;
-    auto tiles = [&](int64_t e) { return ((p.M + e - 1) / e) * ((p.N + e - 1) / e); };
-    // The tiled kernels' 32-bit offsets span 256 rows: K below 2^24.
-    if (mx_pitch(p.K) * 256 >= (1ll << 31) - 256) {
-      hipLaunchKernelGGL((k_mx_gemm_plain<T>), dim3((unsigned)tiles(16)), dim3(64), 0, stream, p);
-      return hipGetLastError();
-    }
-    const MxApply none{};
-    // Nothing to add up: zeros, in the fewest workgroups of those kernels that
-    // take an empty contraction.
-    if (p.K == 0) return launch_few<4, 4, T, -1>(p, none, stream);
-    const int cus = device_cus();
-    // The large tiles where they occupy most of the chip (2048 x 4096 x 4096, 128
-    // tiles on 256 units: 33.9 us, 24.4 us in tiles of 128; 4096^3, 256 tiles:
-    // 37.1 against 43.3 us).
-    if (tiles(256) * 8 >= 5 * cus) {
-      hipLaunchKernelGGL((k_mx_pingpong<T>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
-      return hipGetLastError();
-    }
-    const double c11 = few_cost(p, 1, 1, FewCost{2.0, 0.7}, cus), c12 = few_cost(p, 1, 2, FewCost{2.4, 0.7}, cus);
-    const double c22 = few_cost(p, 2, 2, FewCost{3.5, 0.6}, cus), c44 = few_cost(p, 4, 4, FewCost{8.8, 0.7}, cus);
-    const double few = std::min(std::min(c11, c12), std::min(c22, c44));
-    if (mid_cost(p, cus) < few) {
-      hipLaunchKernelGGL((k_mx_mid<T>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
-      return hipGetLastError();
-    }
-    if (few == c11) return launch_few<1, 1, T, -1>(p, none, stream);
-    if (few == c12) return launch_few<1, 2, T, -1>(p, none, stream);
-    if (few == c22) return launch_few<2, 2, T, -1>(p, none, stream);
-    return launch_few<4, 4, T, -1>(p, none, stream);
-  });
+  return by_type(out, [&](auto t) { return launch_product<decltype(t)::value>(p, stream); });
+}
+
+hipError_t launch_mx_gemm_epilogue(const MxGemmEpiProblem& p, hipStream_t stream) {
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  return p.epi.type == FP8SG_OUT_F32 ? launch_product<FP8SG_OUT_F32>(p, stream)
+                                     : launch_product<FP8SG_OUT_BF16>(p, stream);
 }
 
 hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1, int out, hipStream_t stream) {
@@ -765,22 +805,42 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
   return e != hipSuccess ? e : launch_mx_gemm(p1, out, stream);
 }
 
+namespace {
+
+// Every workgroup quantises x again, so in the product's own launch only for
+// a few rows, and only k-tiles that fit its LDS.
+bool apply_fused(const MxGemmProblem& p) {
+  return p.M <= kFusedRows && p.K > 0 && mx_ktiles(p.K) <= 4 * kFusedTiles;
+}
+template <int T, class Prob>
+hipError_t launch_apply_fused(const MxQuantJob& j, int type, bool fit, const Prob& p, hipStream_t stream) {
+  return by_type(type, [&](auto f) {
+    constexpr int X = decltype(f)::value;
+    const MxApply ap{j.x, fit};
+    return (p.N + 31) / 32 >= device_cus() ? launch_few<1, 2, T, X>(p, ap, stream)
+                                           : launch_few<1, 1, T, X>(p, ap, stream);
+  });
+}
+
+}  // namespace
+
 hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemmProblem& p, int out,
                            hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  // Every workgroup quantises x again, so in the product's own launch only for
-  // a few rows, and only k-tiles that fit its LDS.
-  if (p.M <= kFusedRows && p.K > 0 && mx_ktiles(p.K) <= 4 * kFusedTiles)
-    return by_type(out, [&](auto t) {
-      return by_type(type, [&](auto f) {
-        constexpr int T = decltype(t)::value, X = decltype(f)::value;
-        const MxApply ap{j.x, fit};
-        return (p.N + 31) / 32 >= device_cus() ? launch_few<1, 2, T, X>(p, ap, stream)
-                                               : launch_few<1, 1, T, X>(p, ap, stream);
-      });
-    });
+  if (apply_fused(p))
+    return by_type(out, [&](auto t) { return launch_apply_fused<decltype(t)::value>(j, type, fit, p, stream); });
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
   return e != hipSuccess ? e : launch_mx_gemm(p, out, stream);
+}
+
+hipError_t launch_mx_apply_epilogue(const MxQuantJob& j, int type, bool fit, const MxGemmEpiProblem& p,
+                                    hipStream_t stream) {
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  if (apply_fused(p))
+    return p.epi.type == FP8SG_OUT_F32 ? launch_apply_fused<FP8SG_OUT_F32>(j, type, fit, p, stream)
+                                       : launch_apply_fused<FP8SG_OUT_BF16>(j, type, fit, p, stream);
+  const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
+  return e != hipSuccess ? e : launch_mx_gemm_epilogue(p, stream);
 }
 
 }  // namespace fp8sg

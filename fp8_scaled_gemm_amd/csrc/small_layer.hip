@@ -70,8 +70,9 @@ __device__ __forceinline__ void write_self_record(fp8sg_scale_rec* rec, uint32_t
   rec->inv32 = v.inv32;
 }
 
-template <int OUT>
-__global__ __launch_bounds__(kSmallThreads) void k_small_fwd(SmallFwdArgs a) {
+// Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT is not used then).
+template <int OUT, class Args>
+__global__ __launch_bounds__(kSmallThreads) void k_small_fwd(Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* red = reinterpret_cast<uint32_t*>(smem);
   const uint32_t bx_bits = block_absmax_bits(a.x, a.p.M * a.p.K, red);
@@ -118,10 +119,17 @@ hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream) 
   const dim3 grid((unsigned)((a.p.N + 127) / 128), (unsigned)((a.p.M + 127) / 128));
   const size_t lds = SmallCfg::kLdsBytes;
   switch (out) {
-    case FP8SG_OUT_BF16: hipLaunchKernelGGL(k_small_fwd<FP8SG_OUT_BF16>, grid, dim3(kSmallThreads), lds, stream, a); break;
-    case FP8SG_OUT_F16: hipLaunchKernelGGL(k_small_fwd<FP8SG_OUT_F16>, grid, dim3(kSmallThreads), lds, stream, a); break;
-    default: hipLaunchKernelGGL(k_small_fwd<FP8SG_OUT_F32>, grid, dim3(kSmallThreads), lds, stream, a); break;
+    case FP8SG_OUT_BF16: hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdArgs>), grid, dim3(kSmallThreads), lds, stream, a); break;
+    case FP8SG_OUT_F16: hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_F16, SmallFwdArgs>), grid, dim3(kSmallThreads), lds, stream, a); break;
+    default: hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_F32, SmallFwdArgs>), grid, dim3(kSmallThreads), lds, stream, a); break;
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.p.N + 127) / 128), (unsigned)((a.p.M + 127) / 128));
+  hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>), grid, dim3(kSmallThreads), SmallCfg::kLdsBytes,
+                     stream, a);
   return hipGetLastError();
 }
 

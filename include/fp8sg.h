@@ -800,6 +800,141 @@ FP8SG_API fp8sg_status layer_norm_bwd(const void* dy, const void* x, const fp8sg
                                       int64_t cols, void* dx, void* dw, void* db, float* ws,
                                       int64_t ws_len, fp8sg_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * What follows a linear layer's product, in the product's own epilogue, its
+ * backward step, and dropout.  Matrices need the alignment of their element type
+ * only; sizes as in the section above (multiples of 16 for the FP8 products).
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+  FP8SG_ACT_NONE = 0,     /* h                                                       */
+  FP8SG_ACT_RELU = 1,     /* max(h, 0)                                               */
+  FP8SG_ACT_SILU = 2,     /* h / (1 + exp(-h))                                       */
+  FP8SG_ACT_GELU = 3,     /* h Phi(h), Phi the normal distribution's                 */
+  FP8SG_ACT_GELU_TANH = 4 /* h / (1 + exp(-2 u)), u = sqrt(2/pi) (h + 0.044715 h^3)  */
+} fp8sg_act;
+
+/*
+ * The epilogue of a product acc[M,N]:
+ *   h = acc + bias[n],   y = residual + drop(act(h)),
+ * in fp32 from the fp32 accumulator (with its scales), rounded once to y and once
+ * to `pre`.  At h = -inf every activation has its limit, 0; a NaN stays.
+ *
+ * drop keeps element (m, n) where u >= t and scales it by 65536 / (65536 - t),
+ * t = round(65536 p), and is exactly 0 elsewhere, whatever the element was.  u are
+ * 16 bits of a counter-based generator, so the mask is never stored: Philox 4x32
+ * with 10 rounds (Salmon, Moraes, Dror, Shaw, SC 2011) with the key rng[0] and the
+ * counter m * ceil(N / 8) + n / 8 in its low, rng[1] in its high 64 bits; element n
+ * takes half n % 2 (low first) of output word (n % 8) / 2.  The two words are read
+ * from device memory when the kernels run, so a captured graph draws other masks
+ * on each replay if they have changed, and the backward pass needs the same two.
+ * p below 2^-17 drops nothing; p = 1 drops everything.
+ *
+ *   bias:     N values of bias_type (the input's type or FP8SG_OUT_F32), or NULL.
+ *   residual: M x N of the output's type, rows ld_residual elements apart, or NULL.
+ *             It may be the output itself (same address and row distance).
+ *   pre:      M x N of the output's type, contiguous: the forward writes h there
+ *             unless NULL; the backward step reads it (needed unless act is none).
+ *   rng:      two words in device memory; not read where p drops nothing, else
+ *             required.  8-byte aligned.
+ *   ld_out:   rows of the output are this many elements apart (>= N).
+ * A backward call reads pre, rng, p, act and bias_type only.
+ */
+typedef struct fp8sg_epilogue {
+  const void* bias;
+  const void* residual;
+  void* pre;
+  const int64_t* rng;
+  int64_t ld_residual;
+  int64_t ld_out;
+  float p;
+  int32_t act;
+  int32_t bias_type;
+} fp8sg_epilogue;
+
+/* fp8_gemm and fp8_gemm_rowwise of two e4m3 operands (the forward product) with an
+ * epilogue.  Kc == 0: acc is 0.  C need only be aligned to its type. */
+FP8SG_API fp8sg_status fp8_gemm_epilogue(const uint8_t* A, const uint8_t* B, const double* inv_a,
+                                         const double* inv_b, const fp8sg_epilogue* epi, void* C,
+                                         fp8sg_out out, int64_t M, int64_t N, int64_t Kc,
+                                         fp8sg_stream stream);
+FP8SG_API fp8sg_status fp8_gemm_rowwise_epilogue(const uint8_t* A, const uint8_t* B,
+                                                 const double* inv_a, const double* inv_b,
+                                                 const fp8sg_epilogue* epi, void* C, fp8sg_out out,
+                                                 int64_t M, int64_t N, int64_t Kc,
+                                                 fp8sg_stream stream);
+
+/* fp8_scaled_linear_fwd (dynamic scaling) with an epilogue.  x and w are of `type`,
+ * bf16 or fp16; bias_type is `type` or FP8SG_OUT_F32. */
+FP8SG_API fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void* w, fp8sg_out type,
+                                                      int64_t M, int64_t N, int64_t K,
+                                                      const fp8_linear_saved* saved,
+                                                      const fp8sg_epilogue* epi, void* y,
+                                                      fp8sg_out out, fp8sg_stream stream);
+
+/*
+ * The backward step of an epilogue: gh = drop(gy) * act'(pre) of `type`, and the
+ * bias's gradient gb[n] = sum over m of the unrounded gh (fp32 sums in an order
+ * that depends on the sizes only, rounded once to bias_type).
+ *   gy, pre, gh: M x N of `type`, contiguous.  gh may be gy; NULL if only gb is
+ *                wanted.  gb may be NULL.  act'(0) of relu is 0.
+ *   ws: float[ws_len], ws_len >= epilogue_workspace_len(M, N); not read before it
+ *       is written; may be NULL where gb is.
+ */
+FP8SG_API int64_t epilogue_workspace_len(int64_t M, int64_t N);
+FP8SG_API fp8sg_status epilogue_bwd(const void* gy, fp8sg_out type, const fp8sg_epilogue* epi,
+                                    int64_t M, int64_t N, void* gh, void* gb, float* ws,
+                                    int64_t ws_len, fp8sg_stream stream);
+
+/* The backward pass of fp8_scaled_linear_fwd_epilogue: epilogue_bwd (whose pass also
+ * takes gh's largest magnitude), then fp8_scaled_linear_bwd's cast and products on
+ * gh.  gh may be NULL where the epilogue neither drops nor has an activation (it
+ * would be gy).  ws_part, part_len: epilogue_bwd's workspace.  gx, gw: of `out`. */
+FP8SG_API fp8sg_status fp8_scaled_linear_bwd_epilogue(
+    const void* gy, fp8sg_out type, const fp8_linear_saved* saved, int64_t M, int64_t N, int64_t K,
+    const fp8_linear_bwd_ws* ws, const fp8sg_epilogue* epi, void* gh, void* gb, float* ws_part,
+    int64_t part_len, void* gx, void* gw, fp8sg_out out, fp8sg_stream stream);
+
+/* mxfp4_gemm, mxfp4_linear_fwd, mxfp4_linear_apply and mxfp4_linear_bwd with an
+ * epilogue.  gx and gw may be NULL as in mxfp4_linear_bwd (both, where gb is wanted
+ * alone), gh as above or where neither is wanted. */
+FP8SG_API fp8sg_status mxfp4_gemm_epilogue(const mxfp4_operand* A, const mxfp4_operand* B,
+                                           const fp8sg_epilogue* epi, void* C, fp8sg_out out,
+                                           int64_t M, int64_t N, int64_t Kc, fp8sg_stream stream);
+FP8SG_API fp8sg_status mxfp4_linear_fwd_epilogue(const void* x, const void* w, fp8sg_out type,
+                                                 int64_t M, int64_t N, int64_t K,
+                                                 fp8sg_mx_rule rule, const mxfp4_linear_ws* ws,
+                                                 const mxfp4_linear_saved* saved,
+                                                 const fp8sg_epilogue* epi, void* y, fp8sg_out out,
+                                                 fp8sg_stream stream);
+FP8SG_API fp8sg_status mxfp4_linear_apply_epilogue(const void* x, fp8sg_out type,
+                                                   const mxfp4_operand* w, int64_t M, int64_t N,
+                                                   int64_t K, fp8sg_mx_rule rule,
+                                                   const mxfp4_operand* x_ws,
+                                                   const fp8sg_epilogue* epi, void* y,
+                                                   fp8sg_out out, fp8sg_stream stream);
+FP8SG_API fp8sg_status mxfp4_linear_bwd_epilogue(const void* gy, fp8sg_out type, int64_t M,
+                                                 int64_t N, int64_t K, fp8sg_mx_rule rule,
+                                                 const mxfp4_linear_ws* ws,
+                                                 const mxfp4_linear_saved* saved,
+                                                 const fp8sg_epilogue* epi, void* gh, void* gb,
+                                                 float* ws_part, int64_t part_len, void* gx,
+                                                 void* gw, fp8sg_out out, fp8sg_stream stream);
+
+/*
+ * Dropout on its own, y = residual + drop(x), and its gradient gx = drop(gy) with
+ * the same p and rng (drop: see fp8sg_epilogue).
+ *   x, residual, y: rows x cols of `type`, rows ldx, ldr and ldy elements apart;
+ *   residual may be NULL.  y may be x or residual (same address and row distance).
+ *   p in [0, 1]; rng may be NULL where p drops nothing.
+ */
+FP8SG_API fp8sg_status dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                   fp8sg_out type, int64_t rows, int64_t cols, float p,
+                                   const int64_t* rng, void* y, int64_t ldy, fp8sg_stream stream);
+FP8SG_API fp8sg_status dropout_bwd(const void* gy, int64_t ldgy, fp8sg_out type, int64_t rows,
+                                   int64_t cols, float p, const int64_t* rng, void* gx,
+                                   int64_t ldgx, fp8sg_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
