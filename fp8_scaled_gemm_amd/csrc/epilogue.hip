@@ -7,16 +7,18 @@ namespace fp8sg {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kRows = 4;  // rows a thread has in flight
+constexpr int kRows = 4;  // rows a thread has in flight (fp32: half as many)
 
 // ---- backward.  A block owns a strip of 8 L columns (a thread 8 of them) and a
 // run of rows, which its 256 / L row groups take in turn; each thread adds up its
 // columns in fp32, lanes and waves join at the end, and where several blocks share
 // a strip each leaves a row of partial sums that k_bias_join adds in a fixed order
 // (no atomics: a repeated call gives the same bits).
+// (Four blocks a compute unit: all of a launch's at most 1024 are resident.)
 template <int T, bool S>
-__global__ __launch_bounds__(kBlock) void k_epilogue_bwd(EpilogueBwdArgs p) {
+__global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
   constexpr bool kFast = T != FP8SG_OUT_F32;
+  constexpr int kU = kFast ? kRows : kRows / 2;
   __shared__ float red[kBlock / kWave][512];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int L = p.lanes, R = kBlock / L, cl = tid & (L - 1), rl = tid / L;
@@ -30,10 +32,10 @@ __global__ __launch_bounds__(kBlock) void k_epilogue_bwd(EpilogueBwdArgs p) {
     const int64_t end = (part + 1) * p.rows_per < p.M ? (part + 1) * p.rows_per : p.M;
     float sum[8] = {};
     if (n > 0) {
-      for (int64_t r0 = part * p.rows_per + rl; r0 < end; r0 += kRows * R) {
-        Row8<T> g[kRows], h[kRows];
+      for (int64_t r0 = part * p.rows_per + rl; r0 < end; r0 += kU * R) {
+        Row8<T> g[kU], h[kU];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
+        for (int u = 0; u < kU; ++u) {
           const int64_t r = r0 + u * R;
           g[u].zero();
           h[u].zero();
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(kBlock) void k_epilogue_bwd(EpilogueBwdArgs p) {
           }
         }
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
+        for (int u = 0; u < kU; ++u) {
           const int64_t r = r0 + u * R;
           if (r >= end) break;
           float v[8], x[8];
@@ -137,16 +139,18 @@ struct Split {
 };
 Split split_of(int64_t M, int64_t N) {
   Split s{1, 0, 1, 0};
-  while (s.lanes < kWave && 8 * s.lanes < N) s.lanes *= 2;
+  // few rows: strips of 64 columns (128 bytes of 16-bit values), whose 32 row groups
+  // take all rows, so nothing is left to join
+  const bool few = M <= 256;
+  while (s.lanes < (few ? 8 : kWave) && 8 * s.lanes < N) s.lanes *= 2;
   s.strips = (N + 8 * s.lanes - 1) / (8 * s.lanes);
-  const int64_t step = (int64_t)(kBlock / s.lanes) * kRows, most = (M + step - 1) / step;
+  const int64_t R = kBlock / s.lanes, most = (M + R * kRows - 1) / (R * kRows);
   // at most as many blocks as a record has slots
-  int64_t parts = s.strips ? FP8SG_AMAX_PARTS / s.strips : 1;
+  int64_t parts = s.strips && !few ? FP8SG_AMAX_PARTS / s.strips : 1;
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
-  s.rows_per = (M + parts - 1) / parts;
-  s.rows_per = (s.rows_per + step - 1) / step * step;
-  if (s.rows_per < step) s.rows_per = step;
+  s.rows_per = ((M + parts - 1) / parts + R - 1) / R * R;
+  if (s.rows_per < R) s.rows_per = R;
   s.parts = M > 0 ? (M + s.rows_per - 1) / s.rows_per : 1;
   return s;
 }

@@ -91,10 +91,13 @@ __device__ __forceinline__ float recip(float d) {
 struct Sigm {
   float at, neg;
 };
-template <bool FAST>
 __device__ __forceinline__ Sigm sigm(float g) {
-  const float t = exp_minus<FAST>(fabsf(g)), r = recip<FAST>(1.0f + t), tr = t * r;
+  const float t = exp_minus<false>(fabsf(g)), r = recip<false>(1.0f + t), tr = t * r;
   return g < 0.f ? Sigm{tr, r} : Sigm{r, tr};
+}
+// 1 / (1 + 2^x), which is what 2^x's overflow makes of it, 0, for large x
+__device__ __forceinline__ float inv_1p_exp2(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
 }
 // The normal distribution's upper tail Q(z) = erfc(z / sqrt 2) / 2 and exp(-z^2 / 2)
 // for z >= 0: Q = exp(-z^2 / 2) m(z), where m falls slowly from 1/2 like 1 / z, so
@@ -102,40 +105,63 @@ __device__ __forceinline__ Sigm sigm(float g) {
 // relative error on [0, 16] (8.6e-6 with six terms, 4e-8 with nine).  The tail keeps
 // its relative precision, which 1 - erf would lose.
 struct Tail {
-  float q, e;
+  float t, p, e;  // Q = t p e
 };
 template <bool FAST>
 __device__ __forceinline__ Tail tail(float z) {
   if constexpr (FAST) {
     const float t = __builtin_amdgcn_rcpf(fmaf(0.46f, z, 1.0f));
     const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170367f);
-    const float p = fmaf(fmaf(fmaf(fmaf(fmaf(0.0722274631f, t, -0.236543089f), t, 0.177799612f), t, 0.116107389f), t, 0.18706657f), t, 0.183346346f);
-    return Tail{p * t * e, e};
+    float p = fmaf(0.0722274631f, t, -0.236543089f);
+    p = fmaf(p, t, 0.177799612f);
+    p = fmaf(p, t, 0.116107389f);
+    p = fmaf(p, t, 0.18706657f);
+    p = fmaf(p, t, 0.183346346f);
+    return Tail{t, p, e};
   } else {
     const float t = recip<false>(fmaf(0.26f, z, 1.0f));
     const float s = z * z, lo = fmaf(z, z, -s);  // z^2 in two parts
     const float e0 = exp_minus<false>(0.5f * s), e = fmaf(e0, -0.5f * lo, e0);
-    const float p = fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(fmaf(0.0294354856f, t, -0.147663906f), t, 0.240891442f), t, -0.138905317f), t, 0.152682543f), t, 0.0545273423f), t, 0.102139488f), t, 0.103141129f), t, 0.103751779f);
-    return Tail{p * t * e, e};
+    float p = fmaf(0.0294354856f, t, -0.147663906f);
+    p = fmaf(p, t, 0.240891442f);
+    p = fmaf(p, t, -0.138905317f);
+    p = fmaf(p, t, 0.152682543f);
+    p = fmaf(p, t, 0.0545273423f);
+    p = fmaf(p, t, 0.102139488f);
+    p = fmaf(p, t, 0.103141129f);
+    p = fmaf(p, t, 0.103751779f);
+    return Tail{t, p, e};
   }
 }
 constexpr float kPhi0 = 0.3989422804014327f;  // 1 / sqrt(2 pi)
 constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.044715f;  // 2 sqrt(2 / pi)
+constexpr float kLog2E = 1.4426950408889634f;
 
 // act(h) and act'(h).  Every one has its limit at h = -inf (0) instead of the
-// formula's NaN, by a bound on h below which the result is 0 in fp32; a NaN stays.
+// formula's NaN: where an exponential has gone to 0 the factor beside it is bounded.
+// A NaN stays (it reaches the result through the exponential, or through h).
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_of(float h) {
   if constexpr (ACT == FP8SG_ACT_RELU) {
     return h <= 0.f ? 0.f : h;
   } else if constexpr (ACT == FP8SG_ACT_SILU) {
-    return (h < -150.f ? -150.f : h) * sigm<FAST>(h).at;
-  } else if constexpr (ACT == FP8SG_ACT_GELU) {
-    const float z = fminf(fabsf(h), 16.f), zq = z * tail<FAST>(z).q;
+    if constexpr (FAST) return fmaxf(h, -150.f) * inv_1p_exp2(h * -kLog2E);
+    return (h < -150.f ? -150.f : h) * sigm(h).at;
+  } else if constexpr (ACT == FP8SG_ACT_GELU) {  // max(h, 0) - |h| Q(|h|)
+    if constexpr (FAST) {
+      const float z = fabsf(h);
+      const Tail q = tail<true>(z);
+      return fmaf(-(fminf(z, 16.f) * q.t), q.p * q.e, fmaxf(h, 0.f));
+    }
+    const float z = fminf(fabsf(h), 16.f);
+    const Tail q = tail<false>(z);
+    const float zq = z * (q.p * q.t * q.e);
     return h <= 0.f ? -zq : h - zq;
   } else if constexpr (ACT == FP8SG_ACT_GELU_TANH) {
+    if constexpr (FAST)
+      return fmaxf(h, -16.f) * inv_1p_exp2(h * fmaf(h * h, -kLog2E * kTanhA * kTanhB, -kLog2E * kTanhA));
     const float c = h < -16.f ? -16.f : h;
-    return c * sigm<FAST>(kTanhA * fmaf(kTanhB * c * c, c, c)).at;
+    return c * sigm(kTanhA * fmaf(kTanhB * c * c, c, c)).at;
   } else {
     return h;
   }
@@ -144,20 +170,33 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ float slope_of(float h) {
   if constexpr (ACT == FP8SG_ACT_RELU) {
     return h <= 0.f ? 0.f : 1.f;
-  } else if constexpr (ACT == FP8SG_ACT_SILU) {
-    const float c = h < -150.f ? -150.f : h > 150.f ? 150.f : h;
-    const Sigm s = sigm<FAST>(c);
-    return s.at * fmaf(c, s.neg, 1.0f);
-  } else if constexpr (ACT == FP8SG_ACT_GELU) {
+  } else if constexpr (ACT == FP8SG_ACT_SILU) {  // s (1 + h (1 - s))
+    const float c = __builtin_amdgcn_fmed3f(h, -150.f, 150.f);
+    if constexpr (FAST) {
+      const float s = inv_1p_exp2(h * -kLog2E);
+      return s * fmaf(c, 1.0f - s, 1.0f);
+    }
+    const Sigm s = sigm(c);
+    return h != h ? h : s.at * fmaf(c, s.neg, 1.0f);
+  } else if constexpr (ACT == FP8SG_ACT_GELU) {  // Q(z) - z phi(z) at -z, 1 minus it at z
+    if constexpr (FAST) {
+      const float z = fabsf(h);
+      const Tail q = tail<true>(z);
+      const float d = q.e * fmaf(q.t, q.p, -kPhi0 * fminf(z, 16.f));
+      return h <= 0.f ? d : 1.0f - d;
+    }
     const float z = fminf(fabsf(h), 16.f);
-    const Tail t = tail<FAST>(z);
-    const float d = fmaf(-kPhi0 * z, t.e, t.q);  // at -z; at z it is 1 - d
+    const Tail q = tail<false>(z);
+    const float d = q.e * fmaf(q.t, q.p, -kPhi0 * z);
     return h != h ? h : h <= 0.f ? d : 1.0f - d;
-  } else if constexpr (ACT == FP8SG_ACT_GELU_TANH) {
-    const float c = h < -16.f ? -16.f : h > 16.f ? 16.f : h;
-    const float cc = c * c;
-    const Sigm s = sigm<FAST>(kTanhA * fmaf(kTanhB * cc, c, c));
-    return s.at * fmaf(s.neg * kTanhA * c, fmaf(3.f * kTanhB, cc, 1.0f), 1.0f);
+  } else if constexpr (ACT == FP8SG_ACT_GELU_TANH) {  // s (1 + h (1 - s) 2 u'(h))
+    const float c = __builtin_amdgcn_fmed3f(h, -16.f, 16.f), cc = c * c;
+    if constexpr (FAST) {
+      const float s = inv_1p_exp2(h * fmaf(h * h, -kLog2E * kTanhA * kTanhB, -kLog2E * kTanhA));
+      return s * fmaf(c * (1.0f - s), fmaf(cc, 3.f * kTanhA * kTanhB, kTanhA), 1.0f);
+    }
+    const Sigm s = sigm(kTanhA * fmaf(kTanhB * cc, c, c));
+    return h != h ? h : s.at * fmaf(s.neg * kTanhA * c, fmaf(3.f * kTanhB, cc, 1.0f), 1.0f);
   } else {
     return 1.0f;
   }
@@ -246,31 +285,55 @@ __device__ __forceinline__ void store_n(void* p, int64_t at, int n, int type, co
   else store_t<N, FP8SG_OUT_F32, S>(p, at, n, v);
 }
 
-// ---- the epilogue of N columns from n on (n % N == 0) of row m: acc (the product
-// times its scales), its bias and the residual as loaded
-template <int N, bool FAST>
-__device__ __forceinline__ void epilogue_n(const EpilogueArgs& e, const Drop& d, float (&v)[N], const float (&bias)[N],
-                                           const Raw<N>& res, int64_t m, int64_t n) {
+// ---- the epilogue of U rows of N columns from n on (n % N == 0): accumulators and
+// their factor alpha, the columns' bias and the residual as loaded.  Row u is row m +
+// u * step; those from `end` on are left alone.
+template <int U, int N, bool FAST>
+__device__ __forceinline__ void epilogue_rows(const EpilogueArgs& e, const Drop& d, float (&v)[U][N],
+                                              float alpha, const float (&bias)[N], const Raw<N> (&res)[U], int64_t m, int step,
+                                              int64_t n, int64_t end) {
   const int cnt = e.N - n < N ? (int)(e.N - n) : N;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] += bias[i];
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[u][i] = fmaf(v[u][i], alpha, bias[i]);
   if (e.pre) {
-    if (e.stream) store_n<N, true>(e.pre, m * e.N + n, cnt, e.type, v);
-    else store_n<N, false>(e.pre, m * e.N + n, cnt, e.type, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = m + u * step;
+      if (r >= end) break;
+      if (e.stream) store_n<N, true>(e.pre, r * e.N + n, cnt, e.type, v[u]);
+      else store_n<N, false>(e.pre, r * e.N + n, cnt, e.type, v[u]);
+    }
   }
   by_act(e.act, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_of<decltype(a)::value, FAST>(v[i]);
-  });
-  if (e.drop.rng) drop_n<N>(d, (uint64_t)m * (uint64_t)((e.N + 7) >> 3) + (uint64_t)(n >> 3), (int)(n & 7), v);
-  if (e.residual) {
-    float r[N];
-    raw_values(res, e.type, r);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += r[i];
+      for (int i = 0; i < N; ++i) v[u][i] = act_of<decltype(a)::value, FAST>(v[u][i]);
+  });
+  if (e.drop.rng) {
+    const uint64_t groups = (uint64_t)((e.N + 7) >> 3);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      drop_n<N>(d, (uint64_t)(m + u * step) * groups + (uint64_t)(n >> 3), (int)(n & 7), v[u]);
   }
-  if (e.stream) store_n<N, true>(e.C, m * e.ldc + n, cnt, e.type, v);
-  else store_n<N, false>(e.C, m * e.ldc + n, cnt, e.type, v);
+  if (e.residual) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float r[N];
+      raw_values(res[u], e.type, r);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[u][i] += r[i];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = m + u * step;
+    if (r >= end) break;
+    if (e.stream) store_n<N, true>(e.C, r * e.ldc + n, cnt, e.type, v[u]);
+    else store_n<N, false>(e.C, r * e.ldc + n, cnt, e.type, v[u]);
+  }
 }
 template <int N>
 __device__ __forceinline__ Raw<N> load_residual(const EpilogueArgs& e, int64_t m, int64_t n) {
@@ -288,9 +351,24 @@ __device__ __forceinline__ void load_bias(const EpilogueArgs& e, int64_t n, floa
 template <int N, bool FAST>
 __device__ __forceinline__ void epilogue_at(const EpilogueArgs& e, float (&v)[N], int64_t m, int64_t n) {
   if (m >= e.M || n >= e.N) return;
-  float b[N];
+  float b[N], w[1][N];
   load_bias<N>(e, n, b);
-  epilogue_n<N, FAST>(e, drop_of(e.drop), v, b, load_residual<N>(e, m, n), m, n);
+  const Raw<N> res[1] = {load_residual<N>(e, m, n)};
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[0][i] = v[i];
+  epilogue_rows<1, N, FAST>(e, drop_of(e.drop), w, 1.0f, b, res, m, 0, n, e.M);
+}
+
+// The lane's number, taken behind the main loop: nothing for that to keep.
+__device__ __forceinline__ int lane_anew() {
+  int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+// The arguments' cache lines, asked for at a kernel's start: read first in the
+// epilogue, each would cost its way from the host's memory there.
+__device__ __forceinline__ void ask_early(const EpilogueArgs& e) {
+  asm volatile("" ::"s"(e.bias), "s"(e.ldc), "s"(e.stream));
 }
 
 // The epilogue of a wave's 16 TM x 64 sub-tile with origin (m0, n0), held as 16 x 16
@@ -302,11 +380,13 @@ __device__ __forceinline__ void epilogue_at(const EpilogueArgs& e, float (&v)[N]
 // columns would be 8 bytes of a line that 16 rows share), the generator's eight
 // elements are one lane's, and the activation is code for 8 values in a loop, not
 // for the tile's 128 a lane.  The next row group's residual is loaded ahead.
-// scale(c, i, j): the product's scales on block (i, j).
+// bias: of the lane's columns (load_bias<8> of n0 + 8 (lane % 8)); alpha: the
+// product's factor; scale(c, i, j): other factors on block (i, j).
 constexpr int kWaveEpilogueLds = 64 * 64 * 4;
-template <int TM, bool FAST, class Scale>
+template <int TM, bool FAST, int kU, class Scale>
 __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[TM][4], uint8_t* lds, int64_t m0,
-                                              int64_t n0, int lane, Scale scale) {
+                                              int64_t n0, const float (&bias)[8], float alpha, Scale scale) {
+  const int lane = lane_anew();
   const int cc = lane & 7, lr = lane >> 3;
   const int64_t n = n0 + 8 * cc;
   float* tile = reinterpret_cast<float*>(lds);
@@ -314,11 +394,11 @@ __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[
   // even chunks of two rows that a load reads, fall on different banks
   auto at = [&](int r, int c) { return tile + r * 64 + ((c ^ (r & 15)) << 2); };
   const Drop d = drop_of(e.drop);
-  float bias[8];
-  load_bias<8>(e, n, bias);
-  Raw<8> next = load_residual<8>(e, m0 + lr, n);
+  Raw<8> res[kU];
 #pragma unroll
-  for (int h = 0; h < TM; h += 4) {
+  for (int u = 0; u < kU; ++u) res[u] = load_residual<8>(e, m0 + lr + 8 * u, n);
+  static_for<(TM + 3) / 4>([&](auto half) {
+    constexpr int h = 4 * decltype(half)::value;
 #pragma unroll
     for (int i = h; i < TM && i < h + 4; ++i)
 #pragma unroll
@@ -329,20 +409,28 @@ __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int rows = 16 * (TM - h < 4 ? TM - h : 4);
+    // (the last half of a 7-block tile has 48 rows: those past it are past its 64 in LDS, and hold an earlier half's)
+    const int64_t end = m0 + 16 * TM < e.M ? m0 + 16 * TM : e.M;
 #pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      const int r = r0 + lr;
-      const int64_t m = m0 + 16 * h + r;
-      const Raw<8> res = next;
-      if (r0 + 8 < rows || h + 4 < TM) next = load_residual<8>(e, m + 8, n);
-      const v4f a = *reinterpret_cast<const v4f*>(at(r, 2 * cc)), b = *reinterpret_cast<const v4f*>(at(r, 2 * cc + 1));
-      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      if (m < e.M && n < e.N) epilogue_n<8, FAST>(e, d, v, bias, res, m, n);
+    for (int r0 = 0; r0 < 64; r0 += 8 * kU) {
+      const int64_t m = m0 + 16 * h + r0 + lr;
+      float v[kU][8];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int r = r0 + 8 * u + lr;
+        const v4f a = *reinterpret_cast<const v4f*>(at(r, 2 * cc)), b = *reinterpret_cast<const v4f*>(at(r, 2 * cc + 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = a[i], v[u][4 + i] = b[i];
+      }
+      if (n < e.N) epilogue_rows<kU, 8, FAST>(e, d, v, alpha, bias, res, m, 8, n, end);
+      if (16 * h + r0 + 8 * kU < 16 * TM) {  // the next rows' residual, while they are read and computed
+#pragma unroll
+        for (int u = 0; u < kU; ++u) res[u] = load_residual<8>(e, m + 8 * (kU + u), n);
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-  }
+  });
 }
 
 }  // namespace fp8sg

@@ -258,11 +258,13 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(Prob p) {
   const int wr0 = grp * 128 + (lane & 15), wc0 = wq * 64 + 4 * (lane >> 4);
   if constexpr (kEpi<Prob>) {
     __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing a slot
+    float bias[8];
+    load_bias<8>(p.epi, bn + wq * 64 + 8 * (lane_anew() & 7), bias);
     barrier();
     static_assert(2 * kWaveEpilogueLds == sizeof(sA0), "two waves a slot");
     uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
-    wave_epilogue<kTM, kFast<OUT>>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + grp * 128, bn + wq * 64, lane,
-                                   [](v4f&, int, int) {});
+    wave_epilogue<kTM, kFast<OUT>, 2>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + grp * 128, bn + wq * 64,
+                                      bias, 1.0f, [](v4f&, int, int) {});
   } else if constexpr (OUT == FP8SG_OUT_F32) {
     float* C = reinterpret_cast<float*>(p.C);
 #pragma unroll
@@ -360,6 +362,11 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   const int frow = lane & 15, fchunk = 2 * (lane >> 4);
+  float bias[8];
+  if constexpr (kEpi<Prob>) {
+    ask_early(p.epi);
+    load_bias<8>(p.epi, bn + 64 * wn + 8 * (lane & 7), bias);
+  }
   issue(0);
   for (int t = 0; t < nk; ++t) {
     if (t + 1 < nk) {
@@ -379,13 +386,13 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
       sav[i] = *reinterpret_cast<const uint32_t*>(a + 32768 + 256 * (2 * wm + i) + 4 * lane);
       sbv[i] = *reinterpret_cast<const uint32_t*>(a + 33792 + 256 * (2 * wn + i) + 4 * lane);
     }
-    static_for<2>([&](auto kk) {
+    auto half = [&](auto kk, int chunk) {
       constexpr int KK = decltype(kk)::value;
       uint4 af[4], bf[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        af[i] = *reinterpret_cast<const uint4*>(a + lds_off2(64 * wm + 16 * i + frow, fchunk + KK));
-        bf[i] = *reinterpret_cast<const uint4*>(b + lds_off2(64 * wn + 16 * i + frow, fchunk + KK));
+        af[i] = *reinterpret_cast<const uint4*>(a + lds_off2(64 * wm + 16 * i + frow, chunk));
+        bf[i] = *reinterpret_cast<const uint4*>(b + lds_off2(64 * wn + 16 * i + frow, chunk));
       }
       static_for<4>([&](auto ic) {
         constexpr int I = decltype(ic)::value;
@@ -394,7 +401,23 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
           acc[I][J] = mfma4<(J & 1) * 2 + KK, (I & 1) * 2 + KK>(bf[J], af[I], acc[I][J], sbv[J / 2], sav[I / 2]);
         });
       });
-    });
+    };
+    if constexpr (kEpi<Prob>) {
+      // one product per accumulator in the loop's body (see few_tile): with two, the
+      // registers that the epilogue needs led to products that do not add in place
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        half(std::integral_constant<int, 0>{}, fchunk + h);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sav[i] >>= 8;
+          sbv[i] >>= 8;
+        }
+      }
+    } else {
+      half(std::integral_constant<int, 0>{}, fchunk);
+      half(std::integral_constant<int, 1>{}, fchunk + 1);
+    }
     // this stage is loaded again two k-tiles on: every wave has read it by then
     __builtin_amdgcn_s_waitcnt(0xC07F);
     __builtin_amdgcn_s_barrier();
@@ -402,8 +425,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
   }
   if constexpr (kEpi<Prob>) {  // (every load has landed, every wave has read its last stage)
     static_assert(4 * kWaveEpilogueLds <= sizeof(lds), "wave sub-tiles");
-    wave_epilogue<4, kFast<OUT>>(p.epi, acc, lds + wave * kWaveEpilogueLds, bm + 64 * wm, bn + 64 * wn, lane,
-                                 [](v4f&, int, int) {});
+    wave_epilogue<4, kFast<OUT>, 4>(p.epi, acc, lds + wave * kWaveEpilogueLds, bm + 64 * wm, bn + 64 * wn, bias,
+                                    1.0f, [](v4f&, int, int) {});
     return;
   }
   Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
@@ -482,6 +505,7 @@ __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64
   const int64_t bm = b % nbm * (16 * TM), bn = b / nbm * (16 * TN);
   uint8_t* my = lds + wave * (2 * kStage + kOwn);
 
+  if constexpr (kEpi<Prob>) ask_early(p.epi);
   // descriptors over the tile's rows (and 32-row scale groups) that exist
   const int64_t lm = M - bm < 16 * TM ? M - bm : 16 * TM, ln = N - bn < 16 * TN ? N - bn : 16 * TN;
   const i32x4 ra = make_rsrc(p.A.q + bm * pitch, kFused ? 0 : lm * pitch);

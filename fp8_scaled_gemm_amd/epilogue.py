@@ -17,6 +17,7 @@ The epilogue's arguments, by keyword in every call:
             device memory that its generator starts from (None where p is 0)
 """
 import ctypes
+import struct
 
 import torch
 
@@ -27,10 +28,10 @@ from .mx import (_TYPE, MX_FLOOR, Mxfp4, Mxfp4LinearSaved, Mxfp4LinearWs, _apart
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 
 
-class _Epilogue(ctypes.Structure):
-    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p),
-                ("rng", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64),
-                ("p", ctypes.c_float), ("act", ctypes.c_int32), ("bias_type", ctypes.c_int32)]
+# fp8sg_epilogue, packed anew for each call: bias, residual, pre, rng, ld_residual,
+# ld_out, p, act, bias_type
+_pack = struct.Struct("=4Q2qfii4x").pack
+_SIZE = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4}
 
 
 def bind(L):
@@ -89,11 +90,21 @@ def _clear(a, name_a, b, name_b):
     raise ValueError(f"{name_a} and {name_b} overlap")
 
 
-def _same_or_clear(a, name_a, lda, b, name_b, ldb):
-    """a is b's memory element for element, or shares none of it."""
-    if a.data_ptr() == b.data_ptr() and lda == ldb:
+def _all_clear(spans, outputs, inputs):
+    """No output shares memory with another output or with an input.  spans: first
+    and last byte address + 1 of each; where these lie apart, which is the common
+    case, nothing more is looked at.  outputs, inputs: (tensor or None, name)."""
+    spans.sort()
+    at = 0
+    for lo, hi in spans:
+        if lo < at:
+            break
+        at = hi
+    else:
         return
-    _clear(a, name_a, b, name_b)
+    for i, (t, name) in enumerate(outputs):
+        for u, other in outputs[i + 1:] + inputs:
+            _clear(t, name, u, other)
 
 
 def _drop(p, rng):
@@ -103,7 +114,7 @@ def _drop(p, rng):
     if rng is None:
         if p >= 2.0 ** -17:
             raise ValueError("rng is needed where p is not 0")
-        return None
+        return 0
     _need(rng, "rng", torch.int64, numel=2)
     _here(rng)
     return rng.data_ptr()
@@ -116,66 +127,86 @@ def _act(act):
 
 
 def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng):
-    """The C struct of a forward epilogue.  in_dtype: the linear's input's, or None."""
-    e = _Epilogue()
-    e.act = _act(act)
+    """The packed struct of a forward epilogue.  in_dtype: the linear's input's, or None."""
     dt = y.dtype
-    e.ld_out = ldy = _row_stride(y, "y", dt, shape, M, N)
+    size, at = _SIZE[dt], y.data_ptr()
+    ldy = _row_stride(y, "y", dt, shape, M, N)
+    spans = [(at, at + ((M - 1) * ldy + N) * size)] if M and N else []
+    pb = pr = pp = bt = ldr = 0
+    inputs = []
     if bias is not None:
         bt = _type(bias, "bias")
         if in_dtype is not None and bias.dtype is not in_dtype and bt != 2:
             raise TypeError(f"bias: dtype {bias.dtype}, expected {in_dtype} or float32")
         _same(bias, "bias", bias.dtype, (N,))
-        _clear(y, "y", bias, "bias")
-        e.bias, e.bias_type = bias.data_ptr(), bt
+        pb = bias.data_ptr()
+        spans.append((pb, pb + N * _SIZE[bias.dtype]))
+        inputs.append((bias, "bias"))
     if residual is not None:
-        e.ld_residual = ldr = _row_stride(residual, "residual", dt, shape, M, N)
-        _same_or_clear(y, "y", ldy, residual, "residual", ldr)
-        e.residual = residual.data_ptr()
+        ldr = _row_stride(residual, "residual", dt, shape, M, N)
+        pr = residual.data_ptr()
+        if pr != at or ldr != ldy:  # (the output itself is allowed)
+            if M and N:
+                spans.append((pr, pr + ((M - 1) * ldr + N) * size))
+            inputs.append((residual, "residual"))
     if pre is not None:
         _same(pre, "pre", dt, shape)
-        _clear(y, "y", pre, "pre")
-        _clear(pre, "pre", residual, "residual")
-        _clear(pre, "pre", bias, "bias")
-        e.pre = pre.data_ptr()
-    e.p, e.rng = p, _drop(p, rng)
+        pp = pre.data_ptr()
+        spans.append((pp, pp + M * N * size))
+    _all_clear(spans, [(y, "y"), (pre, "pre")], inputs)
+    words = _drop(p, rng) if p or rng is not None else 0
+    e = _pack(pb, pr, pp, words, ldr, ldy, p, _act(act), bt)
     _here(y, bias, residual, pre)
     return e
 
 
-def _backward(gy, gh, gb, pre, act, p, rng, part, M, N, alone):
-    """The C struct of a backward step, and the workspace's length."""
-    e = _Epilogue()
-    e.act, e.p, e.rng = _act(act), p, _drop(p, rng)
-    changes = act != ACT_NONE or p >= 2.0 ** -17
+def _backward(gy, gh, gb, pre, act, p, rng, part, M, N, alone, *out):
+    """The packed struct of a backward step, and the workspace's length.  out: the
+    call's other outputs, (tensor or None, name)."""
+    dt = gy.dtype
+    size = _SIZE[dt]
+    pg, n, bt, pp = gy.data_ptr(), 0, 0, 0
+    words = _drop(p, rng) if p or rng is not None else 0
+    changes = _act(act) != ACT_NONE or p >= 2.0 ** -17
+    spans, outputs, inputs = [(pg, pg + M * N * size)], list(out), [(gy, "gy")]
     if gh is not None:
-        _same(gh, "gh", gy.dtype, gy.shape)
-        _same_or_clear(gh, "gh", N, gy, "gy", N)
+        _same(gh, "gh", dt, gy.shape)
+        at = gh.data_ptr()
+        if at != pg:  # (gy itself is allowed)
+            spans.append((at, at + M * N * size))
+            outputs.append((gh, "gh"))
     elif changes and not alone:
         raise ValueError("gh is needed where the epilogue has an activation or drops")
     if act != ACT_NONE:
         if pre is None:
             raise ValueError("pre is needed where the epilogue has an activation")
-        _same(pre, "pre", gy.dtype, gy.shape)
-        _clear(gh, "gh", pre, "pre")
-        e.pre = pre.data_ptr()
-    n = 0
+        _same(pre, "pre", dt, gy.shape)
+        pp = pre.data_ptr()
+        spans.append((pp, pp + M * N * size))
+        inputs.append((pre, "pre"))
+        if gh is not None and gh.data_ptr() == pg:
+            _clear(gh, "gh", pre, "pre")
     if gb is not None:
-        if gb.__class__ is not torch.Tensor and not isinstance(gb, torch.Tensor):
+        if not isinstance(gb, torch.Tensor):
             raise TypeError(f"gb: expected a torch.Tensor, got {type(gb).__name__}")
-        if gb.dtype is not gy.dtype and gb.dtype is not torch.float32:
-            raise TypeError(f"gb: dtype {gb.dtype}, expected {gy.dtype} or float32")
+        if gb.dtype is not dt and gb.dtype is not torch.float32:
+            raise TypeError(f"gb: dtype {gb.dtype}, expected {dt} or float32")
         _same(gb, "gb", gb.dtype, (N,))
-        for t, name in ((gy, "gy"), (gh, "gh"), (pre if act != ACT_NONE else None, "pre")):
-            _clear(gb, "gb", t, name)
-        e.bias_type = _TYPE[gb.dtype]
+        at, bt = gb.data_ptr(), _TYPE[gb.dtype]
+        spans.append((at, at + N * _SIZE[gb.dtype]))
+        outputs.append((gb, "gb"))
         if part is not None:
             _need(part, "part", torch.float32)
-            n = part.numel()
-            for t, name in ((gy, "gy"), (gh, "gh"), (gb, "gb"), (pre if act != ACT_NONE else None, "pre")):
-                _clear(part, "part", t, name)
+            n, at = part.numel(), part.data_ptr()
+            spans.append((at, at + 4 * n))
+            outputs.append((part, "part"))
+    for t, _name in out:
+        if t is not None:
+            at = t.data_ptr()
+            spans.append((at, at + t.nbytes))
+    _all_clear(spans, outputs, inputs)
     _here(gy, gh, gb, pre, part)
-    return e, n
+    return _pack(0, 0, pp, words, 0, 0, p, act, bt), n
 
 
 def _lead(shape, n):
@@ -192,7 +223,7 @@ def _fp8_gemm(fn, A, B, ia, ib, C, bias, act, residual, pre, p, rng, stream):
     ct = _type(C, "C")
     e = _epilogue(C, (M, N), M, N, None, bias, act, residual, pre, p, rng)
     _here(A, B)
-    _check(getattr(lib(), fn)(_ptr(A), _ptr(B), ia, ib, ctypes.byref(e), _ptr(C), ct, M, N, K, _stream(stream)), fn)
+    _check(getattr(lib(), fn)(_ptr(A), _ptr(B), ia, ib, e, _ptr(C), ct, M, N, K, _stream(stream)), fn)
 
 
 def fp8_gemm_epilogue(A: torch.Tensor, B: torch.Tensor, inv_a_ptr: int, inv_b_ptr: int, C: torch.Tensor, *, bias=None,
@@ -217,7 +248,7 @@ def _saved(saved, M, N, K):
     if not isinstance(saved, LinearSaved):
         raise TypeError(f"saved: expected LinearSaved, got {type(saved).__name__}")
     saved.check(M, N, K)
-    return saved.struct()
+    return ctypes.addressof(saved.struct())
 
 
 def fp8_scaled_linear_fwd_epilogue(x: torch.Tensor, w: torch.Tensor, saved: LinearSaved, y: torch.Tensor, *, bias=None,
@@ -235,8 +266,8 @@ def fp8_scaled_linear_fwd_epilogue(x: torch.Tensor, w: torch.Tensor, saved: Line
     sv = _saved(saved, M, N, K)
     e = _epilogue(y, (M, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
     _here(x, w, saved.x_q, saved.w_q, saved.x_sc.buf, saved.w_sc.buf)
-    _check(lib().fp8_scaled_linear_fwd_epilogue(_ptr(x), _ptr(w), _TYPE[x.dtype], M, N, K, ctypes.byref(sv),
-                                                ctypes.byref(e), _ptr(y), yt, _stream(stream)),
+    _check(lib().fp8_scaled_linear_fwd_epilogue(x.data_ptr(), w.data_ptr(), _TYPE[x.dtype], M, N, K, sv,
+                                                e, _ptr(y), yt, _stream(stream)),
            "fp8_scaled_linear_fwd_epilogue")
 
 
@@ -259,16 +290,11 @@ def fp8_scaled_linear_bwd_epilogue(gy: torch.Tensor, saved: LinearSaved, ws: Lin
     if not isinstance(ws, LinearBwdWs):
         raise TypeError(f"ws: expected LinearBwdWs, got {type(ws).__name__}")
     ws.check(M, N)
-    wc = ws.struct()
-    e, n = _backward(gy, gh, gb, pre, act, p, rng, part, M, N, False)
-    for a, name in ((gx, "gx"), (gw, "gw")):
-        _clear(a, name, gh, "gh")
-        _clear(a, name, gb, "gb")
-        _clear(a, name, gy, "gy")
-    _clear(gx, "gx", gw, "gw")
+    wc = ctypes.addressof(ws.struct())
+    e, n = _backward(gy, gh, gb, pre, act, p, rng, part, M, N, False, (gx, "gx"), (gw, "gw"))
     _here(gx, gw, saved.x_q, saved.w_q, saved.x_sc.buf, saved.w_sc.buf, ws.gy_q, ws.gy_sc.buf)
-    _check(lib().fp8_scaled_linear_bwd_epilogue(_ptr(gy), _TYPE[gy.dtype], ctypes.byref(sv), M, N, K, ctypes.byref(wc),
-                                                ctypes.byref(e), _ptr(gh), _ptr(gb), _ptr(part), n, _ptr(gx), _ptr(gw),
+    _check(lib().fp8_scaled_linear_bwd_epilogue(_ptr(gy), _TYPE[gy.dtype], sv, M, N, K, wc,
+                                                e, _ptr(gh), _ptr(gb), _ptr(part), n, _ptr(gx), _ptr(gw),
                                                 ot, _stream(stream)), "fp8_scaled_linear_bwd_epilogue")
 
 
@@ -287,7 +313,7 @@ def epilogue_bwd(gy: torch.Tensor, gh=None, gb=None, *, pre=None, act: int = ACT
     if gh is None and gb is None:
         raise ValueError("epilogue_bwd: gh or gb is needed")
     e, n = _backward(gy, gh, gb, pre, act, p, rng, part, M, N, True)
-    _check(lib().epilogue_bwd(_ptr(gy), _TYPE[gy.dtype], ctypes.byref(e), M, N, _ptr(gh), _ptr(gb), _ptr(part), n,
+    _check(lib().epilogue_bwd(_ptr(gy), _TYPE[gy.dtype], e, M, N, _ptr(gh), _ptr(gb), _ptr(part), n,
                               _stream(stream)), "epilogue_bwd")
 
 
@@ -306,7 +332,7 @@ def mxfp4_gemm_epilogue(A: Mxfp4, B: Mxfp4, C: torch.Tensor, *, bias=None, act: 
         raise ValueError(f"C: shape {tuple(C.shape)}, expected {M} x {N}")
     e = _epilogue(C, C.shape, M, N, None, bias, act, residual, pre, p, rng)
     _here(A.q, A.s, B.q, B.s)
-    _check(lib().mxfp4_gemm_epilogue(A.c(), B.c(), ctypes.byref(e), _ptr(C), ct, M, N, A.k, _stream(stream)),
+    _check(lib().mxfp4_gemm_epilogue(A.c(), B.c(), e, _ptr(C), ct, M, N, A.k, _stream(stream)),
            "mxfp4_gemm_epilogue")
 
 
@@ -329,7 +355,7 @@ def mxfp4_linear_fwd_epilogue(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearW
         _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
         sv = saved.c()
     _check(lib().mxfp4_linear_fwd_epilogue(_ptr(x), _ptr(w), _TYPE[x.dtype], M, N, K, _rule(rule), ws.c(), sv,
-                                           ctypes.byref(e), _ptr(y), yt, _stream(stream)), "mxfp4_linear_fwd_epilogue")
+                                           e, _ptr(y), yt, _stream(stream)), "mxfp4_linear_fwd_epilogue")
 
 
 def mxfp4_linear_apply_epilogue(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: Mxfp4, *, bias=None,
@@ -346,7 +372,7 @@ def mxfp4_linear_apply_epilogue(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: 
     e = _epilogue(y, _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
     _here(x, w.q, w.s, ws.q, ws.s)
     _check(lib().mxfp4_linear_apply_epilogue(_ptr(x), _TYPE[x.dtype], w.c(), M, N, K, _rule(rule), ws.c(),
-                                             ctypes.byref(e), _ptr(y), yt, _stream(stream)),
+                                             e, _ptr(y), yt, _stream(stream)),
            "mxfp4_linear_apply_epilogue")
 
 
@@ -371,53 +397,59 @@ def mxfp4_linear_bwd_epilogue(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4L
     if gw is not None:
         _same(gw, "gw", out.dtype, (N, K))
         need += ("gy_qT",)
-    e, n = _backward(gy, gh, gb, pre, act, p, rng, part, M, N, out is None)
-    for a, name in ((gx, "gx"), (gw, "gw")):
-        _clear(a, name, gh, "gh")
-        _clear(a, name, gb, "gb")
-        _clear(a, name, gy, "gy")
-    _clear(gx, "gx", gw, "gw")
+    e, n = _backward(gy, gh, gb, pre, act, p, rng, part, M, N, out is None, (gx, "gx"), (gw, "gw"))
     _here(gx, gw)
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), need)
     _linear(saved, Mxfp4LinearSaved, "saved", (M, N, K), ("x_qT", "w_qT"))
     _check(lib().mxfp4_linear_bwd_epilogue(_ptr(gy), _TYPE[gy.dtype], M, N, K, _rule(rule), ws.c(), saved.c(),
-                                           ctypes.byref(e), _ptr(gh), _ptr(gb), _ptr(part), n, _ptr(gx), _ptr(gw), ot,
+                                           e, _ptr(gh), _ptr(gb), _ptr(part), n, _ptr(gx), _ptr(gw), ot,
                                            _stream(stream)), "mxfp4_linear_bwd_epilogue")
 
 
 # ------------------------------------------------------------------------- dropout
 
+def _rows_at(t, name, like, rows, cols):
+    """(address, row distance, span) of a dropout operand."""
+    ld = _row_stride(t, name, like.dtype, like.shape, rows, cols)
+    at = t.data_ptr()
+    return at, ld, (at, at + ((rows - 1) * ld + cols) * _SIZE[like.dtype])
+
+
+def _dropout(x, name_x, p, rng, y, name_y, residual):
+    """(x, ldx, residual, ldr, type, rows, cols, p, rng, y, ldy), checked."""
+    xt = _type(x, name_x)
+    shape = x.shape
+    if not shape:
+        raise ValueError(f"{name_x}: expected at least one dimension")
+    cols = shape[-1]
+    rows = shape[0] if len(shape) == 2 else _rows(x)
+    px, ldx, sx = _rows_at(x, name_x, x, rows, cols)
+    py, ldy, sy = _rows_at(y, name_y, x, rows, cols)
+    spans, inputs = [sy], []
+    if px != py or ldx != ldy:  # (in place is allowed)
+        spans.append(sx)
+        inputs.append((x, name_x))
+    pr = ldr = 0
+    if residual is not None:
+        pr, ldr, sr = _rows_at(residual, "residual", x, rows, cols)
+        if pr != py or ldr != ldy:
+            spans.append(sr)
+            inputs.append((residual, "residual"))
+    if rows and cols:
+        _all_clear(spans, [(y, name_y)], inputs)
+    words = _drop(p, rng) if p or rng is not None else 0
+    _here(x, y, residual)
+    return px, ldx, pr, ldr, xt, rows, cols, p, words, py, ldy
+
+
 def dropout_fwd(x: torch.Tensor, p: float, rng, y: torch.Tensor, residual=None, stream=None):
     """y = residual + drop(x): an element is kept with probability 1 - p and then
     scaled by its inverse.  rng: the generator's two int64 words on the device (None
     where p is 0).  Rows of the last dimension may be apart; y may be x or residual."""
-    xt = _type(x, "x")
-    if not x.shape:
-        raise ValueError("x: expected at least one dimension")
-    rows, cols = _rows(x), x.shape[-1]
-    ldx = _row_stride(x, "x", x.dtype, x.shape, rows, cols)
-    ldy = _row_stride(y, "y", x.dtype, x.shape, rows, cols)
-    _same_or_clear(y, "y", ldy, x, "x", ldx)
-    ldr = 0
-    if residual is not None:
-        ldr = _row_stride(residual, "residual", x.dtype, x.shape, rows, cols)
-        _same_or_clear(y, "y", ldy, residual, "residual", ldr)
-    r = _drop(p, rng)
-    _here(x, y, residual)
-    _check(lib().dropout_fwd(x.data_ptr(), ldx, _ptr(residual), ldr, xt, rows, cols, p, r, y.data_ptr(), ldy,
-                             _stream(stream)), "dropout_fwd")
+    _check(lib().dropout_fwd(*_dropout(x, "x", p, rng, y, "y", residual), _stream(stream)), "dropout_fwd")
 
 
 def dropout_bwd(gy: torch.Tensor, p: float, rng, gx: torch.Tensor, stream=None):
     """gx = drop(gy) with the forward's p and rng; gx may be gy."""
-    t = _type(gy, "gy")
-    if not gy.shape:
-        raise ValueError("gy: expected at least one dimension")
-    rows, cols = _rows(gy), gy.shape[-1]
-    ld = _row_stride(gy, "gy", gy.dtype, gy.shape, rows, cols)
-    ldx = _row_stride(gx, "gx", gy.dtype, gy.shape, rows, cols)
-    _same_or_clear(gx, "gx", ldx, gy, "gy", ld)
-    r = _drop(p, rng)
-    _here(gy, gx)
-    _check(lib().dropout_bwd(gy.data_ptr(), ld, t, rows, cols, p, r, gx.data_ptr(), ldx, _stream(stream)),
-           "dropout_bwd")
+    g, ld, _, _, t, rows, cols, p, words, gx, ldx = _dropout(gy, "gy", p, rng, gx, "gx", None)
+    _check(lib().dropout_bwd(g, ld, t, rows, cols, p, words, gx, ldx, _stream(stream)), "dropout_bwd")

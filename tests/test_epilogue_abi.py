@@ -1,6 +1,8 @@
 """Refusals of the products with an epilogue, their backward pass and dropout, all
 before any launch (no GPU needed): the C ABI's and the binding's."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -13,20 +15,35 @@ OK, ENULL, ESHAPE, EALIGN, EFORMAT = 0, 1, 2, 3, 4
 A = 0x10000  # fake addresses: validation fails before any use
 BIG = (1 << 29) + 1
 BF16, F16, F32 = 0, 1, 2
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fp8sg.h")
 PAIR = mx._Pair(A, A)
 
 
+FIELDS = (("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p), ("rng", ctypes.c_void_p),
+          ("ld_residual", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("p", ctypes.c_float), ("act", ctypes.c_int32),
+          ("bias_type", ctypes.c_int32))
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = FIELDS
+
+
 def E(**kw):
-    e = B._Epilogue(ld_out=kw.pop("ld_out", 64), ld_residual=kw.pop("ld_residual", 64))
+    e = Epilogue(ld_out=kw.pop("ld_out", 64), ld_residual=kw.pop("ld_residual", 64))
     for k, v in kw.items():
         setattr(e, k, v)
     return ctypes.byref(e)
 
 
-def test_struct_layout():
-    assert ctypes.sizeof(B._Epilogue) == 64
-    assert [getattr(B._Epilogue, n).offset for n in ("bias", "residual", "pre", "rng", "ld_residual", "ld_out", "p",
-                                                    "act", "bias_type")] == [0, 8, 16, 24, 32, 40, 48, 52, 56]
+def test_struct_layout_matches_header():
+    body = re.search(r"typedef struct fp8sg_epilogue \{(.*?)\} fp8sg_epilogue;", open(HEADER).read(), re.S).group(1)
+    c = {"const void*": ctypes.c_void_p, "void*": ctypes.c_void_p, "const int64_t*": ctypes.c_void_p,
+         "int64_t": ctypes.c_int64, "float": ctypes.c_float, "int32_t": ctypes.c_int32}
+    assert tuple((n, c[t]) for t, n in re.findall(r"^\s*([\w ]+\*?)\s(\w+);", body, re.M)) == FIELDS
+    packed = B._pack(1, 2, 3, 4, 5, 6, 0.5, 7, 8)
+    e = Epilogue.from_buffer_copy(packed)
+    assert ctypes.sizeof(Epilogue) == len(packed) == 64
+    assert [getattr(e, n) for n, _ in FIELDS] == [1, 2, 3, 4, 5, 6, 0.5, 7, 8]
 
 
 BAD = [  # of a 32 x 64 bf16 result
