@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
           p.part[part * p.N + col] = v;
         } else {
           const float one[1] = {v};
-          store_n<1, false>(p.gb, col, 1, p.bias_type, one);
+          store_n<1, false>(reinterpret_cast<uint8_t*>(p.gb) + col * esize(p.bias_type), 1, p.bias_type, one);
         }
       }
     }
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kBlock) void k_bias_join(const float* part, int par
   __syncthreads();
   if (wave == 0 && n < N) {
     const float one[1] = {(red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])};
-    store_n<1, false>(gb, n, 1, type, one);
+    store_n<1, false>(reinterpret_cast<uint8_t*>(gb) + n * esize(type), 1, type, one);
   }
 }
 

@@ -213,19 +213,20 @@ __device__ __forceinline__ void by_act(int act, F f) {
   }
 }
 
-// ---- elements of a type known at run time (one branch a group)
+// ---- elements of a type known at run time (one branch a group), at a byte address
+__device__ __forceinline__ int esize(int type) { return type == FP8SG_OUT_F32 ? 4 : 2; }
 template <int N>
 struct Raw {  // N elements as loaded: N dwords of fp32, N / 2 of 16 bits
   uint32_t w[N];
 };
 // Elements past `n` read as 0.
 template <int N>
-__device__ __forceinline__ Raw<N> load_raw(const void* p, int64_t at, int n, int type) {
+__device__ __forceinline__ Raw<N> load_raw(const uint8_t* p, int n, int type) {
   Raw<N> r;
 #pragma unroll
   for (int i = 0; i < N; ++i) r.w[i] = 0u;
   if (type == FP8SG_OUT_F32) {
-    const float* q = reinterpret_cast<const float*>(p) + at;
+    const float* q = reinterpret_cast<const float*>(p);
     if constexpr (N == 8) {
       if (n >= 8) {
         const u32x4 a = ld_any<false>(q), b = ld_any<false>(q + 4);
@@ -238,7 +239,7 @@ __device__ __forceinline__ Raw<N> load_raw(const void* p, int64_t at, int n, int
     for (int i = 0; i < N; ++i)
       if (i < n) r.w[i] = __float_as_uint(q[i]);
   } else {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
     if constexpr (N == 8) {
       if (n >= 8) {
         const u32x4 a = ld_any<false>(q);
@@ -262,13 +263,9 @@ __device__ __forceinline__ void raw_values(const Raw<N>& r, int type, float (&v)
     else v[i] = (i & 1) ? in_hi<false>(r.w[i / 2]) : in_lo<false>(r.w[i / 2]);
   }
 }
-template <int N>
-__device__ __forceinline__ void load_n(const void* p, int64_t at, int n, int type, float (&v)[N]) {
-  raw_values(load_raw<N>(p, at, n, type), type, v);
-}
 template <int N, int T, bool S>
-__device__ __forceinline__ void store_t(void* p, int64_t at, int n, const float (&v)[N]) {
-  Elem<T>* q = reinterpret_cast<Elem<T>*>(p) + at;
+__device__ __forceinline__ void store_t(uint8_t* p, int n, const float (&v)[N]) {
+  Elem<T>* q = reinterpret_cast<Elem<T>*>(p);
   if constexpr (N == 8) {
     store8<T, S>(q, n, v);
   } else {
@@ -279,44 +276,74 @@ __device__ __forceinline__ void store_t(void* p, int64_t at, int n, const float 
 }
 // S: non-temporal
 template <int N, bool S>
-__device__ __forceinline__ void store_n(void* p, int64_t at, int n, int type, const float (&v)[N]) {
-  if (type == FP8SG_OUT_BF16) store_t<N, FP8SG_OUT_BF16, S>(p, at, n, v);
-  else if (type == FP8SG_OUT_F16) store_t<N, FP8SG_OUT_F16, S>(p, at, n, v);
-  else store_t<N, FP8SG_OUT_F32, S>(p, at, n, v);
+__device__ __forceinline__ void store_n(uint8_t* p, int n, int type, const float (&v)[N]) {
+  if (type == FP8SG_OUT_BF16) store_t<N, FP8SG_OUT_BF16, S>(p, n, v);
+  else if (type == FP8SG_OUT_F16) store_t<N, FP8SG_OUT_F16, S>(p, n, v);
+  else store_t<N, FP8SG_OUT_F32, S>(p, n, v);
 }
 
-// ---- the epilogue of U rows of N columns from n on (n % N == 0): accumulators and
-// their factor alpha, the columns' bias and the residual as loaded.  Row u is row m +
-// u * step; those from `end` on are left alone.
-template <int U, int N, bool FAST>
-__device__ __forceinline__ void epilogue_rows(const EpilogueArgs& e, const Drop& d, float (&v)[U][N],
-                                              float alpha, const float (&bias)[N], const Raw<N> (&res)[U], int64_t m, int step,
-                                              int64_t n, int64_t end) {
-  const int cnt = e.N - n < N ? (int)(e.N - n) : N;
+// What a kernel's epilogue may meet, so that small kernels carry no code for the
+// rest.  FAST: see above; TAIL: rows that end inside a group of columns; NT: results
+// that leave with non-temporal stores.
+template <bool FAST_, bool TAIL_, bool NT_>
+struct EpiMode {
+  static constexpr bool FAST = FAST_, TAIL = TAIL_, NT = NT_;
+};
+
+// Where a lane's N columns of a row lie in each matrix, and in the generator's
+// sequence; from row to row by additions (products of 64 bits run at a quarter of the
+// vector rate, and took as long as the activation).
+struct EpiAt {
+  uint8_t *c, *pre;
+  const uint8_t* res;
+  uint64_t group;
+  __device__ __forceinline__ EpiAt(const EpilogueArgs& e, int64_t m, int64_t n) {
+    const int es = esize(e.type);
+    c = reinterpret_cast<uint8_t*>(e.C) + (m * e.ldc + n) * es;
+    pre = reinterpret_cast<uint8_t*>(e.pre) + (m * e.N + n) * es;
+    res = reinterpret_cast<const uint8_t*>(e.residual) + (m * e.ldr + n) * es;
+    group = (uint64_t)m * (uint64_t)((e.N + 7) >> 3) + (uint64_t)(n >> 3);
+  }
+  __device__ __forceinline__ void down(const EpilogueArgs& e, int rows) {
+    const int es = esize(e.type) * rows;
+    c += e.ldc * es;
+    pre += e.N * es;
+    res += e.ldr * es;
+    group += (uint64_t)rows * (uint64_t)((e.N + 7) >> 3);
+  }
+};
+
+// The epilogue of U rows, 8 apart, of N columns: accumulators and their factor alpha,
+// the columns' bias and the residual as loaded.  `first`: the first column mod 8;
+// `cnt`: columns that exist; `rows`: of the U, those with 8 u < rows exist.
+template <int U, int N, class Mode>
+__device__ __forceinline__ void epilogue_rows(const EpilogueArgs& e, const Drop& d, float (&v)[U][N], float alpha,
+                                              const float (&bias)[N], const Raw<N> (&res)[U], const EpiAt& at,
+                                              int first, int cnt, int rows) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[u][i] = fmaf(v[u][i], alpha, bias[i]);
+  const int es8 = 8 * esize(e.type);
   if (e.pre) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = m + u * step;
-      if (r >= end) break;
-      if (e.stream) store_n<N, true>(e.pre, r * e.N + n, cnt, e.type, v[u]);
-      else store_n<N, false>(e.pre, r * e.N + n, cnt, e.type, v[u]);
+      if (8 * u >= rows) break;
+      uint8_t* to = at.pre + u * (e.N * es8);
+      if (Mode::NT && e.stream) store_n<N, true>(to, cnt, e.type, v[u]);
+      else store_n<N, false>(to, cnt, e.type, v[u]);
     }
   }
   by_act(e.act, [&](auto a) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[u][i] = act_of<decltype(a)::value, FAST>(v[u][i]);
+      for (int i = 0; i < N; ++i) v[u][i] = act_of<decltype(a)::value, Mode::FAST>(v[u][i]);
   });
   if (e.drop.rng) {
-    const uint64_t groups = (uint64_t)((e.N + 7) >> 3);
+    const uint64_t step = 8 * (uint64_t)((e.N + 7) >> 3);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      drop_n<N>(d, (uint64_t)(m + u * step) * groups + (uint64_t)(n >> 3), (int)(n & 7), v[u]);
+    for (int u = 0; u < U; ++u) drop_n<N>(d, at.group + u * step, first, v[u]);
   }
   if (e.residual) {
 #pragma unroll
@@ -329,34 +356,34 @@ __device__ __forceinline__ void epilogue_rows(const EpilogueArgs& e, const Drop&
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t r = m + u * step;
-    if (r >= end) break;
-    if (e.stream) store_n<N, true>(e.C, r * e.ldc + n, cnt, e.type, v[u]);
-    else store_n<N, false>(e.C, r * e.ldc + n, cnt, e.type, v[u]);
+    if (8 * u >= rows) break;
+    uint8_t* to = at.c + u * (e.ldc * es8);
+    if (Mode::NT && e.stream) store_n<N, true>(to, cnt, e.type, v[u]);
+    else store_n<N, false>(to, cnt, e.type, v[u]);
   }
 }
-template <int N>
-__device__ __forceinline__ Raw<N> load_residual(const EpilogueArgs& e, int64_t m, int64_t n) {
-  if (e.residual && m < e.M && n < e.N)
-    return load_raw<N>(e.residual, m * e.ldr + n, e.N - n < N ? (int)(e.N - n) : N, e.type);
-  return Raw<N>{};
-}
-template <int N>
+template <int N, bool TAIL = true>
 __device__ __forceinline__ void load_bias(const EpilogueArgs& e, int64_t n, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
-  if (e.bias && n < e.N) load_n<N>(e.bias, n, e.N - n < N ? (int)(e.N - n) : N, e.bias_type, v);
+  if (e.bias && n < e.N)
+    raw_values(load_raw<N>(reinterpret_cast<const uint8_t*>(e.bias) + n * esize(e.bias_type),
+                           TAIL && e.N - n < N ? (int)(e.N - n) : N, e.bias_type),
+               e.bias_type, v);
 }
 // N columns whose inputs were not loaded ahead
 template <int N, bool FAST>
 __device__ __forceinline__ void epilogue_at(const EpilogueArgs& e, float (&v)[N], int64_t m, int64_t n) {
   if (m >= e.M || n >= e.N) return;
+  const int cnt = e.N - n < N ? (int)(e.N - n) : N;
+  const EpiAt at(e, m, n);
   float b[N], w[1][N];
   load_bias<N>(e, n, b);
-  const Raw<N> res[1] = {load_residual<N>(e, m, n)};
+  Raw<N> res[1] = {};
+  if (e.residual) res[0] = load_raw<N>(at.res, cnt, e.type);
 #pragma unroll
   for (int i = 0; i < N; ++i) w[0][i] = v[i];
-  epilogue_rows<1, N, FAST>(e, drop_of(e.drop), w, 1.0f, b, res, m, 0, n, e.M);
+  epilogue_rows<1, N, EpiMode<FAST, true, false>>(e, drop_of(e.drop), w, 1.0f, b, res, at, (int)(n & 7), cnt, 1);
 }
 
 // The lane's number, taken behind the main loop: nothing for that to keep.
@@ -383,20 +410,29 @@ __device__ __forceinline__ void ask_early(const EpilogueArgs& e) {
 // bias: of the lane's columns (load_bias<8> of n0 + 8 (lane % 8)); alpha: the
 // product's factor; scale(c, i, j): other factors on block (i, j).
 constexpr int kWaveEpilogueLds = 64 * 64 * 4;
-template <int TM, bool FAST, int kU, class Scale>
+template <int TM, class Mode, int kU, class Scale>
 __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[TM][4], uint8_t* lds, int64_t m0,
                                               int64_t n0, const float (&bias)[8], float alpha, Scale scale) {
   const int lane = lane_anew();
   const int cc = lane & 7, lr = lane >> 3;
   const int64_t n = n0 + 8 * cc;
+  const int cnt = n >= e.N ? 0 : Mode::TAIL && e.N - n < 8 ? (int)(e.N - n) : 8;
+  // rows of the sub-tile that exist, counted from the lane's first
+  const int left = (int)(e.M - m0 < 16 * TM ? e.M - m0 : 16 * TM) - lr;
   float* tile = reinterpret_cast<float*>(lds);
   // 16-byte chunk c of row r at c ^ r % 16: the 16 rows that a store writes, and the
   // even chunks of two rows that a load reads, fall on different banks
-  auto at = [&](int r, int c) { return tile + r * 64 + ((c ^ (r & 15)) << 2); };
+  auto place = [&](int r, int c) { return tile + r * 64 + ((c ^ (r & 15)) << 2); };
   const Drop d = drop_of(e.drop);
-  Raw<8> res[kU];
+  EpiAt at(e, m0 + lr, n);
+  Raw<8> res[kU] = {};
+  auto load_res = [&](int r0) {  // of rows r0 + 8 u, seen from `at`
 #pragma unroll
-  for (int u = 0; u < kU; ++u) res[u] = load_residual<8>(e, m0 + lr + 8 * u, n);
+    for (int u = 0; u < kU; ++u)
+      if (e.residual && cnt > 0 && r0 + 8 * u < left)
+        res[u] = load_raw<8>(at.res + u * (e.ldr * 8 * esize(e.type)), Mode::TAIL ? cnt : 8, e.type);
+  };
+  load_res(0);
   static_for<(TM + 3) / 4>([&](auto half) {
     constexpr int h = 4 * decltype(half)::value;
 #pragma unroll
@@ -405,28 +441,27 @@ __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[
       for (int j = 0; j < 4; ++j) {
         v4f c = acc[i][j];
         scale(c, i, j);
-        *reinterpret_cast<v4f*>(at(16 * (i - h) + (lane & 15), 4 * j + (lane >> 4))) = c;
+        *reinterpret_cast<v4f*>(place(16 * (i - h) + (lane & 15), 4 * j + (lane >> 4))) = c;
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    // (the last half of a 7-block tile has 48 rows: those past it are past its 64 in LDS, and hold an earlier half's)
-    const int64_t end = m0 + 16 * TM < e.M ? m0 + 16 * TM : e.M;
+    // (the last half of a 7-block tile has 48 rows; what LDS holds behind them is not stored)
 #pragma unroll 1
     for (int r0 = 0; r0 < 64; r0 += 8 * kU) {
-      const int64_t m = m0 + 16 * h + r0 + lr;
       float v[kU][8];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int r = r0 + 8 * u + lr;
-        const v4f a = *reinterpret_cast<const v4f*>(at(r, 2 * cc)), b = *reinterpret_cast<const v4f*>(at(r, 2 * cc + 1));
+        const v4f a = *reinterpret_cast<const v4f*>(place(r, 2 * cc));
+        const v4f b = *reinterpret_cast<const v4f*>(place(r, 2 * cc + 1));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[u][i] = a[i], v[u][4 + i] = b[i];
       }
-      if (n < e.N) epilogue_rows<kU, 8, FAST>(e, d, v, alpha, bias, res, m, 8, n, end);
-      if (16 * h + r0 + 8 * kU < 16 * TM) {  // the next rows' residual, while they are read and computed
-#pragma unroll
-        for (int u = 0; u < kU; ++u) res[u] = load_residual<8>(e, m + 8 * (kU + u), n);
-      }
+      const int row = 16 * h + r0;
+      if (cnt > 0)
+        epilogue_rows<kU, 8, Mode>(e, d, v, alpha, bias, res, at, 0, Mode::TAIL ? cnt : 8, left - row);
+      at.down(e, 8 * kU);
+      load_res(row + 8 * kU);  // the next rows' residual, while they are read and computed
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();

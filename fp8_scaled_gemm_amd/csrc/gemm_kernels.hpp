@@ -213,7 +213,7 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   float bias[8];  // an epilogue's, loaded ahead: what few k-tiles there are would not hide it
   if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {
     ask_early(p.epi);
-    load_bias<8>(p.epi, bn + wn * 64 + 8 * (lane & 7), bias);
+    load_bias<8, false>(p.epi, bn + wn * 64 + 8 * (lane & 7), bias);
   }
 
   // global -> register prefetch of one k-tile (a cast operand's chunk is 16
@@ -398,7 +398,7 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   const Alpha<RW, Cfg::kTM, Cfg::kTN> alpha = make_alpha();
   if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {  // (the loop ended with a barrier: the tiles are free)
     static_assert(BN / WN == 64 && (BM / WM) % 64 == 0 && Cfg::kLdsBytes >= WM * WN * kWaveEpilogueLds, "wave sub-tile");
-    wave_epilogue<Cfg::kTM, true, 4>(p.epi, acc, smem + wave * kWaveEpilogueLds, bm + wm * (BM / WM), bn + wn * 64,
+    wave_epilogue<Cfg::kTM, EpiMode<true, false, false>, 2>(p.epi, acc, smem + wave * kWaveEpilogueLds, bm + wm * (BM / WM), bn + wn * 64,
                                      bias, RW ? 1.0f : alpha.a, [&](v4f& c, int i, int j) {
                                        if constexpr (RW) alpha.apply(c, i, j);
                                      });
@@ -863,11 +863,11 @@ __global__ __launch_bounds__(512) void k_gemm_pingpong(Prob p) {
   if constexpr (kEpi) {
     __builtin_amdgcn_s_waitcnt(0);  // no load may still be writing a slot
     float bias[8];
-    load_bias<8>(p.epi, bn + wc0 + 8 * (lane_anew() & 7), bias);
+    load_bias<8, false>(p.epi, bn + wc0 + 8 * (lane_anew() & 7), bias);
     barrier();
     static_assert(2 * kWaveEpilogueLds == 256 * kBK, "two waves a slot");
     uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
-    wave_epilogue<kTM, true, 4>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + wr0, bn + wc0, bias,
+    wave_epilogue<kTM, EpiMode<true, false, true>, 4>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + wr0, bn + wc0, bias,
                                 RW ? 1.0f : alpha.a, [&](v4f& c, int i, int j) {
                                   if constexpr (RW) alpha.apply(c, i, j);
                                 });

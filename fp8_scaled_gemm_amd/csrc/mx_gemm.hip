@@ -263,7 +263,7 @@ __global__ __launch_bounds__(512) void k_mx_pingpong(Prob p) {
     barrier();
     static_assert(2 * kWaveEpilogueLds == sizeof(sA0), "two waves a slot");
     uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
-    wave_epilogue<kTM, kFast<OUT>, 2>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + grp * 128, bn + wq * 64,
+    wave_epilogue<kTM, EpiMode<kFast<OUT>, true, true>, 2>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + grp * 128, bn + wq * 64,
                                       bias, 1.0f, [](v4f&, int, int) {});
   } else if constexpr (OUT == FP8SG_OUT_F32) {
     float* C = reinterpret_cast<float*>(p.C);
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
   }
   if constexpr (kEpi<Prob>) {  // (every load has landed, every wave has read its last stage)
     static_assert(4 * kWaveEpilogueLds <= sizeof(lds), "wave sub-tiles");
-    wave_epilogue<4, kFast<OUT>, 4>(p.epi, acc, lds + wave * kWaveEpilogueLds, bm + 64 * wm, bn + 64 * wn, bias,
+    wave_epilogue<4, EpiMode<kFast<OUT>, true, false>, 4>(p.epi, acc, lds + wave * kWaveEpilogueLds, bm + 64 * wm, bn + 64 * wn, bias,
                                     1.0f, [](v4f&, int, int) {});
     return;
   }

@@ -90,33 +90,26 @@ def _clear(a, name_a, b, name_b):
     raise ValueError(f"{name_a} and {name_b} overlap")
 
 
-def _all_clear(spans, outputs, inputs):
-    """No output shares memory with another output or with an input.  spans: first
-    and last byte address + 1 of each; where these lie apart, which is the common
-    case, nothing more is looked at.  outputs, inputs: (tensor or None, name)."""
-    spans.sort()
-    at = 0
-    for lo, hi in spans:
-        if lo < at:
-            break
-        at = hi
-    else:
-        return
+def _all_clear(outputs, inputs):
+    """No output shares memory with another output or with an input; each is a
+    (tensor or None, name)."""
     for i, (t, name) in enumerate(outputs):
         for u, other in outputs[i + 1:] + inputs:
             _clear(t, name, u, other)
 
 
 def _drop(p, rng):
-    """(p, address of rng)"""
-    if not 0.0 <= p <= 1.0:
-        raise ValueError(f"p: {p} is not a probability")
+    """Address of rng (0: nothing is dropped), whose device _here checks."""
     if rng is None:
-        if p >= 2.0 ** -17:
+        if p and not 0.0 <= p < 2.0 ** -17:
+            if not 0.0 <= p <= 1.0:
+                raise ValueError(f"p: {p} is not a probability")
             raise ValueError("rng is needed where p is not 0")
         return 0
-    _need(rng, "rng", torch.int64, numel=2)
-    _here(rng)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p: {p} is not a probability")
+    if rng.__class__ is not torch.Tensor or rng.dtype is not torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
+        _need(rng, "rng", torch.int64, numel=2)
     return rng.data_ptr()
 
 
@@ -129,83 +122,104 @@ def _act(act):
 def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng):
     """The packed struct of a forward epilogue.  in_dtype: the linear's input's, or None."""
     dt = y.dtype
-    size, at = _SIZE[dt], y.data_ptr()
-    ldy = _row_stride(y, "y", dt, shape, M, N)
-    spans = [(at, at + ((M - 1) * ldy + N) * size)] if M and N else []
+    ldy = N if y.shape == shape and y.is_contiguous() else _row_stride(y, "y", dt, shape, M, N)
+    at = y.data_ptr()
+    end = at + (M * ldy if M else 0) * _SIZE[dt]  # (or a little past the last row)
     pb = pr = pp = bt = ldr = 0
-    inputs = []
+    near = False  # whether an output comes near another tensor: looked at more closely then
     if bias is not None:
-        bt = _type(bias, "bias")
-        if in_dtype is not None and bias.dtype is not in_dtype and bt != 2:
-            raise TypeError(f"bias: dtype {bias.dtype}, expected {in_dtype} or float32")
-        _same(bias, "bias", bias.dtype, (N,))
+        bd = bias.dtype if isinstance(bias, torch.Tensor) else None
+        if bd is not dt:
+            bt = _type(bias, "bias")
+        else:
+            bt = _TYPE[dt]
+        if in_dtype is not None and bd is not in_dtype and bt != 2:
+            raise TypeError(f"bias: dtype {bd}, expected {in_dtype} or float32")
+        _same(bias, "bias", bd, (N,))
         pb = bias.data_ptr()
-        spans.append((pb, pb + N * _SIZE[bias.dtype]))
-        inputs.append((bias, "bias"))
+        near = at < pb + 4 * N and pb < end
     if residual is not None:
         ldr = _row_stride(residual, "residual", dt, shape, M, N)
         pr = residual.data_ptr()
-        if pr != at or ldr != ldy:  # (the output itself is allowed)
-            if M and N:
-                spans.append((pr, pr + ((M - 1) * ldr + N) * size))
-            inputs.append((residual, "residual"))
+        if pr == at and ldr == ldy:  # the output itself is allowed
+            residual = y
+        elif at < pr + M * ldr * _SIZE[dt] and pr < end:
+            near = True
     if pre is not None:
         _same(pre, "pre", dt, shape)
         pp = pre.data_ptr()
-        spans.append((pp, pp + M * N * size))
-    _all_clear(spans, [(y, "y"), (pre, "pre")], inputs)
-    words = _drop(p, rng) if p or rng is not None else 0
-    e = _pack(pb, pr, pp, words, ldr, ldy, p, _act(act), bt)
-    _here(y, bias, residual, pre)
+        pe = pp + M * N * _SIZE[dt]
+        if (at < pe and pp < end) or (pb and pb < pe and pp < pb + 4 * N) or \
+                (pr and pr < pe and pp < pr + M * ldr * _SIZE[dt]):
+            near = True
+    if near:
+        _all_clear([(y, "y"), (pre, "pre")], [(bias, "bias"), (residual if residual is not y else None, "residual")])
+        if residual is y:
+            _clear(pre, "pre", y, "residual")
+    e = _pack(pb, pr, pp, _drop(p, rng), ldr, ldy, p, _act(act), bt)
+    _here(y, bias, residual, pre, rng)
     return e
 
 
 def _backward(gy, gh, gb, pre, act, p, rng, part, M, N, alone, *out):
     """The packed struct of a backward step, and the workspace's length.  out: the
     call's other outputs, (tensor or None, name)."""
-    dt = gy.dtype
-    size = _SIZE[dt]
+    dt, shape = gy.dtype, gy.shape
+    size = M * N * _SIZE[dt]
     pg, n, bt, pp = gy.data_ptr(), 0, 0, 0
-    words = _drop(p, rng) if p or rng is not None else 0
+    words = _drop(p, rng)
     changes = _act(act) != ACT_NONE or p >= 2.0 ** -17
-    spans, outputs, inputs = [(pg, pg + M * N * size)], list(out), [(gy, "gy")]
+    spans, outputs, inputs = [(pg, pg + size)], [], [(gy, "gy")]
     if gh is not None:
-        _same(gh, "gh", dt, gy.shape)
+        _same(gh, "gh", dt, shape)
         at = gh.data_ptr()
         if at != pg:  # (gy itself is allowed)
-            spans.append((at, at + M * N * size))
+            spans.append((at, at + size))
             outputs.append((gh, "gh"))
     elif changes and not alone:
         raise ValueError("gh is needed where the epilogue has an activation or drops")
     if act != ACT_NONE:
         if pre is None:
             raise ValueError("pre is needed where the epilogue has an activation")
-        _same(pre, "pre", dt, gy.shape)
+        _same(pre, "pre", dt, shape)
         pp = pre.data_ptr()
-        spans.append((pp, pp + M * N * size))
+        if pp != pg or gh is not None and gh.data_ptr() == pg:
+            spans.append((pp, pp + size))
         inputs.append((pre, "pre"))
-        if gh is not None and gh.data_ptr() == pg:
-            _clear(gh, "gh", pre, "pre")
+    else:
+        pre = None
     if gb is not None:
-        if not isinstance(gb, torch.Tensor):
-            raise TypeError(f"gb: expected a torch.Tensor, got {type(gb).__name__}")
-        if gb.dtype is not dt and gb.dtype is not torch.float32:
-            raise TypeError(f"gb: dtype {gb.dtype}, expected {dt} or float32")
-        _same(gb, "gb", gb.dtype, (N,))
-        at, bt = gb.data_ptr(), _TYPE[gb.dtype]
-        spans.append((at, at + N * _SIZE[gb.dtype]))
+        gd = gb.dtype if isinstance(gb, torch.Tensor) else _type(gb, "gb")
+        if gd is not dt and gd is not torch.float32:
+            raise TypeError(f"gb: dtype {gd}, expected {dt} or float32")
+        _same(gb, "gb", gd, (N,))
+        at, bt = gb.data_ptr(), _TYPE[gd]
+        spans.append((at, at + N * _SIZE[gd]))
         outputs.append((gb, "gb"))
         if part is not None:
-            _need(part, "part", torch.float32)
+            if part.__class__ is not torch.Tensor or part.dtype is not torch.float32 or not part.is_contiguous():
+                _need(part, "part", torch.float32)
             n, at = part.numel(), part.data_ptr()
             spans.append((at, at + 4 * n))
             outputs.append((part, "part"))
-    for t, _name in out:
+    else:
+        part = None
+    for t, name in out:
         if t is not None:
             at = t.data_ptr()
             spans.append((at, at + t.nbytes))
-    _all_clear(spans, outputs, inputs)
-    _here(gy, gh, gb, pre, part)
+            outputs.append((t, name))
+    spans.sort()
+    at = 0
+    for lo, hi in spans:
+        if lo < at:  # two come near each other: looked at more closely
+            if gh is not None and gh.data_ptr() == pg:
+                inputs[0] = (None, "gy")
+                outputs.append((gh, "gh"))
+            _all_clear(outputs, inputs)
+            break
+        at = hi
+    _here(gy, gh, gb, pre, part, rng)
     return _pack(0, 0, pp, words, 0, 0, p, act, bt), n
 
 
@@ -369,7 +383,7 @@ def mxfp4_linear_apply_epilogue(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: 
     _need_codes(w, "w", Mxfp4, N, K)
     _need_codes(ws, "ws", Mxfp4, M, K)
     yt = _type(y, "y")
-    e = _epilogue(y, _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
+    e = _epilogue(y, (M, N) if x.dim() == 2 else _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
     _here(x, w.q, w.s, ws.q, ws.s)
     _check(lib().mxfp4_linear_apply_epilogue(_ptr(x), _TYPE[x.dtype], w.c(), M, N, K, _rule(rule), ws.c(),
                                              e, _ptr(y), yt, _stream(stream)),
@@ -408,37 +422,29 @@ def mxfp4_linear_bwd_epilogue(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4L
 
 # ------------------------------------------------------------------------- dropout
 
-def _rows_at(t, name, like, rows, cols):
-    """(address, row distance, span) of a dropout operand."""
-    ld = _row_stride(t, name, like.dtype, like.shape, rows, cols)
-    at = t.data_ptr()
-    return at, ld, (at, at + ((rows - 1) * ld + cols) * _SIZE[like.dtype])
-
-
 def _dropout(x, name_x, p, rng, y, name_y, residual):
     """(x, ldx, residual, ldr, type, rows, cols, p, rng, y, ldy), checked."""
     xt = _type(x, name_x)
-    shape = x.shape
+    dt, shape = x.dtype, x.shape
     if not shape:
         raise ValueError(f"{name_x}: expected at least one dimension")
     cols = shape[-1]
     rows = shape[0] if len(shape) == 2 else _rows(x)
-    px, ldx, sx = _rows_at(x, name_x, x, rows, cols)
-    py, ldy, sy = _rows_at(y, name_y, x, rows, cols)
-    spans, inputs = [sy], []
-    if px != py or ldx != ldy:  # (in place is allowed)
-        spans.append(sx)
-        inputs.append((x, name_x))
+    ldx = _row_stride(x, name_x, dt, shape, rows, cols)
+    ldy = _row_stride(y, name_y, dt, shape, rows, cols)
+    px, py, size = x.data_ptr(), y.data_ptr(), rows * _SIZE[dt]
+    end = py + ldy * size
+    # in place is allowed; what comes near in another way is looked at more closely
+    if (px != py or ldx != ldy) and py < px + ldx * size and px < end and cols:
+        _clear(y, name_y, x, name_x)
     pr = ldr = 0
     if residual is not None:
-        pr, ldr, sr = _rows_at(residual, "residual", x, rows, cols)
-        if pr != py or ldr != ldy:
-            spans.append(sr)
-            inputs.append((residual, "residual"))
-    if rows and cols:
-        _all_clear(spans, [(y, name_y)], inputs)
-    words = _drop(p, rng) if p or rng is not None else 0
-    _here(x, y, residual)
+        ldr = _row_stride(residual, "residual", dt, shape, rows, cols)
+        pr = residual.data_ptr()
+        if (pr != py or ldr != ldy) and py < pr + ldr * size and pr < end and cols:
+            _clear(y, name_y, residual, "residual")
+    words = _drop(p, rng)
+    _here(x, y, residual, rng)
     return px, ldx, pr, ldr, xt, rows, cols, p, words, py, ldy
 
 
