@@ -488,6 +488,13 @@ constexpr int few_waves(int tm, int tn, bool fused) {
   return (int)kLds / few_wave_bytes(tm, tn, fused) < 16 ? (int)kLds / few_wave_bytes(tm, tn, fused) : 16;
 }
 
+// Columns a thread takes in a join with an epilogue: more share a call of the
+// generator, fewer are done sooner.  us with 1 / 4 / 8, bias and gelu, then silu with
+// dropout, residual and h kept: one token 14336 x 4096 (tiles 16 x 32) 7.1 / 7.7 / 8.0;
+// tiles 16 x 16, 300 x 2000 x 1000, fp32 8.2 / 9.6 / 11.2, 10.0 / 11.9 / 13.1; 16 x 32,
+// 1000 x 1031 x 2085, 13.7 / 12.0 / 13.8, 18.4 / 14.9 / 16.2; 32 x 32 (8) 11.1, 13.1.
+constexpr int few_share(int tm, int tn, bool fused) { return fused || tm * tn == 1 ? 1 : tm * tn == 2 ? 4 : 8; }
+
 // blk of blocks: this workgroup's place among the problem's.
 template <int TM, int TN, int OUT, int FT, class Prob>
 __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64_t blk, int64_t blocks) {
@@ -645,7 +652,7 @@ __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64
   }
 
   Elem<OUT>* C = reinterpret_cast<Elem<OUT>*>(p.C);
-  if (!kEpi<Prob> && W == 1) {  // nothing to join (an epilogue takes the join's element order all the same)
+  if (!kEpi<Prob> && W == 1) {  // nothing to join (an epilogue takes the join's order all the same)
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int64_t m = bm + 16 * i + r;
@@ -655,8 +662,33 @@ __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64
     }
     return;
   }
-  // join: a row of blocks at a time, [wave][j][lane] in LDS
   float* red = reinterpret_cast<float*>(lds);
+  if constexpr (kEpi<Prob>) {
+    // join with an epilogue: all blocks at once, [wave][i][j][lane] in LDS, then NV
+    // neighbouring columns a thread, which share a call of the generator
+    constexpr int NV = few_share(TM, TN, kFused);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<v4f*>(red + (((wave * TM + i) * TN + j) * 64 + lane) * 4) = acc[i][j];
+    __syncthreads();
+    for (int u = threadIdx.x; u < 256 / NV * TM * TN; u += blockDim.x) {
+      const int ml = u / (16 / NV * TN), c = u % (16 / NV * TN) * NV;
+      if (bm + ml >= M) continue;
+      const float* src = red + (((ml >> 4) * TN + (c >> 4)) * 64 + (c & 15) / 4 * 16 + (ml & 15)) * 4 + (c & 3);
+      float v[NV];
+#pragma unroll
+      for (int e = 0; e < NV; ++e) v[e] = 0.f;
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) v[e] += src[w * TM * TN * 256 + e / 4 * 64 + e % 4];
+      epilogue_at<NV, kFast<OUT>>(p.epi, v, bm + ml, bn + c);
+    }
+    return;
+  }
+  // join: a row of blocks at a time, [wave][j][lane] in LDS
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     __syncthreads();
@@ -670,12 +702,7 @@ __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64
       const float* src = red + ((nl >> 4) * 64 + ((nl & 15) >> 2) * 16 + ml) * 4 + (nl & 3);
       float v = 0.f;
       for (int w = 0; w < W; ++w) v += src[w * TN * 256];
-      if constexpr (kEpi<Prob>) {
-        float one[1] = {v};
-        epilogue_at<1, kFast<OUT>>(p.epi, one, m, n);
-      } else {
-        C[m * N + n] = from_f32<OUT>(v);
-      }
+      C[m * N + n] = from_f32<OUT>(v);
     }
   }
 }
@@ -722,7 +749,7 @@ hipError_t launch_few(const Prob& p, const MxApply& ap, hipStream_t stream) {
   const hipError_t attr = allow_lds(kern, done);
   if (attr != hipSuccess) return attr;
   constexpr int64_t kWaveBytes = few_wave_bytes(TM, TN, FT >= 0);
-  static_assert(kWaveBytes >= TN * 1024, "the join fits a wave's stages");
+  static_assert(kWaveBytes >= TM * TN * 1024, "the join fits a wave's stages");
   const int64_t blocks = ((p.M + 16 * TM - 1) / (16 * TM)) * ((p.N + 16 * TN - 1) / (16 * TN));
   const int W = split_waves(mx_ktiles(p.K), blocks, kWaveBytes, few_waves(TM, TN, FT >= 0));
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), W * kWaveBytes, stream, p, ap);
@@ -756,6 +783,25 @@ double mid_cost(const MxGemmProblem& p, int cus) {
   return 2.8 + nk * 1.35 * ((tiles + 2 * cus - 1) / (2 * cus));
 }
 
+// What an epilogue adds to those times.  Vector operations an element (activation: 20
+// for 16-bit results, 40 for fp32; a call of the generator 200, shared), at 64 a cycle
+// and unit where a tile's waves share them; in tiles of 128 one wave of 64 elements a
+// lane works on its own (us, 1000 x 1031 x 2085 fp32, without / gelu / silu with dropout,
+// residual and h kept: tiles of 128 10.0, 16.3, 22.9, of 32 10.5, 11.1, 13.1).
+double epilogue_slots(const EpilogueArgs& e, int share) {
+  const double act = e.act == FP8SG_ACT_NONE ? 0 : e.type == FP8SG_OUT_F32 ? 40 : 20;
+  return 10 + act + (e.drop.rng ? 200.0 / share : 0) + (e.pre ? 5 : 0) + (e.residual ? 5 : 0);
+}
+double few_epilogue(const MxGemmProblem&, int, int, int) { return 0; }
+double few_epilogue(const MxGemmEpiProblem& p, int tm, int tn, int cus) {
+  return (double)p.M * p.N * epilogue_slots(p.epi, few_share(tm, tn, false)) / (64 * 2400.0 * cus);
+}
+double mid_epilogue(const MxGemmProblem&, int) { return 0; }
+double mid_epilogue(const MxGemmEpiProblem& p, int cus) {
+  const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
+  return 0.14 * epilogue_slots(p.epi, 8) * ((tiles + 2 * cus - 1) / (2 * cus));
+}
+
 // A product with or without an epilogue.
 template <int T, class Prob>
 hipError_t launch_product(const Prob& p, hipStream_t stream) {
@@ -777,10 +823,11 @@ hipError_t launch_product(const Prob& p, hipStream_t stream) {
     hipLaunchKernelGGL((k_mx_pingpong<T, Prob>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
     return hipGetLastError();
   }
-  const double c11 = few_cost(p, 1, 1, FewCost{2.0, 0.7}, cus), c12 = few_cost(p, 1, 2, FewCost{2.4, 0.7}, cus);
-  const double c22 = few_cost(p, 2, 2, FewCost{3.5, 0.6}, cus), c44 = few_cost(p, 4, 4, FewCost{8.8, 0.7}, cus);
+  auto cost = [&](int tm, int tn, FewCost c) { return few_cost(p, tm, tn, c, cus) + few_epilogue(p, tm, tn, cus); };
+  const double c11 = cost(1, 1, FewCost{2.0, 0.7}), c12 = cost(1, 2, FewCost{2.4, 0.7});
+  const double c22 = cost(2, 2, FewCost{3.5, 0.6}), c44 = cost(4, 4, FewCost{kEpi<Prob> ? 6.8 : 8.8, 0.7});
   const double few = std::min(std::min(c11, c12), std::min(c22, c44));
-  if (mid_cost(p, cus) < few) {
+  if (mid_cost(p, cus) + mid_epilogue(p, cus) < few) {
     hipLaunchKernelGGL((k_mx_mid<T, Prob>), dim3((unsigned)tiles(128)), dim3(256), 0, stream, p);
     return hipGetLastError();
   }
