@@ -35,6 +35,9 @@ below.
     same layer with 4-bit microscaled operands, for training and for serving.
   - SwiGLU, LayerNorm: the gated activation and the norm around those linears,
     which may keep what their backward pass needs in 8 bits.
+  - Float8EpilogueLinear, MXFP4EpilogueLinear, PackedMXFP4EpilogueLinear, Dropout: the
+    linears with bias, activation, dropout and residual in the product's epilogue,
+    and dropout on its own.
 
 Limits of Float8Linear: inputs and weights are bf16 or fp16; Float8Linear has no bias (the method's linear has none; the default
 filter leaves biased layers alone); leading dimensions of the input are
@@ -57,6 +60,9 @@ from . import (E4M3FN, E5M2, LinearBwdWs, LinearBwdWsRW, LinearSaved, LinearSave
 from . import (MX_FIT, MX_FLOOR, Act8, Mxfp4, Mxfp4LinearSaved, Mxfp4LinearWs, layer_norm_bwd,
                layer_norm_fwd, layer_norm_workspace_len, mxfp4_linear_apply, mxfp4_linear_bwd,
                mxfp4_linear_fwd, mxfp4_quantize, swiglu_bwd, swiglu_fwd)
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, dropout_bwd, dropout_fwd,
+               epilogue_workspace_len, fp8_scaled_linear_bwd_epilogue, fp8_scaled_linear_fwd_epilogue,
+               mxfp4_linear_apply_epilogue, mxfp4_linear_bwd_epilogue, mxfp4_linear_fwd_epilogue)
 
 SCALINGS = ("dynamic", "delayed", "rowwise")
 
@@ -371,22 +377,42 @@ def default_module_filter(mod: nn.Linear, fqn: str) -> bool:
             last not in HIGH_PRECISION_NAMES)
 
 
+def _has_own_bias(mod) -> bool:
+    """A bias in the weight's dtype or fp32, as the products' epilogue takes it."""
+    b = getattr(mod, "bias", None)
+    return b is not None and b.dtype in (mod.weight.dtype, torch.float32)
+
+
+def _biased_filter(mod: nn.Linear, fqn: str) -> bool:
+    """default_module_filter, layers with a bias included."""
+    return ((mod.bias is None or _has_own_bias(mod)) and mod.weight.dtype in (torch.bfloat16, torch.float16) and
+            mod.in_features % 16 == 0 and mod.out_features % 16 == 0 and
+            fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES)
+
+
 def convert_to_float8_training(model: nn.Module,
                                module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
                                scaling: str = "dynamic", history_len: int = 16,
-                               grad_scaler: Optional["GradScaler"] = None) -> nn.Module:
+                               grad_scaler: Optional["GradScaler"] = None, biased: bool = False) -> nn.Module:
     """Replace, in place and post-order, every nn.Linear child that
     module_filter_fn(child, fully_qualified_name) accepts (default:
     default_module_filter) with a Float8Linear sharing its weight.  With
     grad_scaler, the fp16 layers unscale and check their weight gradients in
-    the wgrad GEMM's epilogue with that scaler."""
-    accept = module_filter_fn or default_module_filter
+    the wgrad GEMM's epilogue with that scaler.  With biased (dynamic scaling
+    only), layers with a bias are replaced too, by a Float8EpilogueLinear that
+    shares both, and the default filter accepts them."""
+    if biased and scaling != "dynamic":
+        raise ValueError("layers with a bias are converted with dynamic scaling only")
+    accept = module_filter_fn or (_biased_filter if biased else default_module_filter)
     # every (parent, attribute, module, dotted path) below the root, each
     # module after all of its own descendants; the swaps are made after the
     # walk, so it never iterates over a tree it is changing
     edges = list(_descendants_post_order(model, ()))
     for parent, attr, child, path in edges:
         if type(child) is nn.Linear and accept(child, ".".join(path)):
+            if biased and child.bias is not None:
+                setattr(parent, attr, Float8EpilogueLinear.from_float(child))
+                continue
             new = Float8Linear.from_float(child, scaling, history_len)
             if grad_scaler is not None and new.weight.dtype == torch.float16:
                 new.attach_grad_scaler(grad_scaler)
@@ -650,37 +676,52 @@ class PackedMXFP4Linear(nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, rule={self.rule}"
 
 
-def _mx_filter(mod: nn.Module, fqn: str) -> bool:
+def _mx_filter(mod: nn.Module, fqn: str, biased: bool = False) -> bool:
     """As default_module_filter, without its rules on sizes (MXFP4 takes any)."""
-    return (getattr(mod, "bias", None) is None and mod.weight.dtype in _MX_DTYPES and
+    b = getattr(mod, "bias", None)
+    return ((b is None or biased and _has_own_bias(mod)) and mod.weight.dtype in _MX_DTYPES and
             fqn.rsplit(".", 1)[-1] not in HIGH_PRECISION_NAMES)
+
+
+def _mx_accept(module_filter_fn, biased):
+    return module_filter_fn or (lambda m, fqn: _mx_filter(m, fqn, biased))
 
 
 def _replace_linears(model, accept, make):
     for parent, attr, child, path in list(_descendants_post_order(model, ())):
-        if type(child) in (nn.Linear, MXFP4Linear) and accept(child, ".".join(path)):
+        if type(child) in (nn.Linear, MXFP4Linear, MXFP4EpilogueLinear) and accept(child, ".".join(path)):
             setattr(parent, attr, make(child))
     return model
 
 
 def convert_to_mxfp4_training(model: nn.Module,
                               module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
-                              rule: str = "floor") -> nn.Module:
+                              rule: str = "floor", biased: bool = False) -> nn.Module:
     """convert_to_float8_training's walk with MXFP4Linear: every nn.Linear child
     that module_filter_fn accepts (default: no bias, not an output head or a
-    router by name) is replaced in place by one that shares its weight."""
-    accept = module_filter_fn or _mx_filter
+    router by name) is replaced in place by one that shares its weight.  With
+    biased, layers with a bias too, by an MXFP4EpilogueLinear that shares both."""
+    accept = _mx_accept(module_filter_fn, biased)
     return _replace_linears(model, lambda m, fqn: type(m) is nn.Linear and accept(m, fqn),
-                            lambda m: MXFP4Linear.from_float(m, rule))
+                            lambda m: MXFP4EpilogueLinear.from_float(m, rule=rule) if biased and m.bias is not None
+                            else MXFP4Linear.from_float(m, rule))
 
 
 def convert_to_mxfp4_serving(model: nn.Module,
                              module_filter_fn: Optional[Callable[[nn.Module, str], bool]] = None,
-                             rule: Optional[str] = None) -> nn.Module:
+                             rule: Optional[str] = None, biased: bool = False) -> nn.Module:
     """Replace, in place, every nn.Linear and MXFP4Linear child that the filter
     accepts by a PackedMXFP4Linear holding its quantised weight.  rule None: each
-    layer's own, "floor" for an nn.Linear."""
-    return _replace_linears(model, module_filter_fn or _mx_filter, lambda m: PackedMXFP4Linear.from_float(m, rule))
+    layer's own, "floor" for an nn.Linear.  With biased, layers with a bias and
+    MXFP4EpilogueLinears too, by a PackedMXFP4EpilogueLinear."""
+    accept = _mx_accept(module_filter_fn, biased)
+
+    def make(m):
+        if type(m) is MXFP4EpilogueLinear or biased and getattr(m, "bias", None) is not None:
+            return PackedMXFP4EpilogueLinear.from_float(m, rule=rule)
+        return PackedMXFP4Linear.from_float(m, rule)
+    return _replace_linears(model, lambda m, fqn: (biased or type(m) is not MXFP4EpilogueLinear) and accept(m, fqn),
+                            make)
 
 
 # ---- gated activation
@@ -865,3 +906,426 @@ class LayerNorm(nn.Module):
 
     def extra_repr(self):
         return f"{self.normalized_shape}, eps={self.eps}, checkpoint={self.checkpoint}"
+
+# ------------------------------- linears with an epilogue in their product, dropout
+# y = residual + dropout(act(x W^T + b)), everything behind the product in its
+# epilogue, and dropout on its own.  Dropout's masks come from a counter-based
+# generator and are never stored: a pass keeps its two words (16 bytes) instead.  The
+# words are drawn from torch's generator of the device, so manual_seed,
+# torch.utils.checkpoint and a replayed graph govern them as they govern torch's own
+# dropout.
+
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+_T = torch.Tensor  # (in the long signatures below)
+
+
+def dropout_words(device) -> torch.Tensor:
+    """Two words for one dropout, from torch's generator of the device."""
+    return torch.randint(-2 ** 63, 2 ** 63 - 1, (2,), device=device, dtype=torch.int64)
+
+
+def _ep_part(like, M, N):
+    return like.new_empty(epilogue_workspace_len(M, N), dtype=torch.float32)
+
+
+def _changes(act, p):
+    """Whether the backward step's result is another tensor than its input."""
+    return act != ACT_NONE or p > 0
+
+
+# ------------------------------------------------------------------------- FP8
+
+@torch.library.custom_op("fp8sg::scaled_linear_epilogue_fwd", mutates_args=())
+def _op_ep_fwd(x: _T, w: _T, bias: Optional[_T], residual: Optional[_T], rng: Optional[_T], act: int, p: float,
+               save: bool) -> tuple[_T, _T, _T, _T, _T, _T, _T]:
+    M, K = x.shape
+    N = w.shape[0]
+    xt, wt, _ = fp8_linear_copies(M, N, K) if save else (False, False, False)
+    # uninitialised records: the forward writes every field the backward reads
+    saved = LinearSaved(M, N, K, tensors=(
+        _u8(x, (M, K)), _u8(x, (K, M)) if xt else None, _u8(x, (N, K)), _u8(x, (K, N)) if wt else None,
+        _u8(x, (2, SCALE_REC_BYTES))))
+    y = x.new_empty((M, N))
+    pre = x.new_empty((M, N)) if save and act != ACT_NONE else None
+    fp8_scaled_linear_fwd_epilogue(x, w, saved, y, bias=bias, act=act, residual=residual, pre=pre, p=p, rng=rng)
+    kept = saved.tensors() if save else (None,) * 5
+    return (y, pre if pre is not None else x.new_empty(0)) + tuple(t if t is not None else _u8(x, 0) for t in kept)
+
+
+@_op_ep_fwd.register_fake
+def _op_ep_fwd_fake(x, w, bias, residual, rng, act, p, save):
+    # (which copies are made depends on the sizes: a traced size becomes a constant)
+    M, N, K = int(x.shape[0]), int(w.shape[0]), int(x.shape[1])
+    xt, wt, _ = fp8_linear_copies(M, N, K) if save else (False, False, False)
+    shapes = ((M, K), (K, M) if xt else (0,), (N, K), (K, N) if wt else (0,), (2, SCALE_REC_BYTES)) if save else \
+        ((0,),) * 5
+    return (x.new_empty((M, N)), x.new_empty((M, N) if save and act != ACT_NONE else (0,))) + \
+        tuple(_u8(x, s) for s in shapes)
+
+
+@torch.library.custom_op("fp8sg::scaled_linear_epilogue_bwd", mutates_args=())
+def _op_ep_bwd(gy: _T, pre: _T, rng: Optional[_T], x_q: _T, x_qT: _T, w_q: _T, w_qT: _T, recs: _T, act: int, p: float,
+               need_b: bool, bdtype: torch.dtype) -> tuple[_T, _T, _T]:
+    M, N = gy.shape
+    K = x_q.shape[1]
+    saved = LinearSaved(M, N, K, tensors=(x_q, _present(x_qT), w_q, _present(w_qT), recs))
+    ws = LinearBwdWs(M, N, device=gy.device, transposed=fp8_linear_copies(M, N, K)[2],
+                     gy_sc=ScaleRec(buf=_u8(gy, SCALE_REC_BYTES)))
+    gx, gw = gy.new_empty((M, K)), gy.new_empty((N, K))
+    gb = gy.new_empty(N if need_b else 0, dtype=bdtype)
+    fp8_scaled_linear_bwd_epilogue(gy, saved, ws, gx, gw, gh=torch.empty_like(gy) if _changes(act, p) else None,
+                                   gb=gb if need_b else None, pre=_present(pre), act=act, p=p, rng=rng,
+                                   part=_ep_part(gy, M, N) if need_b else None)
+    return gx, gw, gb
+
+
+@_op_ep_bwd.register_fake
+def _op_ep_bwd_fake(gy, pre, rng, x_q, x_qT, w_q, w_qT, recs, act, p, need_b, bdtype):
+    M, N = gy.shape
+    K = x_q.shape[1]
+    return gy.new_empty((M, K)), gy.new_empty((N, K)), gy.new_empty(N if need_b else 0, dtype=bdtype)
+
+
+def _ep_setup(ctx, inputs, output):
+    x, _w, bias, _res, rng, act, p = inputs[:7]
+    ctx.act, ctx.p, ctx.rest = act, p, inputs[7:]
+    ctx.saved = inputs[-1]
+    ctx.K = x.shape[1]
+    ctx.bdtype = bias.dtype if bias is not None else x.dtype
+    ctx.save_for_backward(rng, *output[1:])
+    ctx.set_materialize_grads(False)
+
+
+def _ep_gy(ctx, gy):
+    """gy for a backward operator; needs the forward to have kept what that reads."""
+    if not ctx.saved:
+        raise RuntimeError("this linear ran without saving for a backward pass")
+    return gy.contiguous()
+
+
+def _ep_backward(ctx, gy, *_unused):
+    need = ctx.needs_input_grad
+    if gy is None or not any(need[:4]):
+        return (None,) * 8
+    gx = gw = gb = None
+    if any(need[:3]):
+        rng, *kept = ctx.saved_tensors
+        gx, gw, gb = torch.ops.fp8sg.scaled_linear_epilogue_bwd(_ep_gy(ctx, gy), kept[0], rng, *kept[1:], ctx.act, ctx.p,
+                                                                need[2], ctx.bdtype)
+    return (gx if need[0] else None, gw if need[1] else None, gb if need[2] else None, gy if need[3] else None,
+            None, None, None, None)
+
+
+_op_ep_fwd.register_autograd(_ep_backward, setup_context=_ep_setup)
+
+
+# ------------------------------------------------------------------------- MXFP4
+
+@torch.library.custom_op("fp8sg::mxfp4_linear_epilogue_fwd", mutates_args=())
+def _op_mxe_fwd(x: _T, w: _T, bias: Optional[_T], residual: Optional[_T], rng: Optional[_T], act: int, p: float, rule: int,
+                save: bool) -> tuple[_T, _T, _T, _T, _T, _T]:
+    M, K = x.shape
+    N = w.shape[0]
+    y = x.new_empty((M, N))
+    pre = x.new_empty((M, N)) if save and act != ACT_NONE else None
+    saved = Mxfp4LinearSaved(M, N, K, x.device) if save else None
+    mxfp4_linear_fwd_epilogue(x, w, Mxfp4LinearWs(M, N, K, x.device, backward=False), saved, y, bias=bias, act=act,
+                              residual=residual, pre=pre, p=p, rng=rng, rule=rule)
+    return (y, pre if pre is not None else x.new_empty(0)) + \
+        (saved.tensors() if save else tuple(_u8(x, 0) for _ in range(4)))
+
+
+@_op_mxe_fwd.register_fake
+def _op_mxe_fwd_fake(x, w, bias, residual, rng, act, p, rule, save):
+    M, K = x.shape
+    N = w.shape[0]
+    sizes = _mx_bytes(K, M) + _mx_bytes(K, N) if save else (0, 0, 0, 0)
+    return (x.new_empty((M, N)), x.new_empty((M, N) if save and act != ACT_NONE else (0,))) + \
+        tuple(_u8(x, n) for n in sizes)
+
+
+@torch.library.custom_op("fp8sg::mxfp4_linear_epilogue_bwd", mutates_args=())
+def _op_mxe_bwd(gy: _T, pre: _T, rng: Optional[_T], xq: _T, xs: _T, wq: _T, ws: _T, K: int, act: int, p: float, rule: int,
+                need: int, bdtype: torch.dtype) -> tuple[_T, _T, _T]:
+    M, N = gy.shape
+    gx = gy.new_empty((M, K) if need & 1 else (0,))
+    gw = gy.new_empty((N, K) if need & 2 else (0,))
+    gb = gy.new_empty(N if need & 4 else 0, dtype=bdtype)
+    products = need & 3
+    mxfp4_linear_bwd_epilogue(gy, Mxfp4LinearWs(M, N, K, gy.device, forward=False),
+                              Mxfp4LinearSaved(M, N, K, tensors=(xq, xs, wq, ws)), gx if need & 1 else None,
+                              gw if need & 2 else None, gh=torch.empty_like(gy) if products and _changes(act, p) else None,
+                              gb=gb if need & 4 else None, pre=pre if act != ACT_NONE else None, act=act, p=p, rng=rng,
+                              part=_ep_part(gy, M, N) if need & 4 else None, rule=rule)
+    return gx, gw, gb
+
+
+@_op_mxe_bwd.register_fake
+def _op_mxe_bwd_fake(gy, pre, rng, xq, xs, wq, ws, K, act, p, rule, need, bdtype):
+    M, N = gy.shape
+    return (gy.new_empty((M, K) if need & 1 else (0,)), gy.new_empty((N, K) if need & 2 else (0,)),
+            gy.new_empty(N if need & 4 else 0, dtype=bdtype))
+
+
+def _mxe_backward(ctx, gy, *_unused):
+    need = ctx.needs_input_grad
+    if gy is None or not any(need[:4]):
+        return (None,) * 9
+    got = [None] * 3
+    if any(need[:3]):
+        rng, *kept = ctx.saved_tensors
+        bits = sum(m for m, f in zip((1, 2, 4), need) if f)
+        got = torch.ops.fp8sg.mxfp4_linear_epilogue_bwd(_ep_gy(ctx, gy), kept[0], rng, *kept[1:], ctx.K, ctx.act, ctx.p,
+                                                        ctx.rest[0], bits, ctx.bdtype)
+    return (*(t if f else None for t, f in zip(got, need)), gy if need[3] else None, None, None, None, None, None)
+
+
+_op_mxe_fwd.register_autograd(_mxe_backward, setup_context=_ep_setup)
+
+
+# ------------------------------------------------------------------------- modules
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}, not {name!r}")
+    return name
+
+
+def _probability(p):
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"dropout must lie in [0, 1], not {p}")
+    return float(p)
+
+
+class _EpilogueLinear(nn.Module):
+    """What the layers share: parameters, checks and shapes."""
+    _dtypes = _MX_DTYPES
+
+    def __init__(self, in_features, out_features, bias, activation, dropout, device, dtype):
+        super().__init__()
+        if dtype not in self._dtypes:
+            raise TypeError(f"{type(self).__name__} takes {', '.join(str(t) for t in self._dtypes)}, not {dtype}")
+        self.in_features, self.out_features = in_features, out_features
+        self.activation, self.dropout = _activation(activation), _probability(dropout)
+        kw = dict(dtype=dtype, device=device)
+        self.weight = nn.Parameter(torch.empty((out_features, in_features), **kw))
+        self.bias = nn.Parameter(torch.empty(out_features, **kw)) if bias else None
+
+    @classmethod
+    def _share(cls, new, lin):
+        new.weight, new.bias = lin.weight, lin.bias
+        return new
+
+    @classmethod
+    def _check_float(cls, lin):
+        w, b = lin.weight, lin.bias
+        if w.dtype not in cls._dtypes:
+            raise TypeError(f"{cls.__name__} needs a weight of {', '.join(str(t) for t in cls._dtypes)}, got {w.dtype}")
+        if b is not None and b.dtype not in (w.dtype, torch.float32):
+            raise TypeError(f"{cls.__name__} needs a bias of {w.dtype} or float32, got {b.dtype}")
+
+    def _inputs(self, x, residual):
+        """(x, residual) as matrices."""
+        if x.dtype != self.weight.dtype:
+            raise TypeError(f"{type(self).__name__} takes inputs of its weight's dtype {self.weight.dtype}")
+        x2d = _flat(x, self.in_features, type(self).__name__).contiguous()
+        return x2d, _residual(residual, x.dtype, x.shape[:-1] + (self.out_features,))
+
+    def _drop(self, x):
+        """(p, words) of this pass."""
+        p = self.dropout if self.training else 0.0
+        return (p, dropout_words(x.device)) if p > 0 else (0.0, None)
+
+    def _saves(self, *tensors):
+        return torch.is_grad_enabled() and any(
+            t is not None and t.requires_grad for t in (self.weight, self.bias) + tensors)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, " \
+               f"activation={self.activation}, dropout={self.dropout}"
+
+
+def _residual(residual, dtype, shape):
+    if residual is None:
+        return None
+    if residual.dtype != dtype or residual.shape != shape:
+        raise ValueError(f"residual {tuple(residual.shape)} {residual.dtype}, expected {tuple(shape)} {dtype}")
+    return _rows_of(residual if residual.dim() == 2 else _flat(residual, shape[-1], "residual"))
+
+
+class Float8EpilogueLinear(_EpilogueLinear):
+    """residual + dropout(activation(x W^T + b)) through FP8 products with dynamic
+    per-tensor scaling, as Float8Linear's; everything behind the product happens in
+    its epilogue, in fp32.  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".
+    Kept for the backward pass: the FP8 codes, with an activation also x W^T + b in
+    the layer's dtype, with dropout its two words.  bf16 or fp16; the sizes and the
+    number of rows are multiples of 16.  Gradients of an fp16 layer carry the loss
+    scale (a GradScaler's unscale_ takes them)."""
+    _dtypes = (torch.bfloat16, torch.float16)
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
+                 dropout: float = 0.0, device=None, dtype=torch.bfloat16):
+        super().__init__(in_features, out_features, bias, activation, dropout, device, dtype)
+
+    @classmethod
+    def from_float(cls, lin: nn.Linear, activation: str = "none", dropout: float = 0.0) -> "Float8EpilogueLinear":
+        """One sharing lin's weight and bias (no copies)."""
+        cls._check_float(lin)
+        with torch.device("meta"):
+            new = cls(lin.in_features, lin.out_features, False, activation, dropout, dtype=lin.weight.dtype)
+        return cls._share(new, lin)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        x2d, res = self._inputs(x, residual)
+        p, rng = self._drop(x)
+        y = torch.ops.fp8sg.scaled_linear_epilogue_fwd(x2d, self.weight.contiguous(), self.bias, res, rng,
+                                                       ACTIVATIONS[self.activation], p, self._saves(x))[0]
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+
+class MXFP4EpilogueLinear(_EpilogueLinear):
+    """The same layer with MXFP4 operands, as MXFP4Linear's (bf16, fp16 or fp32; any
+    sizes; `rule`: see there).  Kept for the backward pass: the 4-bit x^T and W^T, with
+    an activation also x W^T + b, with dropout its two words."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
+                 dropout: float = 0.0, rule: str = "floor", device=None, dtype=torch.bfloat16):
+        super().__init__(in_features, out_features, bias, activation, dropout, device, dtype)
+        self.rule = _mx_rule(rule)
+
+    @classmethod
+    def from_float(cls, lin: nn.Module, activation: str = "none", dropout: float = 0.0,
+                   rule: str = "floor") -> "MXFP4EpilogueLinear":
+        """One sharing lin's weight and bias (no copies)."""
+        cls._check_float(lin)
+        with torch.device("meta"):
+            new = cls(lin.in_features, lin.out_features, False, activation, dropout, rule, dtype=lin.weight.dtype)
+        return cls._share(new, lin)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        x2d, res = self._inputs(x, residual)
+        p, rng = self._drop(x)
+        y = torch.ops.fp8sg.mxfp4_linear_epilogue_fwd(x2d, self.weight.contiguous(), self.bias, res, rng,
+                                                      ACTIVATIONS[self.activation], p, MX_RULES[self.rule],
+                                                      self._saves(x))[0]
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self):
+        return super().extra_repr() + f", rule={self.rule}"
+
+
+class PackedMXFP4EpilogueLinear(nn.Module):
+    """The layer for serving: residual + activation(x W^T + b) with the weight held as
+    MXFP4, as PackedMXFP4Linear's.  No dropout, no gradients."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
+                 rule: str = "floor", device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if dtype not in _MX_DTYPES:
+            raise TypeError(f"PackedMXFP4EpilogueLinear takes a bias of bf16, fp16 or fp32, not {dtype}")
+        self.in_features, self.out_features = in_features, out_features
+        self.activation, self.rule = _activation(activation), _mx_rule(rule)
+        nq, ns = _mx_bytes(out_features, in_features)
+        self.register_buffer("weight_q", torch.zeros(nq, dtype=torch.uint8, device=device))
+        self.register_buffer("weight_s", torch.zeros(ns, dtype=torch.uint8, device=device))
+        self.register_buffer("bias", torch.zeros(out_features, dtype=dtype, device=device) if bias else None)
+
+    @classmethod
+    def from_float(cls, lin: nn.Module, activation: Optional[str] = None,
+                   rule: Optional[str] = None) -> "PackedMXFP4EpilogueLinear":
+        """The packed form of a linear with or without bias.  activation and rule None:
+        those the layer was trained with, "none" and "floor" for an nn.Linear."""
+        w, b = lin.weight.detach(), getattr(lin, "bias", None)
+        if w.dtype not in _MX_DTYPES:
+            raise TypeError(f"PackedMXFP4EpilogueLinear needs a bf16, fp16 or fp32 weight, got {w.dtype}")
+        new = cls(w.shape[1], w.shape[0], b is not None,
+                  activation if activation is not None else getattr(lin, "activation", "none"),
+                  rule if rule is not None else getattr(lin, "rule", "floor"), device=w.device,
+                  dtype=b.dtype if b is not None else w.dtype)
+        mxfp4_quantize(w.contiguous(), new._packed(), rule=MX_RULES[new.rule])
+        if b is not None:
+            new.bias.copy_(b.detach())
+        return new
+
+    def _packed(self):
+        return Mxfp4(self.out_features, self.in_features, tensors=(self.weight_q, self.weight_s))
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        x2d = _flat(x, self.in_features, "PackedMXFP4EpilogueLinear").contiguous()
+        shape = x.shape[:-1] + (self.out_features,)
+        y = x2d.new_empty((x2d.shape[0], self.out_features))
+        mxfp4_linear_apply_epilogue(x2d, self._packed(), y, Mxfp4(x2d.shape[0], self.in_features, x.device),
+                                    bias=self.bias, act=ACTIVATIONS[self.activation],
+                                    residual=_residual(residual, x.dtype, shape), rule=MX_RULES[self.rule])
+        return y.reshape(shape)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, " \
+               f"activation={self.activation}, rule={self.rule}"
+
+
+# ------------------------------------------------------------------------- dropout
+
+@torch.library.custom_op("fp8sg::dropout_fwd", mutates_args=())
+def _op_drop(x: _T, residual: Optional[_T], rng: _T, p: float) -> _T:
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dropout_fwd(x, p, rng, y, residual=residual)
+    return y
+
+
+@_op_drop.register_fake
+def _op_drop_fake(x, residual, rng, p):
+    return x.new_empty(x.shape)
+
+
+@torch.library.custom_op("fp8sg::dropout_bwd", mutates_args=())
+def _op_drop_bwd(gy: _T, rng: _T, p: float) -> _T:
+    gx = torch.empty(gy.shape, dtype=gy.dtype, device=gy.device)
+    dropout_bwd(gy, p, rng, gx)
+    return gx
+
+
+@_op_drop_bwd.register_fake
+def _op_drop_bwd_fake(gy, rng, p):
+    return gy.new_empty(gy.shape)
+
+
+def _drop_setup(ctx, inputs, output):
+    ctx.p = inputs[3]
+    ctx.save_for_backward(inputs[2])
+    ctx.set_materialize_grads(False)
+
+
+def _drop_backward(ctx, gy):
+    need = ctx.needs_input_grad
+    if gy is None:
+        return None, None, None, None
+    gx = torch.ops.fp8sg.dropout_bwd(_rows_of(gy), ctx.saved_tensors[0], ctx.p) if need[0] else None
+    return gx, gy if need[1] else None, None, None
+
+
+_op_drop.register_autograd(_drop_backward, setup_context=_drop_setup)
+
+
+class Dropout(nn.Module):
+    """residual + dropout(x) in one pass, forward and backward, with no stored mask.
+    p in steps of 2^-16.  In evaluation x (+ residual)."""
+
+    def __init__(self, p: float = 0.5):
+        super().__init__()
+        self.p = _probability(p)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if x.dtype not in _MX_DTYPES:
+            raise TypeError(f"Dropout takes bf16, fp16 or fp32, not {x.dtype}")
+        if x.dim() < 1:
+            raise ValueError("Dropout takes at least one dimension")
+        res = _residual(residual, x.dtype, x.shape)
+        if not self.training or self.p == 0:
+            return x if residual is None else x + residual
+        x2d = _rows_of(x if x.dim() == 2 else _flat(x, x.shape[-1], "Dropout"))
+        return torch.ops.fp8sg.dropout_fwd(x2d, res, dropout_words(x.device), self.p).reshape(x.shape)
+
+    def extra_repr(self):
+        return f"p={self.p}"
