@@ -6,22 +6,28 @@
 namespace fp8sg {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kRows = 4;  // rows a thread has in flight (fp32: half as many)
+constexpr int kBlock = 256;  // threads of a block; of the backward step's:
+constexpr int kBwd = 512;
+constexpr int kRows = 2;  // rows a thread of the backward step has in flight (fp32: one)
 
-// ---- backward.  A block owns a strip of 8 L columns (a thread 8 of them) and a
-// run of rows, which its 256 / L row groups take in turn; each thread adds up its
-// columns in fp32, lanes and waves join at the end, and where several blocks share
-// a strip each leaves a row of partial sums that k_bias_join adds in a fixed order
-// (no atomics: a repeated call gives the same bits).
-// (Four blocks a compute unit: all of a launch's at most 1024 are resident.)
+// ---- backward.  A block owns a strip of 8 L columns (a thread 8 of them); the
+// blocks of a strip, its parts, take its rows in turns of kRows rows for each of their
+// 512 / L row groups, so that all blocks in flight read one short run of rows (each a
+// run of its own: 8192 x 4096, bf16, 54 -> 46 us).  Each thread adds up its columns
+// in fp32, lanes and waves join at the end, and with several parts each leaves a row
+// of partial sums that k_bias_join adds in a fixed order (no atomics: a repeated call
+// gives the same bits).  Two blocks a compute unit: all of a launch's at most 1024
+// (a record's slots) are resident.  us for 8192 x 14336 bf16 with gelu and gb, 705 MB,
+// past the caches: 132 (5.3 TB/s; a copy 5.2), of which gelu 7, gb 2; 4 rows and 256
+// threads a block 136; cached accesses 146.  fp32 takes cached ones at any size: its
+// lanes' 16-byte halves of 32 bytes meet in the caches (4096 x 14336 142, non-temporal 153).
 template <int T, bool S>
-__global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
+__global__ __launch_bounds__(kBwd, 2) void k_epilogue_bwd(EpilogueBwdArgs p) {
   constexpr bool kFast = T != FP8SG_OUT_F32;
   constexpr int kU = kFast ? kRows : kRows / 2;
-  __shared__ float red[kBlock / kWave][512];
+  __shared__ float red[kBwd / kWave][8 * kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int L = p.lanes, R = kBlock / L, cl = tid & (L - 1), rl = tid / L;
+  const int L = p.lanes, R = kBwd / L, cl = tid & (L - 1), rl = tid / L;
   const Drop d = drop_of(p.drop);
   const uint64_t groups = (uint64_t)((p.N + 7) >> 3);
   uint32_t amax = 0;  // packed 16-bit magnitudes
@@ -29,17 +35,16 @@ __global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
     const int64_t part = task / p.strips, strip = task - part * p.strips;
     const int64_t c = (strip * L + cl) * 8;
     const int n = c < p.N ? left8(p.N, c) : 0;
-    const int64_t end = (part + 1) * p.rows_per < p.M ? (part + 1) * p.rows_per : p.M;
     float sum[8] = {};
     if (n > 0) {
-      for (int64_t r0 = part * p.rows_per + rl; r0 < end; r0 += kU * R) {
+      for (int64_t r0 = part * kU * R + rl; r0 < p.M; r0 += (int64_t)p.parts * kU * R) {
         Row8<T> g[kU], h[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int64_t r = r0 + u * R;
           g[u].zero();
           h[u].zero();
-          if (r < end) {
+          if (r < p.M) {
             g[u] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.gy) + r * p.N + c, n);
             if (p.act != FP8SG_ACT_NONE) h[u] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.pre) + r * p.N + c, n);
           }
@@ -47,7 +52,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int64_t r = r0 + u * R;
-          if (r >= end) break;
+          if (r >= p.M) break;
           float v[8], x[8];
           g[u].values(v);
           by_act(p.act, [&](auto a) {
@@ -90,10 +95,11 @@ __global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) red[wave][8 * lane + i] = sum[i];
       __syncthreads();
-      for (int i = tid; i < 8 * L; i += kBlock) {
+      for (int i = tid; i < 8 * L; i += kBwd) {
         const int64_t col = strip * L * 8 + i;
         if (col >= p.N) continue;
-        const float v = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+        const float v = ((red[0][i] + red[1][i]) + (red[2][i] + red[3][i])) +
+                        ((red[4][i] + red[5][i]) + (red[6][i] + red[7][i]));
         if (p.parts > 1) {
           p.part[part * p.N + col] = v;
         } else {
@@ -104,54 +110,55 @@ __global__ __launch_bounds__(kBlock, 4) void k_epilogue_bwd(EpilogueBwdArgs p) {
     }
   }
   if (p.rec) {  // this block's slot of the record, as the amax kernel leaves it
-    const uint32_t bits = block_max_u32<kBlock>(absmax_bits<T == FP8SG_OUT_F16>(amax));
+    const uint32_t bits = block_max_u32<kBwd>(absmax_bits<T == FP8SG_OUT_F16>(amax));
     if (tid == 0) {
       p.rec->_part[blockIdx.x] = bits;
       if (blockIdx.x == 0) p.rec->_nparts = gridDim.x;
     }
     if (blockIdx.x == 0)
-      for (int i = gridDim.x + tid; i < FP8SG_AMAX_PARTS; i += kBlock) p.rec->_part[i] = 0;
+      for (int i = gridDim.x + tid; i < FP8SG_AMAX_PARTS; i += kBwd) p.rec->_part[i] = 0;
   }
 }
 
-// gb[n] = the sum of `parts` partial rows: 64 columns a block, a quarter of the
-// rows a wave.
+// gb[n] = the sum of `parts` partial rows: 16 columns a block, a sixteenth of the
+// rows for each of 16 threads a column (with 64 columns a block too few blocks share
+// the loads' latency: 4096 x 4096 with gb 24.8 -> 24.4 us).
+constexpr int kJoin = 16;
 __global__ __launch_bounds__(kBlock) void k_bias_join(const float* part, int parts, int64_t N, void* gb, int type) {
-  __shared__ float red[kBlock / kWave][kWave];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t n = (int64_t)blockIdx.x * kWave + lane;
+  __shared__ float red[kBlock / kJoin][kJoin];
+  const int c = threadIdx.x % kJoin, g = threadIdx.x / kJoin;
+  const int64_t n = (int64_t)blockIdx.x * kJoin + c;
   float s = 0.f;
   if (n < N)
 #pragma unroll 8
-    for (int r = wave; r < parts; r += kBlock / kWave) s += part[r * N + n];
-  red[wave][lane] = s;
+    for (int r = g; r < parts; r += kBlock / kJoin) s += part[r * N + n];
+  red[g][c] = s;
   __syncthreads();
-  if (wave == 0 && n < N) {
-    const float one[1] = {(red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])};
+  if (g == 0 && n < N) {
+    float one[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < kBlock / kJoin; ++i) one[0] += red[i][c];
     store_n<1, false>(reinterpret_cast<uint8_t*>(gb) + n * esize(type), 1, type, one);
   }
 }
 
-// Strips, parts and rows of a part of an M x N gradient.
+// Strips and parts of an M x N gradient.
 struct Split {
   int lanes;
-  int64_t strips, parts, rows_per;
+  int64_t strips, parts;
 };
 Split split_of(int64_t M, int64_t N) {
-  Split s{1, 0, 1, 0};
-  // few rows: strips of 64 columns (128 bytes of 16-bit values), whose 32 row groups
-  // take all rows, so nothing is left to join
+  Split s{1, 0, 1};
+  // few rows: strips of 64 columns (128 bytes of 16-bit values), whose 64 row groups
+  // take all rows, so nothing is left to join (64 x 256 with gb 7.5 -> 5.0 us)
   const bool few = M <= 256;
   while (s.lanes < (few ? 8 : kWave) && 8 * s.lanes < N) s.lanes *= 2;
   s.strips = (N + 8 * s.lanes - 1) / (8 * s.lanes);
-  const int64_t R = kBlock / s.lanes, most = (M + R * kRows - 1) / (R * kRows);
+  const int64_t turn = (int64_t)(kBwd / s.lanes) * kRows, turns = (M + turn - 1) / turn;
   // at most as many blocks as a record has slots
-  int64_t parts = s.strips && !few ? FP8SG_AMAX_PARTS / s.strips : 1;
-  if (parts > most) parts = most;
-  if (parts < 1) parts = 1;
-  s.rows_per = ((M + parts - 1) / parts + R - 1) / R * R;
-  if (s.rows_per < R) s.rows_per = R;
-  s.parts = M > 0 ? (M + s.rows_per - 1) / s.rows_per : 1;
+  if (s.strips && !few) s.parts = FP8SG_AMAX_PARTS / s.strips;
+  if (s.parts > turns) s.parts = turns;
+  if (s.parts < 1) s.parts = 1;
   return s;
 }
 
@@ -196,18 +203,22 @@ hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream) {
   a.lanes = s.lanes;
   a.parts = (int32_t)s.parts;
   a.strips = s.strips;
-  a.rows_per = s.rows_per;
-  const int64_t tasks = s.strips * s.parts, e = a.type == FP8SG_OUT_F32 ? 4 : 2;
+  const int64_t tasks = s.strips * s.parts;
   const dim3 grid((unsigned)(tasks < FP8SG_AMAX_PARTS ? tasks : FP8SG_AMAX_PARTS));
-  const bool st = a.M * a.N * e * 3 >= kStreamBytes;
+  const bool st = a.M * a.N * 6 >= kStreamBytes;
   hipError_t err = by_type(a.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    if (st) hipLaunchKernelGGL((k_epilogue_bwd<T, true>), grid, dim3(kBlock), 0, stream, a);
-    else hipLaunchKernelGGL((k_epilogue_bwd<T, false>), grid, dim3(kBlock), 0, stream, a);
+    if constexpr (T != FP8SG_OUT_F32) {
+      if (st) {
+        hipLaunchKernelGGL((k_epilogue_bwd<T, true>), grid, dim3(kBwd), 0, stream, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((k_epilogue_bwd<T, false>), grid, dim3(kBwd), 0, stream, a);
     return hipGetLastError();
   });
   if (err != hipSuccess || !a.gb || s.parts == 1) return err;
-  hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((a.N + kWave - 1) / kWave)), dim3(kBlock), 0, stream, a.part,
+  hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((a.N + kJoin - 1) / kJoin)), dim3(kBlock), 0, stream, a.part,
                      a.parts, a.N, a.gb, a.bias_type);
   return hipGetLastError();
 }

@@ -71,8 +71,8 @@ struct EpilogueBwdArgs {
   DropArgs drop;
   int32_t act, type, bias_type;
   // filled by the launcher
-  int32_t lanes, parts, stream;
-  int64_t strips, rows_per;
+  int32_t lanes, parts;
+  int64_t strips;
 };
 int64_t epilogue_ws_len(int64_t M, int64_t N);
 hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream);
