@@ -114,13 +114,14 @@ def _drop(p, rng):
 
 
 def _act(act):
-    if act not in (0, 1, 2, 3, 4):
+    if act.__class__ is not int or not 0 <= act <= 4:
         raise ValueError(f"act must be one of ACT_NONE .. ACT_GELU_TANH, not {act!r}")
     return act
 
 
-def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng):
-    """The packed struct of a forward epilogue.  in_dtype: the linear's input's, or None."""
+def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng, *others):
+    """The packed struct of a forward epilogue.  in_dtype: the linear's input's, or
+    None.  others: the call's other tensors, for their device."""
     dt = y.dtype
     ldy = N if y.shape == shape and y.is_contiguous() else _row_stride(y, "y", dt, shape, M, N)
     at = y.data_ptr()
@@ -128,14 +129,13 @@ def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng):
     pb = pr = pp = bt = ldr = 0
     near = False  # whether an output comes near another tensor: looked at more closely then
     if bias is not None:
-        bd = bias.dtype if isinstance(bias, torch.Tensor) else None
-        if bd is not dt:
-            bt = _type(bias, "bias")
-        else:
-            bt = _TYPE[dt]
-        if in_dtype is not None and bd is not in_dtype and bt != 2:
-            raise TypeError(f"bias: dtype {bd}, expected {in_dtype} or float32")
-        _same(bias, "bias", bd, (N,))
+        bt = _TYPE.get(bias.dtype) if isinstance(bias, torch.Tensor) else None
+        if bt is None:
+            _type(bias, "bias")  # (says what it is)
+        if in_dtype is not None and bt != 2 and bias.dtype is not in_dtype:
+            raise TypeError(f"bias: dtype {bias.dtype}, expected {in_dtype} or float32")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            _need(bias, "bias", None, shape=(N,))
         pb = bias.data_ptr()
         near = at < pb + 4 * N and pb < end
     if residual is not None:
@@ -156,8 +156,8 @@ def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng):
         _all_clear([(y, "y"), (pre, "pre")], [(bias, "bias"), (residual if residual is not y else None, "residual")])
         if residual is y:
             _clear(pre, "pre", y, "residual")
-    e = _pack(pb, pr, pp, _drop(p, rng), ldr, ldy, p, _act(act), bt)
-    _here(y, bias, residual, pre, rng)
+    e = _pack(pb, pr, pp, _drop(p, rng) if rng is not None or p else 0, ldr, ldy, p, _act(act), bt)
+    _here(y, bias, residual, pre, rng, *others)
     return e
 
 
@@ -235,8 +235,7 @@ def _fp8_gemm(fn, A, B, ia, ib, C, bias, act, residual, pre, p, rng, stream):
     _need(A, "A", torch.uint8)
     _need(B, "B", torch.uint8, shape=(N, K))
     ct = _type(C, "C")
-    e = _epilogue(C, (M, N), M, N, None, bias, act, residual, pre, p, rng)
-    _here(A, B)
+    e = _epilogue(C, (M, N), M, N, None, bias, act, residual, pre, p, rng, A, B)
     _check(getattr(lib(), fn)(_ptr(A), _ptr(B), ia, ib, e, _ptr(C), ct, M, N, K, _stream(stream)), fn)
 
 
@@ -278,8 +277,8 @@ def fp8_scaled_linear_fwd_epilogue(x: torch.Tensor, w: torch.Tensor, saved: Line
     _need(w, "w", x.dtype, shape=(N, K))
     yt = _type(y, "y")
     sv = _saved(saved, M, N, K)
-    e = _epilogue(y, (M, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
-    _here(x, w, saved.x_q, saved.w_q, saved.x_sc.buf, saved.w_sc.buf)
+    e = _epilogue(y, (M, N), M, N, x.dtype, bias, act, residual, pre, p, rng, x, w, saved.x_q, saved.w_q,
+                  saved.x_sc.buf, saved.w_sc.buf)
     _check(lib().fp8_scaled_linear_fwd_epilogue(x.data_ptr(), w.data_ptr(), _TYPE[x.dtype], M, N, K, sv,
                                                 e, _ptr(y), yt, _stream(stream)),
            "fp8_scaled_linear_fwd_epilogue")
@@ -344,8 +343,7 @@ def mxfp4_gemm_epilogue(A: Mxfp4, B: Mxfp4, C: torch.Tensor, *, bias=None, act: 
     ct = _type(C, "C")
     if C.dim() < 1 or C.shape[-1] != N or _rows(C) != M:
         raise ValueError(f"C: shape {tuple(C.shape)}, expected {M} x {N}")
-    e = _epilogue(C, C.shape, M, N, None, bias, act, residual, pre, p, rng)
-    _here(A.q, A.s, B.q, B.s)
+    e = _epilogue(C, C.shape, M, N, None, bias, act, residual, pre, p, rng, A.q, A.s, B.q, B.s)
     _check(lib().mxfp4_gemm_epilogue(A.c(), B.c(), e, _ptr(C), ct, M, N, A.k, _stream(stream)),
            "mxfp4_gemm_epilogue")
 
@@ -361,8 +359,7 @@ def mxfp4_linear_fwd_epilogue(x: torch.Tensor, w: torch.Tensor, ws: Mxfp4LinearW
     if K2 != K:
         raise ValueError(f"w: {K2} columns, expected {K}")
     yt = _type(y, "y")
-    e = _epilogue(y, _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
-    _here(x, w)
+    e = _epilogue(y, _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng, x, w)
     _linear(ws, Mxfp4LinearWs, "ws", (M, N, K), ("x_q", "w_q"))
     sv = None
     if saved is not None:
@@ -383,8 +380,8 @@ def mxfp4_linear_apply_epilogue(x: torch.Tensor, w: Mxfp4, y: torch.Tensor, ws: 
     _need_codes(w, "w", Mxfp4, N, K)
     _need_codes(ws, "ws", Mxfp4, M, K)
     yt = _type(y, "y")
-    e = _epilogue(y, (M, N) if x.dim() == 2 else _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng)
-    _here(x, w.q, w.s, ws.q, ws.s)
+    e = _epilogue(y, (M, N) if x.dim() == 2 else _lead(x.shape, N), M, N, x.dtype, bias, act, residual, pre, p, rng,
+                  x, w.q, w.s, ws.q, ws.s)
     _check(lib().mxfp4_linear_apply_epilogue(_ptr(x), _TYPE[x.dtype], w.c(), M, N, K, _rule(rule), ws.c(),
                                              e, _ptr(y), yt, _stream(stream)),
            "mxfp4_linear_apply_epilogue")
