@@ -303,7 +303,7 @@ hipError_t launch_linear_bwd(const uint16_t* gy, const fp8_linear_saved& sv, int
   // [M, N] as A^T and x codes [M, K] as B^T.
   const bool tb_d = !sv.w_qT, ta_w = !w.gy_qT, tb_w = !sv.x_qT;
   const int o = amp_scale ? kOutF16Unscale : out;
-  if (!hist_gy && !f16 && tb_d && ta_w && tb_w && small_layer_fits(M, N, K)) {
+  if (!hist_gy && tb_d && ta_w && tb_w && small_layer_fits(M, N, K)) {
     // small layer without transposed copies: the cast of gy and both GEMMs
     // in one launch
     SmallBwdArgs a{gy, M, N,
@@ -312,7 +312,7 @@ hipError_t launch_linear_bwd(const uint16_t* gy, const fp8_linear_saved& sv, int
                    GemmProblem{w.gy_q, sv.x_q, gw, nullptr, &sv.x_sc->inv, N, K, M,
                                amp_scale, found_inf},
                    w.gy_sc, w.gy_q};
-    return launch_small_bwd(a, o, s);
+    return launch_small_bwd(a, o, f16, s);
   }
   QuantArgs qa{};
   qa.job[0] = QuantJob{gy, M, N, w.gy_sc, w.gy_q, w.gy_qT, 0, 0, 0, hist_gy, hist_len};

@@ -161,9 +161,9 @@ fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void* w, fp8sg_
   if (epi->bias && epi->bias_type != type && epi->bias_type != FP8SG_OUT_F32) return FP8SG_ERR_FORMAT;
   const uint16_t *x16 = static_cast<const uint16_t*>(x), *w16 = static_cast<const uint16_t*>(w);
   const bool f16 = type == FP8SG_OUT_F16;
-  if (!f16 && !saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K)) {
+  if (!saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K)) {
     const SmallFwdEpiArgs a{x16, w16, p, saved->x_sc, saved->w_sc, saved->x_q, saved->w_q};
-    return hip_status(launch_small_fwd_epilogue(a, S(stream)));
+    return hip_status(launch_small_fwd_epilogue(a, f16, S(stream)));
   }
   const hipError_t e = launch_linear_casts(x16, w16, M, N, K, *saved, nullptr, nullptr, 0, f16, S(stream));
   return e != hipSuccess ? FP8SG_ERR_HIP : hip_status(launch_gemm_epilogue(p, false, S(stream)));
@@ -197,7 +197,9 @@ fp8sg_status fp8_scaled_linear_bwd_epilogue(const void* gy, fp8sg_out type, cons
   if (changes(a) && !gh) return FP8SG_ERR_NULL;
   const bool step = changes(a) || gb;  // otherwise there is nothing to do before the cast
   if (step) {
-    a.rec = ws->gy_sc;
+    // (a small layer's launch takes the maximum itself)
+    const bool small = !saved->x_qT && !saved->w_qT && !ws->gy_qT && small_layer_fits(M, N, K);
+    a.rec = small ? nullptr : ws->gy_sc;
     if (!changes(a)) a.gh = nullptr;
     if (launch_epilogue_bwd(a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
   }

@@ -169,7 +169,7 @@ __device__ __forceinline__ Alpha<RW, TM, TN> epilogue_alpha(const GemmProblem& p
   else return Alpha<RW, TM, TN>(inv_a, inv_b);
 }
 
-// A bf16 operand cast to FP8 on its way into LDS (the small layers' one-launch
+// A bf16 or fp16 operand cast to FP8 on its way into LDS (the small layers' one-launch
 // passes, small_layer.hip): each 16-element chunk is quantized by quant8 at
 // the tensor's scale32, the codes the cast kernels write; a block given `q`
 // also stores its chunks' codes there, at the elements' own positions (the
@@ -191,9 +191,9 @@ struct CastSrc {
 // its k-tile is staged as 128 rows of 128 bytes (one per k, the tile's 128
 // output rows or columns) and its fragments are read with ds_read_b64_tr_b8,
 // as in the large-tile kernel below.
-// CA / CB: the operand is a bf16 tensor cast on the fly (CastSrc ca / cb).
+// CA / CB: the operand is a bf16 (F16: fp16) tensor cast on the fly (CastSrc ca / cb).
 template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, bool RW, bool TA = false,
-          bool TB = false, bool CA = false, bool CB = false, class Prob = GemmProblem>
+          bool TB = false, bool CA = false, bool CB = false, bool F16 = false, class Prob = GemmProblem>
 __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
                                                 CastSrc ca = CastSrc{}, CastSrc cb = CastSrc{}) {
   static_assert(!(TA || TB) || (BM == 128 && BN == 128), "contraction-major: 128 x 128 tiles");
@@ -280,7 +280,7 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   auto cast_chunk = [&](const CastSrc& cs, auto fmt, const uint4& lo, const uint4& hi, bool ok,
                         int64_t idx) {
     constexpr int F = decltype(fmt)::value;
-    const uint2 a = quant8<F>(lo, cs.s32), b = quant8<F>(hi, cs.s32);
+    const uint2 a = quant8<F, F16>(lo, cs.s32), b = quant8<F, F16>(hi, cs.s32);
     const uint4 q = ok ? make_uint4(a.x, a.y, b.x, b.y) : zero();
     if (ok && cs.q) *reinterpret_cast<uint4*>(cs.q + idx) = q;
     return q;

@@ -116,7 +116,8 @@ struct SmallBwdArgs {
 };
 bool small_layer_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream);
-hipError_t launch_small_bwd(const SmallBwdArgs& a, int out, hipStream_t stream);
+// f16: gy is fp16 (out is then not kOutF16Unscale)
+hipError_t launch_small_bwd(const SmallBwdArgs& a, int out, bool f16, hipStream_t stream);
 // A linear layer's passes behind the validated entry points (api.hip).  Casts of x
 // and W (dynamic: amax and quantize; delayed: histories given) of bf16 or fp16
 // tensors; and the cast of gy with the two backward GEMMs.  have_amax: gy's

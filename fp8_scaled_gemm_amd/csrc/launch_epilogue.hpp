@@ -54,7 +54,7 @@ struct SmallFwdEpiArgs {
   uint8_t* x_q;
   uint8_t* w_q;
 };
-hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, hipStream_t stream);
+hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, bool f16, hipStream_t stream);
 hipError_t launch_mx_gemm_epilogue(const MxGemmEpiProblem& p, hipStream_t stream);
 hipError_t launch_mx_apply_epilogue(const MxQuantJob& j, int type, bool fit, const MxGemmEpiProblem& p,
                                     hipStream_t stream);

@@ -29,9 +29,10 @@ constexpr int kSmallThreads = 256;
 using SmallCfg = GemmCfg<128, 128, 2, 2>;
 static_assert(SmallCfg::kThreads == kSmallThreads, "one block shape");
 
-// max |x| over n bf16 values (n a multiple of 8), every thread of the block
+// max |x| over n bf16 or fp16 values (n a multiple of 8), every thread of the block
 // gets it; canonical NaN for any NaN.  The partial maxima meet in the
 // kernel's dynamic LDS, before the GEMM uses it.
+template <bool F16>
 __device__ __forceinline__ uint32_t block_absmax_bits(const uint16_t* x, int64_t n, uint32_t* red) {
   const uint4* xv = reinterpret_cast<const uint4*>(x);
   const int64_t nv = n >> 3;
@@ -47,7 +48,7 @@ __device__ __forceinline__ uint32_t block_absmax_bits(const uint16_t* x, int64_t
 #pragma unroll
     for (int u = 0; u < kU; ++u) m = absmax8(m, t[u]);
   }
-  uint32_t b = wave_max_u32(absmax_bits(m));
+  uint32_t b = wave_max_u32(absmax_bits<F16>(m));
   __syncthreads();  // red may hold an earlier reduction's values
   if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = b;
   __syncthreads();
@@ -71,12 +72,12 @@ __device__ __forceinline__ void write_self_record(fp8sg_scale_rec* rec, uint32_t
 }
 
 // Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT is not used then).
-template <int OUT, class Args>
+template <int OUT, class Args, bool F16 = false>
 __global__ __launch_bounds__(kSmallThreads) void k_small_fwd(Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* red = reinterpret_cast<uint32_t*>(smem);
-  const uint32_t bx_bits = block_absmax_bits(a.x, a.p.M * a.p.K, red);
-  const uint32_t bw_bits = block_absmax_bits(a.w, a.p.N * a.p.K, red);
+  const uint32_t bx_bits = block_absmax_bits<F16>(a.x, a.p.M * a.p.K, red);
+  const uint32_t bw_bits = block_absmax_bits<F16>(a.w, a.p.N * a.p.K, red);
   __syncthreads();  // the GEMM's tiles overwrite red
   const ScaleVals sx = scale_from_amax(__uint_as_float(bx_bits), FP8SG_E4M3FN);
   const ScaleVals sw = scale_from_amax(__uint_as_float(bw_bits), FP8SG_E4M3FN);
@@ -86,17 +87,17 @@ __global__ __launch_bounds__(kSmallThreads) void k_small_fwd(Args a) {
   }
   const CastSrc cx{a.x, sx.s32, sx.inv, blockIdx.x == 0 ? a.x_q : nullptr};
   const CastSrc cw{a.w, sw.s32, sw.inv, blockIdx.y == 0 ? a.w_q : nullptr};
-  gemm_small_tile<128, 128, 2, 2, FP8SG_E4M3FN, FP8SG_E4M3FN, OUT, false, false, false, true, true>(
+  gemm_small_tile<128, 128, 2, 2, FP8SG_E4M3FN, FP8SG_E4M3FN, OUT, false, false, false, true, true, F16>(
       a.p, blockIdx.x, blockIdx.y, cx, cw);
 }
 
-template <int OUT>
+template <int OUT, bool F16 = false>
 __global__ __launch_bounds__(kSmallThreads) void k_small_bwd(SmallBwdArgs a) {
   const int64_t pm = blockIdx.z ? a.wg.M : a.dg.M, pn = blockIdx.z ? a.wg.N : a.dg.N;
   if ((int64_t)blockIdx.y * 128 >= pm || (int64_t)blockIdx.x * 128 >= pn) return;  // whole block
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* red = reinterpret_cast<uint32_t*>(smem);
-  const uint32_t bg_bits = block_absmax_bits(a.gy, a.rows * a.cols, red);
+  const uint32_t bg_bits = block_absmax_bits<F16>(a.gy, a.rows * a.cols, red);
   __syncthreads();  // the GEMM's tiles overwrite red
   const ScaleVals sg = scale_from_amax(__uint_as_float(bg_bits), FP8SG_E5M2);
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
@@ -104,10 +105,10 @@ __global__ __launch_bounds__(kSmallThreads) void k_small_bwd(SmallBwdArgs a) {
   // gy's codes are stored by the dgrad blocks of the first tile column
   const CastSrc cg{a.gy, sg.s32, sg.inv, blockIdx.z == 0 && blockIdx.x == 0 ? a.gy_q : nullptr};
   if (blockIdx.z == 0)  // dgrad: gy rows cast, W codes as B^T
-    gemm_small_tile<128, 128, 2, 2, FP8SG_E5M2, FP8SG_E4M3FN, OUT, false, false, true, true, false>(
+    gemm_small_tile<128, 128, 2, 2, FP8SG_E5M2, FP8SG_E4M3FN, OUT, false, false, true, true, false, F16>(
         a.dg, blockIdx.x, blockIdx.y, cg);
   else  // wgrad: gy as A^T cast, x codes as B^T
-    gemm_small_tile<128, 128, 2, 2, FP8SG_E5M2, FP8SG_E4M3FN, OUT, false, true, true, true, false>(
+    gemm_small_tile<128, 128, 2, 2, FP8SG_E5M2, FP8SG_E4M3FN, OUT, false, true, true, true, false, F16>(
         a.wg, blockIdx.x, blockIdx.y, cg);
 }
 
@@ -126,19 +127,31 @@ hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream) 
   return hipGetLastError();
 }
 
-hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, hipStream_t stream) {
+hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, bool f16, hipStream_t stream) {
   const dim3 grid((unsigned)((a.p.N + 127) / 128), (unsigned)((a.p.M + 127) / 128));
-  hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>), grid, dim3(kSmallThreads), SmallCfg::kLdsBytes,
-                     stream, a);
+  if (f16)
+    hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs, true>), grid, dim3(kSmallThreads),
+                       SmallCfg::kLdsBytes, stream, a);
+  else
+    hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>), grid, dim3(kSmallThreads),
+                       SmallCfg::kLdsBytes, stream, a);
   return hipGetLastError();
 }
 
-hipError_t launch_small_bwd(const SmallBwdArgs& a, int out, hipStream_t stream) {
+hipError_t launch_small_bwd(const SmallBwdArgs& a, int out, bool f16, hipStream_t stream) {
   auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const int64_t gx = cdiv(a.dg.N, 128) > cdiv(a.wg.N, 128) ? cdiv(a.dg.N, 128) : cdiv(a.wg.N, 128);
   const int64_t gy = cdiv(a.dg.M, 128) > cdiv(a.wg.M, 128) ? cdiv(a.dg.M, 128) : cdiv(a.wg.M, 128);
   const dim3 grid((unsigned)gx, (unsigned)gy, 2);
   const size_t lds = SmallCfg::kLdsBytes;
+  if (f16) {
+    switch (out) {
+      case FP8SG_OUT_BF16: hipLaunchKernelGGL((k_small_bwd<FP8SG_OUT_BF16, true>), grid, dim3(kSmallThreads), lds, stream, a); break;
+      case FP8SG_OUT_F16: hipLaunchKernelGGL((k_small_bwd<FP8SG_OUT_F16, true>), grid, dim3(kSmallThreads), lds, stream, a); break;
+      default: hipLaunchKernelGGL((k_small_bwd<FP8SG_OUT_F32, true>), grid, dim3(kSmallThreads), lds, stream, a); break;
+    }
+    return hipGetLastError();
+  }
   switch (out) {
     case FP8SG_OUT_BF16: hipLaunchKernelGGL(k_small_bwd<FP8SG_OUT_BF16>, grid, dim3(kSmallThreads), lds, stream, a); break;
     case FP8SG_OUT_F16: hipLaunchKernelGGL(k_small_bwd<FP8SG_OUT_F16>, grid, dim3(kSmallThreads), lds, stream, a); break;
