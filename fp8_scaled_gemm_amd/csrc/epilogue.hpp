@@ -409,7 +409,7 @@ __device__ __forceinline__ void ask_early(const EpilogueArgs& e) {
 // for the tile's 128 a lane.  The next row group's residual is loaded ahead.
 // bias: of the lane's columns (load_bias<8> of n0 + 8 (lane % 8)); alpha: the
 // product's factor; scale(c, i, j): other factors on block (i, j).
-constexpr int kWaveEpilogueLds = 64 * 64 * 4;
+constexpr int kWaveEpilogueLds = 64 * 64 * 4;  // (with fewer than 64 rows, 256 bytes a row)
 template <int TM, class Mode, int kU, class Scale>
 __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[TM][4], uint8_t* lds, int64_t m0,
                                               int64_t n0, const float (&bias)[8], float alpha, Scale scale) {
@@ -447,7 +447,7 @@ __device__ __forceinline__ void wave_epilogue(const EpilogueArgs& e, v4f (&acc)[
     __builtin_amdgcn_wave_barrier();
     // (the last half of a 7-block tile has 48 rows; what LDS holds behind them is not stored)
 #pragma unroll 1
-    for (int r0 = 0; r0 < 64; r0 += 8 * kU) {
+    for (int r0 = 0; r0 < (TM < 4 ? 16 * TM : 64); r0 += 8 * kU) {
       float v[kU][8];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {

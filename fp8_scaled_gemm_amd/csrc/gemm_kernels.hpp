@@ -397,8 +397,9 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   };
   const Alpha<RW, Cfg::kTM, Cfg::kTN> alpha = make_alpha();
   if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {  // (the loop ended with a barrier: the tiles are free)
-    static_assert(BN / WN == 64 && (BM / WM) % 64 == 0 && Cfg::kLdsBytes >= WM * WN * kWaveEpilogueLds, "wave sub-tile");
-    wave_epilogue<Cfg::kTM, EpiMode<true, false, false>, 2>(p.epi, acc, smem + wave * kWaveEpilogueLds, bm + wm * (BM / WM), bn + wn * 64,
+    constexpr int kLds = Cfg::kTM < 4 ? Cfg::kTM * 4096 : kWaveEpilogueLds;
+    static_assert(BN / WN == 64 && Cfg::kLdsBytes >= WM * WN * kLds, "wave sub-tile");
+    wave_epilogue<Cfg::kTM, EpiMode<true, false, false>, 2>(p.epi, acc, smem + wave * kLds, bm + wm * (BM / WM), bn + wn * 64,
                                      bias, RW ? 1.0f : alpha.a, [&](v4f& c, int i, int j) {
                                        if constexpr (RW) alpha.apply(c, i, j);
                                      });

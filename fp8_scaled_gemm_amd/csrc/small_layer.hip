@@ -71,7 +71,11 @@ __device__ __forceinline__ void write_self_record(fp8sg_scale_rec* rec, uint32_t
   rec->inv32 = v.inv32;
 }
 
-// Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT is not used then).
+// Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT is not used
+// then), whose tiles are smaller: a wave's epilogue is a chain of instructions for each
+// of its rows, so four times the waves take a quarter of it each.
+template <class Args>
+using SmallTile = std::conditional_t<std::is_same_v<Args, SmallFwdEpiArgs>, GemmCfg<64, 64, 4, 1>, SmallCfg>;
 template <int OUT, class Args, bool F16 = false>
 __global__ __launch_bounds__(kSmallThreads) void k_small_fwd(Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -87,8 +91,12 @@ __global__ __launch_bounds__(kSmallThreads) void k_small_fwd(Args a) {
   }
   const CastSrc cx{a.x, sx.s32, sx.inv, blockIdx.x == 0 ? a.x_q : nullptr};
   const CastSrc cw{a.w, sw.s32, sw.inv, blockIdx.y == 0 ? a.w_q : nullptr};
-  gemm_small_tile<128, 128, 2, 2, FP8SG_E4M3FN, FP8SG_E4M3FN, OUT, false, false, false, true, true, F16>(
-      a.p, blockIdx.x, blockIdx.y, cx, cw);
+  if constexpr (std::is_same_v<Args, SmallFwdEpiArgs>)
+    gemm_small_tile<64, 64, 4, 1, FP8SG_E4M3FN, FP8SG_E4M3FN, OUT, false, false, false, true, true, F16>(
+        a.p, blockIdx.x, blockIdx.y, cx, cw);
+  else
+    gemm_small_tile<128, 128, 2, 2, FP8SG_E4M3FN, FP8SG_E4M3FN, OUT, false, false, false, true, true, F16>(
+        a.p, blockIdx.x, blockIdx.y, cx, cw);
 }
 
 template <int OUT, bool F16 = false>
@@ -128,13 +136,13 @@ hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream) 
 }
 
 hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, bool f16, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.p.N + 127) / 128), (unsigned)((a.p.M + 127) / 128));
+  const dim3 grid((unsigned)((a.p.N + 63) / 64), (unsigned)((a.p.M + 63) / 64));
   if (f16)
     hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs, true>), grid, dim3(kSmallThreads),
-                       SmallCfg::kLdsBytes, stream, a);
+                       SmallTile<SmallFwdEpiArgs>::kLdsBytes, stream, a);
   else
     hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>), grid, dim3(kSmallThreads),
-                       SmallCfg::kLdsBytes, stream, a);
+                       SmallTile<SmallFwdEpiArgs>::kLdsBytes, stream, a);
   return hipGetLastError();
 }
 
