@@ -20,6 +20,26 @@ hipError_t launch_big(const GemmEpiProblem& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int BM, int BN, int WM, int WN, bool RW>
+hipError_t launch_small(const GemmEpiProblem& p, hipStream_t stream) {
+  using Cfg = GemmCfg<BM, BN, WM, WN>;
+  static_assert(Cfg::kLdsBytes <= 64 * 1024, "no raised LDS limit");
+  hipLaunchKernelGGL((k_gemm<BM, BN, WM, WN, 0, 0, FP8SG_OUT_BF16, RW, false, false, GemmEpiProblem>),
+                     dim3((unsigned)((p.N + BN - 1) / BN), (unsigned)((p.M + BM - 1) / BM)), dim3(Cfg::kThreads),
+                     Cfg::kLdsBytes, stream, p);
+  return hipGetLastError();
+}
+
+// Tiles of 64 x 64 in place of 128 x 128 while those would not go round all compute
+// units: a wave's epilogue is a chain of instructions for each of its rows, which four
+// times the waves share, and so do they the k-tiles' latency.  us, tiles of 128 / 64,
+// with bias, then with gelu and h kept: 64 x 4096 x 4096 (32 tiles of 128) 32.5 / 17.4,
+// 35.2 / 18.2; 1024^3 (64) 12.6 / 7.2, 15.8 / 8.0; 2048^3 (256) 21.1 / 21.5, 25.1 / 22.7;
+// 2048 x 3584 x 1024 (448) 17.8 / 19.6, 22.3 / 22.4.
+bool small_tiles(const GemmEpiProblem& p) {
+  return ((p.M + 127) / 128) * ((p.N + 127) / 128) <= device_cus();
+}
+
 template <bool RW>
 hipError_t launch_any(const GemmEpiProblem& p, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
@@ -27,12 +47,7 @@ hipError_t launch_any(const GemmEpiProblem& p, hipStream_t stream) {
   if (big_tiles_wanted(p.M, p.N) && big_tiles_fit<false, false>(p))
     return big_tiling(p.M, p.N, device_cus(), false) == kTile224 ? launch_big<RW, 224>(p, stream)
                                                                  : launch_big<RW, 256>(p, stream);
-  using Cfg = GemmCfg<128, 128, 2, 2>;
-  static_assert(Cfg::kLdsBytes <= 64 * 1024, "no raised LDS limit");
-  hipLaunchKernelGGL((k_gemm<128, 128, 2, 2, 0, 0, FP8SG_OUT_BF16, RW, false, false, GemmEpiProblem>),
-                     dim3((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 127) / 128)), dim3(Cfg::kThreads),
-                     Cfg::kLdsBytes, stream, p);
-  return hipGetLastError();
+  return small_tiles(p) ? launch_small<64, 64, 4, 1, RW>(p, stream) : launch_small<128, 128, 2, 2, RW>(p, stream);
 }
 
 }  // namespace
