@@ -421,24 +421,26 @@ def mxfp4_linear_bwd_epilogue(gy: torch.Tensor, ws: Mxfp4LinearWs, saved: Mxfp4L
 
 def _dropout(x, name_x, p, rng, y, name_y, residual):
     """(x, ldx, residual, ldr, type, rows, cols, p, rng, y, ldy), checked."""
-    xt = _type(x, name_x)
+    xt = _TYPE.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if xt is None:
+        _type(x, name_x)  # (says what it is)
     dt, shape = x.dtype, x.shape
     if not shape:
         raise ValueError(f"{name_x}: expected at least one dimension")
     cols = shape[-1]
     rows = shape[0] if len(shape) == 2 else _rows(x)
-    ldx = _row_stride(x, name_x, dt, shape, rows, cols)
+    ldx = cols if x.is_contiguous() else _row_stride(x, name_x, dt, shape, rows, cols)
     ldy = _row_stride(y, name_y, dt, shape, rows, cols)
     px, py, size = x.data_ptr(), y.data_ptr(), rows * _SIZE[dt]
     end = py + ldy * size
     # in place is allowed; what comes near in another way is looked at more closely
-    if (px != py or ldx != ldy) and py < px + ldx * size and px < end and cols:
+    if py < px + ldx * size and px < end and (px != py or ldx != ldy) and cols:
         _clear(y, name_y, x, name_x)
     pr = ldr = 0
     if residual is not None:
         ldr = _row_stride(residual, "residual", dt, shape, rows, cols)
         pr = residual.data_ptr()
-        if (pr != py or ldr != ldy) and py < pr + ldr * size and pr < end and cols:
+        if py < pr + ldr * size and pr < end and (pr != py or ldr != ldy) and cols:
             _clear(y, name_y, residual, "residual")
     words = _drop(p, rng)
     _here(x, y, residual, rng)
