@@ -211,10 +211,7 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   const int64_t M = p.M, N = p.N, K = p.K;
   const int nk = (int)((K + kBK - 1) / kBK);
   float bias[8];  // an epilogue's, loaded ahead: what few k-tiles there are would not hide it
-  if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {
-    ask_early(p.epi);
-    load_bias<8, false>(p.epi, bn + wn * 64 + 8 * (lane & 7), bias);
-  }
+  if constexpr (std::is_same_v<Prob, GemmEpiProblem>) load_bias<8, false>(p.epi, bn + wn * 64 + 8 * (lane & 7), bias);
 
   // global -> register prefetch of one k-tile (a cast operand's chunk is 16
   // bf16 values, two 16-byte loads)

@@ -364,7 +364,6 @@ __global__ __launch_bounds__(256, 2) void k_mx_mid(Prob p) {
   const int frow = lane & 15, fchunk = 2 * (lane >> 4);
   float bias[8];
   if constexpr (kEpi<Prob>) {
-    ask_early(p.epi);
     load_bias<8>(p.epi, bn + 64 * wn + 8 * (lane & 7), bias);
   }
   issue(0);
@@ -512,7 +511,6 @@ __device__ __forceinline__ void few_tile(const Prob& p, const MxApply& ap, int64
   const int64_t bm = b % nbm * (16 * TM), bn = b / nbm * (16 * TN);
   uint8_t* my = lds + wave * (2 * kStage + kOwn);
 
-  if constexpr (kEpi<Prob>) ask_early(p.epi);
   // descriptors over the tile's rows (and 32-row scale groups) that exist
   const int64_t lm = M - bm < 16 * TM ? M - bm : 16 * TM, ln = N - bn < 16 * TN ? N - bn : 16 * TN;
   const i32x4 ra = make_rsrc(p.A.q + bm * pitch, kFused ? 0 : lm * pitch);
