@@ -282,8 +282,15 @@ fp8sg_status mxfp4_linear_bwd_epilogue(const void* gy, fp8sg_out type, int64_t M
     FP8SG_TRY(check_tensor(gw, N * K, esize(out)));
   }
   if (!products && !gb && M * K > 0 && N * K > 0) return FP8SG_ERR_NULL;
-  if (gb || (changes(a) && products))
-    if (launch_epilogue_bwd(a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
+  const bool step = gb || (changes(a) && products);
+  if (step && products && mx_epilogue_parts(M, N) > 0) {
+    const MxQuantJob j{gy, M, N, gx ? ws->gy_q : mxfp4_operand{}, gw ? ws->gy_qT : mxfp4_operand{}};
+    if (launch_mx_quantize_epilogue(j, type, rule == FP8SG_MX_FIT, a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
+    const MxGemmProblem dgrad{ws->gy_q, saved->w_qT, gx, M, K, N}, wgrad{ws->gy_qT, saved->x_qT, gw, N, K, M};
+    return hip_status(gx && gw ? launch_mx_gemm_pair(dgrad, wgrad, out, S(stream))
+                               : launch_mx_gemm(gx ? dgrad : wgrad, out, S(stream)));
+  }
+  if (step && launch_epilogue_bwd(a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
   if (!products) return FP8SG_OK;
   return mxfp4_linear_bwd(changes(a) ? gh : gy, type, M, N, K, rule, ws, saved, gx, gw, out, stream);
 }

@@ -193,8 +193,9 @@ __global__ __launch_bounds__(kBlock) void k_dropout(DropoutArgs p) {
 }  // namespace
 
 int64_t epilogue_ws_len(int64_t M, int64_t N) {
-  const Split s = split_of(M, N);
-  return s.parts > 1 ? s.parts * N : 0;
+  // (of either form: with MXFP4 the step is part of the quantising pass)
+  const int64_t a = split_of(M, N).parts, b = mx_epilogue_parts(M, N), parts = a > b ? a : b;
+  return parts > 1 ? parts * N : 0;
 }
 
 hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream) {
@@ -217,7 +218,10 @@ hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((k_epilogue_bwd<T, false>), grid, dim3(kBwd), 0, stream, a);
     return hipGetLastError();
   });
-  if (err != hipSuccess || !a.gb || s.parts == 1) return err;
+  return err != hipSuccess || !a.gb || s.parts == 1 ? err : launch_bias_join(a, stream);
+}
+
+hipError_t launch_bias_join(const EpilogueBwdArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((a.N + kJoin - 1) / kJoin)), dim3(kBlock), 0, stream, a.part,
                      a.parts, a.N, a.gb, a.bias_type);
   return hipGetLastError();

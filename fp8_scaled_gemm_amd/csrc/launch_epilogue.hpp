@@ -76,6 +76,14 @@ struct EpilogueBwdArgs {
 };
 int64_t epilogue_ws_len(int64_t M, int64_t N);
 hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream);
+// gb from the a.parts rows of partial sums in a.part
+hipError_t launch_bias_join(const EpilogueBwdArgs& a, hipStream_t stream);
+// The backward step and gh's MXFP4 codes (of a job whose x is gy) in one pass, where
+// M rows leave at most kMxEpiParts rows of partial sums, one for 64 rows (their join
+// takes 7 of 82 us at 65536 x 512).  mx_epilogue_parts: how many, 0 where it does not apply.
+constexpr int64_t kMxEpiParts = 1024;
+int64_t mx_epilogue_parts(int64_t M, int64_t N);
+hipError_t launch_mx_quantize_epilogue(const MxQuantJob& j, int type, bool fit, EpilogueBwdArgs e, hipStream_t stream);
 
 // y = residual + drop(x) (residual may be nullptr), rows ldx, ldr and ldy apart
 struct DropoutArgs {

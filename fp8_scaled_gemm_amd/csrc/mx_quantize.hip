@@ -3,7 +3,7 @@
 // For each block of 32 along the contraction: amax, its power-of-two scale,
 // 32 codes of 4 bits.  Bound by memory: per element 2 bytes in (bf16) and
 // 17/32 bytes out per direction.
-#include "mx.hpp"
+#include "epilogue.hpp"
 
 namespace fp8sg {
 namespace {
@@ -78,6 +78,54 @@ struct MxQuantArgs {
   uint32_t blocks0;  // blocks of job 0
   int32_t fit;
 };
+// A job whose x is gy and what is quantised gh (EpilogueBwdArgs).
+struct MxQuantEpiArgs : MxQuantArgs {
+  EpilogueBwdArgs epi;
+};
+
+// A lane's rows of gy to those of gh, rounded as a stored one is, which they are as
+// well where p.gh is given; and the sums of its columns before the rounding.
+template <int T, int RL, bool S>
+__device__ __forceinline__ void epilogue_step(const EpilogueBwdArgs& p, Row8<T> (&v)[RL], int64_t rw, int64_t c,
+                                              float (&sum)[8]) {
+  constexpr bool kFast = T != FP8SG_OUT_F32;
+  const int n = c < p.N ? left8(p.N, c) : 0;
+  const Drop d = drop_of(p.drop);
+  const uint64_t groups = (uint64_t)((p.N + 7) >> 3);
+  Row8<T> h[RL];
+#pragma unroll
+  for (int i = 0; i < RL; ++i) {
+    if (p.act != FP8SG_ACT_NONE && rw + i < p.M && n > 0) {
+      h[i] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.pre) + (rw + i) * p.N + c, n);
+    } else {
+      h[i].zero();
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < RL; ++i) {
+    float w[8], x[8];
+    v[i].values(w);
+    by_act(p.act, [&](auto a) {
+      h[i].values(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= slope_of<decltype(a)::value, kFast>(x[e]);
+    });
+    if (p.drop.rng) drop_n<8>(d, (uint64_t)(rw + i) * groups + (uint64_t)(c >> 3), 0, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += w[e];
+    if constexpr (kFast) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[i].w[e] = (uint32_t)from_f32<T>(w[2 * e]) | ((uint32_t)from_f32<T>(w[2 * e + 1]) << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i].w[e] = __float_as_uint(w[e]);
+    }
+    if (p.gh && rw + i < p.M && n > 0) store8<T, S>(reinterpret_cast<Elem<T>*>(p.gh) + (rw + i) * p.N + c, n, w);
+  }
+}
 
 // A block quantises 32 G rows x 256 columns, read once: a wave holds 32 rows x
 // 8 C columns, C = 2 RL lanes across, each with RL rows x 8 columns (RL = 16: one
@@ -93,8 +141,9 @@ struct MxQuantArgs {
 // with the fewest instructions; G = 2, RL = 4 gives small matrices four times the
 // blocks and 16 times the waves (37 x 1001 fp32, both ways: 9.2 us with RL = 16; so,
 // less than the call's 6.1 us on the host).
-template <int T, int G, int RL, bool S>
-__global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 ? 2 : 4) void k_mxq(MxQuantArgs args) {
+template <int T, int G, int RL, bool S, class Args>
+__global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 ? 2 : 4) void k_mxq(Args args) {
+  constexpr bool kEpi = std::is_same_v<Args, MxQuantEpiArgs>;
   constexpr int kRows = 32 * G, C = 2 * RL, kAcross = 32 / C, kThreads = 64 * G * kAcross;
   // column c's codes start at tcol(c); the 16-byte pieces (G = 8) or the
   // columns (G = 2) are shifted so that lanes 8 columns apart write to
@@ -103,6 +152,7 @@ __global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 
   __shared__ __attribute__((aligned(16))) uint8_t tq[G == 8 ? 256 * 128 : 256 * 32 + 32 * 16];
   __shared__ __attribute__((aligned(16))) uint8_t rs[G * 256];  // row scales: G groups of 256 bytes
   __shared__ __attribute__((aligned(16))) uint8_t ts[G * 256];  // column scales: 8 groups of 32 G bytes
+  __shared__ float sums[kEpi ? G * 256 : 1];                    // column sums of the row groups
 
   const bool second = blockIdx.x >= args.blocks0;
   const MxQuantJob& j = args.job[second];
@@ -124,6 +174,20 @@ __global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 
       v[i] = load_row8<T, S>(x + (rw + i) * j.cols + c, left8(j.cols, c));
     } else {
       v[i].zero();
+    }
+  }
+
+  if constexpr (kEpi) {
+    float sum[8];
+    epilogue_step<T, RL, S>(args.epi, v, rw, c, sum);
+    if (args.epi.gb) {  // of the lanes with the same columns, then (below) of the row groups
+#pragma unroll
+      for (int d = C; d < 64; d *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor(sum[i], d, kWave);
+      if (rg == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[wg * 256 + 8 * cc + i] = sum[i];
     }
   }
 
@@ -176,6 +240,16 @@ __global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 
     });
   }
   __syncthreads();
+  if constexpr (kEpi) {
+    const EpilogueBwdArgs& p = args.epi;
+    if (p.gb && tid < 256 && c0 + tid < p.N && r0 < p.M) {  // (a tile may lie in the transposed copy's padding)
+      float one[1] = {sums[tid]};
+#pragma unroll
+      for (int g = 1; g < G; ++g) one[0] += sums[g * 256 + tid];
+      if (p.parts > 1) p.part[rt * p.N + c0 + tid] = one[0];
+      else store_n<1, false>(reinterpret_cast<uint8_t*>(p.gb) + (c0 + tid) * esize(p.bias_type), 1, p.bias_type, one);
+    }
+  }
   if (j.q.q && tid < 16 * G && r0 + (tid >> 4) * 32 < j.rows)
     *reinterpret_cast<uint4*>(j.q.s + ((r0 / 32 + (tid >> 4)) * nkc + ct) * 256 + (tid & 15) * 16) =
         *reinterpret_cast<const uint4*>(rs + tid * 16);
@@ -187,7 +261,8 @@ __global__ __launch_bounds__(64 * G * (16 / RL), T == FP8SG_OUT_F32 && RL == 16 
       const int id = p * kThreads + tid, cl = id / G, k = id % G;
       const int piece = G == 8 ? (k ^ ((cl >> 3) & 7)) : k;
       if (c0 + cl < j.cols)
-        st16<S>(j.t.q + ((c0 + cl) * nkr + kt) * 128 + sub + k * 16, *reinterpret_cast<const uint4*>(tq + tcol(cl) + piece * 16));
+        st16<S && G == 8>(j.t.q + ((c0 + cl) * nkr + kt) * 128 + sub + k * 16,
+                          *reinterpret_cast<const uint4*>(tq + tcol(cl) + piece * 16));
     }
     // 8 groups of 32 columns, of each the bytes of the tile's block pairs
     if (tid < 16 * G) {
@@ -274,8 +349,8 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
       const int64_t b0 = tiles_of<G>(a.job[0]), b1 = n > 1 ? tiles_of<G>(a.job[1]) : 0;
       if (b0 + b1 == 0) return hipSuccess;
       a.blocks0 = (uint32_t)b0;
-      hipLaunchKernelGGL((k_mxq<T, G, RL, decltype(st)::value>), dim3((unsigned)(b0 + b1)), dim3(64 * G * (16 / RL)), 0,
-                         stream, a);
+      hipLaunchKernelGGL((k_mxq<T, G, RL, decltype(st)::value, MxQuantArgs>), dim3((unsigned)(b0 + b1)),
+                         dim3(64 * G * (16 / RL)), 0, stream, a);
       return hipGetLastError();
     };
     if (wide < cus && n == 1 && !a.job[0].t.q) {
@@ -291,6 +366,46 @@ hipError_t launch_mx_quantize(const MxQuantJob* jobs, int n, int type, bool fit,
     if (bytes >= kStreamBytes) return launch(C8{}, C16{}, std::true_type{});
     return launch(C8{}, C16{}, std::false_type{});
   });
+}
+
+int64_t mx_epilogue_parts(int64_t M, int64_t N) {
+  const int64_t parts = (M + 63) / 64;
+  return N == 0 || parts > kMxEpiParts || N > (1ll << 27) ? 0 : parts;  // (and at most 2^21 blocks)
+}
+
+// The backward step, gh's codes both ways and the bias's gradient in one pass (us of
+// the whole backward pass with gelu and gb, in a graph, against the step and the cast
+// one after the other; K = 64, so the products take little: 8192 x 14336 bf16 206, 241;
+// 4096 x 4096 bf16 45, 50, fp32 56, 68; 600 x 520 14.0, 16.7; but 64 x 256 fp32 12.8,
+// 12.0).  Bound by memory where there are many rows.  Tiles of 64 rows with 4 of them
+// a lane at any size: with 256 and 8, whose values and temporaries bf16's registers did
+// not hold, 8192 x 14336 bf16 255, 8192 x 4096 fp16 108 instead of 72.  Non-temporal
+// accesses for large 16-bit matrices (8192 x 14336 bf16 224 without; fp32, whose lanes
+// read 32 bytes in two halves, 374 with, 372 without), but not for the columns' codes:
+// their runs of 32 bytes meet in the caches.
+hipError_t launch_mx_quantize_epilogue(const MxQuantJob& j, int type, bool fit, EpilogueBwdArgs e, hipStream_t stream) {
+  MxQuantEpiArgs a{};
+  a.job[0] = j;
+  a.fit = fit;
+  a.epi = e;
+  a.epi.parts = (int32_t)mx_epilogue_parts(e.M, e.N);
+  const int64_t blocks = tiles_of<2>(j);
+  if (blocks == 0) return hipSuccess;
+  a.blocks0 = (uint32_t)blocks;
+  const bool st = e.M * e.N * (2 * (1 + (e.act != FP8SG_ACT_NONE) + (e.gh != nullptr)) + 1) >= kStreamBytes;
+  const hipError_t err = by_type(type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    const dim3 grid((unsigned)blocks), block(512);
+    if constexpr (T != FP8SG_OUT_F32) {
+      if (st) {
+        hipLaunchKernelGGL((k_mxq<T, 2, 4, true, MxQuantEpiArgs>), grid, block, 0, stream, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((k_mxq<T, 2, 4, false, MxQuantEpiArgs>), grid, block, 0, stream, a);
+    return hipGetLastError();
+  });
+  return err != hipSuccess || !e.gb || a.epi.parts == 1 ? err : launch_bias_join(a.epi, stream);
 }
 
 hipError_t launch_mx_dequantize(const mxfp4_operand& m, int64_t rows, int64_t k, void* y, int type, hipStream_t stream) {

@@ -188,3 +188,42 @@ def test_the_same_tensor_twice():
     F.dropout_fwd(x, 0.5, rng, a, residual=x)
     F.dropout_fwd(x, 0.5, rng, b, residual=x.clone())
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N_,dtype", [(64, 256, "f32"), (63, 255, "f16"), (257, 1000, "bf16"), (4100, 520, "f16"),
+                                        (1, 8200, "bf16"), (65536, 40, "bf16"), (65537, 40, "bf16"), (300, 72, "f32"),
+                                        (9100, 4232, "bf16")])
+def test_mx_backward_in_one_pass_or_two(M, N_, dtype):
+    """gh, its codes and gb of one pass, or past 65536 rows of two, are those of the
+    step and the plain backward pass one after the other; all kinds, and in place."""
+    K = 40
+    x, w = rand((M, K), dtype, 1), rand((N_, K), dtype, 2, 0.05)
+    gy, pre, rng = rand((M, N_), dtype, 3, 0.1), rand((M, N_), dtype, 4, 2.0), rng_words(5)
+    gy.view(-1)[0] = float("inf")
+    ws, saved = F.Mxfp4LinearWs(M, N_, K), F.Mxfp4LinearSaved(M, N_, K)
+    F.mxfp4_linear_fwd(x, w, ws, saved, torch.empty(M, N_, dtype=gy.dtype, device=DEV))
+    part = torch.full((F.epilogue_workspace_len(M, N_) + 5,), GUARD, device=DEV)
+    new = lambda *s: torch.full(s, GUARD, dtype=gy.dtype, device=DEV)  # noqa: E731
+    for act, p in ((F.ACT_GELU, 0.25), (F.ACT_RELU, 0.0), (F.ACT_NONE, 0.5), (F.ACT_GELU_TANH, 1.0)):
+        kw = {"pre": pre if act else None, "act": act, "p": p, "rng": rng if p else None, "part": part}
+        gh, gb = torch.empty_like(gy), torch.empty(N_, device=DEV)
+        F.epilogue_bwd(gy, gh, gb, **kw)
+        for kinds in ("xwb", "xw", "xb", "w"):
+            gx, gw = (new(M, K) if "x" in kinds else None), (new(N_, K) if "w" in kinds else None)
+            want = [None if g is None else torch.empty_like(g) for g in (gx, gw)]
+            F.mxfp4_linear_bwd(gh, ws, saved, *want)
+            b = new(N_).float() if "b" in kinds else None
+            gh2 = gy.clone() if kinds == "xb" else new(M, N_)  # (in place)
+            ws.gy_q.q.fill_(255), ws.gy_qT.q.fill_(255)
+            F.mxfp4_linear_bwd_epilogue(gh2 if kinds == "xb" else gy, ws, saved, gx, gw, gh=gh2, gb=b, **kw)
+            assert torch.equal(gh2.view(torch.uint8), gh.view(torch.uint8)), (act, kinds)
+            for got, ref in ((gx, want[0]), (gw, want[1])):
+                assert got is None or torch.equal(got.view(torch.uint8), ref.view(torch.uint8)), (act, kinds)
+            if b is not None:
+                # each of the two orders rounds M times, by 2^-24 of the magnitudes' sum at
+                # most; a magnitude is at most |gy| 1.13 (the largest slope) / (1 - p)
+                live = torch.isfinite(gb)
+                assert torch.equal(torch.isfinite(b), live)
+                tol = 2 * M * 2.0 ** -24 * 1.2 * gy.double().abs().sum(0) / (1 - p if p < 1 else 1)
+                assert ((b - gb).double().abs() <= tol)[live].all(), (act, kinds)
+        assert (part[F.epilogue_workspace_len(M, N_):] == GUARD).all()
