@@ -46,7 +46,8 @@ __global__ __launch_bounds__(kBwd, 2) void k_epilogue_bwd(EpilogueBwdArgs p) {
           h[u].zero();
           if (r < p.M) {
             g[u] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.gy) + r * p.N + c, n);
-            if (p.act != FP8SG_ACT_NONE) h[u] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.pre) + r * p.N + c, n);
+            if (p.act != FP8SG_ACT_NONE)
+              h[u] = load_row8<T, S>(reinterpret_cast<const Elem<T>*>(p.pre) + r * p.N + c, n);
           }
         }
 #pragma unroll

@@ -39,9 +39,10 @@ below.
     linears with bias, activation, dropout and residual in the product's epilogue,
     and dropout on its own.
 
-Limits of Float8Linear: inputs and weights are bf16 or fp16; Float8Linear has no bias (the method's linear has none; the default
-filter leaves biased layers alone); leading dimensions of the input are
-flattened into M; M, N, K must be multiples of 16.
+Limits of Float8Linear: inputs and weights are bf16 or fp16; no bias (the method's
+linear has none; the default filter leaves biased layers alone, biased=True makes
+them Float8EpilogueLinear); leading dimensions of the input are flattened into M;
+M, N, K must be multiples of 16.
 """
 import math
 from typing import Callable, Optional
@@ -1010,8 +1011,8 @@ def _ep_backward(ctx, gy, *_unused):
     gx = gw = gb = None
     if any(need[:3]):
         rng, *kept = ctx.saved_tensors
-        gx, gw, gb = torch.ops.fp8sg.scaled_linear_epilogue_bwd(_ep_gy(ctx, gy), kept[0], rng, *kept[1:], ctx.act, ctx.p,
-                                                                need[2], ctx.bdtype)
+        gx, gw, gb = torch.ops.fp8sg.scaled_linear_epilogue_bwd(_ep_gy(ctx, gy), kept[0], rng, *kept[1:], ctx.act,
+                                                                ctx.p, need[2], ctx.bdtype)
     return (gx if need[0] else None, gw if need[1] else None, gb if need[2] else None, gy if need[3] else None,
             None, None, None, None)
 
@@ -1022,8 +1023,8 @@ _op_ep_fwd.register_autograd(_ep_backward, setup_context=_ep_setup)
 # ------------------------------------------------------------------------- MXFP4
 
 @torch.library.custom_op("fp8sg::mxfp4_linear_epilogue_fwd", mutates_args=())
-def _op_mxe_fwd(x: _T, w: _T, bias: Optional[_T], residual: Optional[_T], rng: Optional[_T], act: int, p: float, rule: int,
-                save: bool) -> tuple[_T, _T, _T, _T, _T, _T]:
+def _op_mxe_fwd(x: _T, w: _T, bias: Optional[_T], residual: Optional[_T], rng: Optional[_T], act: int, p: float,
+                rule: int, save: bool) -> tuple[_T, _T, _T, _T, _T, _T]:
     M, K = x.shape
     N = w.shape[0]
     y = x.new_empty((M, N))
@@ -1045,8 +1046,8 @@ def _op_mxe_fwd_fake(x, w, bias, residual, rng, act, p, rule, save):
 
 
 @torch.library.custom_op("fp8sg::mxfp4_linear_epilogue_bwd", mutates_args=())
-def _op_mxe_bwd(gy: _T, pre: _T, rng: Optional[_T], xq: _T, xs: _T, wq: _T, ws: _T, K: int, act: int, p: float, rule: int,
-                need: int, bdtype: torch.dtype) -> tuple[_T, _T, _T]:
+def _op_mxe_bwd(gy: _T, pre: _T, rng: Optional[_T], xq: _T, xs: _T, wq: _T, ws: _T, K: int, act: int, p: float,
+                rule: int, need: int, bdtype: torch.dtype) -> tuple[_T, _T, _T]:
     M, N = gy.shape
     gx = gy.new_empty((M, K) if need & 1 else (0,))
     gw = gy.new_empty((N, K) if need & 2 else (0,))
@@ -1054,9 +1055,10 @@ def _op_mxe_bwd(gy: _T, pre: _T, rng: Optional[_T], xq: _T, xs: _T, wq: _T, ws: 
     products = need & 3
     mxfp4_linear_bwd_epilogue(gy, Mxfp4LinearWs(M, N, K, gy.device, forward=False),
                               Mxfp4LinearSaved(M, N, K, tensors=(xq, xs, wq, ws)), gx if need & 1 else None,
-                              gw if need & 2 else None, gh=torch.empty_like(gy) if products and _changes(act, p) else None,
-                              gb=gb if need & 4 else None, pre=pre if act != ACT_NONE else None, act=act, p=p, rng=rng,
-                              part=_ep_part(gy, M, N) if need & 4 else None, rule=rule)
+                              gw if need & 2 else None,
+                              gh=torch.empty_like(gy) if products and _changes(act, p) else None,
+                              gb=gb if need & 4 else None, pre=pre if act != ACT_NONE else None, act=act, p=p,
+                              rng=rng, part=_ep_part(gy, M, N) if need & 4 else None, rule=rule)
     return gx, gw, gb
 
 

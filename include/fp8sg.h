@@ -1,8 +1,8 @@
 /*
  * fp8sg -- FP8 per-tensor dynamically scaled linear layer and GradScaler step
- * for AMD Instinct MI355X (gfx950), and the MXFP4 linear layer, the gated
- * activation and the layer norm of the same transformer block (last section).
- * C ABI.
+ * for AMD Instinct MI355X (gfx950), the MXFP4 linear layer, the gated activation
+ * and the layer norm of the same transformer block, and bias, activation, residual
+ * and dropout behind those linears' products (the last two sections).  C ABI.
  *
  * The operations follow these web pages (cited by title and section):
  *   [FP8-TRAIN]  "FP8训练：量化、自动微分、Torchao" (lzwjava.github.io)
