@@ -99,7 +99,7 @@ fp8sg_status check_backward(const void* gy, int type, const fp8sg_epilogue* e, i
   if (e->act != FP8SG_ACT_NONE) FP8SG_TRY(check_tensor(e->pre, M * N, esize(type)));
   FP8SG_TRY(check_drop(e->p, e->rng, a.drop));
   if (gb) {
-    const int64_t need = epilogue_ws_len(M, N);
+    const int64_t need = epilogue_ws_need(M, N);
     if (need > 0 && !ws) return FP8SG_ERR_NULL;
     if (need > ws_len) return FP8SG_ERR_SHAPE;
     if (!aligned(ws, 4)) return FP8SG_ERR_ALIGN;
@@ -283,7 +283,9 @@ fp8sg_status mxfp4_linear_bwd_epilogue(const void* gy, fp8sg_out type, int64_t M
   }
   if (!products && !gb && M * K > 0 && N * K > 0) return FP8SG_ERR_NULL;
   const bool step = gb || (changes(a) && products);
-  if (step && products && mx_epilogue_parts(M, N) > 0) {
+  const int64_t parts = mx_epilogue_parts(M, N);
+  // (few rows' sums need no workspace in the step alone: without one it is that)
+  if (step && products && parts > 0 && (!gb || parts == 1 || (ws_part && part_len >= parts * N))) {
     const MxQuantJob j{gy, M, N, gx ? ws->gy_q : mxfp4_operand{}, gw ? ws->gy_qT : mxfp4_operand{}};
     if (launch_mx_quantize_epilogue(j, type, rule == FP8SG_MX_FIT, a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
     const MxGemmProblem dgrad{ws->gy_q, saved->w_qT, gx, M, K, N}, wgrad{ws->gy_qT, saved->x_qT, gw, N, K, M};

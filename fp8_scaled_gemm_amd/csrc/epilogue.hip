@@ -198,6 +198,7 @@ int64_t epilogue_ws_len(int64_t M, int64_t N) {
   const int64_t a = split_of(M, N).parts, b = mx_epilogue_parts(M, N), parts = a > b ? a : b;
   return parts > 1 ? parts * N : 0;
 }
+int64_t epilogue_ws_need(int64_t M, int64_t N) { return split_of(M, N).parts > 1 ? epilogue_ws_len(M, N) : 0; }
 
 hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream) {
   if (a.N == 0) return hipSuccess;

@@ -75,6 +75,8 @@ struct EpilogueBwdArgs {
   int64_t strips;
 };
 int64_t epilogue_ws_len(int64_t M, int64_t N);
+// ... without which a call is refused: none where the step alone does with one part
+int64_t epilogue_ws_need(int64_t M, int64_t N);
 hipError_t launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream);
 // gb from the a.parts rows of partial sums in a.part
 hipError_t launch_bias_join(const EpilogueBwdArgs& a, hipStream_t stream);

@@ -290,7 +290,8 @@ def fp8_scaled_linear_bwd_epilogue(gy: torch.Tensor, saved: LinearSaved, ws: Lin
     """The gradients gx, gw (of one dtype) and gb (or None) of
     fp8_scaled_linear_fwd_epilogue from gy and the forward's saved, pre, act, p and rng.
     gh: scratch like gy, or gy itself; None where the epilogue leaves gy as it is.
-    part: float32, epilogue_workspace_len(M, N) of them, where gb is wanted."""
+    part: float32, epilogue_workspace_len(M, N) of them, where gb is wanted (up to 256
+    rows optional, though mxfp4_linear_bwd_epilogue takes a pass less with it)."""
     M, N = _need_2d(gy, "gy")
     if gy.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"gy: dtype {gy.dtype}, expected bfloat16 or float16")

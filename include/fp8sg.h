@@ -879,7 +879,8 @@ FP8SG_API fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void*
  *   gy, pre, gh: M x N of `type`, contiguous.  gh may be gy; NULL if only gb is
  *                wanted.  gb may be NULL.  act'(0) of relu is 0.
  *   ws: float[ws_len], ws_len >= epilogue_workspace_len(M, N); not read before it
- *       is written; may be NULL where gb is.
+ *       is written; may be NULL where gb is, and up to 256 rows (where
+ *       mxfp4_linear_bwd_epilogue takes one pass less with it).
  */
 FP8SG_API int64_t epilogue_workspace_len(int64_t M, int64_t N);
 FP8SG_API fp8sg_status epilogue_bwd(const void* gy, fp8sg_out type, const fp8sg_epilogue* epi,

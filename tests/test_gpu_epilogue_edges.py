@@ -227,3 +227,24 @@ def test_mx_backward_in_one_pass_or_two(M, N_, dtype):
                 tol = 2 * M * 2.0 ** -24 * 1.2 * gy.double().abs().sum(0) / (1 - p if p < 1 else 1)
                 assert ((b - gb).double().abs() <= tol)[live].all(), (act, kinds)
         assert (part[F.epilogue_workspace_len(M, N_):] == GUARD).all()
+
+
+@pytest.mark.parametrize("M", [64, 65, 256])
+def test_few_rows_need_no_workspace(M):
+    N_, K = 144, 48
+    gy, pre = rand((M, N_), "bf16", 3, 0.1), rand((M, N_), "bf16", 4, 2.0)
+    ws, saved = F.Mxfp4LinearWs(M, N_, K), F.Mxfp4LinearSaved(M, N_, K)
+    F.mxfp4_linear_fwd(rand((M, K), "bf16", 1), rand((N_, K), "bf16", 2), ws, saved, torch.empty_like(gy))
+    got = []
+    for part in (None, torch.empty(F.epilogue_workspace_len(M, N_), device=DEV)):
+        out = [torch.empty(s, dtype=gy.dtype, device=DEV) for s in ((M, N_), (M, K), (N_, K))] + [torch.empty(N_, device=DEV)]
+        F.mxfp4_linear_bwd_epilogue(gy, ws, saved, out[1], out[2], gh=out[0], gb=out[3], pre=pre, act=F.ACT_SILU, part=part)
+        got.append(out)
+    for a, b in zip(*(g[:3] for g in got)):
+        assert torch.equal(a, b)
+    # two orders of M roundings, of magnitudes up to |gy| 1.1 (the largest slope)
+    tol = 2 * M * 2.0 ** -24 * 1.1 * gy.double().abs().sum(0)
+    assert ((got[0][3] - got[1][3]).double().abs() <= tol).all()
+    gb = torch.empty(N_, device=DEV)  # and the step on its own
+    F.epilogue_bwd(gy, None, gb, pre=pre, act=F.ACT_SILU)
+    assert ((gb - got[0][3]).double().abs() <= tol).all()
