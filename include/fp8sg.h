@@ -875,7 +875,8 @@ FP8SG_API fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void*
 /*
  * The backward step of an epilogue: gh = drop(gy) * act'(pre) of `type`, and the
  * bias's gradient gb[n] = sum over m of the unrounded gh (fp32 sums in an order
- * that depends on the sizes only, rounded once to bias_type).
+ * that depends on the entry point, the sizes and which outputs and workspace are
+ * given, never on timing; rounded once to bias_type).
  *   gy, pre, gh: M x N of `type`, contiguous.  gh may be gy; NULL if only gb is
  *                wanted.  gb may be NULL.  act'(0) of relu is 0.
  *   ws: float[ws_len], ws_len >= epilogue_workspace_len(M, N); not read before it
