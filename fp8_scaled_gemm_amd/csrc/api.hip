@@ -303,7 +303,9 @@ hipError_t launch_linear_bwd(const uint16_t* gy, const fp8_linear_saved& sv, int
   // [M, N] as A^T and x codes [M, K] as B^T.
   const bool tb_d = !sv.w_qT, ta_w = !w.gy_qT, tb_w = !sv.x_qT;
   const int o = amp_scale ? kOutF16Unscale : out;
-  if (!hist_gy && tb_d && ta_w && tb_w && small_layer_fits(M, N, K)) {
+  const int64_t es = o == FP8SG_OUT_F32 ? 4 : 2;
+  const bool over = shares(gx, M * K * es, gy, M * N * 2) || shares(gw, N * K * es, gy, M * N * 2);
+  if (!hist_gy && tb_d && ta_w && tb_w && small_layer_fits(M, N, K) && !over) {
     // small layer without transposed copies: the cast of gy and both GEMMs
     // in one launch
     SmallBwdArgs a{gy, M, N,
@@ -373,7 +375,9 @@ fp8sg_status linear_fwd(const uint16_t* x, const uint16_t* w, int64_t M, int64_t
     if (!hist_ok(hist_x) || !hist_ok(hist_w)) return FP8SG_ERR_ALIGN;
   }
   hipStream_t s = S(stream);
-  if (!delayed && !saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K)) {
+  const int64_t ny = M * N * (out == FP8SG_OUT_F32 ? 4 : 2);
+  const bool over = shares(y, ny, x, M * K * 2) || shares(y, ny, w, N * K * 2);
+  if (!delayed && !saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K) && !over) {
     // small layer without transposed copies: casts and GEMM in one launch
     SmallFwdArgs a{x, w, GemmProblem{saved->x_q, saved->w_q, y, nullptr, nullptr, M, N, K},
                    saved->x_sc, saved->w_sc, saved->x_q, saved->w_q};

@@ -161,7 +161,8 @@ fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void* w, fp8sg_
   if (epi->bias && epi->bias_type != type && epi->bias_type != FP8SG_OUT_F32) return FP8SG_ERR_FORMAT;
   const uint16_t *x16 = static_cast<const uint16_t*>(x), *w16 = static_cast<const uint16_t*>(w);
   const bool f16 = type == FP8SG_OUT_F16;
-  if (!saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K)) {
+  const bool over = stored_over(p.epi, x, M * K * 2) || stored_over(p.epi, w, N * K * 2);
+  if (!saved->x_qT && !saved->w_qT && small_layer_fits(M, N, K) && !over) {
     const SmallFwdEpiArgs a{x16, w16, p, saved->x_sc, saved->w_sc, saved->x_q, saved->w_q};
     return hip_status(launch_small_fwd_epilogue(a, f16, S(stream)));
   }
@@ -196,15 +197,16 @@ fp8sg_status fp8_scaled_linear_bwd_epilogue(const void* gy, fp8sg_out type, cons
   FP8SG_TRY(check_backward(gy, type, epi, M, N, gh, gb, ws_part, part_len, 16, a));
   if (changes(a) && !gh) return FP8SG_ERR_NULL;
   const bool step = changes(a) || gb;  // otherwise there is nothing to do before the cast
+  // (a small layer's launch takes the maximum itself)
+  const bool small = !saved->x_qT && !saved->w_qT && !ws->gy_qT && small_layer_fits(M, N, K);
   if (step) {
-    // (a small layer's launch takes the maximum itself)
-    const bool small = !saved->x_qT && !saved->w_qT && !ws->gy_qT && small_layer_fits(M, N, K);
     a.rec = small ? nullptr : ws->gy_sc;
     if (!changes(a)) a.gh = nullptr;
     if (launch_epilogue_bwd(a, S(stream)) != hipSuccess) return FP8SG_ERR_HIP;
   }
   return hip_status(launch_linear_bwd(static_cast<const uint16_t*>(changes(a) ? gh : gy), *saved, M, N, K, *ws, nullptr,
-                                      0, gx, gw, out, nullptr, nullptr, type == FP8SG_OUT_F16, step, S(stream)));
+                                      0, gx, gw, out, nullptr, nullptr, type == FP8SG_OUT_F16, step && !small,
+                                      S(stream)));
 }
 
 fp8sg_status mxfp4_gemm_epilogue(const mxfp4_operand* A, const mxfp4_operand* B, const fp8sg_epilogue* epi, void* C,

@@ -91,9 +91,17 @@ hipError_t launch_gemm_km_pair(const GemmProblem& dgrad, const GemmProblem& wgra
 // fastest on the current device (fp8_linear_copies).
 void linear_copies(int64_t M, int64_t N, int64_t K, bool& x_t, bool& w_t, bool& gy_t);
 
+// Whether two runs of bytes share any.  A launch in which some workgroups still read
+// an input while others store results is not taken for results that lie over that
+// input: the casts then have launches of their own, behind which the input is free.
+inline bool shares(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + (uintptr_t)nb && q < p + (uintptr_t)na;
+}
+
 // Small layers in one launch per pass (small_layer.hip), for layers whose x,
-// W and gy each hold at most kSelfCastMaxElems elements and that keep no
-// transposed copies.  Forward: p is the forward GEMM (A = x_q, B = w_q, C = y;
+// W and gy each hold at most kSelfCastMaxElems elements, that keep no
+// transposed copies and whose results lie over none of the inputs.  Forward: p is the forward GEMM (A = x_q, B = w_q, C = y;
 // its inverse pointers are not read), x and w the bf16 inputs.  Backward: dg
 // and wg are the dgrad and wgrad problems on contraction-major codes (their
 // inv_b point to the saved records' inverses), gy the bf16 gradient

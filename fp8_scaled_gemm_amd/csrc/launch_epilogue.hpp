@@ -36,6 +36,13 @@ struct EpilogueArgs {
   int32_t stream;  // results leave with non-temporal stores
 };
 
+// Whether y or pre lies over n bytes at in.
+inline bool stored_over(const EpilogueArgs& e, const void* in, int64_t n) {
+  const int64_t es = e.type == FP8SG_OUT_F32 ? 4 : 2;
+  if (e.M == 0 || e.N == 0) return false;
+  return shares(e.C, ((e.M - 1) * e.ldc + e.N) * es, in, n) || (e.pre && shares(e.pre, e.M * e.N * es, in, n));
+}
+
 struct GemmEpiProblem : GemmProblem {
   EpilogueArgs epi;
 };

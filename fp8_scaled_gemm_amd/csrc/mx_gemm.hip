@@ -877,10 +877,11 @@ hipError_t launch_mx_gemm_pair(const MxGemmProblem& p0, const MxGemmProblem& p1,
 namespace {
 
 // Every workgroup quantises x again, so in the product's own launch only for
-// a few rows, and only k-tiles that fit its LDS.
-bool apply_fused(const MxGemmProblem& p) {
-  return p.M <= kFusedRows && p.K > 0 && mx_ktiles(p.K) <= 4 * kFusedTiles;
+// a few rows, only k-tiles that fit its LDS, and not where results lie over x (`over`).
+bool apply_fused(const MxGemmProblem& p, bool over) {
+  return p.M <= kFusedRows && p.K > 0 && mx_ktiles(p.K) <= 4 * kFusedTiles && !over;
 }
+int64_t bytes_of(int64_t n, int type) { return n * (type == FP8SG_OUT_F32 ? 4 : 2); }
 template <int T, class Prob>
 hipError_t launch_apply_fused(const MxQuantJob& j, int type, bool fit, const Prob& p, hipStream_t stream) {
   return by_type(type, [&](auto f) {
@@ -896,7 +897,7 @@ hipError_t launch_apply_fused(const MxQuantJob& j, int type, bool fit, const Pro
 hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemmProblem& p, int out,
                            hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (apply_fused(p))
+  if (apply_fused(p, shares(p.C, bytes_of(p.M * p.N, out), j.x, bytes_of(p.M * p.K, type))))
     return by_type(out, [&](auto t) { return launch_apply_fused<decltype(t)::value>(j, type, fit, p, stream); });
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);
   return e != hipSuccess ? e : launch_mx_gemm(p, out, stream);
@@ -905,7 +906,7 @@ hipError_t launch_mx_apply(const MxQuantJob& j, int type, bool fit, const MxGemm
 hipError_t launch_mx_apply_epilogue(const MxQuantJob& j, int type, bool fit, const MxGemmEpiProblem& p,
                                     hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (apply_fused(p))
+  if (apply_fused(p, stored_over(p.epi, j.x, bytes_of(p.M * p.K, type))))
     return p.epi.type == FP8SG_OUT_F32 ? launch_apply_fused<FP8SG_OUT_F32>(j, type, fit, p, stream)
                                        : launch_apply_fused<FP8SG_OUT_BF16>(j, type, fit, p, stream);
   const hipError_t e = launch_mx_quantize(&j, 1, type, fit, stream);

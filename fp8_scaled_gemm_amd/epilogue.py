@@ -15,6 +15,8 @@ The epilogue's arguments, by keyword in every call:
             dtype), or None
   p, rng    dropout's probability, in steps of 2^-16, and the two int64 words in
             device memory that its generator starts from (None where p is 0)
+The output and pre may lie over a linear's x or w (with the residual the output
+itself too: a residual stream updated in place), over no other buffer of a call.
 """
 import ctypes
 import struct
@@ -98,6 +100,16 @@ def _all_clear(outputs, inputs):
             _clear(t, name, u, other)
 
 
+def _off_codes(C, pre, *codes):
+    """C and pre lie over none of a product's operands, which it reads as it stores."""
+    for t, name in ((C, "C"), (pre, "pre")):
+        if t is not None and t.numel():
+            a0, a1 = _span(t)
+            for q in codes:
+                if q.numel() and a0 < q.data_ptr() + q.nbytes and q.data_ptr() < a1:
+                    raise ValueError(f"{name} and an operand overlap")
+
+
 def _drop(p, rng):
     """Address of rng (0: nothing is dropped), whose device _here checks."""
     if rng is None:
@@ -119,9 +131,10 @@ def _act(act):
     return act
 
 
-def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng, *others):
+def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng, *others, clear=()):
     """The packed struct of a forward epilogue.  in_dtype: the linear's input's, or
-    None.  others: the call's other tensors, for their device."""
+    None.  others: the call's other tensors, for their device.  clear: those that
+    neither y nor pre may lie over."""
     dt = y.dtype
     ldy = N if y.shape == shape and y.is_contiguous() else _row_stride(y, "y", dt, shape, M, N)
     at = y.data_ptr()
@@ -156,6 +169,8 @@ def _epilogue(y, shape, M, N, in_dtype, bias, act, residual, pre, p, rng, *other
         _all_clear([(y, "y"), (pre, "pre")], [(bias, "bias"), (residual if residual is not y else None, "residual")])
         if residual is y:
             _clear(pre, "pre", y, "residual")
+    if clear:
+        _off_codes(y, pre, *clear)
     e = _pack(pb, pr, pp, _drop(p, rng) if rng is not None or p else 0, ldr, ldy, p, _act(act), bt)
     _here(y, bias, residual, pre, rng, *others)
     return e
@@ -235,7 +250,7 @@ def _fp8_gemm(fn, A, B, ia, ib, C, bias, act, residual, pre, p, rng, stream):
     _need(A, "A", torch.uint8)
     _need(B, "B", torch.uint8, shape=(N, K))
     ct = _type(C, "C")
-    e = _epilogue(C, (M, N), M, N, None, bias, act, residual, pre, p, rng, A, B)
+    e = _epilogue(C, (M, N), M, N, None, bias, act, residual, pre, p, rng, A, B, clear=(A, B))
     _check(getattr(lib(), fn)(_ptr(A), _ptr(B), ia, ib, e, _ptr(C), ct, M, N, K, _stream(stream)), fn)
 
 
@@ -344,7 +359,8 @@ def mxfp4_gemm_epilogue(A: Mxfp4, B: Mxfp4, C: torch.Tensor, *, bias=None, act: 
     ct = _type(C, "C")
     if C.dim() < 1 or C.shape[-1] != N or _rows(C) != M:
         raise ValueError(f"C: shape {tuple(C.shape)}, expected {M} x {N}")
-    e = _epilogue(C, C.shape, M, N, None, bias, act, residual, pre, p, rng, A.q, A.s, B.q, B.s)
+    e = _epilogue(C, C.shape, M, N, None, bias, act, residual, pre, p, rng, A.q, A.s, B.q, B.s,
+                  clear=(A.q, A.s, B.q, B.s))
     _check(lib().mxfp4_gemm_epilogue(A.c(), B.c(), e, _ptr(C), ct, M, N, A.k, _stream(stream)),
            "mxfp4_gemm_epilogue")
 

@@ -293,6 +293,8 @@ typedef struct fp8_linear_bwd_ws {
  * A layer with M*K, N*K and M*N all at most 65536 and no transposed copies
  * runs in one launch (the GEMM blocks reduce and cast what they need); the
  * codes, records and y are the same bits as the separate launches give.
+ * y may lie over x or w (any common bytes): the casts are then launches of
+ * their own, before the product.  It shares no memory with `saved`.
  */
 FP8SG_API fp8sg_status fp8_scaled_linear_fwd(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
                                    int64_t K, const fp8_linear_saved* saved, void* y,
@@ -308,7 +310,7 @@ FP8SG_API fp8sg_status fp8_scaled_linear_fwd(const uint16_t* x, const uint16_t* 
  *   gy: [M,N] bf16; gx, gw of type `out` (FP8SG_OUT_F16 feeds fp16 AMP).
  *   `saved` must come from fp8_scaled_linear_fwd with the same M, N, K.
  * Small layers without transposed copies (as for the forward) run the cast
- * of gy and both GEMMs in one launch.
+ * of gy and both GEMMs in one launch, unless gx or gw lies over gy (allowed).
  */
 FP8SG_API fp8sg_status fp8_scaled_linear_bwd(const uint16_t* gy, const fp8_linear_saved* saved,
                                    int64_t M, int64_t N, int64_t K, const fp8_linear_bwd_ws* ws,
@@ -603,7 +605,8 @@ FP8SG_API fp8sg_status amp_update_scale(float* scale, int32_t* growth_tracker, i
  * output matrices of this section need the alignment of their element type
  * only (2 or 4 bytes) and any row length; 16-byte aligned tensors whose rows
  * keep that alignment take the fast paths.  Codes and scales need 16 bytes.
- * The buffers of one call do not overlap, except where swiglu_bwd says so.
+ * The buffers of one call do not overlap, except where swiglu_bwd and
+ * mxfp4_linear_apply say so.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -711,7 +714,8 @@ FP8SG_API fp8sg_status mxfp4_linear_bwd(const void* gy, fp8sg_out type, int64_t 
  * Serving linear: y[M,N] = x[M,K] W^T with the weight held as MXFP4 (w: N x K,
  * quantised once).  x (of `type`) is quantised along K as mxfp4_quantize does;
  * the result is that of mxfp4_quantize and mxfp4_gemm up to the order of the
- * fp32 sums.  x_ws (M x K) is scratch, written or not.
+ * fp32 sums.  x_ws (M x K) is scratch, written or not.  y may lie over x: x is
+ * then quantised in a launch of its own.
  */
 FP8SG_API fp8sg_status mxfp4_linear_apply(const void* x, fp8sg_out type, const mxfp4_operand* w,
                                           int64_t M, int64_t N, int64_t K, fp8sg_mx_rule rule,
@@ -835,6 +839,8 @@ typedef enum {
  *             It may be the output itself (same address and row distance).
  *   pre:      M x N of the output's type, contiguous: the forward writes h there
  *             unless NULL; the backward step reads it (needed unless act is none).
+ *             The output and pre may lie over the linear's x or w, which are cast in
+ *             launches of their own then, and over no other buffer of the call.
  *   rng:      two words in device memory; not read where p drops nothing, else
  *             required.  8-byte aligned.
  *   ld_out:   rows of the output are this many elements apart (>= N).
