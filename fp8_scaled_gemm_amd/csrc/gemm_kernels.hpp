@@ -396,7 +396,7 @@ __device__ __forceinline__ void gemm_small_tile(const Prob& p, int bx, int by,
   if constexpr (std::is_same_v<Prob, GemmEpiProblem>) {  // (the loop ended with a barrier: the tiles are free)
     constexpr int kLds = Cfg::kTM < 4 ? Cfg::kTM * 4096 : kWaveEpilogueLds;
     static_assert(BN / WN == 64 && Cfg::kLdsBytes >= WM * WN * kLds, "wave sub-tile");
-    wave_epilogue<Cfg::kTM, EpiMode<true, false, false>, 2>(p.epi, acc, smem + wave * kLds, bm + wm * (BM / WM), bn + wn * 64,
+    wave_epilogue<Cfg::kTM, EpiMode<OUT != FP8SG_OUT_F32, false, false>, 2>(p.epi, acc, smem + wave * kLds, bm + wm * (BM / WM), bn + wn * 64,
                                      bias, RW ? 1.0f : alpha.a, [&](v4f& c, int i, int j) {
                                        if constexpr (RW) alpha.apply(c, i, j);
                                      });
@@ -865,7 +865,7 @@ __global__ __launch_bounds__(512) void k_gemm_pingpong(Prob p) {
     barrier();
     static_assert(2 * kWaveEpilogueLds == 256 * kBK, "two waves a slot");
     uint8_t* slot = wave < 2 ? sA0 : wave < 4 ? sA1 : wave < 6 ? sB0 : sB1;
-    wave_epilogue<kTM, EpiMode<true, false, true>, 4>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + wr0, bn + wc0, bias,
+    wave_epilogue<kTM, EpiMode<OUT != FP8SG_OUT_F32, false, true>, 4>(p.epi, acc, slot + (wave & 1) * kWaveEpilogueLds, bm + wr0, bn + wc0, bias,
                                 RW ? 1.0f : alpha.a, [&](v4f& c, int i, int j) {
                                   if constexpr (RW) alpha.apply(c, i, j);
                                 });

@@ -71,9 +71,10 @@ __device__ __forceinline__ void write_self_record(fp8sg_scale_rec* rec, uint32_t
   rec->inv32 = v.inv32;
 }
 
-// Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT is not used
-// then), whose tiles are smaller: a wave's epilogue is a chain of instructions for each
-// of its rows, so four times the waves take a quarter of it each.
+// Args: SmallFwdArgs, or SmallFwdEpiArgs for a product with an epilogue (OUT then only
+// says whether the result is fp32 or has 16 bits), whose tiles are smaller: a wave's
+// epilogue is a chain of instructions for each of its rows, so four times the waves take
+// a quarter of it each.
 template <class Args>
 using SmallTile = std::conditional_t<std::is_same_v<Args, SmallFwdEpiArgs>, GemmCfg<64, 64, 4, 1>, SmallCfg>;
 template <int OUT, class Args, bool F16 = false>
@@ -137,12 +138,15 @@ hipError_t launch_small_fwd(const SmallFwdArgs& a, int out, hipStream_t stream) 
 
 hipError_t launch_small_fwd_epilogue(const SmallFwdEpiArgs& a, bool f16, hipStream_t stream) {
   const dim3 grid((unsigned)((a.p.N + 63) / 64), (unsigned)((a.p.M + 63) / 64));
-  if (f16)
-    hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs, true>), grid, dim3(kSmallThreads),
-                       SmallTile<SmallFwdEpiArgs>::kLdsBytes, stream, a);
-  else
-    hipLaunchKernelGGL((k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>), grid, dim3(kSmallThreads),
-                       SmallTile<SmallFwdEpiArgs>::kLdsBytes, stream, a);
+  const size_t lds = SmallTile<SmallFwdEpiArgs>::kLdsBytes;
+  auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kSmallThreads), lds, stream, a); };
+  if (a.p.epi.type == FP8SG_OUT_F32) {
+    if (f16) launch(k_small_fwd<FP8SG_OUT_F32, SmallFwdEpiArgs, true>);
+    else launch(k_small_fwd<FP8SG_OUT_F32, SmallFwdEpiArgs>);
+  } else {
+    if (f16) launch(k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs, true>);
+    else launch(k_small_fwd<FP8SG_OUT_BF16, SmallFwdEpiArgs>);
+  }
   return hipGetLastError();
 }
 
