@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kBwd, 2) void k_epilogue_bwd(EpilogueBwdArgs p) {
           by_act(p.act, [&](auto a) {
             h[u].values(x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= slope_of<decltype(a)::value, kFast>(x[i]);
+            for (int i = 0; i < 8; ++i) v[i] = through<decltype(a)::value, kFast>(v[i], x[i]);
           });
           if (p.drop.rng) drop_n<8>(d, (uint64_t)r * groups + (uint64_t)(c >> 3), 0, v);
 #pragma unroll

@@ -168,9 +168,7 @@ __device__ __forceinline__ float act_of(float h) {
 }
 template <int ACT, bool FAST>
 __device__ __forceinline__ float slope_of(float h) {
-  if constexpr (ACT == FP8SG_ACT_RELU) {
-    return h <= 0.f ? 0.f : 1.f;
-  } else if constexpr (ACT == FP8SG_ACT_SILU) {  // s (1 + h (1 - s))
+  if constexpr (ACT == FP8SG_ACT_SILU) {  // s (1 + h (1 - s))
     const float c = __builtin_amdgcn_fmed3f(h, -150.f, 150.f);
     if constexpr (FAST) {
       const float s = inv_1p_exp2(h * -kLog2E);
@@ -200,6 +198,13 @@ __device__ __forceinline__ float slope_of(float h) {
   } else {
     return 1.0f;
   }
+}
+// The gradient g behind act at h.  relu selects: an inactive unit passes exactly 0,
+// where a product would make a NaN of an infinity.
+template <int ACT, bool FAST>
+__device__ __forceinline__ float through(float g, float h) {
+  if constexpr (ACT == FP8SG_ACT_RELU) return h <= 0.f ? 0.f : g;
+  return g * slope_of<ACT, FAST>(h);
 }
 // f(integral constant of the activation): one branch for a whole group of values
 template <class F>

@@ -110,7 +110,7 @@ __device__ __forceinline__ void epilogue_step(const EpilogueBwdArgs& p, Row8<T> 
     by_act(p.act, [&](auto a) {
       h[i].values(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] *= slope_of<decltype(a)::value, kFast>(x[e]);
+      for (int e = 0; e < 8; ++e) w[e] = through<decltype(a)::value, kFast>(w[e], x[e]);
     });
     if (p.drop.rng) drop_n<8>(d, (uint64_t)(rw + i) * groups + (uint64_t)(c >> 3), 0, w);
 #pragma unroll

@@ -884,7 +884,8 @@ FP8SG_API fp8sg_status fp8_scaled_linear_fwd_epilogue(const void* x, const void*
  * that depends on the entry point, the sizes and which outputs and workspace are
  * given, never on timing; rounded once to bias_type).
  *   gy, pre, gh: M x N of `type`, contiguous.  gh may be gy; NULL if only gb is
- *                wanted.  gb may be NULL.  act'(0) of relu is 0.
+ *                wanted.  gb may be NULL.  Where relu's pre <= 0, gh is exactly 0,
+ *                whatever gy is (relu selects); elsewhere it is gy, dropped.
  *   ws: float[ws_len], ws_len >= epilogue_workspace_len(M, N); not read before it
  *       is written; may be NULL where gb is, and up to 256 rows (where
  *       mxfp4_linear_bwd_epilogue takes one pass less with it).
