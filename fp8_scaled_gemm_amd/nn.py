@@ -1116,7 +1116,7 @@ class _EpilogueLinear(nn.Module):
     @classmethod
     def _share(cls, new, lin):
         new.weight, new.bias = lin.weight, lin.bias
-        return new
+        return new.train(lin.training)  # (a layer in evaluation does not begin to drop)
 
     @classmethod
     def _check_float(cls, lin):
@@ -1171,7 +1171,7 @@ class Float8EpilogueLinear(_EpilogueLinear):
 
     @classmethod
     def from_float(cls, lin: nn.Linear, activation: str = "none", dropout: float = 0.0) -> "Float8EpilogueLinear":
-        """One sharing lin's weight and bias (no copies)."""
+        """One sharing lin's weight and bias (no copies), in lin's mode."""
         cls._check_float(lin)
         with torch.device("meta"):
             new = cls(lin.in_features, lin.out_features, False, activation, dropout, dtype=lin.weight.dtype)
@@ -1196,9 +1196,9 @@ class MXFP4EpilogueLinear(_EpilogueLinear):
         self.rule = _mx_rule(rule)
 
     @classmethod
-    def from_float(cls, lin: nn.Module, activation: str = "none", dropout: float = 0.0,
+    def from_float(cls, lin: nn.Linear, activation: str = "none", dropout: float = 0.0,
                    rule: str = "floor") -> "MXFP4EpilogueLinear":
-        """One sharing lin's weight and bias (no copies)."""
+        """One sharing lin's weight and bias (no copies), in lin's mode."""
         cls._check_float(lin)
         with torch.device("meta"):
             new = cls(lin.in_features, lin.out_features, False, activation, dropout, rule, dtype=lin.weight.dtype)
