@@ -16,8 +16,9 @@ constexpr int kRows = 2;  // rows a thread of the backward step has in flight (f
 // run of its own: 8192 x 4096, bf16, 54 -> 46 us).  Each thread adds up its columns
 // in fp32, lanes and waves join at the end, and with several parts each leaves a row
 // of partial sums that k_bias_join adds in a fixed order (no atomics: a repeated call
-// gives the same bits).  Two blocks a compute unit: all of a launch's at most 1024
-// (a record's slots) are resident.  us for 8192 x 14336 bf16 with gelu and gb, 705 MB,
+// gives the same bits).  Two blocks fit a compute unit (87 registers: five waves a
+// SIMD; three of fp32's 72), so 512 of a launch's at most 1024 (a record's slots) are
+// in flight, the first half of the parts and then the second.  us for 8192 x 14336 bf16 with gelu and gb, 705 MB,
 // past the caches: 132 (5.3 TB/s; a copy 5.2), of which gelu 7, gb 2; 4 rows and 256
 // threads a block 136; cached accesses 146.  fp32 takes cached ones at any size: its
 // lanes' 16-byte halves of 32 bytes meet in the caches (4096 x 14336 142, non-temporal 153).

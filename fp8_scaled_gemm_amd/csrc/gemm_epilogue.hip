@@ -34,8 +34,10 @@ hipError_t launch_small(const GemmEpiProblem& p, hipStream_t stream) {
 // units: a wave's epilogue is a chain of instructions for each of its rows, which four
 // times the waves share, and so do they the k-tiles' latency.  us, tiles of 128 / 64,
 // with bias, then with gelu and h kept: 64 x 4096 x 4096 (32 tiles of 128) 32.5 / 17.4,
-// 35.2 / 18.2; 1024^3 (64) 12.6 / 7.2, 15.8 / 8.0; 2048^3 (256) 21.1 / 21.5, 25.1 / 22.7;
-// 2048 x 3584 x 1024 (448) 17.8 / 19.6, 22.3 / 22.4.
+// 35.2 / 18.2; 1024^3 (64) 12.6 / 7.2, 15.8 / 8.0; 2048 x 3584 x 1024 (448) 17.8 / 19.6,
+// 22.3 / 22.4.  At 256 of them, one for each unit, the small ones lose where little stands
+// behind a long contraction: 2048 x 2048 with K = 512 10.5 / 9.5, 14.3 / 11.3, 2048
+// 21.4 / 22.2, 25.3 / 23.4, 4096 35.8 / 39.0, 39.6 / 39.6.
 bool small_tiles(const GemmEpiProblem& p) {
   return ((p.M + 127) / 128) * ((p.N + 127) / 128) <= device_cus();
 }

@@ -794,6 +794,9 @@ double few_epilogue(const MxGemmProblem&, int, int, int) { return 0; }
 double few_epilogue(const MxGemmEpiProblem& p, int tm, int tn, int cus) {
   return (double)p.M * p.N * epilogue_slots(p.epi, few_share(tm, tn, false)) / (64 * 2400.0 * cus);
 }
+// (2048 x 2048 x 512 in tiles of 128, one round: bf16 6.5 without an epilogue, 8.0 with
+// a bias, 10 slots, 10.0 with gelu, 30, 16.7 with silu, dropout, residual and h kept, 65;
+// fp32 7.5, 9.7, 13.7 with 50, 21.1 with 85: 0.14 us a slot.)
 double mid_epilogue(const MxGemmProblem&, int) { return 0; }
 double mid_epilogue(const MxGemmEpiProblem& p, int cus) {
   const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
@@ -821,6 +824,9 @@ hipError_t launch_product(const Prob& p, hipStream_t stream) {
     hipLaunchKernelGGL((k_mx_pingpong<T, Prob>), dim3((unsigned)tiles(256)), dim3(512), 0, stream, p);
     return hipGetLastError();
   }
+  // (64 x 64 tiles have two microseconds less of fixed time with an epilogue, which joins
+  // all blocks at once instead of row by row: plain and with a bias 512 x 512 x 4096 11.4,
+  // 9.3, 1024 x 1024 x 4096 11.7, 9.6)
   auto cost = [&](int tm, int tn, FewCost c) { return few_cost(p, tm, tn, c, cus) + few_epilogue(p, tm, tn, cus); };
   const double c11 = cost(1, 1, FewCost{2.0, 0.7}), c12 = cost(1, 2, FewCost{2.4, 0.7});
   const double c22 = cost(2, 2, FewCost{3.5, 0.6}), c44 = cost(4, 4, FewCost{kEpi<Prob> ? 6.8 : 8.8, 0.7});
