@@ -401,7 +401,8 @@ def convert_to_float8_training(model: nn.Module,
     grad_scaler, the fp16 layers unscale and check their weight gradients in
     the wgrad GEMM's epilogue with that scaler.  With biased (dynamic scaling
     only), layers with a bias are replaced too, by a Float8EpilogueLinear that
-    shares both, and the default filter accepts them."""
+    shares both, and the default filter accepts them (grad_scaler is not attached to
+    those: its unscale_ takes their gradients)."""
     if biased and scaling != "dynamic":
         raise ValueError("layers with a bias are converted with dynamic scaling only")
     accept = module_filter_fn or (_biased_filter if biased else default_module_filter)
@@ -1162,7 +1163,7 @@ class Float8EpilogueLinear(_EpilogueLinear):
     Kept for the backward pass: the FP8 codes, with an activation also x W^T + b in
     the layer's dtype, with dropout its two words.  bf16 or fp16; the sizes and the
     number of rows are multiples of 16.  Gradients of an fp16 layer carry the loss
-    scale (a GradScaler's unscale_ takes them)."""
+    scale; a GradScaler's unscale_ takes them (fp16 ones: with an fp32 bias it raises)."""
     _dtypes = (torch.bfloat16, torch.float16)
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
